@@ -395,6 +395,91 @@ enum tfla_knob {
 };
 int tfla_dbg_set_knob(int knob, int value);
 
+/*
+ * ---- The operators around the recurrences -----------------------------------
+ *
+ * What stands before and after a gated linear recurrence in a model, and the
+ * recurrence with a diagonal state per channel: a short causal convolution
+ * (tfla_conv_*), a selective state space scan (tfla_scan_*) and a group norm
+ * with an activation or a gate (tfla_norm_*).  Tensors have their channels
+ * last, [B,T,D]; the element type of the activations is bf16 with
+ * TFLA_IO_BF16 in `flags`, else fp32, and parameters are fp32.
+ *
+ * Strides.  Activations may be views: a tfla_rows names the data and its
+ * batch and row strides in elements, the channels being contiguous (x as one
+ * half of a projection's output, say).  Strides are >= 0; those of an output
+ * must keep its rows apart.  Outputs must not overlap inputs or each other,
+ * except where a state is named as updated in place; views of one buffer
+ * that interleave without sharing an element are fine.  Data needs the
+ * alignment of its element type; wider alignment is faster.
+ *
+ * Padded batches.  `lengths` (device int32 [B], or NULL) gives each
+ * sequence's number of rows, clamped to [0, T].  Rows behind it count as
+ * absent whatever they hold (NaN included): outputs and gradients there are
+ * 0, states are those after the last row, a sequence of length 0 keeps its
+ * state.
+ *
+ * All calls are deterministic: the same arguments give the same bits.
+ */
+typedef struct tfla_rows {
+    void* data;
+    long long batch;   /* stride of b, elements */
+    long long row;     /* stride of t, elements */
+} tfla_rows;
+
+enum tfla_act {
+    TFLA_ACT_NONE = 0,
+    TFLA_ACT_SILU = 1,      /* u sigmoid(u) */
+    TFLA_ACT_SIGMOID = 2    /* tfla_norm_* only */
+};
+
+/*
+ * Causal depthwise convolution.  With X the K-1 rows of `state` (zeros when
+ * NULL) followed by the rows of x,
+ *
+ *     u[b,t,c] = bias[c] + sum_{j<K} weight[c,j] X[b, t-K+1+j, c],   y = act(u)
+ *
+ * state_out receives the last K-1 rows of X: what the next call takes as
+ * `state`, so that a prompt and then single tokens (T = 1) give the rows of
+ * one long call.  It may be `state` itself (updated in place).
+ *
+ *   B, T, D >= 1, B T <= 2^30, K 1 to 8; act TFLA_ACT_NONE or _SILU; flags TFLA_IO_BF16 or 0
+ *   weight [D,K], bias [D] or NULL; state, state_out [B,K-1,D] contiguous,
+ *   element type of x, or NULL (unused when K = 1)
+ *
+ * Backward: from dy and dstate_out (the gradient of state_out, or NULL) the
+ * gradients dx, dweight, dbias (NULL exactly when bias is) and dstate (the
+ * gradient of `state`; NULL when not wanted).  Fields of the other direction
+ * are ignored.
+ */
+typedef struct tfla_conv_args {
+    int B, T, D, K, flags, act;
+    tfla_rows x;
+    const float* weight;
+    const float* bias;
+    const void* state;
+    const int* lengths;
+    /* tfla_conv_fwd */
+    tfla_rows y;
+    void* state_out;
+    /* tfla_conv_bwd */
+    tfla_rows dy;
+    const void* dstate_out;
+    tfla_rows dx;
+    float* dweight;
+    float* dbias;
+    void* dstate;
+} tfla_conv_args;
+
+int tfla_conv_fwd(const tfla_conv_args* args, void* stream);
+
+/* Workspace: `workspace` of at least tfla_conv_bwd_workspace_bytes bytes,
+ * 256-byte aligned and disjoint from every tensor; NULL lets the call
+ * allocate it stream-ordered (as tfla_bwd does).  The size depends on
+ * B, T, D, K, flags only; 0 for arguments out of range. */
+size_t tfla_conv_bwd_workspace_bytes(int B, int T, int D, int K, int flags);
+int tfla_conv_bwd(const tfla_conv_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* tfla_error_string(int code);
 /* Thread-local detail of the last failing call on this thread ("" if none). */

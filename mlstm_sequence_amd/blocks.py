@@ -1,0 +1,182 @@
+"""The operators around the recurrences on torch tensors (include/tfla.h):
+causal depthwise convolution, selective state space scan, and group norm with
+an activation or a gate; :mod:`mlstm_sequence_amd.tfla` offers the same names.
+
+Argument checks, output allocation and marshalling only; the work runs in the
+library's HIP kernels on torch's current stream of the tensors' device (or the
+given one).  Activations are [B,T,...] with contiguous channels and any batch
+and row strides, so views of projections need no copy; a tensor that does not
+fit is refused, never copied.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+ACT_NONE, ACT_SILU, ACT_SIGMOID = 0, 1, 2
+
+_IO = {torch.bfloat16: 0x100, torch.float32: 0}
+_i, _p, _ll = ctypes.c_int, ctypes.c_void_p, ctypes.c_longlong
+
+
+class Rows(ctypes.Structure):
+    """tfla_rows: data pointer, batch and row strides in elements."""
+    _fields_ = [("data", _p), ("batch", _ll), ("row", _ll)]
+
+
+class ConvArgs(ctypes.Structure):
+    """tfla_conv_args."""
+    _fields_ = [("B", _i), ("T", _i), ("D", _i), ("K", _i), ("flags", _i), ("act", _i),
+                ("x", Rows), ("weight", _p), ("bias", _p), ("state", _p), ("lengths", _p),
+                ("y", Rows), ("state_out", _p),
+                ("dy", Rows), ("dstate_out", _p), ("dx", Rows), ("dweight", _p), ("dbias", _p), ("dstate", _p)]
+
+
+def bind(L):
+    """Argument types of this module's entry points."""
+    vp, sz = ctypes.c_void_p, ctypes.c_size_t
+    for name, args, res in (
+            ("tfla_conv_fwd", [ctypes.POINTER(ConvArgs), vp], _i),
+            ("tfla_conv_bwd_workspace_bytes", [_i] * 5, sz),
+            ("tfla_conv_bwd", [ctypes.POINTER(ConvArgs), vp, sz, vp], _i)):
+        f = getattr(L, name)
+        f.argtypes, f.restype = args, res
+
+
+def _lib():
+    from . import tfla
+    return tfla.lib()
+
+
+# ---- checks ------------------------------------------------------------------
+
+def _first(x, name, dims):
+    """The tensor that sets type and device."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(x).__name__}")
+    if x.dtype not in _IO:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {x.dtype}")
+    if x.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(x.shape)}")
+    if max(x.shape, default=0) > 0x7FFFFFFF:
+        raise ValueError(f"{name}: dimensions above 2^31 - 1 are not supported, got {tuple(x.shape)}")
+    if not x.is_cuda:
+        raise ValueError(f"tensors must live in GPU memory, got {name} on {x.device}")
+    return x.device
+
+
+def _like(t, name, shape, dtype, dev):
+    """Shape, type and device of ``t``; whether its last dimension is contiguous is left to the caller."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, other tensors on {dev}")
+
+
+def _flat(t, name, shape, dtype, dev):
+    """Pointer of a contiguous tensor (None: NULL)."""
+    if t is None:
+        return None
+    _like(t, name, shape, dtype, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous (row-major), got strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _rows(t, name, shape, dtype, dev):
+    """tfla_rows of a [B,T,D] tensor with contiguous channels."""
+    _like(t, name, shape, dtype, dev)
+    st = t.stride()
+    if st[2] != 1 and shape[2] > 1:
+        raise ValueError(f"{name} must have contiguous channels (last stride 1), got strides {st}")
+    return Rows(t.data_ptr(), st[0], st[1])
+
+
+def _call(name, args, dev, stream, nbytes=None, workspace=None):
+    """Calls entry point ``name`` on ``stream`` (None: the device's current
+    one) with the tensors' device current; ``nbytes``: the workspace it needs."""
+    from . import tfla
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(name, args, dev, stream, nbytes, workspace)
+    current = torch.cuda.current_stream().cuda_stream
+    s = current if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
+    fn = getattr(tfla.lib(), name)
+    if nbytes is None:
+        rc = fn(ctypes.byref(args), s)
+    else:
+        if workspace is not None:
+            tfla._check_workspace(workspace, nbytes, dev)
+            size = workspace.numel() * workspace.element_size()
+        elif nbytes and s == current:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            size = nbytes
+        else:
+            size = 0   # another stream than torch's current one: the library allocates in that stream's order
+        rc = fn(ctypes.byref(args), None if workspace is None else workspace.data_ptr(), size, s)
+    if rc:
+        tfla._check(rc, name)
+
+
+# ---- causal convolution --------------------------------------------------------
+
+def _conv_args(x, weight, bias, act, state, lengths):
+    dev = _first(x, "x", 3)
+    B, T, D = x.shape
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be a [D,K] tensor")
+    K = weight.shape[1]
+    a = ConvArgs()
+    a.B, a.T, a.D, a.K, a.flags, a.act = B, T, D, K, _IO[x.dtype], act
+    a.x = _rows(x, "x", x.shape, x.dtype, dev)
+    a.weight = _flat(weight, "weight", (D, K), torch.float32, dev)
+    a.bias = _flat(bias, "bias", (D,), torch.float32, dev)
+    a.state = _flat(state, "state", (B, K - 1, D), x.dtype, dev)
+    a.lengths = _flat(lengths, "lengths", (B,), torch.int32, dev)
+    return a, dev
+
+
+def conv_forward(x, weight, bias=None, act: int = ACT_SILU, state=None, lengths=None, want_state: bool = False,
+                 y=None, state_out=None, stream=None):
+    """Causal depthwise convolution of x [B,T,D] with weight [D,K] (fp32),
+    ``y = act(conv(x) + bias)``; returns ``(y, state_out)``.
+
+    ``state`` [B,K-1,D] holds the inputs before the first row (None: zeros);
+    ``state_out`` (allocated with ``want_state``, may be ``state`` itself)
+    receives the last K-1 inputs, what the next call continues from.
+    ``lengths`` int32 [B]: valid rows of each sequence of a padded batch."""
+    a, dev = _conv_args(x, weight, bias, act, state, lengths)
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    if state_out is None and want_state:
+        state_out = torch.empty((a.B, a.K - 1, a.D), dtype=x.dtype, device=dev)
+    a.y = _rows(y, "y", x.shape, x.dtype, dev)
+    a.state_out = _flat(state_out, "state_out", (a.B, a.K - 1, a.D), x.dtype, dev)
+    _call("tfla_conv_fwd", a, dev, stream)
+    return y, state_out
+
+
+def conv_backward(x, weight, dy, bias=None, act: int = ACT_SILU, state=None, lengths=None, dstate_out=None, dx=None,
+                  workspace=None, stream=None):
+    """Gradients of :func:`conv_forward` for ``dy`` and (with carried states)
+    ``dstate_out``; returns ``(dx, dweight, dbias, dstate)``, dbias None
+    without bias, dstate None without state."""
+    a, dev = _conv_args(x, weight, bias, act, state, lengths)
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dweight = torch.empty_like(weight)
+    dbias = None if bias is None else torch.empty_like(bias)
+    dstate = None if state is None else torch.empty_like(state)
+    a.dy = _rows(dy, "dy", x.shape, x.dtype, dev)
+    a.dx = _rows(dx, "dx", x.shape, x.dtype, dev)
+    a.dstate_out = _flat(dstate_out, "dstate_out", (a.B, a.K - 1, a.D), x.dtype, dev)
+    a.dweight = dweight.data_ptr()
+    a.dbias = None if dbias is None else dbias.data_ptr()
+    a.dstate = None if dstate is None else dstate.data_ptr()
+    _call("tfla_conv_bwd", a, dev, stream, _lib().tfla_conv_bwd_workspace_bytes(a.B, a.T, a.D, a.K, a.flags), workspace)
+    return dx, dweight, dbias, dstate

@@ -1,0 +1,42 @@
+// blocks.hpp -- the operators around the recurrences (internal): problem
+// descriptions and launchers of the causal convolution, the selective scan
+// and the group norm.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include <string>
+
+namespace tfla {
+
+// Records the thread's error message and returns `code` (tfla_api.cpp).
+int fail(int code, const std::string& msg);
+// Whether a test asked the library's own allocations to fail.
+bool inject_alloc_fault();
+
+// Rows of a [B,T,width] tensor: element (b,t,c) at p[b * batch + t * row + c].
+struct Rows {
+    void* p = nullptr;
+    int64_t batch = 0, row = 0;
+};
+
+// ---- causal depthwise convolution (conv.hip) ------------------------------------
+struct ConvProblem {
+    int B, T, D, K;
+    bool bf16, silu;
+    Rows x, y, dy, dx;
+    const float *weight, *bias;
+    const int* lengths;
+    const void *state, *dstate_out;
+    void *state_out, *dstate;
+    float *dweight, *dbias;
+    float* part;      // backward workspace [parts][K+1][D]: weight and bias gradients of runs of rows
+};
+
+size_t conv_bwd_workspace(int B, int T, int D, int K, bool bf16);
+hipError_t launch_conv_fwd(const ConvProblem& p, hipStream_t stream);
+hipError_t launch_conv_bwd(const ConvProblem& p, hipStream_t stream);
+
+}  // namespace tfla

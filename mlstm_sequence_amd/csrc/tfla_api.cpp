@@ -11,17 +11,28 @@
 #include <mutex>
 #include <string>
 
+#include "blocks.hpp"
 #include "kernels.hpp"
 
 namespace {
 
 thread_local std::string g_last_error;
 
+}  // namespace
+
+namespace tfla {
+
 int fail(int code, const std::string& msg)
 {
     g_last_error = msg;
     return code;
 }
+
+}  // namespace tfla
+
+namespace {
+
+using tfla::fail;
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -205,7 +216,7 @@ std::atomic<int> g_knobs[TFLA_KNOB_COUNT] = {-1, -1, -1, -1, -1, -1, -1};
 
 // Failure injection for tests of the error paths: the fault knob set to 1
 // makes the library's own workspace allocation fail before any launch.
-bool inject_alloc_fault() { return tfla::knob(TFLA_KNOB_FAULT_ALLOC) == 1; }
+using tfla::inject_alloc_fault;
 
 int hip_fail(hipError_t e, const char* what)
 {
@@ -550,6 +561,8 @@ int bwd_entry(const void* q, const void* k, const void* v, const float* igate_pr
 }  // namespace
 
 namespace tfla {
+
+bool inject_alloc_fault() { return knob(TFLA_KNOB_FAULT_ALLOC) == 1; }
 
 int knob(int which)
 {

@@ -12,6 +12,11 @@ import os
 
 import torch  # loaded first: libtfla then shares torch's HIP runtime (same SONAME)
 
+from . import blocks as _blocks
+from .blocks import (  # noqa: F401
+    ACT_NONE, ACT_SIGMOID, ACT_SILU, ConvArgs, Rows, conv_backward, conv_forward,
+)
+
 MLSTM_SIG = 0
 SCALAR_DECAY = 1
 GLA_KEY = 2
@@ -89,6 +94,7 @@ def lib():
         L.tfla_last_error.restype = ctypes.c_char_p
         L.tfla_version.argtypes = []
         L.tfla_version.restype = i
+        _blocks.bind(L)
         _lib = L
     return _lib
 

@@ -1,0 +1,119 @@
+"""Refusals of the operators around the recurrences, on the CPU: bad
+arguments are answered by the host checks, before any HIP call.  Pointers are
+fake aligned device addresses that no check follows."""
+import ctypes
+
+import pytest
+import torch
+
+tfla = pytest.importorskip("mlstm_sequence_amd.tfla")
+from mlstm_sequence_amd import blocks  # noqa: E402
+
+BF16 = 0x100
+INVALID, UNSUPPORTED, OOM = 1, 2, 4
+
+
+def at(n):
+    return 0x100000000 * (n + 1)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import os
+    if not os.path.exists(tfla.LIB_PATH):
+        pytest.skip("libtfla.so not built")
+    tfla.lib()
+
+
+def put(args, kw):
+    """Sets fields; "x.row" names a field of a field."""
+    for k, v in kw.items():
+        o = args
+        *path, last = k.split(".")
+        for name in path:
+            o = getattr(o, name)
+        setattr(o, last, v)
+    return args
+
+
+# ---- convolution -------------------------------------------------------------------
+
+def conv_args(**kw):
+    B, T, D, K = 2, 300, 64, 4
+    a = blocks.ConvArgs(B=B, T=T, D=D, K=K, flags=BF16, act=1)
+    rows = lambda p: blocks.Rows(p, T * D, D)  # noqa: E731
+    a.x, a.y, a.dy, a.dx = rows(at(0)), rows(at(1)), rows(at(2)), rows(at(3))
+    a.weight, a.bias, a.state, a.state_out, a.lengths = at(4), at(5), at(6), at(7), at(8)
+    a.dstate_out, a.dweight, a.dbias, a.dstate = at(9), at(10), at(11), at(12)
+    return put(a, kw)
+
+
+CONV_BOTH = [
+    ({"B": 0}, INVALID), ({"T": 0}, INVALID), ({"D": -1}, INVALID), ({"K": 0}, INVALID), ({"K": 9}, UNSUPPORTED),
+    ({"flags": 0x200}, INVALID), ({"act": 2}, INVALID), ({"act": -1}, INVALID),
+    ({"B": 1 << 16, "T": 1 << 15}, UNSUPPORTED), ({"D": (1 << 24) + 1}, UNSUPPORTED),
+    ({"x.data": None}, INVALID), ({"weight": None}, INVALID), ({"x.data": at(0) + 1}, INVALID),
+    ({"weight": at(4) + 2}, INVALID), ({"bias": at(5) + 1}, INVALID), ({"lengths": at(8) + 2}, INVALID),
+    ({"state": at(6) + 1}, INVALID), ({"x.row": -1}, INVALID), ({"x.batch": -64}, INVALID),
+    ({"x.row": 1 << 62}, INVALID), ({"x.batch": 1 << 50}, INVALID),
+]
+
+
+@pytest.mark.parametrize("kw,code", CONV_BOTH + [
+    ({"y.data": None}, INVALID), ({"y.row": 63}, INVALID), ({"y.batch": 0}, INVALID), ({"y.batch": 64}, INVALID),
+    ({"y.data": at(0)}, INVALID), ({"y.data": at(4)}, INVALID), ({"state_out": at(0) + 128}, INVALID),
+    ({"state_out": at(6) + 2}, INVALID), ({"state_out": at(1)}, INVALID), ({"y.data": at(8) - 2}, INVALID),
+])
+def test_conv_fwd_refuses(kw, code):
+    assert tfla.lib().tfla_conv_fwd(ctypes.byref(conv_args(**kw)), None) == code
+    assert tfla.tfla_last_error()
+
+
+@pytest.mark.parametrize("kw,code", CONV_BOTH + [
+    ({"dy.data": None}, INVALID), ({"dx.data": None}, INVALID), ({"dweight": None}, INVALID), ({"dbias": None}, INVALID),
+    ({"bias": None}, INVALID), ({"dx.row": 32}, INVALID), ({"dx.data": at(2)}, INVALID), ({"dx.data": at(0)}, INVALID),
+    ({"dstate": at(9)}, INVALID), ({"dstate": at(6)}, INVALID), ({"dweight": at(10) + 2}, INVALID),
+    ({"dbias": at(10)}, INVALID),
+])
+def test_conv_bwd_refuses(kw, code):
+    a = conv_args(**kw)
+    assert tfla.lib().tfla_conv_bwd(ctypes.byref(a), None, 0, None) == code
+    assert tfla.tfla_last_error()
+
+
+def test_conv_bwd_workspace():
+    L = tfla.lib()
+    n = L.tfla_conv_bwd_workspace_bytes(2, 300, 64, 4, BF16)
+    assert n > 0
+    for bad in ((0, 300, 64, 4, BF16), (2, 300, 64, 9, BF16), (2, 300, 64, 4, 0x400)):
+        assert L.tfla_conv_bwd_workspace_bytes(*bad) == 0
+    a = conv_args()
+    assert L.tfla_conv_bwd(ctypes.byref(a), at(20), n - 1, None) == OOM
+    assert L.tfla_conv_bwd(ctypes.byref(a), at(20) + 16, n, None) == INVALID
+    assert L.tfla_conv_bwd(ctypes.byref(a), at(2), n, None) == INVALID     # on top of dy
+    assert "workspace overlaps dy" in tfla.tfla_last_error()
+
+
+def test_null_args():
+    L = tfla.lib()
+    assert L.tfla_conv_fwd(None, None) == INVALID
+    assert L.tfla_conv_bwd(None, None, 0, None) == INVALID
+
+
+def test_injected_allocation_failure(set_knob):
+    set_knob(tfla.KNOB_FAULT_ALLOC, 1)
+    a = conv_args()
+    assert tfla.lib().tfla_conv_bwd(ctypes.byref(a), None, 0, None) == OOM
+    assert "injected" in tfla.tfla_last_error()
+
+
+def test_python_checks_refuse():
+    x, w = torch.zeros(2, 5, 8), torch.zeros(8, 4)
+    with pytest.raises(ValueError, match="GPU memory"):
+        tfla.conv_forward(x, w)
+    with pytest.raises(TypeError):
+        tfla.conv_forward(x.half(), w)
+    with pytest.raises(ValueError, match="3 dimensions"):
+        tfla.conv_forward(x[0], w)
+    with pytest.raises(TypeError):
+        tfla.conv_forward(None, w)
