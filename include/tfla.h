@@ -480,6 +480,62 @@ int tfla_conv_fwd(const tfla_conv_args* args, void* stream);
 size_t tfla_conv_bwd_workspace_bytes(int B, int T, int D, int K, int flags);
 int tfla_conv_bwd(const tfla_conv_args* args, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Selective state space scan.  Per channel c (of group g = c / (D/G)) and
+ * state n,
+ *
+ *     delta_t = softplus(dt_t + dt_bias)      (dt_t + dt_bias without TFLA_SCAN_SOFTPLUS)
+ *     h_t[n]  = exp(delta_t a[c,n]) h_{t-1}[n] + delta_t x_t bmat[t,g,n]
+ *     o_t     = sum_n cmat[t,g,n] h_t[n] + skip[c] x_t,      y_t = o_t  or  o_t z_t sigmoid(z_t)
+ *
+ * from h_{-1} = `state` (zeros when NULL); state_out receives the state after
+ * the last row and may be `state` itself (updated in place), so the same call
+ * serves prompts and single tokens (T = 1).  States are fp32 throughout.
+ *
+ *   B, T, D >= 1, B T <= 2^30; G divides D; N a multiple of 4 up to 64
+ *   x, dt, z, y   [B,T,D], z.data NULL for no gate; dt is x's type
+ *   bmat, cmat    [B,T,G,N], the last two dimensions contiguous; addresses and strides
+ *                 multiples of 4 bytes
+ *   a [D,N], skip [D] or NULL, dt_bias [D] or NULL, state, state_out [B,D,N] or NULL: fp32
+ *   flags         TFLA_IO_BF16 and/or TFLA_SCAN_SOFTPLUS
+ *
+ * exp(delta a) has to stay finite (a <= 0 in use); steps of any size are
+ * exact to rounding, a decay below the smallest fp32 value is 0.
+ *
+ * Backward: from dy and dstate_out (or NULL) the gradients dx, ddt, dbmat,
+ * dcmat (element type of x), da, and dskip, ddt_bias, dz (each NULL exactly
+ * when its input is), dstate (or NULL).  It recomputes the states from the
+ * inputs.
+ */
+#define TFLA_SCAN_SOFTPLUS 0x1000
+typedef struct tfla_scan_args {
+    int B, T, D, N, G, flags;
+    tfla_rows x, dt, z, bmat, cmat;
+    const float* a;
+    const float* skip;
+    const float* dt_bias;
+    const float* state;
+    const int* lengths;
+    /* tfla_scan_fwd */
+    tfla_rows y;
+    float* state_out;
+    /* tfla_scan_bwd */
+    tfla_rows dy;
+    const float* dstate_out;
+    tfla_rows dx, ddt, dz, dbmat, dcmat;
+    float* da;
+    float* dskip;
+    float* ddt_bias;
+    float* dstate;
+} tfla_scan_args;
+
+/* Workspaces as for tfla_conv_bwd; the forward pass needs one (of a size that
+ * may be 0) when it splits a long axis over workgroups. */
+size_t tfla_scan_workspace_bytes(int B, int T, int D, int N, int G, int flags);
+int tfla_scan_fwd(const tfla_scan_args* args, void* workspace, size_t workspace_bytes, void* stream);
+size_t tfla_scan_bwd_workspace_bytes(int B, int T, int D, int N, int G, int flags);
+int tfla_scan_bwd(const tfla_scan_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* tfla_error_string(int code);
 /* Thread-local detail of the last failing call on this thread ("" if none). */

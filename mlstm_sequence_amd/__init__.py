@@ -6,7 +6,7 @@ The compute path is the C-ABI library ``libtfla.so`` built from ``csrc/``;
 """
 from .tfla import (  # noqa: F401
     ACT_NONE, ACT_SIGMOID, ACT_SILU, GLA_KEY, IO_BF16, MLSTM_SIG, SCALAR_DECAY, TflaError, conv_backward,
-    conv_forward, forward, tfla_dbg_gates, tfla_dbg_states,
+    conv_forward, forward, scan_backward, scan_forward, tfla_dbg_gates, tfla_dbg_states,
     tfla_fwd, tfla_fwd_ws, tfla_last_error, tfla_version, tfla_workspace_bytes, variant_of,
     workspace_for,
 )

@@ -11,10 +11,13 @@ fit is refused, never copied.
 from __future__ import annotations
 
 import ctypes
+from typing import NamedTuple, Optional
 
 import torch
 
 ACT_NONE, ACT_SILU, ACT_SIGMOID = 0, 1, 2
+
+SCAN_SOFTPLUS = 0x1000
 
 _IO = {torch.bfloat16: 0x100, torch.float32: 0}
 _i, _p, _ll = ctypes.c_int, ctypes.c_void_p, ctypes.c_longlong
@@ -33,13 +36,27 @@ class ConvArgs(ctypes.Structure):
                 ("dy", Rows), ("dstate_out", _p), ("dx", Rows), ("dweight", _p), ("dbias", _p), ("dstate", _p)]
 
 
+class ScanArgs(ctypes.Structure):
+    """tfla_scan_args."""
+    _fields_ = [("B", _i), ("T", _i), ("D", _i), ("N", _i), ("G", _i), ("flags", _i),
+                ("x", Rows), ("dt", Rows), ("z", Rows), ("bmat", Rows), ("cmat", Rows),
+                ("a", _p), ("skip", _p), ("dt_bias", _p), ("state", _p), ("lengths", _p),
+                ("y", Rows), ("state_out", _p),
+                ("dy", Rows), ("dstate_out", _p), ("dx", Rows), ("ddt", Rows), ("dz", Rows), ("dbmat", Rows),
+                ("dcmat", Rows), ("da", _p), ("dskip", _p), ("ddt_bias", _p), ("dstate", _p)]
+
+
 def bind(L):
     """Argument types of this module's entry points."""
     vp, sz = ctypes.c_void_p, ctypes.c_size_t
     for name, args, res in (
             ("tfla_conv_fwd", [ctypes.POINTER(ConvArgs), vp], _i),
             ("tfla_conv_bwd_workspace_bytes", [_i] * 5, sz),
-            ("tfla_conv_bwd", [ctypes.POINTER(ConvArgs), vp, sz, vp], _i)):
+            ("tfla_conv_bwd", [ctypes.POINTER(ConvArgs), vp, sz, vp], _i),
+            ("tfla_scan_workspace_bytes", [_i] * 6, sz),
+            ("tfla_scan_fwd", [ctypes.POINTER(ScanArgs), vp, sz, vp], _i),
+            ("tfla_scan_bwd_workspace_bytes", [_i] * 6, sz),
+            ("tfla_scan_bwd", [ctypes.POINTER(ScanArgs), vp, sz, vp], _i)):
         f = getattr(L, name)
         f.argtypes, f.restype = args, res
 
@@ -180,3 +197,104 @@ def conv_backward(x, weight, dy, bias=None, act: int = ACT_SILU, state=None, len
     a.dstate = None if dstate is None else dstate.data_ptr()
     _call("tfla_conv_bwd", a, dev, stream, _lib().tfla_conv_bwd_workspace_bytes(a.B, a.T, a.D, a.K, a.flags), workspace)
     return dx, dweight, dbias, dstate
+
+
+# ---- selective scan ------------------------------------------------------------------
+
+class ScanGrads(NamedTuple):
+    """Gradients of :func:`scan_forward`; None where the input was None."""
+    dx: torch.Tensor
+    ddt: torch.Tensor
+    da: torch.Tensor
+    dbmat: torch.Tensor
+    dcmat: torch.Tensor
+    dskip: Optional[torch.Tensor]
+    dz: Optional[torch.Tensor]
+    ddt_bias: Optional[torch.Tensor]
+    dstate: Optional[torch.Tensor]
+
+
+def _group_rows(t, name, shape, dtype, dev):
+    """tfla_rows of a [B,T,G,N] tensor whose last two dimensions are contiguous."""
+    _like(t, name, shape, dtype, dev)
+    st = t.stride()
+    if (st[3] != 1 and shape[3] > 1) or (st[2] != shape[3] and shape[2] > 1):
+        raise ValueError(f"{name} must have its last two dimensions contiguous, got strides {st}")
+    return Rows(t.data_ptr(), st[0], st[1])
+
+
+def _scan_args(x, dt, a, bmat, cmat, skip, z, dt_bias, softplus, state, lengths):
+    dev = _first(x, "x", 3)
+    shape, dtype = x.shape, x.dtype
+    B, T, D = shape
+    if not isinstance(bmat, torch.Tensor) or bmat.dim() != 4:
+        raise ValueError("bmat and cmat must be [B,T,G,N] tensors")
+    G, N = bmat.shape[2:]
+    s = ScanArgs()
+    s.B, s.T, s.D, s.N, s.G, s.flags = B, T, D, N, G, _IO[dtype] | (SCAN_SOFTPLUS if softplus else 0)
+    s.x = _rows(x, "x", shape, dtype, dev)
+    s.dt = _rows(dt, "dt", shape, dtype, dev)
+    if z is not None:
+        s.z = _rows(z, "z", shape, dtype, dev)
+    s.bmat = _group_rows(bmat, "bmat", (B, T, G, N), dtype, dev)
+    s.cmat = _group_rows(cmat, "cmat", (B, T, G, N), dtype, dev)
+    s.a = _flat(a, "a", (D, N), torch.float32, dev)
+    s.skip = _flat(skip, "skip", (D,), torch.float32, dev)
+    s.dt_bias = _flat(dt_bias, "dt_bias", (D,), torch.float32, dev)
+    s.state = _flat(state, "state", (B, D, N), torch.float32, dev)
+    s.lengths = _flat(lengths, "lengths", (B,), torch.int32, dev)
+    return s, dev
+
+
+def scan_forward(x, dt, a, bmat, cmat, skip=None, z=None, dt_bias=None, softplus: bool = True, state=None, lengths=None,
+                 want_state: bool = False, y=None, state_out=None, workspace=None, stream=None):
+    """Selective state space scan of x [B,T,D]: ``delta = softplus(dt + dt_bias)``,
+    ``h = exp(delta a) h + delta x bmat``, ``y = cmat . h + skip x``, times
+    ``z sigmoid(z)`` when z is given; returns ``(y, state_out)``.
+
+    a [D,N], skip and dt_bias [D] are fp32; bmat, cmat [B,T,G,N] serve D/G
+    channels each.  ``state`` fp32 [B,D,N] is the state before the first row;
+    ``state_out`` (allocated with ``want_state``, may be ``state`` itself) the
+    one after the last.  ``lengths`` int32 [B]: valid rows of a padded batch."""
+    s, dev = _scan_args(x, dt, a, bmat, cmat, skip, z, dt_bias, softplus, state, lengths)
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    if state_out is None and want_state:
+        state_out = torch.empty((s.B, s.D, s.N), dtype=torch.float32, device=dev)
+    s.y = _rows(y, "y", x.shape, x.dtype, dev)
+    s.state_out = _flat(state_out, "state_out", (s.B, s.D, s.N), torch.float32, dev)
+    n = _lib().tfla_scan_workspace_bytes(s.B, s.T, s.D, s.N, s.G, s.flags)
+    _call("tfla_scan_fwd", s, dev, stream, n, workspace)
+    return y, state_out
+
+
+def scan_backward(x, dt, a, bmat, cmat, dy, skip=None, z=None, dt_bias=None, softplus: bool = True, state=None,
+                  lengths=None, dstate_out=None, dx=None, ddt=None, dz=None, dbmat=None, dcmat=None, workspace=None,
+                  stream=None) -> ScanGrads:
+    """Gradients of :func:`scan_forward` for ``dy`` and (with carried states)
+    ``dstate_out``.  dx, ddt, dz, dbmat and dcmat may be given, as parts of
+    a projection's gradient for instance."""
+    s, dev = _scan_args(x, dt, a, bmat, cmat, skip, z, dt_bias, softplus, state, lengths)
+    shape, dtype, bc = x.shape, x.dtype, bmat.shape
+    new = lambda like, t: torch.empty(like, dtype=dtype, device=dev) if t is None else t  # noqa: E731
+    dx, ddt, dbmat, dcmat = new(shape, dx), new(shape, ddt), new(bc, dbmat), new(bc, dcmat)
+    dz = None if z is None else new(shape, dz)
+    da = torch.empty_like(a)
+    dskip = None if skip is None else torch.empty_like(skip)
+    ddt_bias = None if dt_bias is None else torch.empty_like(dt_bias)
+    dstate = None if state is None else torch.empty_like(state)
+    s.dy = _rows(dy, "dy", shape, dtype, dev)
+    s.dstate_out = _flat(dstate_out, "dstate_out", (s.B, s.D, s.N), torch.float32, dev)
+    s.dx = _rows(dx, "dx", shape, dtype, dev)
+    s.ddt = _rows(ddt, "ddt", shape, dtype, dev)
+    if z is not None:
+        s.dz = _rows(dz, "dz", shape, dtype, dev)
+    s.dbmat = _group_rows(dbmat, "dbmat", bc, dtype, dev)
+    s.dcmat = _group_rows(dcmat, "dcmat", bc, dtype, dev)
+    s.da = da.data_ptr()
+    s.dskip = None if dskip is None else dskip.data_ptr()
+    s.ddt_bias = None if ddt_bias is None else ddt_bias.data_ptr()
+    s.dstate = None if dstate is None else dstate.data_ptr()
+    n = _lib().tfla_scan_bwd_workspace_bytes(s.B, s.T, s.D, s.N, s.G, s.flags)
+    _call("tfla_scan_bwd", s, dev, stream, n, workspace)
+    return ScanGrads(dx, ddt, da, dbmat, dcmat, dskip, dz, ddt_bias, dstate)

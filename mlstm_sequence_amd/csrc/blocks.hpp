@@ -39,4 +39,26 @@ size_t conv_bwd_workspace(int B, int T, int D, int K, bool bf16);
 hipError_t launch_conv_fwd(const ConvProblem& p, hipStream_t stream);
 hipError_t launch_conv_bwd(const ConvProblem& p, hipStream_t stream);
 
+// ---- selective state space scan (scan.hip, scan_bwd.hip) ----------------------------
+struct ScanProblem {
+    int B, T, D, N, G;
+    bool bf16, softplus;
+    Rows x, dt, z, bmat, cmat;              // z.p NULL: no gate; bmat, cmat rows of [G][N]
+    const float *a, *skip, *dt_bias;        // [D,N], [D] or NULL, [D] or NULL
+    const float* state;                     // [B,D,N] or NULL
+    const int* lengths;
+    Rows y;
+    float* state_out;
+    // backward
+    Rows dy, dx, ddt, dz, dbmat, dcmat;
+    const float* dstate_out;
+    float *da, *dskip, *ddt_bias, *dstate;
+    char* ws;
+};
+
+size_t scan_workspace(const ScanProblem& p);
+hipError_t launch_scan_fwd(const ScanProblem& p, hipStream_t stream);
+size_t scan_bwd_workspace(const ScanProblem& p);
+hipError_t launch_scan_bwd(const ScanProblem& p, hipStream_t stream);
+
 }  // namespace tfla

@@ -311,9 +311,153 @@ int check_conv(const tfla_conv_args* a, bool bwd, tfla::ConvProblem* p, View* vi
     return TFLA_OK;
 }
 
+// ---- selective scan ---------------------------------------------------------------------
+
+int check_scan_sizes(int B, int T, int D, int N, int G, int flags, tfla::ScanProblem* p)
+{
+    if (flags & ~(TFLA_IO_BF16 | TFLA_SCAN_SOFTPLUS))
+        return fail(TFLA_ERR_INVALID_ARG, "unknown flags " + std::to_string(flags));
+    if (B < 1 || T < 1 || D < 1 || N < 1 || G < 1)
+        return fail(TFLA_ERR_INVALID_ARG, "B, T, D, N and G must be >= 1");
+    if (D % G) return fail(TFLA_ERR_INVALID_ARG, "G must divide D");
+    if (N % 4 || N > 64) return fail(TFLA_ERR_UNSUPPORTED, "N must be a multiple of 4 up to 64, got " + std::to_string(N));
+    if ((int64_t)B * T > kMaxRows) return fail(TFLA_ERR_UNSUPPORTED, "B*T must be <= 2^30");
+    if (D > (1 << 24)) return fail(TFLA_ERR_UNSUPPORTED, "D must be <= 2^24");
+    const int64_t lim = (int64_t(1) << 31) - 1;
+    if ((int64_t)B * G * ((D / G + 63) / 64) > lim || (int64_t)B * T * G * N / 128 + (int64_t)D * N / 256 + D > lim)
+        return fail(TFLA_ERR_UNSUPPORTED, "problem too large for one launch grid");
+    *p = tfla::ScanProblem{};
+    p->B = B;
+    p->T = T;
+    p->D = D;
+    p->N = N;
+    p->G = G;
+    p->bf16 = (flags & TFLA_IO_BF16) != 0;
+    p->softplus = (flags & TFLA_SCAN_SOFTPLUS) != 0;
+    return TFLA_OK;
+}
+
+// B and C are read in scalar loads of whole words.
+int check_words(const char* name, const tfla_rows& r, int B, int T, int64_t esz)
+{
+    if (reinterpret_cast<uintptr_t>(r.data) % 4 || (B > 1 && r.batch * esz % 4) || (T > 1 && r.row * esz % 4))
+        return fail(TFLA_ERR_INVALID_ARG, std::string(name) + ": address and strides must be multiples of 4 bytes");
+    return TFLA_OK;
+}
+
+int check_scan(const tfla_scan_args* a, bool bwd, tfla::ScanProblem* p, View* views, size_t* nv)
+{
+    if (!a) return fail(TFLA_ERR_INVALID_ARG, "args is NULL");
+    const int B = a->B, T = a->T;
+    int rc = check_scan_sizes(B, T, a->D, a->N, a->G, a->flags, p);
+    if (rc) return rc;
+    const int64_t D = a->D, GN = (int64_t)a->G * a->N, e = p->bf16 ? 2 : 4;
+    const int64_t sb = (int64_t)B * D * a->N * 4, ab = D * a->N * 4;
+    size_t n = 0;
+    auto in_rows = [&](const char* name, const tfla_rows& r, int64_t w, bool required) {
+        views[n++] = rows(name, r, B, T, w, e);
+        return check_aligned(name, r.data, e, required);
+    };
+    auto in_flat = [&](const char* name, const void* q, int64_t bytes, bool required) {
+        views[n++] = flat(name, q, bytes);
+        return check_aligned(name, q, 4, required);
+    };
+    if ((rc = in_rows("x", a->x, D, true)) || (rc = in_rows("dt", a->dt, D, true)) ||
+        (rc = in_rows("z", a->z, D, false)) || (rc = in_rows("bmat", a->bmat, GN, true)) ||
+        (rc = in_rows("cmat", a->cmat, GN, true)) || (rc = in_flat("a", a->a, ab, true)) ||
+        (rc = in_flat("skip", a->skip, D * 4, false)) || (rc = in_flat("dt_bias", a->dt_bias, D * 4, false)) ||
+        (rc = in_flat("state", a->state, sb, false)) || (rc = in_flat("lengths", a->lengths, (int64_t)B * 4, false)))
+        return rc;
+    if (bwd && ((rc = in_rows("dy", a->dy, D, true)) || (rc = in_flat("dstate_out", a->dstate_out, sb, false))))
+        return rc;
+    const size_t ni = n;
+    if (!bwd) {
+        if ((rc = in_rows("y", a->y, D, true)) || (rc = in_flat("state_out", a->state_out, sb, false))) return rc;
+    } else {
+        if ((rc = in_rows("dx", a->dx, D, true)) || (rc = in_rows("ddt", a->ddt, D, true)) ||
+            (rc = in_rows("dz", a->dz, D, false)) || (rc = in_rows("dbmat", a->dbmat, GN, true)) ||
+            (rc = in_rows("dcmat", a->dcmat, GN, true)) || (rc = in_flat("da", a->da, ab, true)) ||
+            (rc = in_flat("dskip", a->dskip, D * 4, false)) || (rc = in_flat("ddt_bias", a->ddt_bias, D * 4, false)) ||
+            (rc = in_flat("dstate", a->dstate, sb, false)))
+            return rc;
+        if (!a->z.data != !a->dz.data || !a->skip != !a->dskip || !a->dt_bias != !a->ddt_bias)
+            return fail(TFLA_ERR_INVALID_ARG, "dz, dskip and ddt_bias must be given exactly when z, skip and dt_bias are");
+    }
+    if ((rc = check_views(views, ni, views + ni, n - ni, !bwd && a->state == a->state_out ? a->state : nullptr))) return rc;
+    if ((rc = check_words("bmat", a->bmat, B, T, e)) || (rc = check_words("cmat", a->cmat, B, T, e))) return rc;
+    *nv = n;
+    p->x = dev(a->x);
+    p->dt = dev(a->dt);
+    p->z = dev(a->z);
+    p->bmat = dev(a->bmat);
+    p->cmat = dev(a->cmat);
+    p->a = a->a;
+    p->skip = a->skip;
+    p->dt_bias = a->dt_bias;
+    p->state = a->state;
+    p->lengths = a->lengths;
+    if (!bwd) {
+        p->y = dev(a->y);
+        p->state_out = a->state_out;
+        return TFLA_OK;
+    }
+    p->dy = dev(a->dy);
+    p->dstate_out = a->dstate_out;
+    p->dx = dev(a->dx);
+    p->ddt = dev(a->ddt);
+    p->dz = dev(a->dz);
+    p->dbmat = dev(a->dbmat);
+    p->dcmat = dev(a->dcmat);
+    p->da = a->da;
+    p->dskip = a->dskip;
+    p->ddt_bias = a->ddt_bias;
+    p->dstate = a->dstate;
+    return TFLA_OK;
+}
+
+int run_scan(const tfla_scan_args* args, bool bwd, void* workspace, size_t workspace_bytes, void* stream)
+{
+    tfla::ScanProblem p;
+    View views[32];
+    size_t nv;
+    int rc = check_scan(args, bwd, &p, views, &nv);
+    if (rc) return rc;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const size_t need = bwd ? tfla::scan_bwd_workspace(p) : tfla::scan_workspace(p);
+    return with_workspace(workspace, workspace_bytes, need, views, nv, s, [&](char* base) {
+        p.ws = base;
+        return bwd ? hip_status(tfla::launch_scan_bwd(p, s), "scan gradient kernel launch")
+                   : hip_status(tfla::launch_scan_fwd(p, s), "scan kernel launch");
+    });
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t tfla_scan_workspace_bytes(int B, int T, int D, int N, int G, int flags)
+{
+    tfla::ScanProblem p;
+    const int rc = guarded([&]() -> int { return check_scan_sizes(B, T, D, N, G, flags, &p); });
+    return rc == TFLA_OK ? tfla::scan_workspace(p) : 0;
+}
+
+int tfla_scan_fwd(const tfla_scan_args* args, void* workspace, size_t workspace_bytes, void* stream)
+{
+    return guarded([&]() -> int { return run_scan(args, false, workspace, workspace_bytes, stream); });
+}
+
+size_t tfla_scan_bwd_workspace_bytes(int B, int T, int D, int N, int G, int flags)
+{
+    tfla::ScanProblem p;
+    const int rc = guarded([&]() -> int { return check_scan_sizes(B, T, D, N, G, flags, &p); });
+    return rc == TFLA_OK ? tfla::scan_bwd_workspace(p) : 0;
+}
+
+int tfla_scan_bwd(const tfla_scan_args* args, void* workspace, size_t workspace_bytes, void* stream)
+{
+    return guarded([&]() -> int { return run_scan(args, true, workspace, workspace_bytes, stream); });
+}
 
 int tfla_conv_fwd(const tfla_conv_args* args, void* stream)
 {

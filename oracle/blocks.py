@@ -93,40 +93,48 @@ def scan(x, dt, a, bm, cm, skip=None, z=None, dt_bias=None, softplus=True, state
 
 
 def scan_grads(x, dt, a, bm, cm, dout, skip=None, z=None, dt_bias=None, softplus=True, state=None, lengths=None,
-               dend=None):
-    """dict of dx, ddt, da, dbmat, dcmat, dskip, dz, ddt_bias, dstate"""
+               dend=None, magnitude=False):
+    """dict of y, end, dx, ddt, da, dbmat, dcmat, dskip, dz, ddt_bias, dstate;
+    with ``magnitude`` the sums of the terms' absolute values instead (for
+    error bounds)."""
     B, T, D = x.shape
+    mag = np.abs if magnitude else (lambda v: v)
+    x, bm, cm, dout = mag(x), mag(bm), mag(cm), mag(dout)
+    skip, state, dend = (None if v is None else mag(v) for v in (skip, state, dend))
     G = bm.shape[2]
     per = D // G
     o = dict(dx=np.zeros_like(x), ddt=np.zeros_like(x), da=np.zeros_like(a), dbmat=np.zeros_like(bm),
              dcmat=np.zeros_like(cm), dskip=np.zeros(D), dz=np.zeros_like(x), ddt_bias=np.zeros(D),
-             dstate=np.zeros((B,) + a.shape))
+             dstate=np.zeros((B,) + a.shape), y=np.zeros_like(x), end=np.zeros((B,) + a.shape))
     for b, n in enumerate(_lens(lengths, B, T)):
         d, slope = _delta(dt[b, :n], dt_bias, softplus)
+        dm = mag(d)
         hs = [np.zeros(a.shape) if state is None else state[b]]
         for t in range(n):
             Bt = np.repeat(bm[b, t], per, 0)
-            hs.append(np.exp(d[t][:, None] * a) * hs[-1] + (d[t] * x[b, t])[:, None] * Bt)
+            hs.append(np.exp(d[t][:, None] * a) * hs[-1] + (dm[t] * x[b, t])[:, None] * Bt)
+        o["end"][b] = hs[-1]
         g = np.zeros(a.shape) if dend is None else dend[b].copy()
         for t in reversed(range(n)):
             Bt, Ct = np.repeat(bm[b, t], per, 0), np.repeat(cm[b, t], per, 0)
             dy = dout[b, t]
+            y = (hs[t + 1] * Ct).sum(1) + (0 if skip is None else skip * x[b, t])
             if z is not None:
-                f, df = act(z[b, t], "silu")
-                y = (hs[t + 1] * Ct).sum(1) + (0 if skip is None else skip * x[b, t])
+                f, df = (mag(v) for v in act(z[b, t], "silu"))
                 o["dz"][b, t] = dy * y * df
-                dy = dy * f
+                dy, y = dy * f, y * f
+            o["y"][b, t] = y
             g = g + dy[:, None] * Ct
             decay = np.exp(d[t][:, None] * a)
             o["dcmat"][b, t] = (dy[:, None] * hs[t + 1]).reshape(G, per, -1).sum(1)
-            o["dbmat"][b, t] = ((d[t] * x[b, t])[:, None] * g).reshape(G, per, -1).sum(1)
+            o["dbmat"][b, t] = ((dm[t] * x[b, t])[:, None] * g).reshape(G, per, -1).sum(1)
             gb = (g * Bt).sum(1)
             dlog = g * decay * hs[t]
-            o["da"] += dlog * d[t][:, None]
-            dd = ((dlog * a).sum(1) + gb * x[b, t]) * slope[t]
+            o["da"] += dlog * dm[t][:, None]
+            dd = ((dlog * mag(a)).sum(1) + gb * x[b, t]) * slope[t]
             o["ddt"][b, t] = dd
             o["ddt_bias"] += dd
-            o["dx"][b, t] = gb * d[t] + (0 if skip is None else skip * dy)
+            o["dx"][b, t] = gb * dm[t] + (0 if skip is None else skip * dy)
             o["dskip"] += dy * x[b, t]
             g = g * decay
         o["dstate"][b] = g

@@ -117,3 +117,75 @@ def test_python_checks_refuse():
         tfla.conv_forward(x[0], w)
     with pytest.raises(TypeError):
         tfla.conv_forward(None, w)
+
+
+# ---- scan ------------------------------------------------------------------------------
+
+def scan_args(**kw):
+    B, T, D, N, G = 2, 300, 128, 16, 2
+    a = blocks.ScanArgs(B=B, T=T, D=D, N=N, G=G, flags=BF16 | blocks.SCAN_SOFTPLUS)
+    rows = lambda n, w=D: blocks.Rows(at(n), T * w, w)  # noqa: E731
+    a.x, a.dt, a.z, a.y, a.dy = rows(0), rows(1), rows(2), rows(3), rows(4)
+    a.bmat, a.cmat, a.dbmat, a.dcmat = rows(5, G * N), rows(6, G * N), rows(7, G * N), rows(8, G * N)
+    a.dx, a.ddt, a.dz = rows(9), rows(10), rows(11)
+    for i, k in enumerate(("a", "skip", "dt_bias", "state", "lengths", "state_out", "dstate_out", "da", "dskip",
+                           "ddt_bias", "dstate")):
+        setattr(a, k, at(12 + i))
+    return put(a, kw)
+
+
+SCAN_BOTH = [
+    ({"B": 0}, INVALID), ({"T": -1}, INVALID), ({"D": 0}, INVALID), ({"G": 0}, INVALID), ({"G": 3}, INVALID),
+    ({"N": 0}, INVALID), ({"N": 6}, UNSUPPORTED), ({"N": 68}, UNSUPPORTED), ({"flags": 0x200}, INVALID),
+    ({"B": 1 << 16, "T": 1 << 15}, UNSUPPORTED), ({"D": 1 << 26}, UNSUPPORTED),
+    ({"x.data": None}, INVALID), ({"dt.data": None}, INVALID), ({"bmat.data": None}, INVALID), ({"a": None}, INVALID),
+    ({"bmat.data": at(5) + 2}, INVALID), ({"cmat.row": 33}, INVALID), ({"bmat.batch": 9601}, INVALID),
+    ({"a": at(12) + 2}, INVALID), ({"state": at(15) + 1}, INVALID), ({"z.row": -1}, INVALID), ({"dt.batch": 1 << 60}, INVALID),
+]
+
+
+@pytest.mark.parametrize("kw,code", SCAN_BOTH + [
+    ({"y.data": None}, INVALID), ({"y.row": 127}, INVALID), ({"y.data": at(1)}, INVALID), ({"y.data": at(5)}, INVALID),
+    ({"state_out": at(15) + 4}, INVALID), ({"state_out": at(3)}, INVALID),
+])
+def test_scan_fwd_refuses(kw, code):
+    assert tfla.lib().tfla_scan_fwd(ctypes.byref(scan_args(**kw)), None, 0, None) == code
+    assert tfla.tfla_last_error()
+
+
+@pytest.mark.parametrize("kw,code", SCAN_BOTH + [
+    ({"dy.data": None}, INVALID), ({"dx.data": None}, INVALID), ({"da": None}, INVALID), ({"dz.data": None}, INVALID),
+    ({"z.data": None}, INVALID), ({"dskip": None}, INVALID), ({"dt_bias": None}, INVALID), ({"dx.data": at(4)}, INVALID),
+    ({"ddt.data": at(9)}, INVALID), ({"dbmat.data": at(5)}, INVALID), ({"dcmat.row": 31}, INVALID),
+    ({"dstate": at(15)}, INVALID), ({"dbmat.data": None}, INVALID),
+])
+def test_scan_bwd_refuses(kw, code):
+    assert tfla.lib().tfla_scan_bwd(ctypes.byref(scan_args(**kw)), None, 0, None) == code
+    assert tfla.tfla_last_error()
+
+
+def test_scan_workspace():
+    L = tfla.lib()
+    n = L.tfla_scan_bwd_workspace_bytes(2, 300, 128, 16, 2, BF16)
+    assert n > 0
+    for bad in ((2, 300, 128, 6, 2, BF16), (2, 300, 128, 16, 3, BF16), (0, 300, 128, 16, 2, BF16), (2, 300, 128, 16, 2, 1)):
+        assert L.tfla_scan_bwd_workspace_bytes(*bad) == 0 and L.tfla_scan_workspace_bytes(*bad) == 0
+    a = scan_args()
+    n = L.tfla_scan_bwd_workspace_bytes(2, 300, 128, 16, 2, a.flags)
+    assert L.tfla_scan_bwd(ctypes.byref(a), at(30), n - 1, None) == OOM
+    assert L.tfla_scan_bwd(ctypes.byref(a), at(30) + 64, n, None) == INVALID
+    assert L.tfla_scan_bwd(ctypes.byref(a), at(9), n, None) == INVALID
+    assert L.tfla_scan_fwd(None, None, 0, None) == INVALID
+    assert L.tfla_scan_bwd(None, None, 0, None) == INVALID
+
+
+def test_interleaved_views_are_told_apart():
+    """Two halves of one row share no element; a byte more and they do."""
+    a = scan_args()
+    a.dx, a.dz = blocks.Rows(at(40), 300 * 256, 256), blocks.Rows(at(40) + 256, 300 * 256, 256)
+    a.T, a.B = 300, 2
+    # the checks pass up to the workspace, which is refused as too small
+    assert tfla.lib().tfla_scan_bwd(ctypes.byref(a), at(60), 256, None) == OOM
+    a.dz = blocks.Rows(at(40) + 254, 300 * 256, 256)
+    assert tfla.lib().tfla_scan_bwd(ctypes.byref(a), at(60), 256, None) == INVALID
+    assert "overlaps" in tfla.tfla_last_error()
