@@ -536,6 +536,56 @@ int tfla_scan_fwd(const tfla_scan_args* args, void* workspace, size_t workspace_
 size_t tfla_scan_bwd_workspace_bytes(int B, int T, int D, int N, int G, int flags);
 int tfla_scan_bwd(const tfla_scan_args* args, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Group norm with an activation or a gate.  Over the C channels of a group
+ * (per token) or, with TFLA_NORM_SEQUENCE, over the T rows and C channels of
+ * a group (a feature map's places as rows),
+ *
+ *     xh = (x - mean) rstd,  rstd = 1 / sqrt(var + eps),  u = xh weight + bias
+ *     y  = act(u)   or, with a gate,   y = u act(gate)
+ *
+ * var is the biased variance.  x may be the head-major output [B,H,T,d_hv] of
+ * tfla_fwd seen as [B,T,H,d_hv] (group stride T d_hv, row stride d_hv).
+ *
+ *   B, T, G, C >= 1, B T <= 2^30, G C <= 2^24; act any tfla_act
+ *   x, gate, y   [B,T,G,C], gate.data NULL for no gate
+ *   weight, bias fp32 [G,C] or NULL (1 and 0); eps > 0
+ *   mean, rstd   fp32 [B,T,G] ([B,G] with TFLA_NORM_SEQUENCE): outputs of the forward pass
+ *                (or NULL), inputs of the backward pass
+ *   flags        TFLA_IO_BF16 and/or TFLA_NORM_SEQUENCE
+ *
+ * Backward: from dy and the saved mean and rstd the gradients dx, dgate
+ * (given exactly when gate is), dweight and dbias (given exactly when weight
+ * and bias are).
+ */
+#define TFLA_NORM_SEQUENCE 0x2000
+typedef struct tfla_heads {
+    void* data;
+    long long batch, row, group;   /* strides of b, t, g, elements */
+} tfla_heads;
+
+typedef struct tfla_norm_args {
+    int B, T, G, C, flags, act;
+    float eps;
+    tfla_heads x, gate;
+    const float* weight;
+    const float* bias;
+    float* mean;
+    float* rstd;
+    /* tfla_norm_fwd */
+    tfla_heads y;
+    /* tfla_norm_bwd */
+    tfla_heads dy, dx, dgate;
+    float* dweight;
+    float* dbias;
+} tfla_norm_args;
+
+/* Workspaces as for tfla_conv_bwd; sizes depend on B, T, G, C, flags only. */
+size_t tfla_norm_workspace_bytes(int B, int T, int G, int C, int flags);
+int tfla_norm_fwd(const tfla_norm_args* args, void* workspace, size_t workspace_bytes, void* stream);
+size_t tfla_norm_bwd_workspace_bytes(int B, int T, int G, int C, int flags);
+int tfla_norm_bwd(const tfla_norm_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* tfla_error_string(int code);
 /* Thread-local detail of the last failing call on this thread ("" if none). */

@@ -18,6 +18,7 @@ import torch
 ACT_NONE, ACT_SILU, ACT_SIGMOID = 0, 1, 2
 
 SCAN_SOFTPLUS = 0x1000
+NORM_TOKEN, NORM_SEQUENCE = 0, 0x2000   # statistics of a group: per token, or over the whole sequence
 
 _IO = {torch.bfloat16: 0x100, torch.float32: 0}
 _i, _p, _ll = ctypes.c_int, ctypes.c_void_p, ctypes.c_longlong
@@ -46,6 +47,18 @@ class ScanArgs(ctypes.Structure):
                 ("dcmat", Rows), ("da", _p), ("dskip", _p), ("ddt_bias", _p), ("dstate", _p)]
 
 
+class Heads(ctypes.Structure):
+    """tfla_heads: data pointer, batch, row and group strides in elements."""
+    _fields_ = [("data", _p), ("batch", _ll), ("row", _ll), ("group", _ll)]
+
+
+class NormArgs(ctypes.Structure):
+    """tfla_norm_args."""
+    _fields_ = [("B", _i), ("T", _i), ("G", _i), ("C", _i), ("flags", _i), ("act", _i), ("eps", ctypes.c_float),
+                ("x", Heads), ("gate", Heads), ("weight", _p), ("bias", _p), ("mean", _p), ("rstd", _p),
+                ("y", Heads), ("dy", Heads), ("dx", Heads), ("dgate", Heads), ("dweight", _p), ("dbias", _p)]
+
+
 def bind(L):
     """Argument types of this module's entry points."""
     vp, sz = ctypes.c_void_p, ctypes.c_size_t
@@ -56,7 +69,11 @@ def bind(L):
             ("tfla_scan_workspace_bytes", [_i] * 6, sz),
             ("tfla_scan_fwd", [ctypes.POINTER(ScanArgs), vp, sz, vp], _i),
             ("tfla_scan_bwd_workspace_bytes", [_i] * 6, sz),
-            ("tfla_scan_bwd", [ctypes.POINTER(ScanArgs), vp, sz, vp], _i)):
+            ("tfla_scan_bwd", [ctypes.POINTER(ScanArgs), vp, sz, vp], _i),
+            ("tfla_norm_workspace_bytes", [_i] * 5, sz),
+            ("tfla_norm_fwd", [ctypes.POINTER(NormArgs), vp, sz, vp], _i),
+            ("tfla_norm_bwd_workspace_bytes", [_i] * 5, sz),
+            ("tfla_norm_bwd", [ctypes.POINTER(NormArgs), vp, sz, vp], _i)):
         f = getattr(L, name)
         f.argtypes, f.restype = args, res
 
@@ -298,3 +315,81 @@ def scan_backward(x, dt, a, bmat, cmat, dy, skip=None, z=None, dt_bias=None, sof
     n = _lib().tfla_scan_bwd_workspace_bytes(s.B, s.T, s.D, s.N, s.G, s.flags)
     _call("tfla_scan_bwd", s, dev, stream, n, workspace)
     return ScanGrads(dx, ddt, da, dbmat, dcmat, dskip, dz, ddt_bias, dstate)
+
+
+# ---- group norm --------------------------------------------------------------------------
+
+def _heads(t, name, shape, dtype, dev):
+    """tfla_heads of a [B,T,G,C] tensor with contiguous channels."""
+    _like(t, name, shape, dtype, dev)
+    st = t.stride()
+    if st[3] != 1 and shape[3] > 1:
+        raise ValueError(f"{name} must have contiguous channels (last stride 1), got strides {st}")
+    return Heads(t.data_ptr(), st[0], st[1], st[2])
+
+
+def _norm_args(x, weight, bias, act, gate, over):
+    dev = _first(x, "x", 4)
+    shape, dtype = x.shape, x.dtype
+    if over not in (NORM_TOKEN, NORM_SEQUENCE):
+        raise ValueError(f"over must be NORM_TOKEN or NORM_SEQUENCE, got {over}")
+    a = NormArgs()
+    a.B, a.T, a.G, a.C = shape
+    a.flags, a.act = _IO[dtype] | over, act
+    a.x = _heads(x, "x", shape, dtype, dev)
+    if gate is not None:
+        a.gate = _heads(gate, "gate", shape, dtype, dev)
+    a.weight = _flat(weight, "weight", shape[2:], torch.float32, dev)
+    a.bias = _flat(bias, "bias", shape[2:], torch.float32, dev)
+    return a, dev
+
+
+def norm_forward(x, weight=None, bias=None, eps: float = 1e-5, act: int = ACT_NONE, gate=None, over: int = NORM_TOKEN,
+                 y=None, workspace=None, stream=None):
+    """Group norm of x [B,T,G,C] over the channels of each group, per token or
+    (``over=NORM_SEQUENCE``) over all T rows, then ``y = act(u)`` or, with a
+    gate, ``y = u act(gate)``; returns ``(y, mean, rstd)``.
+
+    weight, bias are fp32 [G,C]; mean, rstd fp32 [B,T,G] or [B,G].  The
+    recurrences' head-major output h [B,H,T,d] goes in as
+    ``h.transpose(1, 2)``; y is contiguous [B,T,G,C] unless given."""
+    a, dev = _norm_args(x, weight, bias, act, gate, over)
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    a.eps = eps
+    a.y = _heads(y, "y", x.shape, x.dtype, dev)
+    stats = (a.B, a.G) if over else (a.B, a.T, a.G)
+    mean = torch.empty(stats, dtype=torch.float32, device=dev)
+    rstd = torch.empty(stats, dtype=torch.float32, device=dev)
+    a.mean, a.rstd = mean.data_ptr(), rstd.data_ptr()
+    n = _lib().tfla_norm_workspace_bytes(a.B, a.T, a.G, a.C, a.flags)
+    _call("tfla_norm_fwd", a, dev, stream, n, workspace)
+    return y, mean, rstd
+
+
+def norm_backward(x, dy, mean, rstd, weight=None, bias=None, act: int = ACT_NONE, gate=None, over: int = NORM_TOKEN,
+                  dx=None, dgate=None, workspace=None, stream=None):
+    """Gradients of :func:`norm_forward` for ``dy`` from its mean and rstd;
+    returns ``(dx, dgate, dweight, dbias)``, None where the input was None."""
+    a, dev = _norm_args(x, weight, bias, act, gate, over)
+    shape, dtype = x.shape, x.dtype
+    if dx is None:
+        dx = torch.empty(shape, dtype=dtype, device=dev)
+    if gate is None:
+        dgate = None
+    else:
+        if dgate is None:
+            dgate = torch.empty(shape, dtype=dtype, device=dev)
+        a.dgate = _heads(dgate, "dgate", shape, dtype, dev)
+    dweight = None if weight is None else torch.empty_like(weight)
+    dbias = None if bias is None else torch.empty_like(bias)
+    stats = (a.B, a.G) if over else (a.B, a.T, a.G)
+    a.dy = _heads(dy, "dy", shape, dtype, dev)
+    a.dx = _heads(dx, "dx", shape, dtype, dev)
+    a.mean = _flat(mean, "mean", stats, torch.float32, dev)
+    a.rstd = _flat(rstd, "rstd", stats, torch.float32, dev)
+    a.dweight = None if dweight is None else dweight.data_ptr()
+    a.dbias = None if dbias is None else dbias.data_ptr()
+    n = _lib().tfla_norm_bwd_workspace_bytes(a.B, a.T, a.G, a.C, a.flags)
+    _call("tfla_norm_bwd", a, dev, stream, n, workspace)
+    return dx, dgate, dweight, dbias

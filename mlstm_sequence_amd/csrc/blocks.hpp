@@ -61,4 +61,30 @@ hipError_t launch_scan_fwd(const ScanProblem& p, hipStream_t stream);
 size_t scan_bwd_workspace(const ScanProblem& p);
 hipError_t launch_scan_bwd(const ScanProblem& p, hipStream_t stream);
 
+// ---- group norm with an activation or a gate (norm.hip) -------------------------------
+// Element (b,t,g,c) at p[b * batch + t * row + g * group + c].
+struct Heads {
+    void* p = nullptr;
+    int64_t batch = 0, row = 0, group = 0;
+};
+
+enum NormAct { kActNone = 0, kActSilu = 1, kActSigmoid = 2 };
+
+struct NormProblem {
+    int B, T, G, C, act;
+    bool bf16, sequence;                    // sequence: statistics over T and C, else over C
+    float eps;
+    Heads x, gate, y;                       // gate.p NULL: y = act(u), else u act(gate)
+    const float *weight, *bias;             // [G,C] or NULL
+    float *mean, *rstd;                     // forward outputs (NULL: not wanted), backward inputs
+    Heads dy, dx, dgate;
+    float *dweight, *dbias;
+    char* ws;
+};
+
+size_t norm_workspace(const NormProblem& p);
+hipError_t launch_norm_fwd(const NormProblem& p, hipStream_t stream);
+size_t norm_bwd_workspace(const NormProblem& p);
+hipError_t launch_norm_bwd(const NormProblem& p, hipStream_t stream);
+
 }  // namespace tfla

@@ -431,9 +431,148 @@ int run_scan(const tfla_scan_args* args, bool bwd, void* workspace, size_t works
     });
 }
 
+// ---- group norm -----------------------------------------------------------------------
+
+View heads(const char* name, const tfla_heads& r, const tfla_norm_args& a, int64_t esz)
+{
+    View v = rows(name, tfla_rows{r.data, r.batch, r.row}, a.B, a.T, a.C, esz);
+    if (!r.data) return v;
+    v.n[2] = a.G;
+    v.stride[2] = r.group > kMaxSpan / esz ? kMaxSpan + 1 : r.group * esz;
+    return v;
+}
+
+tfla::Heads dev(const tfla_heads& r)
+{
+    tfla::Heads o;
+    o.p = r.data;
+    o.batch = r.batch;
+    o.row = r.row;
+    o.group = r.group;
+    return o;
+}
+
+int check_norm_sizes(int B, int T, int G, int C, int flags, tfla::NormProblem* p)
+{
+    if (flags & ~(TFLA_IO_BF16 | TFLA_NORM_SEQUENCE))
+        return fail(TFLA_ERR_INVALID_ARG, "unknown flags " + std::to_string(flags));
+    if (B < 1 || T < 1 || G < 1 || C < 1) return fail(TFLA_ERR_INVALID_ARG, "B, T, G and C must be >= 1");
+    if ((int64_t)B * T > kMaxRows) return fail(TFLA_ERR_UNSUPPORTED, "B*T must be <= 2^30");
+    if ((int64_t)G * C > (1 << 24)) return fail(TFLA_ERR_UNSUPPORTED, "G*C must be <= 2^24");
+    if ((int64_t)B * T * G >= (int64_t(1) << 32) || (int64_t)B * T * G * C / 256 >= (int64_t(1) << 31) - 1)
+        return fail(TFLA_ERR_UNSUPPORTED, "problem too large for one launch grid");
+    *p = tfla::NormProblem{};
+    p->B = B;
+    p->T = T;
+    p->G = G;
+    p->C = C;
+    p->bf16 = (flags & TFLA_IO_BF16) != 0;
+    p->sequence = (flags & TFLA_NORM_SEQUENCE) != 0;
+    return TFLA_OK;
+}
+
+int check_norm(const tfla_norm_args* a, bool bwd, tfla::NormProblem* p, View* views, size_t* nv)
+{
+    if (!a) return fail(TFLA_ERR_INVALID_ARG, "args is NULL");
+    int rc = check_norm_sizes(a->B, a->T, a->G, a->C, a->flags, p);
+    if (rc) return rc;
+    if (a->act != TFLA_ACT_NONE && a->act != TFLA_ACT_SILU && a->act != TFLA_ACT_SIGMOID)
+        return fail(TFLA_ERR_INVALID_ARG, "unknown act " + std::to_string(a->act));
+    if (!bwd && !(a->eps > 0.0f)) return fail(TFLA_ERR_INVALID_ARG, "eps must be > 0");
+    const int64_t e = p->bf16 ? 2 : 4, wb = (int64_t)a->G * a->C * 4;
+    const int64_t sb = (int64_t)a->B * (p->sequence ? 1 : a->T) * a->G * 4;
+    size_t n = 0;
+    auto strided = [&](const char* name, const tfla_heads& r, bool required) {
+        views[n++] = heads(name, r, *a, e);
+        return check_aligned(name, r.data, e, required);
+    };
+    auto plain = [&](const char* name, const void* q, int64_t bytes, bool required) {
+        views[n++] = flat(name, q, bytes);
+        return check_aligned(name, q, 4, required);
+    };
+    if ((rc = strided("x", a->x, true)) || (rc = strided("gate", a->gate, false)) ||
+        (rc = plain("weight", a->weight, wb, false)) || (rc = plain("bias", a->bias, wb, false)))
+        return rc;
+    if (bwd && ((rc = strided("dy", a->dy, true)) || (rc = plain("mean", a->mean, sb, true)) ||
+                (rc = plain("rstd", a->rstd, sb, true))))
+        return rc;
+    const size_t ni = n;
+    if (!bwd) {
+        if ((rc = strided("y", a->y, true)) || (rc = plain("mean", a->mean, sb, false)) ||
+            (rc = plain("rstd", a->rstd, sb, false)))
+            return rc;
+    } else {
+        if ((rc = strided("dx", a->dx, true)) || (rc = strided("dgate", a->dgate, false)) ||
+            (rc = plain("dweight", a->dweight, wb, false)) || (rc = plain("dbias", a->dbias, wb, false)))
+            return rc;
+        if (!a->gate.data != !a->dgate.data || !a->weight != !a->dweight || !a->bias != !a->dbias)
+            return fail(TFLA_ERR_INVALID_ARG, "dgate, dweight and dbias must be given exactly when gate, weight and bias are");
+    }
+    if ((rc = check_views(views, ni, views + ni, n - ni))) return rc;
+    *nv = n;
+    p->act = a->act;
+    p->eps = a->eps;
+    p->x = dev(a->x);
+    p->gate = dev(a->gate);
+    p->weight = a->weight;
+    p->bias = a->bias;
+    p->mean = a->mean;
+    p->rstd = a->rstd;
+    if (!bwd) {
+        p->y = dev(a->y);
+        return TFLA_OK;
+    }
+    p->dy = dev(a->dy);
+    p->dx = dev(a->dx);
+    p->dgate = dev(a->dgate);
+    p->dweight = a->dweight;
+    p->dbias = a->dbias;
+    return TFLA_OK;
+}
+
+int run_norm(const tfla_norm_args* args, bool bwd, void* workspace, size_t workspace_bytes, void* stream)
+{
+    tfla::NormProblem p;
+    View views[16];
+    size_t nv;
+    int rc = check_norm(args, bwd, &p, views, &nv);
+    if (rc) return rc;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const size_t need = bwd ? tfla::norm_bwd_workspace(p) : tfla::norm_workspace(p);
+    return with_workspace(workspace, workspace_bytes, need, views, nv, s, [&](char* base) {
+        p.ws = base;
+        return bwd ? hip_status(tfla::launch_norm_bwd(p, s), "norm gradient kernel launch")
+                   : hip_status(tfla::launch_norm_fwd(p, s), "norm kernel launch");
+    });
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t tfla_norm_workspace_bytes(int B, int T, int G, int C, int flags)
+{
+    tfla::NormProblem p;
+    const int rc = guarded([&]() -> int { return check_norm_sizes(B, T, G, C, flags, &p); });
+    return rc == TFLA_OK ? tfla::norm_workspace(p) : 0;
+}
+
+int tfla_norm_fwd(const tfla_norm_args* args, void* workspace, size_t workspace_bytes, void* stream)
+{
+    return guarded([&]() -> int { return run_norm(args, false, workspace, workspace_bytes, stream); });
+}
+
+size_t tfla_norm_bwd_workspace_bytes(int B, int T, int G, int C, int flags)
+{
+    tfla::NormProblem p;
+    const int rc = guarded([&]() -> int { return check_norm_sizes(B, T, G, C, flags, &p); });
+    return rc == TFLA_OK ? tfla::norm_bwd_workspace(p) : 0;
+}
+
+int tfla_norm_bwd(const tfla_norm_args* args, void* workspace, size_t workspace_bytes, void* stream)
+{
+    return guarded([&]() -> int { return run_norm(args, true, workspace, workspace_bytes, stream); });
+}
 
 size_t tfla_scan_workspace_bytes(int B, int T, int D, int N, int G, int flags)
 {

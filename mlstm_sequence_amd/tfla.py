@@ -14,8 +14,8 @@ import torch  # loaded first: libtfla then shares torch's HIP runtime (same SONA
 
 from . import blocks as _blocks
 from .blocks import (  # noqa: F401
-    ACT_NONE, ACT_SIGMOID, ACT_SILU, ConvArgs, Rows, ScanArgs, ScanGrads, conv_backward, conv_forward, scan_backward,
-    scan_forward,
+    ACT_NONE, ACT_SIGMOID, ACT_SILU, NORM_SEQUENCE, NORM_TOKEN, ConvArgs, Heads, NormArgs, Rows, ScanArgs, ScanGrads,
+    conv_backward, conv_forward, norm_backward, norm_forward, scan_backward, scan_forward,
 )
 
 MLSTM_SIG = 0

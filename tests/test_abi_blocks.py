@@ -189,3 +189,69 @@ def test_interleaved_views_are_told_apart():
     a.dz = blocks.Rows(at(40) + 254, 300 * 256, 256)
     assert tfla.lib().tfla_scan_bwd(ctypes.byref(a), at(60), 256, None) == INVALID
     assert "overlaps" in tfla.tfla_last_error()
+
+
+# ---- norm --------------------------------------------------------------------------------
+
+def norm_args(**kw):
+    B, T, G, C = 2, 100, 4, 64
+    a = blocks.NormArgs(B=B, T=T, G=G, C=C, flags=BF16, act=1, eps=1e-5)
+    heads = lambda n: blocks.Heads(at(n), T * G * C, G * C, C)  # noqa: E731
+    a.x, a.gate, a.y, a.dy, a.dx, a.dgate = (heads(i) for i in range(6))
+    for i, k in enumerate(("weight", "bias", "mean", "rstd", "dweight", "dbias")):
+        setattr(a, k, at(10 + i))
+    return put(a, kw)
+
+
+NORM_BOTH = [
+    ({"B": 0}, INVALID), ({"T": 0}, INVALID), ({"G": -1}, INVALID), ({"C": 0}, INVALID), ({"flags": 0x1000}, INVALID),
+    ({"act": 3}, INVALID), ({"act": -1}, INVALID), ({"B": 1 << 16, "T": 1 << 15}, UNSUPPORTED),
+    ({"G": 1 << 13, "C": 1 << 12}, UNSUPPORTED), ({"x.data": None}, INVALID), ({"x.data": at(0) + 1}, INVALID),
+    ({"gate.data": at(1) + 1}, INVALID), ({"weight": at(10) + 2}, INVALID), ({"x.group": -1}, INVALID),
+    ({"x.group": 1 << 61}, INVALID), ({"mean": at(12) + 1}, INVALID),
+]
+
+
+@pytest.mark.parametrize("kw,code", NORM_BOTH + [
+    ({"y.data": None}, INVALID), ({"eps": 0.0}, INVALID), ({"eps": -1.0}, INVALID), ({"eps": float("nan")}, INVALID),
+    ({"y.group": 32}, INVALID), ({"y.row": 64}, INVALID), ({"y.data": at(0)}, INVALID), ({"y.data": at(1)}, INVALID),
+    ({"mean": at(2)}, INVALID), ({"rstd": at(12)}, INVALID),
+])
+def test_norm_fwd_refuses(kw, code):
+    assert tfla.lib().tfla_norm_fwd(ctypes.byref(norm_args(**kw)), None, 0, None) == code
+    assert tfla.tfla_last_error()
+
+
+@pytest.mark.parametrize("kw,code", NORM_BOTH + [
+    ({"dy.data": None}, INVALID), ({"dx.data": None}, INVALID), ({"mean": None}, INVALID), ({"rstd": None}, INVALID),
+    ({"dgate.data": None}, INVALID), ({"gate.data": None}, INVALID), ({"dweight": None}, INVALID), ({"bias": None}, INVALID),
+    ({"dx.data": at(3)}, INVALID), ({"dgate.data": at(4)}, INVALID), ({"dweight": at(10)}, INVALID),
+])
+def test_norm_bwd_refuses(kw, code):
+    assert tfla.lib().tfla_norm_bwd(ctypes.byref(norm_args(**kw)), None, 0, None) == code
+    assert tfla.tfla_last_error()
+
+
+def test_norm_workspace():
+    L = tfla.lib()
+    assert L.tfla_norm_bwd_workspace_bytes(2, 100, 4, 64, BF16) > 0
+    for bad in ((0, 100, 4, 64, 0), (2, 100, 4, 64, 0x1000), (2, 100, 1 << 13, 1 << 12, 0)):
+        assert L.tfla_norm_bwd_workspace_bytes(*bad) == 0 and L.tfla_norm_workspace_bytes(*bad) == 0
+    assert L.tfla_norm_fwd(None, None, 0, None) == INVALID
+    assert L.tfla_norm_bwd(None, None, 0, None) == INVALID
+    n = L.tfla_norm_bwd_workspace_bytes(2, 100, 4, 64, BF16)
+    a = norm_args()
+    assert L.tfla_norm_bwd(ctypes.byref(a), at(30), n - 1, None) == OOM
+    assert L.tfla_norm_bwd(ctypes.byref(a), at(4), n, None) == INVALID
+
+
+def test_head_major_and_interleaved_heads_are_told_apart():
+    """Two outputs interleaved head by head, and one written head-major."""
+    a = norm_args()
+    a.dx, a.dgate = blocks.Heads(at(40), 100 * 512, 512, 128), blocks.Heads(at(40) + 128, 100 * 512, 512, 128)
+    assert tfla.lib().tfla_norm_bwd(ctypes.byref(a), at(60), 0, None) == OOM
+    a.dgate = blocks.Heads(at(40) + 126, 100 * 512, 512, 128)
+    assert tfla.lib().tfla_norm_bwd(ctypes.byref(a), at(60), 0, None) == INVALID
+    a = norm_args()
+    a.dx = blocks.Heads(at(40), 100 * 256, 64, 100 * 64)
+    assert tfla.lib().tfla_norm_bwd(ctypes.byref(a), at(60), 0, None) == OOM
