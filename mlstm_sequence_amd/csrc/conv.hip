@@ -6,8 +6,8 @@
 // channels and a run of rows: the K-1 rows before it in registers, each row
 // of x loaded once.  2 K flops an element against 2 elements moved: bound by
 // memory.
+#include "act.hpp"
 #include "blocks.hpp"
-#include "gfx950.hpp"
 
 namespace tfla {
 namespace {
@@ -16,8 +16,6 @@ __device__ __forceinline__ int clamp_len(const int* lengths, int b, int T)
 {
     return lengths ? min(max(lengths[b], 0), T) : T;
 }
-
-__device__ __forceinline__ float sigmoid_f(float u) { return 1.0f / (1.0f + expf(-u)); }
 
 struct ConvGeom {
     int B, T, D, nv;      // nv: vectors of VEC channels in a row

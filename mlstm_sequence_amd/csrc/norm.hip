@@ -6,13 +6,11 @@
 //
 // A set is what shares one mean: the C channels of a token's group, or the
 // T x C values of a sequence's group.
+#include "act.hpp"
 #include "blocks.hpp"
-#include "gfx950.hpp"
 
 namespace tfla {
 namespace {
-
-__device__ __forceinline__ float sigmoid_f(float u) { return 1.0f / (1.0f + expf(-u)); }
 
 __device__ __forceinline__ float act_f(float u, int act)
 {

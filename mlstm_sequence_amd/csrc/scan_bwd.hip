@@ -24,12 +24,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-int waves_of(int N)
-{
-    const int w = (N + kStates - 1) / kStates;
-    return w <= 1 ? 1 : w <= 2 ? 2 : w <= 4 ? 4 : w <= 8 ? 8 : 16;
-}
-
 // steps of a tile: 16 waves leave half the registers to each
 constexpr int tile_steps(int w) { return w > 8 ? 8 : 16; }
 
@@ -70,7 +64,7 @@ __global__ __launch_bounds__(64 * W) void scan_tiles_kernel(ScanProblem p, f32x4
 {
     constexpr int TS = tile_steps(W);
     __shared__ f32x2 du[TS][64];
-    const Place q = place(p);
+    const Place q = place(p, Segments{p.T, 1});
     const int len = clamp_len(p.lengths, q.b, p.T);
     const int n0 = q.wave * kStates;
     const bool has = n0 < p.N;
@@ -104,7 +98,7 @@ __global__ __launch_bounds__(64 * W) void scan_tiles_kernel(ScanProblem p, f32x4
             Uniform4<T> Bv;
             Bv.load(Bp + (t0 + s) * p.bmat.row);
 #pragma unroll
-            for (int n = 0; n < kStates; ++n) h[n] = exp2_fast(v[0] * A[n]) * h[n] + v[1] * Bv.v[n];
+            for (int n = 0; n < kStates; ++n) h[n] = exp2_fast(v[0] * A[n]) * h[n] + v[1] * Bv.get(n);
         }
     }
 }
@@ -156,7 +150,7 @@ __global__ __launch_bounds__(64 * W) void scan_bwd_kernel(ScanProblem p, Ws ws)
     constexpr int OWN = TS / W > 0 ? TS / W : 1;
     __shared__ f32x4 in[TS][64];              // delta, delta x, dy after the gate
     __shared__ float part[W][3][TS][64];      // sum_n g B, sum_n w A, sum_n C h
-    const Place q = place(p);
+    const Place q = place(p, Segments{p.T, 1});
     const int len = clamp_len(p.lengths, q.b, p.T);
     const int n0 = q.wave * kStates;
     const bool has = n0 < p.N;
@@ -225,8 +219,8 @@ __global__ __launch_bounds__(64 * W) void scan_bwd_kernel(ScanProblem p, Ws ws)
 #pragma unroll
                     for (int n = 0; n < kStates; ++n) {
                         a[s][n] = exp2_fast(v[0] * A[n]);
-                        h[s][n] = a[s][n] * (s ? h[s ? s - 1 : 0][n] : h0[n]) + v[1] * Bv.v[n];
-                        o += Cv.v[n] * h[s][n];
+                        h[s][n] = a[s][n] * (s ? h[s ? s - 1 : 0][n] : h0[n]) + v[1] * Bv.get(n);
+                        o += Cv.get(n) * h[s][n];
                     }
                     if (zp) part[q.wave][2][s][q.lane] = o;
                 }
@@ -242,10 +236,10 @@ __global__ __launch_bounds__(64 * W) void scan_bwd_kernel(ScanProblem p, Ws ws)
                     float s1 = 0.0f, s2 = 0.0f, sum[8];
 #pragma unroll
                     for (int n = 0; n < kStates; ++n) {
-                        const float gn = Cv.v[n] * v[2] + ag[n];
+                        const float gn = Cv.get(n) * v[2] + ag[n];
                         sum[n] = gn * v[1];
                         sum[4 + n] = v[2] * h[s][n];
-                        s1 += gn * Bv.v[n];
+                        s1 += gn * Bv.get(n);
                         ag[n] = gn * a[s][n];
                         const float wn = ag[n] * (s ? h[s ? s - 1 : 0][n] : h0[n]);
                         s2 += wn * A[n];

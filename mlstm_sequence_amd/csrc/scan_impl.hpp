@@ -14,8 +14,8 @@
 // others through LDS.
 #pragma once
 
+#include "act.hpp"
 #include "blocks.hpp"
-#include "gfx950.hpp"
 
 namespace tfla {
 namespace scan {
@@ -23,32 +23,36 @@ namespace scan {
 constexpr int kStates = 4;    // states of a wave
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef f32x4 f32x4u __attribute__((aligned(4)));   // four states of the caller's arrays
 
-// kStates values of B or C at a wave-uniform address (scalar loads; the data
-// is read-only during the launch).
+// kStates values of B or C at a wave-uniform address: scalar loads (the data
+// is read-only during the launch), unpacked by the scalar unit.
 template <typename T> struct Uniform4;
 template <> struct Uniform4<bf16> {
-    float v[4];
+    u32x2 r;
     __device__ __forceinline__ void load(const bf16* p)
     {
-        typedef const u32x2 __attribute__((address_space(4))) cvec;
-        const u32x2 r = *(cvec*)(uintptr_t)p;
-        v[0] = __builtin_bit_cast(float, r[0] << 16);
-        v[1] = __builtin_bit_cast(float, r[0] & 0xffff0000u);
-        v[2] = __builtin_bit_cast(float, r[1] << 16);
-        v[3] = __builtin_bit_cast(float, r[1] & 0xffff0000u);
+        typedef const u32x2 __attribute__((address_space(4), aligned(4))) cvec;
+        r = *(cvec*)(uintptr_t)p;
+    }
+    __device__ __forceinline__ float get(int n) const
+    {
+        const uint32_t w = n < 2 ? r[0] : r[1];
+        return __builtin_bit_cast(float, (n & 1) ? w & 0xffff0000u : w << 16);
     }
 };
 template <> struct Uniform4<float> {
-    float v[4];
+    u32x4 r;
     __device__ __forceinline__ void load(const float* p)
     {
-        typedef const f32x4 __attribute__((address_space(4))) cvec;
-        const f32x4 r = *(cvec*)(uintptr_t)p;
-        v[0] = r[0];
-        v[1] = r[1];
-        v[2] = r[2];
-        v[3] = r[3];
+        typedef const u32x4 __attribute__((address_space(4), aligned(4))) cvec;
+        r = *(cvec*)(uintptr_t)p;
+    }
+    __device__ __forceinline__ float get(int n) const
+    {
+        const uint32_t w = r[n];
+        return __builtin_bit_cast(float, w);
     }
 };
 
@@ -57,34 +61,46 @@ __device__ __forceinline__ int clamp_len(const int* lengths, int b, int T)
     return lengths ? min(max(lengths[b], 0), T) : T;
 }
 
-__device__ __forceinline__ float sigmoid_f(float u) { return 1.0f / (1.0f + expf(-u)); }
-
-// softplus(u) = max(u, 0) + log1p(e^{-|u|})
-__device__ __forceinline__ float softplus_f(float u) { return fmaxf(u, 0.0f) + log1pf(expf(-fabsf(u))); }
-
-// Where a workgroup stands: sequence, channels, states.
-struct Place {
-    int b, g, cb, lane, wave, c;   // c: the lane's channel (clamped to a valid one when !live)
-    bool live;
+// How a sequence is cut: nseg segments of len steps (a multiple of the tile),
+// walked by workgroups of their own.
+struct Segments {
+    int len, nseg;
 };
 
-__device__ __forceinline__ Place place(const ScanProblem& p)
+// Where a workgroup stands: sequence, segment, channels, states.
+struct Place {
+    int b, seg, g, cb, lane, wave, c;   // c: the lane's channel (clamped to a valid one when !live)
+    bool live;
+    int blk;                            // block of channels within the sequence
+};
+
+__device__ __forceinline__ Place place(const ScanProblem& p, const Segments& sg)
 {
     Place q;
     const int per = p.D / p.G;
     const int ncb = (per + 63) / 64;
-    int blk = blockIdx.x;
-    q.cb = blk % ncb;
-    blk /= ncb;
-    q.g = blk % p.G;
-    q.b = blk / p.G;
+    int i = blockIdx.x;
+    q.blk = i % (ncb * p.G);
+    i /= ncb * p.G;
+    q.seg = i % sg.nseg;
+    q.b = i / sg.nseg;
+    q.cb = q.blk % ncb;
+    q.g = q.blk / ncb;
     q.lane = threadIdx.x & 63;
     q.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int i = q.cb * 64 + q.lane;
-    q.live = i < per;
-    q.c = q.g * per + min(i, per - 1);
+    const int k = q.cb * 64 + q.lane;
+    q.live = k < per;
+    q.c = q.g * per + min(k, per - 1);
     return q;
 }
+
+inline int waves_of(int N)
+{
+    const int w = (N + kStates - 1) / kStates;
+    return w <= 1 ? 1 : w <= 2 ? 2 : w <= 4 ? 4 : w <= 8 ? 8 : 16;
+}
+
+inline int channel_blocks(const ScanProblem& p) { return p.G * ((p.D / p.G + 63) / 64); }
 
 }  // namespace scan
 }  // namespace tfla

@@ -120,7 +120,10 @@ def scan_grads(x, dt, a, bm, cm, dout, skip=None, z=None, dt_bias=None, softplus
             dy = dout[b, t]
             y = (hs[t + 1] * Ct).sum(1) + (0 if skip is None else skip * x[b, t])
             if z is not None:
-                f, df = (mag(v) for v in act(z[b, t], "silu"))
+                f, df = act(z[b, t], "silu")
+                if magnitude:   # SiLU' = s + s z (1 - s) is itself a sum, which cancels near z = -1.28
+                    sg = sigmoid(z[b, t])
+                    f, df = np.abs(f), sg + sg * np.abs(z[b, t]) * (1 - sg)
                 o["dz"][b, t] = dy * y * df
                 dy, y = dy * f, y * f
             o["y"][b, t] = y

@@ -8,7 +8,9 @@ exponential's argument is rounded).  A product holds at most the decays of a
 whole sequence, twice in the backward pass; beside them at most 8 factors of
 up to 12 U each; a sum of n terms adds (n + 1) U.  So an output is within
 (2 sum_t rho_t + (n + 100) U) times the sum of its terms' magnitudes, which
-the reference computes, and half a step of its type."""
+the reference computes, and half a step of its type.  SiLU's slope
+s (1 + z (1 - s)) counts as its two terms: 1 + z (1 - s) passes through 0 near
+z = -1.28, where fp32 leaves about 2 U s, whatever is left of the sum."""
 import numpy as np
 import pytest
 import torch
