@@ -23,14 +23,27 @@ __device__ __forceinline__ float exp_f(float x)
 
 __device__ __forceinline__ float sigmoid_f(float u) { return __builtin_amdgcn_rcpf(1.0f + exp_f(-u)); }
 
-// softplus(u) = max(u, 0) + log1p(e^{-|u|}); log1p as in log_sigmoid_fast.
-__device__ __forceinline__ float softplus_f(float u)
+// softplus(u) = max(u, 0) + log1p(y), y = e^{-|u|}.  With v = 1 + y rounded,
+// log1p(y) = log(v) + (y - (v - 1)) / v: the last term is what rounding took
+// from y, at most half a step of v, and leaving out its division by v changes
+// the sum by less than half a step of y.
+__device__ __forceinline__ float softplus_of(float u, float y)
 {
     constexpr float kLn2 = 0.6931471805599453f;
-    const float y = exp_f(-fabsf(u));
     const float v = 1.0f + y;
-    const float l = v == 1.0f ? y : __builtin_amdgcn_logf(v) * kLn2 * (y * __builtin_amdgcn_rcpf(v - 1.0f));
-    return fmaxf(u, 0.0f) + l;
+    return fmaxf(u, 0.0f) + fmaf(__builtin_amdgcn_logf(v), kLn2, y - (v - 1.0f));
 }
+__device__ __forceinline__ float softplus_f(float u) { return softplus_of(u, exp_f(-fabsf(u))); }
+
+// The same for bf16 data, whose own half step (2^-8) is far above the
+// exponential's error of |x| 2^-24 without the product's low part.
+__device__ __forceinline__ float sigmoid_fast(float u)
+{
+    return __builtin_amdgcn_rcpf(1.0f + exp2_fast(u * -kLog2e));
+}
+__device__ __forceinline__ float softplus_fast(float u) { return softplus_of(u, exp2_fast(fabsf(u) * -kLog2e)); }
+
+template <typename T> __device__ __forceinline__ float sigmoid_t(float u) { return sizeof(T) == 2 ? sigmoid_fast(u) : sigmoid_f(u); }
+template <typename T> __device__ __forceinline__ float softplus_t(float u) { return sizeof(T) == 2 ? softplus_fast(u) : softplus_f(u); }
 
 }  // namespace tfla

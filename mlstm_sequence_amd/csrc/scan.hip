@@ -41,13 +41,20 @@ __global__ __launch_bounds__(64 * W) void scan_fwd_kernel(ScanProblem p, Segment
     const int n0 = q.wave * kStates;
     const bool has = n0 < p.N;                        // a wave behind the last state only shares the steps' work
     const int nn = has ? n0 : 0;
-    const T* xp = (const T*)p.x.p + q.b * p.x.batch + s0 * p.x.row + q.c;
-    const T* dp = (const T*)p.dt.p + q.b * p.dt.batch + s0 * p.dt.row + q.c;
+    // Rows are addressed as a uniform pointer to the tile and 32-bit byte offsets within it
+    // (the host refuses row strides for which those would not do).
+    constexpr unsigned E = sizeof(T);
+    const unsigned xr = (unsigned)p.x.row * E, dr = (unsigned)p.dt.row * E, zr = (unsigned)p.z.row * E,
+                   yr = (unsigned)p.y.row * E, br = (unsigned)p.bmat.row * E, cr = (unsigned)p.cmat.row * E;
+    const char* xp = (const char*)p.x.p + (q.b * p.x.batch + s0 * p.x.row) * E;
+    const char* dp = (const char*)p.dt.p + (q.b * p.dt.batch + s0 * p.dt.row) * E;
     const bool gated = OUT && p.z.p;
-    const T* zp = gated ? (const T*)p.z.p + q.b * p.z.batch + s0 * p.z.row + q.c : nullptr;
-    T* yp = OUT ? (T*)p.y.p + q.b * p.y.batch + s0 * p.y.row + q.c : nullptr;
-    const T* Bp = (const T*)p.bmat.p + q.b * p.bmat.batch + s0 * p.bmat.row + q.g * p.N + nn;
-    const T* Cp = (const T*)p.cmat.p + q.b * p.cmat.batch + s0 * p.cmat.row + q.g * p.N + nn;
+    const char* zp = gated ? (const char*)p.z.p + (q.b * p.z.batch + s0 * p.z.row) * E : nullptr;
+    char* yp = OUT ? (char*)p.y.p + (q.b * p.y.batch + s0 * p.y.row) * E : nullptr;
+    const char* Bp = (const char*)p.bmat.p + (q.b * p.bmat.batch + s0 * p.bmat.row + q.g * p.N + nn) * E;
+    const char* Cp = (const char*)p.cmat.p + (q.b * p.cmat.batch + s0 * p.cmat.row + q.g * p.N + nn) * E;
+    const unsigned c = q.c * E, own = q.wave * OWN;   // the wave's steps of a tile: own .. own + OWN - 1
+    auto in = [&](const char* base, unsigned row, int s) { return *(const T*)(base + (s * row + c)); };
     const float skip = OUT && p.skip ? p.skip[q.c] : 0.0f;
     const float bias = p.dt_bias ? p.dt_bias[q.c] : 0.0f;
     const size_t srow = ((size_t)q.b * p.D + q.c) * p.N + nn;
@@ -68,43 +75,51 @@ __global__ __launch_bounds__(64 * W) void scan_fwd_kernel(ScanProblem p, Segment
     }
     float dsum = 0.0f;                                // this wave's steps
 
-    float rx[OWN], rd[OWN], rz[OWN];                  // the next tile's inputs
-    float fx[OWN], fz[OWN];                           // inputs the current tile's finish needs
-    auto fetch = [&](int t0) {
+    // The next tile's inputs, and those that the current tile's finish needs, as they were loaded: a
+    // conversion beside the load would wait for it there.
+    T rx[OWN] = {}, rd[OWN] = {}, rz[OWN] = {}, fx[OWN] = {}, fz[OWN] = {};
+    auto fetch = [&](int t0) {                        // the tile at xp, dp, zp, then on to the next
+        if (t0 + TS <= len) {
 #pragma unroll
-        for (int i = 0; i < OWN; ++i) {
-            const int t = t0 + q.wave + i * W;
-            if (t < len) {
-                rx[i] = to_float(xp[t * p.x.row]);
-                rd[i] = to_float(dp[t * p.dt.row]);
-                if (gated) rz[i] = to_float(zp[t * p.z.row]);
+            for (int i = 0; i < OWN; ++i) {
+                rx[i] = in(xp, xr, own + i);
+                rd[i] = in(dp, dr, own + i);
+                if (gated) rz[i] = in(zp, zr, own + i);
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < OWN; ++i)
+                if (t0 + own + i < (unsigned)len) {
+                    rx[i] = in(xp, xr, own + i);
+                    rd[i] = in(dp, dr, own + i);
+                    if (gated) rz[i] = in(zp, zr, own + i);
+                }
         }
+        xp += (uint64_t)TS * xr;
+        dp += (uint64_t)TS * dr;
+        if (gated) zp += (uint64_t)TS * zr;
     };
     auto publish = [&](int t0, int buf) {
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
-            const int s = q.wave + i * W;
-            if (t0 + s < len) {
-                const float u = rd[i] + bias;
-                const float d = p.softplus ? softplus_f(u) : u;
-                du[buf][s][q.lane] = f32x2{d, d * rx[i]};
-                if (!OUT) dsum += d;
-            }
+            const float u = to_float(rd[i]) + bias;
+            const float d = p.softplus ? softplus_t<T>(u) : u;
+            du[buf][own + i][q.lane] = f32x2{d, d * to_float(rx[i])};   // behind the end: never read
+            if (!OUT && t0 + own + i < (unsigned)len) dsum += d;
         }
     };
-    auto finish = [&](int t0, int buf) {
+    auto finish = [&](int t0, int buf) {              // the tile at yp, then on to the next
+        const int n = len - t0 - (int)own;
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
-            const int s = q.wave + i * W;
-            if (t0 + s < len) {
-                float o = skip * fx[i];
+            float o = skip * to_float(fx[i]);
+            const float z = to_float(fz[i]);
 #pragma unroll
-                for (int w = 0; w < W; ++w) o += part[buf][w][s][q.lane];
-                if (gated) o *= fz[i] * sigmoid_f(fz[i]);
-                if (q.live) yp[(t0 + s) * p.y.row] = from_float<T>(o);
-            }
+            for (int w = 0; w < W; ++w) o += part[buf][w][own + i][q.lane];
+            if (gated) o *= z * sigmoid_t<T>(z);
+            if (q.live && i < n) *(T*)(yp + ((own + i) * yr + c)) = from_float<T>(o);
         }
+        yp += (uint64_t)TS * yr;
     };
     auto step = [&](const f32x2 v, const Uniform4<T>& Bv, const Uniform4<T>& Cv) {
         float o = 0.0f;
@@ -120,7 +135,7 @@ __global__ __launch_bounds__(64 * W) void scan_fwd_kernel(ScanProblem p, Segment
     publish(0, 0);
     for (int t0 = 0, k = 0; t0 < len; t0 += TS, ++k) {
         const int buf = k & 1, cnt = min(TS, len - t0);
-        float nx[OWN], nz[OWN];
+        T nx[OWN], nz[OWN];
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
             nx[i] = rx[i];
@@ -135,25 +150,25 @@ __global__ __launch_bounds__(64 * W) void scan_fwd_kernel(ScanProblem p, Segment
             fz[i] = nz[i];
         }
         if (has && cnt == TS) {
-            const T* Bt = Bp + t0 * p.bmat.row;
-            const T* Ct = Cp + t0 * p.cmat.row;
+            const char *Bt = Bp, *Ct = Cp;
             Uniform4<T> Bv[2][U4], Cv[2][U4];
             f32x2 v[2][U4];
 #pragma unroll
             for (int j = 0; j < U4; ++j) {
-                Bv[0][j].load(Bt + j * p.bmat.row);
-                if (OUT) Cv[0][j].load(Ct + j * p.cmat.row);
+                Bv[0][j].load((const T*)(Bt + j * br));
+                if (OUT) Cv[0][j].load((const T*)(Ct + j * cr));
                 v[0][j] = du[buf][j][q.lane];
             }
 #pragma unroll
             for (int g = 0; g < TS / U4; ++g) {
                 if (g + 1 < TS / U4) {
+                    Bt += (uint64_t)U4 * br;
+                    Ct += (uint64_t)U4 * cr;
 #pragma unroll
                     for (int j = 0; j < U4; ++j) {
-                        const int s = (g + 1) * U4 + j;
-                        Bv[(g + 1) & 1][j].load(Bt + s * p.bmat.row);
-                        if (OUT) Cv[(g + 1) & 1][j].load(Ct + s * p.cmat.row);
-                        v[(g + 1) & 1][j] = du[buf][s][q.lane];
+                        Bv[(g + 1) & 1][j].load((const T*)(Bt + j * br));
+                        if (OUT) Cv[(g + 1) & 1][j].load((const T*)(Ct + j * cr));
+                        v[(g + 1) & 1][j] = du[buf][(g + 1) * U4 + j][q.lane];
                     }
                 }
                 __builtin_amdgcn_sched_barrier(0);
@@ -166,21 +181,24 @@ __global__ __launch_bounds__(64 * W) void scan_fwd_kernel(ScanProblem p, Segment
         } else if (has) {
             for (int s = 0; s < cnt; ++s) {
                 Uniform4<T> Bv, Cv;
-                Bv.load(Bp + (t0 + s) * p.bmat.row);
-                if (OUT) Cv.load(Cp + (t0 + s) * p.cmat.row);
+                Bv.load((const T*)(Bp + s * br));
+                if (OUT) Cv.load((const T*)(Cp + s * cr));
                 const float o = step(du[buf][s][q.lane], Bv, Cv);
                 if (OUT) part[buf][q.wave][s][q.lane] = o;
             }
         } else if (OUT) {
             for (int s = 0; s < cnt; ++s) part[buf][q.wave][s][q.lane] = 0.0f;
         }
+        Bp += (uint64_t)TS * br;
+        Cp += (uint64_t)TS * cr;
         publish(t0 + TS, buf ^ 1);
     }
     if (OUT) {
         __syncthreads();
         if (len > 0) finish((len - 1) / TS * TS, ((len - 1) / TS) & 1);
+        T* y0 = (T*)p.y.p + q.b * p.y.batch + s0 * p.y.row + q.c;
         for (int t = len + q.wave; t < s1 - s0; t += W)
-            if (q.live) yp[t * p.y.row] = from_float<T>(0.0f);
+            if (q.live) y0[t * p.y.row] = from_float<T>(0.0f);
         if (p.state_out && q.seg == sg.nseg - 1 && has && q.live)
             *(f32x4u*)(p.state_out + srow) = f32x4{h[0], h[1], h[2], h[3]};
     } else {

@@ -89,7 +89,7 @@ __global__ __launch_bounds__(64 * W) void scan_tiles_kernel(ScanProblem p, f32x4
         for (int s = q.wave; s < cnt; s += W) {
             const float xv = to_float(xp[(t0 + s) * p.x.row]);
             const float u = to_float(dp[(t0 + s) * p.dt.row]) + bias;
-            const float d = p.softplus ? softplus_f(u) : u;
+            const float d = p.softplus ? softplus_t<T>(u) : u;
             du[s][q.lane] = f32x2{d, d * xv};
         }
         __syncthreads();
@@ -191,13 +191,13 @@ __global__ __launch_bounds__(64 * W) void scan_bwd_kernel(ScanProblem p, Ws ws)
             if (s < cnt) {
                 xv[i] = q.live ? to_float(xp[(t0 + s) * p.x.row]) : 0.0f;
                 const float u = to_float(dp[(t0 + s) * p.dt.row]) + bias;
-                dv[i] = p.softplus ? softplus_f(u) : u;
-                sl[i] = p.softplus ? sigmoid_f(u) : 1.0f;
+                dv[i] = p.softplus ? softplus_t<T>(u) : u;
+                sl[i] = p.softplus ? sigmoid_t<T>(u) : 1.0f;
                 gv[i] = q.live ? to_float(gp[(t0 + s) * p.dy.row]) : 0.0f;
                 ge[i] = gv[i];
                 if (zp) {
                     const float z = to_float(zp[(t0 + s) * p.z.row]);
-                    const float sg = sigmoid_f(z);
+                    const float sg = sigmoid_t<T>(z);
                     ge[i] = gv[i] * z * sg;
                     dzv[i] = gv[i] * sg * (1.0f + z * (1.0f - sg));
                 }
