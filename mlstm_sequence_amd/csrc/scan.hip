@@ -1,12 +1,17 @@
 // scan.hip -- forward pass of the selective scan (scan_impl.hpp).
 //
-// A workgroup walks its segment in tiles of TS steps, with one barrier a
-// tile: the waves publish the next tile's (delta, delta x) into the other of
-// two LDS buffers while the current tile is walked, and finish the previous
-// tile's outputs (the sum over the waves' shares of C h, the skip, the gate)
-// from the other of two buffers of shares.  Inside a tile, B, C and the
-// published steps of the next four steps are fetched before the current four
-// are computed, so no product waits for a load.
+// A workgroup walks its segment in tiles: while one is walked, the next
+// tile's inputs load into registers and are published into the other of two
+// LDS buffers, (delta, delta x) for each channel and B and C as fp32 for the
+// whole group; after a barrier the tile's outputs are finished (the sum over
+// the waves' shares of C h, the skip, the gate).  All lanes of a wave read the
+// same four values of B and C, so these reads cost LDS 16 of about 136 cycles
+// a wave and step.  Read by scalar loads instead they cost none, but the
+// scalar cache misses on every row and a wait for one such load is a wait for
+// all: with one wave on a SIMD a step took 512 cycles.
+// The arithmetic bounds it: 6 issue slots a state and step (four products and
+// an exponential of two), 24 of about 35 that a wave of four states spends on
+// a step; the rest is softplus, gate and conversions.
 //
 // A long axis over few sequences and channels is cut into segments: every
 // segment is first walked from a zero state for its end state (no outputs),
@@ -19,54 +24,64 @@ namespace {
 
 using namespace scan;
 
-constexpr int TS = 16;   // steps of a tile
-constexpr int U4 = 4;    // steps fetched together
+// Steps of a tile: short ones leave LDS for more workgroups on a CU (W = 4: 16 KB each).
+constexpr int tile_steps(int W) { return W > 8 ? 16 : 8; }
+constexpr int U = 2;     // steps fetched from LDS together
+constexpr int kVm0 = 0x0f70;   // s_waitcnt: no vector load outstanding
+constexpr int AHEAD = 2; // tiles whose inputs are under way (even: two LDS buffers in turn)
 
 struct SegWs {
     float* ends;   // [B][nseg][D][N]
     float* sums;   // [B][nseg][D]
 };
 
-// OUT: the outputs; else the end state and the sum of the steps.
-template <typename T, int W, bool OUT>
+// OUT: the outputs; else the end state and the sum of the steps.  GATED: y times z sigmoid(z).
+template <typename T, int W, bool OUT, bool GATED>
 __global__ __launch_bounds__(64 * W) void scan_fwd_kernel(ScanProblem p, Segments sg, SegWs ws)
 {
-    constexpr int OWN = TS / W;                       // steps of a tile that a wave prepares and finishes
+    constexpr int TS = tile_steps(W), OWN = TS / W;                       // steps of a tile that a wave prepares and finishes
+    constexpr int NP = W * kStates, BC = OUT ? 2 : 1;  // states with padding; B alone, or B and C
+    constexpr int PER = (TS * BC * NP + 64 * W - 1) / (64 * W);
     __shared__ f32x2 du[2][TS][64];                   // delta, delta x
-    __shared__ float part[OUT ? 2 : 1][OUT ? W : 1][OUT ? TS : 1][64];
+    __shared__ f32x4 bc[2][TS][BC][W];                // B, C
+    __shared__ float part[OUT ? W : 1][OUT ? TS : 1][64];
     const Place q = place(p, sg);
     const int all = clamp_len(p.lengths, q.b, p.T);
     const int s0 = q.seg * sg.len, s1 = min(s0 + sg.len, p.T);
     const int len = max(0, min(all, s1) - s0);        // steps of this segment
     const int n0 = q.wave * kStates;
-    const bool has = n0 < p.N;                        // a wave behind the last state only shares the steps' work
-    const int nn = has ? n0 : 0;
-    // Rows are addressed as a uniform pointer to the tile and 32-bit byte offsets within it
-    // (the host refuses row strides for which those would not do).
-    constexpr unsigned E = sizeof(T);
-    const unsigned xr = (unsigned)p.x.row * E, dr = (unsigned)p.dt.row * E, zr = (unsigned)p.z.row * E,
-                   yr = (unsigned)p.y.row * E, br = (unsigned)p.bmat.row * E, cr = (unsigned)p.cmat.row * E;
-    const char* xp = (const char*)p.x.p + (q.b * p.x.batch + s0 * p.x.row) * E;
-    const char* dp = (const char*)p.dt.p + (q.b * p.dt.batch + s0 * p.dt.row) * E;
-    const bool gated = OUT && p.z.p;
-    const char* zp = gated ? (const char*)p.z.p + (q.b * p.z.batch + s0 * p.z.row) * E : nullptr;
-    char* yp = OUT ? (char*)p.y.p + (q.b * p.y.batch + s0 * p.y.row) * E : nullptr;
-    const char* Bp = (const char*)p.bmat.p + (q.b * p.bmat.batch + s0 * p.bmat.row + q.g * p.N + nn) * E;
-    const char* Cp = (const char*)p.cmat.p + (q.b * p.cmat.batch + s0 * p.cmat.row + q.g * p.N + nn) * E;
-    const unsigned c = q.c * E, own = q.wave * OWN;   // the wave's steps of a tile: own .. own + OWN - 1
-    auto in = [&](const char* base, unsigned row, int s) { return *(const T*)(base + (s * row + c)); };
+    const int ns = min(kStates, p.N - n0);            // the wave's states (<= 0: it only shares the steps' work)
+    const T* xp = (const T*)p.x.p + q.b * p.x.batch + s0 * p.x.row;
+    const T* dp = (const T*)p.dt.p + q.b * p.dt.batch + s0 * p.dt.row;
+    const T* zp = GATED ? (const T*)p.z.p + q.b * p.z.batch + s0 * p.z.row : nullptr;
+    T* yp = OUT ? (T*)p.y.p + q.b * p.y.batch + s0 * p.y.row : nullptr;
+    const unsigned c = q.c;
+    const int own = q.wave * OWN;                     // the wave's steps of a tile: own .. own + OWN - 1
+    // this thread's elements of the tile's B and C: element e of the tile is step, matrix, state in that order
+    const T* mp[PER];
+    int64_t mr[PER];
+    int ms[PER];
+    bool mv[PER];                                     // padding is 0
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int e = threadIdx.x + k * 64 * W, n = e % NP, isc = e / NP % BC;
+        const Rows& m = isc ? p.cmat : p.bmat;
+        mv[k] = n < p.N;
+        ms[k] = min(e / NP / BC, TS - 1);
+        mr[k] = m.row;
+        mp[k] = (const T*)m.p + q.b * m.batch + s0 * m.row + q.g * p.N + min(n, p.N - 1);
+    }
     const float skip = OUT && p.skip ? p.skip[q.c] : 0.0f;
     const float bias = p.dt_bias ? p.dt_bias[q.c] : 0.0f;
-    const size_t srow = ((size_t)q.b * p.D + q.c) * p.N + nn;
-    const size_t erow = (((size_t)q.b * sg.nseg + q.seg) * p.D + q.c) * p.N + nn;
+    const size_t srow = ((size_t)q.b * p.D + q.c) * p.N + n0;
+    const size_t erow = (((size_t)q.b * sg.nseg + q.seg) * p.D + q.c) * p.N + n0;
 
-    float A[kStates], h[kStates] = {0.0f, 0.0f, 0.0f, 0.0f};
+    // the start: the folded one of a segmented walk's second pass, else the caller's; 0 in its first pass
+    float A[kStates], h[kStates];
     {
-        const f32x4 av = *(const f32x4u*)(p.a + (size_t)q.c * p.N + nn);
-        // the start: the folded one of a segmented walk's second pass, else the caller's; 0 in its first pass
         const float* st = !OUT ? nullptr : sg.nseg > 1 ? ws.ends + erow : p.state ? p.state + srow : nullptr;
-        f32x4 hv = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (st) hv = *(const f32x4u*)st;
+        const f32x4 av = load_states(p.a + (size_t)q.c * p.N + n0, ns);
+        const f32x4 hv = st ? load_states(st, ns) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int n = 0; n < kStates; ++n) {
             A[n] = av[n] * kLog2e;
@@ -75,136 +90,130 @@ __global__ __launch_bounds__(64 * W) void scan_fwd_kernel(ScanProblem p, Segment
     }
     float dsum = 0.0f;                                // this wave's steps
 
-    // The next tile's inputs, and those that the current tile's finish needs, as they were loaded: a
-    // conversion beside the load would wait for it there.
-    T rx[OWN] = {}, rd[OWN] = {}, rz[OWN] = {}, fx[OWN] = {}, fz[OWN] = {};
-    auto fetch = [&](int t0) {                        // the tile at xp, dp, zp, then on to the next
-        if (t0 + TS <= len) {
-#pragma unroll
-            for (int i = 0; i < OWN; ++i) {
-                rx[i] = in(xp, xr, own + i);
-                rd[i] = in(dp, dr, own + i);
-                if (gated) rz[i] = in(zp, zr, own + i);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < OWN; ++i)
-                if (t0 + own + i < (unsigned)len) {
-                    rx[i] = in(xp, xr, own + i);
-                    rd[i] = in(dp, dr, own + i);
-                    if (gated) rz[i] = in(zp, zr, own + i);
-                }
-        }
-        xp += (uint64_t)TS * xr;
-        dp += (uint64_t)TS * dr;
-        if (gated) zp += (uint64_t)TS * zr;
+    // The inputs of the next AHEAD tiles, as they were loaded: a conversion beside the load would wait for it
+    // there.  A tile's walk is shorter than a trip to memory, so with few waves on a SIMD one tile ahead is late.
+    struct Raw {
+        T x[OWN], dt[OWN], z[OWN], m[PER];
     };
-    auto publish = [&](int t0, int buf) {
+    Raw raw[AHEAD];
+    T fx[OWN], fz[OWN];                     // what the current tile's finish needs
+    // No branch stands around a load (rows behind the end are read as the last one, and never used): where
+    // paths with and without the load meet, its register would be copied, which waits for it.
+    auto fetch = [&](Raw& r, int t0) {
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
-            const float u = to_float(rd[i]) + bias;
+            const int64_t t = min(t0 + own + i, len - 1);
+            r.x[i] = (xp + t * p.x.row)[c];
+            r.dt[i] = (dp + t * p.dt.row)[c];
+            if (GATED) r.z[i] = (zp + t * p.z.row)[c];
+        }
+#pragma unroll
+        for (int k = 0; k < PER; ++k) r.m[k] = mp[k][min(t0 + ms[k], len - 1) * mr[k]];
+    };
+    auto publish = [&](const Raw& r, int t0, int buf) {
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+            const float u = to_float(r.dt[i]) + bias;
             const float d = p.softplus ? softplus_t<T>(u) : u;
-            du[buf][own + i][q.lane] = f32x2{d, d * to_float(rx[i])};   // behind the end: never read
-            if (!OUT && t0 + own + i < (unsigned)len) dsum += d;
+            du[buf][own + i][q.lane] = f32x2{d, d * to_float(r.x[i])};   // behind the end: never read
+            if (!OUT && t0 + own + i < len) dsum += d;
+        }
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int e = threadIdx.x + k * 64 * W;
+            if (e < TS * BC * NP) ((float*)bc[buf])[e] = mv[k] ? to_float(r.m[k]) : 0.0f;
         }
     };
-    auto finish = [&](int t0, int buf) {              // the tile at yp, then on to the next
-        const int n = len - t0 - (int)own;
+    auto finish = [&](int t0) {
+        const int n = len - t0 - own;
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
             float o = skip * to_float(fx[i]);
-            const float z = to_float(fz[i]);
 #pragma unroll
-            for (int w = 0; w < W; ++w) o += part[buf][w][own + i][q.lane];
-            if (gated) o *= z * sigmoid_t<T>(z);
-            if (q.live && i < n) *(T*)(yp + ((own + i) * yr + c)) = from_float<T>(o);
+            for (int w = 0; w < W; ++w) o += part[w][own + i][q.lane];
+            if (GATED) {
+                const float z = to_float(fz[i]);
+                o *= z * sigmoid_t<T>(z);
+            }
+            if (q.live && i < n) (yp + (int64_t)(t0 + own + i) * p.y.row)[c] = from_float<T>(o);
         }
-        yp += (uint64_t)TS * yr;
     };
-    auto step = [&](const f32x2 v, const Uniform4<T>& Bv, const Uniform4<T>& Cv) {
+    auto step = [&](const f32x2 v, const f32x4 Bv, const f32x4 Cv) {
         float o = 0.0f;
 #pragma unroll
         for (int n = 0; n < kStates; ++n) {
-            h[n] = exp2_fast(v[0] * A[n]) * h[n] + v[1] * Bv.get(n);
-            if (OUT) o += Cv.get(n) * h[n];
+            h[n] = exp2_fast(v[0] * A[n]) * h[n] + v[1] * Bv[n];
+            if (OUT) o += Cv[n] * h[n];
         }
         return o;
     };
 
-    fetch(0);
-    publish(0, 0);
-    for (int t0 = 0, k = 0; t0 < len; t0 += TS, ++k) {
-        const int buf = k & 1, cnt = min(TS, len - t0);
-        T nx[OWN], nz[OWN];
+    // Everything loaded so far arrives before the walk's own loads start: a value still under way at the loop's
+    // head would make every tile wait there for all loads, the next tiles' among them.
+    __builtin_amdgcn_s_waitcnt(kVm0);
+    __builtin_amdgcn_sched_barrier(0);
+    if (len > 0) {
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) fetch(raw[a], a * TS);
+        publish(raw[0], 0, 0);
+    }
+    auto tile = [&](int t0, Raw& r, const Raw& next, int buf) {
+        const int cnt = min(TS, len - t0);
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
-            nx[i] = rx[i];
-            nz[i] = rz[i];
+            fx[i] = r.x[i];
+            if (GATED) fz[i] = r.z[i];
         }
-        fetch(t0 + TS);
+        fetch(r, t0 + AHEAD * TS);
         __syncthreads();
-        if (OUT && k > 0) finish(t0 - TS, buf ^ 1);
+        if (cnt == TS) {
+            f32x4 Bv[2][U], Cv[2][U];
+            f32x2 v[2][U];
+            auto load = [&](int slot, int s) {
 #pragma unroll
-        for (int i = 0; i < OWN; ++i) {
-            fx[i] = nx[i];
-            fz[i] = nz[i];
-        }
-        if (has && cnt == TS) {
-            const char *Bt = Bp, *Ct = Cp;
-            Uniform4<T> Bv[2][U4], Cv[2][U4];
-            f32x2 v[2][U4];
-#pragma unroll
-            for (int j = 0; j < U4; ++j) {
-                Bv[0][j].load((const T*)(Bt + j * br));
-                if (OUT) Cv[0][j].load((const T*)(Ct + j * cr));
-                v[0][j] = du[buf][j][q.lane];
-            }
-#pragma unroll
-            for (int g = 0; g < TS / U4; ++g) {
-                if (g + 1 < TS / U4) {
-                    Bt += (uint64_t)U4 * br;
-                    Ct += (uint64_t)U4 * cr;
-#pragma unroll
-                    for (int j = 0; j < U4; ++j) {
-                        Bv[(g + 1) & 1][j].load((const T*)(Bt + j * br));
-                        if (OUT) Cv[(g + 1) & 1][j].load((const T*)(Ct + j * cr));
-                        v[(g + 1) & 1][j] = du[buf][(g + 1) * U4 + j][q.lane];
-                    }
+                for (int j = 0; j < U; ++j) {
+                    v[slot][j] = du[buf][s + j][q.lane];
+                    Bv[slot][j] = bc[buf][s + j][0][q.wave];
+                    if (OUT) Cv[slot][j] = bc[buf][s + j][BC - 1][q.wave];
                 }
+            };
+            load(0, 0);
+#pragma unroll
+            for (int g = 0; g < TS / U; ++g) {
+                if (g + 1 < TS / U) load((g + 1) & 1, (g + 1) * U);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int j = 0; j < U4; ++j) {
-                    const float o = step(v[g & 1][j], Bv[g & 1][j], Cv[g & 1][j]);
-                    if (OUT) part[buf][q.wave][g * U4 + j][q.lane] = o;
+                for (int j = 0; j < U; ++j) {
+                    const float o = step(v[g & 1][j], Bv[g & 1][j], OUT ? Cv[g & 1][j] : Bv[g & 1][j]);
+                    if (OUT) part[q.wave][g * U + j][q.lane] = o;
                 }
             }
-        } else if (has) {
+        } else {
             for (int s = 0; s < cnt; ++s) {
-                Uniform4<T> Bv, Cv;
-                Bv.load((const T*)(Bp + s * br));
-                if (OUT) Cv.load((const T*)(Cp + s * cr));
-                const float o = step(du[buf][s][q.lane], Bv, Cv);
-                if (OUT) part[buf][q.wave][s][q.lane] = o;
+                const float o = step(du[buf][s][q.lane], bc[buf][s][0][q.wave], bc[buf][s][BC - 1][q.wave]);
+                if (OUT) part[q.wave][s][q.lane] = o;
             }
-        } else if (OUT) {
-            for (int s = 0; s < cnt; ++s) part[buf][q.wave][s][q.lane] = 0.0f;
         }
-        Bp += (uint64_t)TS * br;
-        Cp += (uint64_t)TS * cr;
-        publish(t0 + TS, buf ^ 1);
+        publish(next, t0 + TS, buf ^ 1);
+        if (OUT) {
+            __syncthreads();
+            finish(t0);
+        }
+    };
+    for (int t0 = 0; t0 < len; t0 += AHEAD * TS) {
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+            if (t0 + a * TS < len) tile(t0 + a * TS, raw[a], raw[(a + 1) % AHEAD], a & 1);
     }
     if (OUT) {
-        __syncthreads();
-        if (len > 0) finish((len - 1) / TS * TS, ((len - 1) / TS) & 1);
-        T* y0 = (T*)p.y.p + q.b * p.y.batch + s0 * p.y.row + q.c;
         for (int t = len + q.wave; t < s1 - s0; t += W)
-            if (q.live) y0[t * p.y.row] = from_float<T>(0.0f);
-        if (p.state_out && q.seg == sg.nseg - 1 && has && q.live)
-            *(f32x4u*)(p.state_out + srow) = f32x4{h[0], h[1], h[2], h[3]};
+            if (q.live) (yp + t * p.y.row)[c] = from_float<T>(0.0f);
+        if (p.state_out && q.seg == sg.nseg - 1 && q.live)
+            store_states(p.state_out + srow, ns, f32x4{h[0], h[1], h[2], h[3]});
     } else {
-        if (has && q.live) *(f32x4u*)(ws.ends + erow) = f32x4{h[0], h[1], h[2], h[3]};
+        if (q.live) store_states(ws.ends + erow, ns, f32x4{h[0], h[1], h[2], h[3]});
         __syncthreads();
-        float* red = &part[0][0][0][0];               // [64], one wave after another in order
+        float* red = &part[0][0][0];               // [64], one wave after another in order
         for (int w = 0; w < W; ++w) {
             if (q.wave == w) red[q.lane] = (w ? red[q.lane] : 0.0f) + dsum;
             __syncthreads();
@@ -237,11 +246,11 @@ __global__ __launch_bounds__(256) void scan_starts_kernel(ScanProblem p, Segment
 // only where a single walk leaves most of the chip idle.
 Segments segments_of(const ScanProblem& p)
 {
-    const int W = waves_of(p.N);
+    const int W = waves_of(p.N), TS = tile_steps(W);
     const int64_t waves = (int64_t)p.B * channel_blocks(p) * W;
     const int tiles = (p.T + TS - 1) / TS;
-    int64_t n = waves >= 1024 ? 1 : 3072 / waves;
-    if (n > tiles / 8) n = tiles / 8;                 // 128 steps at least
+    int64_t n = waves >= 1024 ? 1 : 8192 / waves;
+    if (n > p.T / 128) n = p.T / 128;                 // 128 steps at least
     if (n < 1) n = 1;
     const int per = (int)((tiles + n - 1) / n);
     return Segments{per * TS, (tiles + per - 1) / per};
@@ -269,14 +278,15 @@ hipError_t fwd_w(const ScanProblem& p, hipStream_t stream)
     const SegWs ws = seg_ws(p, sg, p.ws, &bytes);
     const unsigned blocks = (unsigned)p.B * sg.nseg * channel_blocks(p);
     if (sg.nseg > 1) {
-        scan_fwd_kernel<T, W, false><<<blocks, 64 * W, 0, stream>>>(p, sg, ws);
+        scan_fwd_kernel<T, W, false, false><<<blocks, 64 * W, 0, stream>>>(p, sg, ws);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         const int64_t n = (int64_t)p.B * p.D * p.N;
         scan_starts_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(p, sg, ws.ends, ws.sums);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    scan_fwd_kernel<T, W, true><<<blocks, 64 * W, 0, stream>>>(p, sg, ws);
+    if (p.z.p) scan_fwd_kernel<T, W, true, true><<<blocks, 64 * W, 0, stream>>>(p, sg, ws);
+    else scan_fwd_kernel<T, W, true, false><<<blocks, 64 * W, 0, stream>>>(p, sg, ws);
     return hipGetLastError();
 }
 

@@ -56,6 +56,24 @@ template <> struct Uniform4<float> {
     }
 };
 
+// ns <= kStates states of a channel, the rest 0 (ns <= 0: none).
+__device__ __forceinline__ f32x4 load_states(const float* p, int ns)
+{
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (ns == kStates) v = *(const f32x4u*)p;
+    else
+        for (int n = 0; n < kStates - 1; ++n)
+            if (n < ns) v[n] = p[n];
+    return v;
+}
+__device__ __forceinline__ void store_states(float* p, int ns, f32x4 v)
+{
+    if (ns == kStates) *(f32x4u*)p = v;
+    else
+        for (int n = 0; n < kStates - 1; ++n)
+            if (n < ns) p[n] = v[n];
+}
+
 __device__ __forceinline__ int clamp_len(const int* lengths, int b, int T)
 {
     return lengths ? min(max(lengths[b], 0), T) : T;
