@@ -24,9 +24,11 @@ namespace {
 
 using namespace scan;
 
-// Steps of a tile: short ones leave LDS for more workgroups on a CU (W = 4: 16 KB each).
-constexpr int tile_steps(int W) { return W > 8 ? 16 : 8; }
-constexpr int U = 2;     // steps fetched from LDS together
+// Steps of a tile.  One or two waves prepare 8 or 16 steps each in a tile of 16 and run out of registers
+// (B=4 T=1024 D=2048, N=8: 67 us with 16, 56 with 8); four or more gain from fewer barriers (N=16, B=8 T=2048
+// D=4096: 326 against 340 us).
+constexpr int tile_steps(int W) { return W > 2 ? 16 : 8; }
+constexpr int U = 1;     // steps fetched from LDS together (2 cost registers and 4 % at N=16)
 constexpr int kVm0 = 0x0f70;   // s_waitcnt: no vector load outstanding
 constexpr int AHEAD = 2; // tiles whose inputs are under way (even: two LDS buffers in turn)
 
@@ -241,16 +243,17 @@ __global__ __launch_bounds__(256) void scan_starts_kernel(ScanProblem p, Segment
     }
 }
 
-// Segments: enough workgroups to fill the chip.  A single walk costs one pass
-// over the states' arithmetic, a segmented one about 1.8, so an axis is cut
-// only where a single walk leaves most of the chip idle.
+// Segments: a single walk costs one pass over the states' arithmetic, a segmented one about 1.8, and a SIMD needs
+// two waves or more to hide a step's latencies.  With two on each (2048 waves) a single walk is faster (B=8 T=2048
+// D=4096 N=16: 326 against 446 us), with one it is not (B=4: 255 against 218 us).  A segmented walk has waves for
+// what the CUs hold, and 64 steps at least to a segment.
 Segments segments_of(const ScanProblem& p)
 {
     const int W = waves_of(p.N), TS = tile_steps(W);
     const int64_t waves = (int64_t)p.B * channel_blocks(p) * W;
     const int tiles = (p.T + TS - 1) / TS;
-    int64_t n = waves >= 1024 ? 1 : 8192 / waves;
-    if (n > p.T / 128) n = p.T / 128;                 // 128 steps at least
+    int64_t n = waves >= 2048 ? 1 : (W > 8 ? 4096 : 8192) / waves;
+    if (n > p.T / 64) n = p.T / 64;
     if (n < 1) n = 1;
     const int per = (int)((tiles + n - 1) / n);
     return Segments{per * TS, (tiles + per - 1) / per};
@@ -269,6 +272,69 @@ SegWs seg_ws(const ScanProblem& p, const Segments& sg, char* base, size_t* bytes
     *bytes = e + s;
     return w;
 }
+
+// Single tokens and very short calls: moving the states is all there is.  L lanes share a channel, kStates states
+// each, so a wave reads and writes its states in whole lines, and the lanes' shares of C h meet by lane swaps.
+template <typename T, int L>
+__global__ __launch_bounds__(256) void scan_step_kernel(ScanProblem p, int per_seq)
+{
+    const int b = blockIdx.x / per_seq;
+    const int i = (blockIdx.x % per_seq) * 256 + threadIdx.x;
+    const int c = min(i / L, p.D - 1), n0 = (i % L) * kStates;
+    const bool live = i / L < p.D;
+    const int ns = min(kStates, p.N - n0);
+    const int len = clamp_len(p.lengths, b, p.T);
+    const T* xp = (const T*)p.x.p + b * p.x.batch + c;
+    const T* dp = (const T*)p.dt.p + b * p.dt.batch + c;
+    const T* zp = p.z.p ? (const T*)p.z.p + b * p.z.batch + c : nullptr;
+    T* yp = (T*)p.y.p + b * p.y.batch + c;
+    const int g = c / (p.D / p.G);
+    const T* Bp = (const T*)p.bmat.p + b * p.bmat.batch + g * p.N + n0;
+    const T* Cp = (const T*)p.cmat.p + b * p.cmat.batch + g * p.N + n0;
+    const size_t srow = ((size_t)b * p.D + c) * p.N + n0;
+    const float skip = p.skip ? p.skip[c] : 0.0f, bias = p.dt_bias ? p.dt_bias[c] : 0.0f;
+    const f32x4 A = load_states(p.a + (size_t)c * p.N + n0, ns);
+    f32x4 h = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (p.state) h = load_states(p.state + srow, ns);
+    for (int t = 0; t < p.T; ++t) {
+        float o = 0.0f;
+        if (t < len) {
+            const float x = to_float(xp[t * p.x.row]), u = to_float(dp[t * p.dt.row]) + bias;
+            const float d = p.softplus ? softplus_t<T>(u) : u;
+            float Bv[kStates], Cv[kStates];
+#pragma unroll
+            for (int n = 0; n < kStates; ++n) {
+                Bv[n] = n < ns ? to_float(Bp[t * p.bmat.row + n]) : 0.0f;
+                Cv[n] = n < ns ? to_float(Cp[t * p.cmat.row + n]) : 0.0f;
+            }
+#pragma unroll
+            for (int n = 0; n < kStates; ++n) {
+                h[n] = exp2_fast(d * (A[n] * kLog2e)) * h[n] + d * x * Bv[n];
+                o += Cv[n] * h[n];
+            }
+#pragma unroll
+            for (int k = 1; k < L; k <<= 1) o += __shfl_xor(o, k);
+            o += skip * x;
+            if (zp) {
+                const float z = to_float(zp[t * p.z.row]);
+                o *= z * sigmoid_t<T>(z);
+            }
+        }
+        if (live && n0 == 0) yp[t * p.y.row] = from_float<T>(o);
+    }
+    if (p.state_out && live) store_states(p.state_out + srow, ns, h);
+}
+
+template <typename T, int L>
+hipError_t step_l(const ScanProblem& p, hipStream_t stream)
+{
+    const int per_seq = (int)(((int64_t)p.D * L + 255) / 256);
+    scan_step_kernel<T, L><<<(unsigned)p.B * per_seq, 256, 0, stream>>>(p, per_seq);
+    return hipGetLastError();
+}
+
+// Calls of up to this many steps go to the step kernel.
+constexpr int kStepRows = 4;
 
 template <typename T, int W>
 hipError_t fwd_w(const ScanProblem& p, hipStream_t stream)
@@ -293,6 +359,13 @@ hipError_t fwd_w(const ScanProblem& p, hipStream_t stream)
 template <typename T>
 hipError_t fwd_t(const ScanProblem& p, hipStream_t stream)
 {
+    if (p.T <= kStepRows) switch (waves_of(p.N)) {
+        case 1: return step_l<T, 1>(p, stream);
+        case 2: return step_l<T, 2>(p, stream);
+        case 4: return step_l<T, 4>(p, stream);
+        case 8: return step_l<T, 8>(p, stream);
+        default: return step_l<T, 16>(p, stream);
+        }
     switch (waves_of(p.N)) {
     case 1: return fwd_w<T, 1>(p, stream);
     case 2: return fwd_w<T, 2>(p, stream);
