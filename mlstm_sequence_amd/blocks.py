@@ -11,6 +11,7 @@ fit is refused, never copied.
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import NamedTuple, Optional
 
 import torch
@@ -59,34 +60,50 @@ class NormArgs(ctypes.Structure):
                 ("y", Heads), ("dy", Heads), ("dx", Heads), ("dgate", Heads), ("dweight", _p), ("dbias", _p)]
 
 
+_fn = {}   # this module's entry points, once the library is loaded
+
+
 def bind(L):
     """Argument types of this module's entry points."""
     vp, sz = ctypes.c_void_p, ctypes.c_size_t
     for name, args, res in (
-            ("tfla_conv_fwd", [ctypes.POINTER(ConvArgs), vp], _i),
+            ("tfla_conv_fwd", [vp, vp], _i),
             ("tfla_conv_bwd_workspace_bytes", [_i] * 5, sz),
-            ("tfla_conv_bwd", [ctypes.POINTER(ConvArgs), vp, sz, vp], _i),
+            ("tfla_conv_bwd", [vp, vp, sz, vp], _i),
             ("tfla_scan_workspace_bytes", [_i] * 6, sz),
-            ("tfla_scan_fwd", [ctypes.POINTER(ScanArgs), vp, sz, vp], _i),
+            ("tfla_scan_fwd", [vp, vp, sz, vp], _i),
             ("tfla_scan_bwd_workspace_bytes", [_i] * 6, sz),
-            ("tfla_scan_bwd", [ctypes.POINTER(ScanArgs), vp, sz, vp], _i),
+            ("tfla_scan_bwd", [vp, vp, sz, vp], _i),
             ("tfla_norm_workspace_bytes", [_i] * 5, sz),
-            ("tfla_norm_fwd", [ctypes.POINTER(NormArgs), vp, sz, vp], _i),
+            ("tfla_norm_fwd", [vp, vp, sz, vp], _i),
             ("tfla_norm_bwd_workspace_bytes", [_i] * 5, sz),
-            ("tfla_norm_bwd", [ctypes.POINTER(NormArgs), vp, sz, vp], _i)):
+            ("tfla_norm_bwd", [vp, vp, sz, vp], _i)):
         f = getattr(L, name)
         f.argtypes, f.restype = args, res
+        _fn[name] = f
 
 
-def _lib():
-    from . import tfla
-    return tfla.lib()
+def _entry(name):
+    if not _fn:
+        from . import tfla
+        tfla.lib()
+    return _fn[name]
+
+
+# The argument structures as the calls below fill them: a tuple of their
+# fields in order, packed at once (a ctypes structure filled field by field
+# takes most of a small call's time).
+_ROWS, _HEADS = "Pqq", "Pqqq"
+_CONV = struct.Struct("@6i" + _ROWS + "4P" + _ROWS + "P" + _ROWS + "P" + _ROWS + "3P")
+_SCAN = struct.Struct("@6i" + _ROWS * 5 + "5P" + _ROWS + "P" + _ROWS + "P" + _ROWS * 5 + "4P")
+_NORM = struct.Struct("@6if" + _HEADS * 2 + "4P" + _HEADS * 4 + "2P")
+_NO_ROWS, _NO_HEADS = (0, 0, 0), (0, 0, 0, 0)
 
 
 # ---- checks ------------------------------------------------------------------
 
 def _first(x, name, dims):
-    """The tensor that sets type and device."""
+    """Checks the tensor that sets type and device; returns the device's index."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(x).__name__}")
     if x.dtype not in _IO:
@@ -97,82 +114,90 @@ def _first(x, name, dims):
         raise ValueError(f"{name}: dimensions above 2^31 - 1 are not supported, got {tuple(x.shape)}")
     if not x.is_cuda:
         raise ValueError(f"tensors must live in GPU memory, got {name} on {x.device}")
-    return x.device
+    return x.get_device()
 
 
-def _like(t, name, shape, dtype, dev):
-    """Shape, type and device of ``t``; whether its last dimension is contiguous is left to the caller."""
+def _bad(t, name, shape, dtype, dev):
+    """Raises for the first thing about ``t`` that does not fit."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, other tensors on {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, other tensors on cuda:{dev}")
+    raise ValueError(f"{name} has strides {t.stride()}: its innermost dimensions must be contiguous")
+
+
+def _fits(t, shape, dtype, dev):
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
 
 
 def _flat(t, name, shape, dtype, dev):
     """Pointer of a contiguous tensor (None: NULL)."""
     if t is None:
-        return None
-    _like(t, name, shape, dtype, dev)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous (row-major), got strides {t.stride()}")
+        return 0
+    if not _fits(t, shape, dtype, dev) or not t.is_contiguous():
+        _bad(t, name, shape, dtype, dev)
     return t.data_ptr()
 
 
 def _rows(t, name, shape, dtype, dev):
     """tfla_rows of a [B,T,D] tensor with contiguous channels."""
-    _like(t, name, shape, dtype, dev)
+    if not _fits(t, shape, dtype, dev):
+        _bad(t, name, shape, dtype, dev)
     st = t.stride()
     if st[2] != 1 and shape[2] > 1:
-        raise ValueError(f"{name} must have contiguous channels (last stride 1), got strides {st}")
-    return Rows(t.data_ptr(), st[0], st[1])
+        _bad(t, name, shape, dtype, dev)
+    return t.data_ptr(), st[0], st[1]
 
 
-def _call(name, args, dev, stream, nbytes=None, workspace=None):
+def _call(name, packed, dev, stream, nbytes=None, workspace=None):
     """Calls entry point ``name`` on ``stream`` (None: the device's current
     one) with the tensors' device current; ``nbytes``: the workspace it needs."""
-    from . import tfla
-    if dev.index != torch.cuda.current_device():
+    if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return _call(name, args, dev, stream, nbytes, workspace)
-    current = torch.cuda.current_stream().cuda_stream
+            return _call(name, packed, dev, stream, nbytes, workspace)
+    current = _raw_stream(dev)
     s = current if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
-    fn = getattr(tfla.lib(), name)
     if nbytes is None:
-        rc = fn(ctypes.byref(args), s)
+        rc = _fn[name](packed, s)
     else:
+        at = size = 0
         if workspace is not None:
-            tfla._check_workspace(workspace, nbytes, dev)
-            size = workspace.numel() * workspace.element_size()
-        elif nbytes and s == current:
+            from . import tfla
+            tfla._check_workspace(workspace, nbytes, torch.device("cuda", dev))
+            at, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        elif nbytes and s == current:   # else the library allocates, in that stream's order
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-            size = nbytes
-        else:
-            size = 0   # another stream than torch's current one: the library allocates in that stream's order
-        rc = fn(ctypes.byref(args), None if workspace is None else workspace.data_ptr(), size, s)
+            at, size = workspace.data_ptr(), nbytes
+        rc = _fn[name](packed, at, size, s)
     if rc:
+        from . import tfla
         tfla._check(rc, name)
+
+
+# the current stream's handle without a Stream object around it, where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 # ---- causal convolution --------------------------------------------------------
 
 def _conv_args(x, weight, bias, act, state, lengths):
+    """(fields shared by both directions, device, K)"""
     dev = _first(x, "x", 3)
-    B, T, D = x.shape
+    shape, dtype = x.shape, x.dtype
+    B, T, D = shape
+    if act not in (ACT_NONE, ACT_SILU):
+        raise ValueError(f"act must be ACT_NONE or ACT_SILU, got {act}")
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be a [D,K] tensor")
     K = weight.shape[1]
-    a = ConvArgs()
-    a.B, a.T, a.D, a.K, a.flags, a.act = B, T, D, K, _IO[x.dtype], act
-    a.x = _rows(x, "x", x.shape, x.dtype, dev)
-    a.weight = _flat(weight, "weight", (D, K), torch.float32, dev)
-    a.bias = _flat(bias, "bias", (D,), torch.float32, dev)
-    a.state = _flat(state, "state", (B, K - 1, D), x.dtype, dev)
-    a.lengths = _flat(lengths, "lengths", (B,), torch.int32, dev)
-    return a, dev
+    return (B, T, D, K, _IO[dtype], act, *_rows(x, "x", shape, dtype, dev),
+            _flat(weight, "weight", (D, K), torch.float32, dev), _flat(bias, "bias", (D,), torch.float32, dev),
+            _flat(state, "state", (B, K - 1, D), dtype, dev), _flat(lengths, "lengths", (B,), torch.int32, dev)), dev, K
 
 
 def conv_forward(x, weight, bias=None, act: int = ACT_SILU, state=None, lengths=None, want_state: bool = False,
@@ -184,14 +209,17 @@ def conv_forward(x, weight, bias=None, act: int = ACT_SILU, state=None, lengths=
     ``state_out`` (allocated with ``want_state``, may be ``state`` itself)
     receives the last K-1 inputs, what the next call continues from.
     ``lengths`` int32 [B]: valid rows of each sequence of a padded batch."""
-    a, dev = _conv_args(x, weight, bias, act, state, lengths)
+    _entry("tfla_conv_fwd")
+    a, dev, K = _conv_args(x, weight, bias, act, state, lengths)
+    shape, dtype = x.shape, x.dtype
+    B, _, D = shape
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        y = x.new_empty(shape)
     if state_out is None and want_state:
-        state_out = torch.empty((a.B, a.K - 1, a.D), dtype=x.dtype, device=dev)
-    a.y = _rows(y, "y", x.shape, x.dtype, dev)
-    a.state_out = _flat(state_out, "state_out", (a.B, a.K - 1, a.D), x.dtype, dev)
-    _call("tfla_conv_fwd", a, dev, stream)
+        state_out = x.new_empty((B, K - 1, D))
+    packed = _CONV.pack(*a, *_rows(y, "y", shape, dtype, dev),
+                        _flat(state_out, "state_out", (B, K - 1, D), dtype, dev), *_NO_ROWS, 0, *_NO_ROWS, 0, 0, 0)
+    _call("tfla_conv_fwd", packed, dev, stream)
     return y, state_out
 
 
@@ -200,20 +228,24 @@ def conv_backward(x, weight, dy, bias=None, act: int = ACT_SILU, state=None, len
     """Gradients of :func:`conv_forward` for ``dy`` and (with carried states)
     ``dstate_out``; returns ``(dx, dweight, dbias, dstate)``, dbias None
     without bias, dstate None without state."""
-    a, dev = _conv_args(x, weight, bias, act, state, lengths)
+    need = _entry("tfla_conv_bwd_workspace_bytes")
+    a, dev, K = _conv_args(x, weight, bias, act, state, lengths)
+    shape, dtype = x.shape, x.dtype
+    B, T, D = shape
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        dx = x.new_empty(shape)
     dweight = torch.empty_like(weight)
     dbias = None if bias is None else torch.empty_like(bias)
     dstate = None if state is None else torch.empty_like(state)
-    a.dy = _rows(dy, "dy", x.shape, x.dtype, dev)
-    a.dx = _rows(dx, "dx", x.shape, x.dtype, dev)
-    a.dstate_out = _flat(dstate_out, "dstate_out", (a.B, a.K - 1, a.D), x.dtype, dev)
-    a.dweight = dweight.data_ptr()
-    a.dbias = None if dbias is None else dbias.data_ptr()
-    a.dstate = None if dstate is None else dstate.data_ptr()
-    _call("tfla_conv_bwd", a, dev, stream, _lib().tfla_conv_bwd_workspace_bytes(a.B, a.T, a.D, a.K, a.flags), workspace)
+    packed = _CONV.pack(*a, *_NO_ROWS, 0, *_rows(dy, "dy", shape, dtype, dev),
+                        _flat(dstate_out, "dstate_out", (B, K - 1, D), dtype, dev),
+                        *_rows(dx, "dx", shape, dtype, dev), *map(_ptr, (dweight, dbias, dstate)))
+    _call("tfla_conv_bwd", packed, dev, stream, need(B, T, D, K, _IO[dtype]), workspace)
     return dx, dweight, dbias, dstate
+
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
 
 
 # ---- selective scan ------------------------------------------------------------------
@@ -233,34 +265,29 @@ class ScanGrads(NamedTuple):
 
 def _group_rows(t, name, shape, dtype, dev):
     """tfla_rows of a [B,T,G,N] tensor whose last two dimensions are contiguous."""
-    _like(t, name, shape, dtype, dev)
+    if not _fits(t, shape, dtype, dev):
+        _bad(t, name, shape, dtype, dev)
     st = t.stride()
     if (st[3] != 1 and shape[3] > 1) or (st[2] != shape[3] and shape[2] > 1):
-        raise ValueError(f"{name} must have its last two dimensions contiguous, got strides {st}")
-    return Rows(t.data_ptr(), st[0], st[1])
+        _bad(t, name, shape, dtype, dev)
+    return t.data_ptr(), st[0], st[1]
 
 
 def _scan_args(x, dt, a, bmat, cmat, skip, z, dt_bias, softplus, state, lengths):
+    """(fields shared by both directions, sizes of the workspace calls, device)"""
     dev = _first(x, "x", 3)
-    shape, dtype = x.shape, x.dtype
+    shape, dtype, f32 = x.shape, x.dtype, torch.float32
     B, T, D = shape
     if not isinstance(bmat, torch.Tensor) or bmat.dim() != 4:
         raise ValueError("bmat and cmat must be [B,T,G,N] tensors")
     G, N = bmat.shape[2:]
-    s = ScanArgs()
-    s.B, s.T, s.D, s.N, s.G, s.flags = B, T, D, N, G, _IO[dtype] | (SCAN_SOFTPLUS if softplus else 0)
-    s.x = _rows(x, "x", shape, dtype, dev)
-    s.dt = _rows(dt, "dt", shape, dtype, dev)
-    if z is not None:
-        s.z = _rows(z, "z", shape, dtype, dev)
-    s.bmat = _group_rows(bmat, "bmat", (B, T, G, N), dtype, dev)
-    s.cmat = _group_rows(cmat, "cmat", (B, T, G, N), dtype, dev)
-    s.a = _flat(a, "a", (D, N), torch.float32, dev)
-    s.skip = _flat(skip, "skip", (D,), torch.float32, dev)
-    s.dt_bias = _flat(dt_bias, "dt_bias", (D,), torch.float32, dev)
-    s.state = _flat(state, "state", (B, D, N), torch.float32, dev)
-    s.lengths = _flat(lengths, "lengths", (B,), torch.int32, dev)
-    return s, dev
+    sizes = (B, T, D, N, G, _IO[dtype] | (SCAN_SOFTPLUS if softplus else 0))
+    return (*sizes, *_rows(x, "x", shape, dtype, dev), *_rows(dt, "dt", shape, dtype, dev),
+            *(_NO_ROWS if z is None else _rows(z, "z", shape, dtype, dev)),
+            *_group_rows(bmat, "bmat", (B, T, G, N), dtype, dev), *_group_rows(cmat, "cmat", (B, T, G, N), dtype, dev),
+            _flat(a, "a", (D, N), f32, dev), _flat(skip, "skip", (D,), f32, dev),
+            _flat(dt_bias, "dt_bias", (D,), f32, dev), _flat(state, "state", (B, D, N), f32, dev),
+            _flat(lengths, "lengths", (B,), torch.int32, dev)), sizes, dev
 
 
 def scan_forward(x, dt, a, bmat, cmat, skip=None, z=None, dt_bias=None, softplus: bool = True, state=None, lengths=None,
@@ -273,15 +300,16 @@ def scan_forward(x, dt, a, bmat, cmat, skip=None, z=None, dt_bias=None, softplus
     channels each.  ``state`` fp32 [B,D,N] is the state before the first row;
     ``state_out`` (allocated with ``want_state``, may be ``state`` itself) the
     one after the last.  ``lengths`` int32 [B]: valid rows of a padded batch."""
-    s, dev = _scan_args(x, dt, a, bmat, cmat, skip, z, dt_bias, softplus, state, lengths)
+    need = _entry("tfla_scan_workspace_bytes")
+    fields, sizes, dev = _scan_args(x, dt, a, bmat, cmat, skip, z, dt_bias, softplus, state, lengths)
+    B, T, D, N = sizes[:4]
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        y = x.new_empty(x.shape)
     if state_out is None and want_state:
-        state_out = torch.empty((s.B, s.D, s.N), dtype=torch.float32, device=dev)
-    s.y = _rows(y, "y", x.shape, x.dtype, dev)
-    s.state_out = _flat(state_out, "state_out", (s.B, s.D, s.N), torch.float32, dev)
-    n = _lib().tfla_scan_workspace_bytes(s.B, s.T, s.D, s.N, s.G, s.flags)
-    _call("tfla_scan_fwd", s, dev, stream, n, workspace)
+        state_out = a.new_empty((B, D, N))
+    packed = _SCAN.pack(*fields, *_rows(y, "y", x.shape, x.dtype, dev),
+                        _flat(state_out, "state_out", (B, D, N), torch.float32, dev), *_NO_ROWS, 0, *_NO_ROWS * 5, 0, 0, 0, 0)
+    _call("tfla_scan_fwd", packed, dev, stream, need(*sizes), workspace)
     return y, state_out
 
 
@@ -291,29 +319,24 @@ def scan_backward(x, dt, a, bmat, cmat, dy, skip=None, z=None, dt_bias=None, sof
     """Gradients of :func:`scan_forward` for ``dy`` and (with carried states)
     ``dstate_out``.  dx, ddt, dz, dbmat and dcmat may be given, as parts of
     a projection's gradient for instance."""
-    s, dev = _scan_args(x, dt, a, bmat, cmat, skip, z, dt_bias, softplus, state, lengths)
+    need = _entry("tfla_scan_bwd_workspace_bytes")
+    fields, sizes, dev = _scan_args(x, dt, a, bmat, cmat, skip, z, dt_bias, softplus, state, lengths)
     shape, dtype, bc = x.shape, x.dtype, bmat.shape
-    new = lambda like, t: torch.empty(like, dtype=dtype, device=dev) if t is None else t  # noqa: E731
-    dx, ddt, dbmat, dcmat = new(shape, dx), new(shape, ddt), new(bc, dbmat), new(bc, dcmat)
-    dz = None if z is None else new(shape, dz)
+    B, T, D, N = sizes[:4]
+    dx, ddt = (x.new_empty(shape) if t is None else t for t in (dx, ddt))
+    dbmat, dcmat = (x.new_empty(bc) if t is None else t for t in (dbmat, dcmat))
+    dz = None if z is None else x.new_empty(shape) if dz is None else dz
     da = torch.empty_like(a)
     dskip = None if skip is None else torch.empty_like(skip)
     ddt_bias = None if dt_bias is None else torch.empty_like(dt_bias)
     dstate = None if state is None else torch.empty_like(state)
-    s.dy = _rows(dy, "dy", shape, dtype, dev)
-    s.dstate_out = _flat(dstate_out, "dstate_out", (s.B, s.D, s.N), torch.float32, dev)
-    s.dx = _rows(dx, "dx", shape, dtype, dev)
-    s.ddt = _rows(ddt, "ddt", shape, dtype, dev)
-    if z is not None:
-        s.dz = _rows(dz, "dz", shape, dtype, dev)
-    s.dbmat = _group_rows(dbmat, "dbmat", bc, dtype, dev)
-    s.dcmat = _group_rows(dcmat, "dcmat", bc, dtype, dev)
-    s.da = da.data_ptr()
-    s.dskip = None if dskip is None else dskip.data_ptr()
-    s.ddt_bias = None if ddt_bias is None else ddt_bias.data_ptr()
-    s.dstate = None if dstate is None else dstate.data_ptr()
-    n = _lib().tfla_scan_bwd_workspace_bytes(s.B, s.T, s.D, s.N, s.G, s.flags)
-    _call("tfla_scan_bwd", s, dev, stream, n, workspace)
+    packed = _SCAN.pack(*fields, *_NO_ROWS, 0, *_rows(dy, "dy", shape, dtype, dev),
+                        _flat(dstate_out, "dstate_out", (B, D, N), torch.float32, dev),
+                        *_rows(dx, "dx", shape, dtype, dev), *_rows(ddt, "ddt", shape, dtype, dev),
+                        *(_NO_ROWS if z is None else _rows(dz, "dz", shape, dtype, dev)),
+                        *_group_rows(dbmat, "dbmat", bc, dtype, dev), *_group_rows(dcmat, "dcmat", bc, dtype, dev),
+                        *map(_ptr, (da, dskip, ddt_bias, dstate)))
+    _call("tfla_scan_bwd", packed, dev, stream, need(*sizes), workspace)
     return ScanGrads(dx, ddt, da, dbmat, dcmat, dskip, dz, ddt_bias, dstate)
 
 
@@ -321,27 +344,27 @@ def scan_backward(x, dt, a, bmat, cmat, dy, skip=None, z=None, dt_bias=None, sof
 
 def _heads(t, name, shape, dtype, dev):
     """tfla_heads of a [B,T,G,C] tensor with contiguous channels."""
-    _like(t, name, shape, dtype, dev)
+    if not _fits(t, shape, dtype, dev):
+        _bad(t, name, shape, dtype, dev)
     st = t.stride()
     if st[3] != 1 and shape[3] > 1:
-        raise ValueError(f"{name} must have contiguous channels (last stride 1), got strides {st}")
-    return Heads(t.data_ptr(), st[0], st[1], st[2])
+        _bad(t, name, shape, dtype, dev)
+    return t.data_ptr(), st[0], st[1], st[2]
 
 
-def _norm_args(x, weight, bias, act, gate, over):
+def _norm_args(x, weight, bias, act, gate, over, eps):
+    """(fields up to bias, sizes of the workspace calls, device)"""
     dev = _first(x, "x", 4)
     shape, dtype = x.shape, x.dtype
     if over not in (NORM_TOKEN, NORM_SEQUENCE):
         raise ValueError(f"over must be NORM_TOKEN or NORM_SEQUENCE, got {over}")
-    a = NormArgs()
-    a.B, a.T, a.G, a.C = shape
-    a.flags, a.act = _IO[dtype] | over, act
-    a.x = _heads(x, "x", shape, dtype, dev)
-    if gate is not None:
-        a.gate = _heads(gate, "gate", shape, dtype, dev)
-    a.weight = _flat(weight, "weight", shape[2:], torch.float32, dev)
-    a.bias = _flat(bias, "bias", shape[2:], torch.float32, dev)
-    return a, dev
+    if act not in (ACT_NONE, ACT_SILU, ACT_SIGMOID):
+        raise ValueError(f"act must be ACT_NONE, ACT_SILU or ACT_SIGMOID, got {act}")
+    sizes = (*shape, _IO[dtype] | over)
+    gc = shape[2:]
+    return (*sizes, act, float(eps), *_heads(x, "x", shape, dtype, dev),
+            *(_NO_HEADS if gate is None else _heads(gate, "gate", shape, dtype, dev)),
+            _flat(weight, "weight", gc, torch.float32, dev), _flat(bias, "bias", gc, torch.float32, dev)), sizes, dev
 
 
 def norm_forward(x, weight=None, bias=None, eps: float = 1e-5, act: int = ACT_NONE, gate=None, over: int = NORM_TOKEN,
@@ -353,17 +376,17 @@ def norm_forward(x, weight=None, bias=None, eps: float = 1e-5, act: int = ACT_NO
     weight, bias are fp32 [G,C]; mean, rstd fp32 [B,T,G] or [B,G].  The
     recurrences' head-major output h [B,H,T,d] goes in as
     ``h.transpose(1, 2)``; y is contiguous [B,T,G,C] unless given."""
-    a, dev = _norm_args(x, weight, bias, act, gate, over)
+    need = _entry("tfla_norm_workspace_bytes")
+    fields, sizes, dev = _norm_args(x, weight, bias, act, gate, over, eps)
+    B, T, G, C = shape = x.shape
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    a.eps = eps
-    a.y = _heads(y, "y", x.shape, x.dtype, dev)
-    stats = (a.B, a.G) if over else (a.B, a.T, a.G)
-    mean = torch.empty(stats, dtype=torch.float32, device=dev)
-    rstd = torch.empty(stats, dtype=torch.float32, device=dev)
-    a.mean, a.rstd = mean.data_ptr(), rstd.data_ptr()
-    n = _lib().tfla_norm_workspace_bytes(a.B, a.T, a.G, a.C, a.flags)
-    _call("tfla_norm_fwd", a, dev, stream, n, workspace)
+        y = x.new_empty(shape)
+    stats = (B, G) if over else (B, T, G)
+    mean = torch.empty(stats, dtype=torch.float32, device=x.device)
+    rstd = torch.empty_like(mean)
+    packed = _NORM.pack(*fields, mean.data_ptr(), rstd.data_ptr(), *_heads(y, "y", shape, x.dtype, dev),
+                        *_NO_HEADS * 3, 0, 0)
+    _call("tfla_norm_fwd", packed, dev, stream, need(*sizes), workspace)
     return y, mean, rstd
 
 
@@ -371,25 +394,20 @@ def norm_backward(x, dy, mean, rstd, weight=None, bias=None, act: int = ACT_NONE
                   dx=None, dgate=None, workspace=None, stream=None):
     """Gradients of :func:`norm_forward` for ``dy`` from its mean and rstd;
     returns ``(dx, dgate, dweight, dbias)``, None where the input was None."""
-    a, dev = _norm_args(x, weight, bias, act, gate, over)
-    shape, dtype = x.shape, x.dtype
+    need = _entry("tfla_norm_bwd_workspace_bytes")
+    fields, sizes, dev = _norm_args(x, weight, bias, act, gate, over, 0.0)
+    B, T, G, C = shape = x.shape
+    dtype = x.dtype
     if dx is None:
-        dx = torch.empty(shape, dtype=dtype, device=dev)
-    if gate is None:
-        dgate = None
-    else:
-        if dgate is None:
-            dgate = torch.empty(shape, dtype=dtype, device=dev)
-        a.dgate = _heads(dgate, "dgate", shape, dtype, dev)
+        dx = x.new_empty(shape)
+    dgate = None if gate is None else x.new_empty(shape) if dgate is None else dgate
     dweight = None if weight is None else torch.empty_like(weight)
     dbias = None if bias is None else torch.empty_like(bias)
-    stats = (a.B, a.G) if over else (a.B, a.T, a.G)
-    a.dy = _heads(dy, "dy", shape, dtype, dev)
-    a.dx = _heads(dx, "dx", shape, dtype, dev)
-    a.mean = _flat(mean, "mean", stats, torch.float32, dev)
-    a.rstd = _flat(rstd, "rstd", stats, torch.float32, dev)
-    a.dweight = None if dweight is None else dweight.data_ptr()
-    a.dbias = None if dbias is None else dbias.data_ptr()
-    n = _lib().tfla_norm_bwd_workspace_bytes(a.B, a.T, a.G, a.C, a.flags)
-    _call("tfla_norm_bwd", a, dev, stream, n, workspace)
+    stats = (B, G) if over else (B, T, G)
+    packed = _NORM.pack(*fields, _flat(mean, "mean", stats, torch.float32, dev),
+                        _flat(rstd, "rstd", stats, torch.float32, dev), *_NO_HEADS,
+                        *_heads(dy, "dy", shape, dtype, dev), *_heads(dx, "dx", shape, dtype, dev),
+                        *(_NO_HEADS if gate is None else _heads(dgate, "dgate", shape, dtype, dev)),
+                        _ptr(dweight), _ptr(dbias))
+    _call("tfla_norm_bwd", packed, dev, stream, need(*sizes), workspace)
     return dx, dgate, dweight, dbias

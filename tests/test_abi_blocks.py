@@ -255,3 +255,24 @@ def test_head_major_and_interleaved_heads_are_told_apart():
     a = norm_args()
     a.dx = blocks.Heads(at(40), 100 * 256, 64, 100 * 64)
     assert tfla.lib().tfla_norm_bwd(ctypes.byref(a), at(60), 0, None) == OOM
+
+
+def test_packed_arguments_match_the_structures():
+    for packed, fields in ((blocks._CONV, blocks.ConvArgs), (blocks._SCAN, blocks.ScanArgs), (blocks._NORM, blocks.NormArgs)):
+        assert packed.size == ctypes.sizeof(fields)
+        # every value lands in the field of its place
+        flat = []
+
+        def walk(s, base):
+            for name, kind in s._fields_:
+                off = base + getattr(s, name).offset
+                if issubclass(kind, ctypes.Structure):
+                    walk(kind, off)
+                else:
+                    flat.append((off, kind))
+
+        walk(fields, 0)
+        values = [float(i) if k is ctypes.c_float else i + 1 for i, (_, k) in enumerate(flat)]
+        raw = packed.pack(*values)
+        for v, (off, kind) in zip(values, flat):
+            assert kind.from_buffer_copy(raw, off).value == v
