@@ -320,7 +320,7 @@ int check_scan_sizes(int B, int T, int D, int N, int G, int flags, tfla::ScanPro
     if (B < 1 || T < 1 || D < 1 || N < 1 || G < 1)
         return fail(TFLA_ERR_INVALID_ARG, "B, T, D, N and G must be >= 1");
     if (D % G) return fail(TFLA_ERR_INVALID_ARG, "G must divide D");
-    if (N % 4 || N > 64) return fail(TFLA_ERR_UNSUPPORTED, "N must be a multiple of 4 up to 64, got " + std::to_string(N));
+    if (N > 64) return fail(TFLA_ERR_UNSUPPORTED, "N must be 1 to 64, got " + std::to_string(N));
     if ((int64_t)B * T > kMaxRows) return fail(TFLA_ERR_UNSUPPORTED, "B*T must be <= 2^30");
     if (D > (1 << 24)) return fail(TFLA_ERR_UNSUPPORTED, "D must be <= 2^24");
     const int64_t lim = (int64_t(1) << 31) - 1;
@@ -334,14 +334,6 @@ int check_scan_sizes(int B, int T, int D, int N, int G, int flags, tfla::ScanPro
     p->G = G;
     p->bf16 = (flags & TFLA_IO_BF16) != 0;
     p->softplus = (flags & TFLA_SCAN_SOFTPLUS) != 0;
-    return TFLA_OK;
-}
-
-// B and C are read in scalar loads of whole words.
-int check_words(const char* name, const tfla_rows& r, int B, int T, int64_t esz)
-{
-    if (reinterpret_cast<uintptr_t>(r.data) % 4 || (B > 1 && r.batch * esz % 4) || (T > 1 && r.row * esz % 4))
-        return fail(TFLA_ERR_INVALID_ARG, std::string(name) + ": address and strides must be multiples of 4 bytes");
     return TFLA_OK;
 }
 
@@ -384,7 +376,6 @@ int check_scan(const tfla_scan_args* a, bool bwd, tfla::ScanProblem* p, View* vi
             return fail(TFLA_ERR_INVALID_ARG, "dz, dskip and ddt_bias must be given exactly when z, skip and dt_bias are");
     }
     if ((rc = check_views(views, ni, views + ni, n - ni, !bwd && a->state == a->state_out ? a->state : nullptr))) return rc;
-    if ((rc = check_words("bmat", a->bmat, B, T, e)) || (rc = check_words("cmat", a->cmat, B, T, e))) return rc;
     *nv = n;
     p->x = dev(a->x);
     p->dt = dev(a->dt);

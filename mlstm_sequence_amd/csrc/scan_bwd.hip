@@ -7,13 +7,27 @@
 //   dx_t = delta_t sum_n g_t B_t + skip dy_t
 //   ddelta_t = x_t sum_n g_t B_t + sum_n w_t A         dA = sum_t w_t delta_t
 //
-// Pass 1 walks forward and keeps the state at the start of every tile of
-// steps.  Pass 2 walks the tiles from the last to the first: it recomputes
-// the tile's states and decays into registers, then runs the adjoint back
-// over them.  Sums over a wave's channels (dB, dC) go through lane swaps and
-// adds; each 64-channel block writes its own sums, and pass 3 adds the blocks
-// and sequences up in a fixed order.
+// Pass 1 walks every segment forward from a zero state and keeps the state
+// and the sum of the steps at the start of each tile of kTile steps; with
+// more than one segment it also forms, with the running product P of the
+// decays, the adjoint that the segment hands to the one before it when it is
+// handed none itself, sum_t P_t C_t dy_t.  Pass 2 (a thread a state) turns
+// the segments' ends into their true start states and incoming adjoints.
+// Pass 3 walks the tiles from the last to the first: it recomputes a tile's
+// states and decays into registers (a state from a zero start needs
+// exp(A sum delta) times the segment's true start added), then runs the
+// adjoint back over them.  Sums over a wave's channels (dB, dC) go through
+// lane swaps and adds, about two a value; each block of 64 channels writes
+// its own sums, and pass 4 adds blocks, segments and sequences in a fixed
+// order.
+//
+// The arithmetic bounds pass 3: of about 100 issue slots that a wave spends
+// on a step of its four states, 20 recompute, 32 run the adjoint, 18 sum over
+// the channels.  Segments cost it next to nothing, so there are enough of
+// them to fill the chip.
 #include "scan_impl.hpp"
+
+#include <type_traits>
 
 namespace tfla {
 namespace {
@@ -21,25 +35,41 @@ namespace {
 using namespace scan;
 
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kVm0 = 0x0f70;   // s_waitcnt: no vector load outstanding
+constexpr int AHEAD = 2;       // tiles whose inputs are under way
+constexpr int kTile = 8;       // steps of a tile: its states and decays take 16 registers a step pair
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// steps of a tile: 16 waves leave half the registers to each
-constexpr int tile_steps(int w) { return w > 8 ? 8 : 16; }
-
 struct Ws {
-    f32x4* tiles;        // [blocks][tiles][W][64]: states at the tiles' starts
+    f32x4* tiles;        // [B][blocks][tiles][W][64]: states at the tiles' starts (from the segment's zero start)
+    float* cums;         // [B][blocks][tiles][64]: sum of the segment's steps before the tile
+    float *ends, *adj;   // [B][nseg][D][N]: end states and handed adjoints, then start states and incoming adjoints
+    float* sums;         // [B][nseg][D]: sum of the segment's steps
     float *pb, *pc;      // [ncb][B][T][G][N]: dB, dC of one block of channels
-    float* pa;           // [B][D][N]
-    float *pskip, *pbias;   // [B][D]
+    float* pa;           // [B][nseg][D][N]
+    float *pskip, *pbias;   // [B][nseg][D]
     size_t bytes;
 };
 
-Ws layout(const ScanProblem& p, char* base)
+// Segments of whole tiles, 64 steps at least, enough for 8192 waves.
+Segments segments_of(const ScanProblem& p)
 {
-    const int W = waves_of(p.N), ts = tile_steps(W);
-    const int per = p.D / p.G, ncb = (per + 63) / 64;
-    const size_t blocks = (size_t)p.B * p.G * ncb, nt = (p.T + ts - 1) / ts;
+    const int64_t waves = (int64_t)p.B * channel_blocks(p) * waves_of(p.N);
+    const int tiles = (p.T + kTile - 1) / kTile;
+    int64_t n = waves >= 4096 ? 1 : 8192 / waves;
+    if (n > p.T / 64) n = p.T / 64;
+    if (n < 1) n = 1;
+    const int per = (int)((tiles + n - 1) / n);
+    return Segments{per * kTile, (tiles + per - 1) / per};
+}
+
+Ws layout(const ScanProblem& p, const Segments& sg, char* base)
+{
+    const int W = waves_of(p.N);
+    const size_t blocks = (size_t)p.B * channel_blocks(p), nt = (p.T + kTile - 1) / kTile;
+    const int ncb = (p.D / p.G + 63) / 64;
+    const size_t bn = (size_t)p.B * sg.nseg * p.D;
     Ws w;
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -48,58 +78,204 @@ Ws layout(const ScanProblem& p, char* base)
         return r;
     };
     w.tiles = (f32x4*)take(blocks * nt * W * 64 * 16);
+    w.cums = (float*)take(blocks * nt * 64 * 4);
+    w.ends = (float*)take(bn * p.N * 4);
+    w.adj = (float*)take(bn * p.N * 4);
+    w.sums = (float*)take(bn * 4);
     const size_t bc = (size_t)ncb * p.B * p.T * p.G * p.N * 4;
     w.pb = (float*)take(bc);
     w.pc = (float*)take(bc);
-    w.pa = (float*)take((size_t)p.B * p.D * p.N * 4);
-    w.pskip = (float*)take((size_t)p.B * p.D * 4);
-    w.pbias = (float*)take((size_t)p.B * p.D * 4);
+    w.pa = (float*)take(bn * p.N * 4);
+    w.pskip = (float*)take(bn * 4);
+    w.pbias = (float*)take(bn * 4);
     w.bytes = off;
     return w;
 }
 
-// Pass 1.
-template <typename T, int W>
-__global__ __launch_bounds__(64 * W) void scan_tiles_kernel(ScanProblem p, f32x4* __restrict__ tiles)
-{
-    constexpr int TS = tile_steps(W);
-    __shared__ f32x2 du[TS][64];
-    const Place q = place(p, Segments{p.T, 1});
-    const int len = clamp_len(p.lengths, q.b, p.T);
-    const int n0 = q.wave * kStates;
-    const bool has = n0 < p.N;
-    const int nn = has ? n0 : 0;
-    const T* xp = (const T*)p.x.p + q.b * p.x.batch + q.c;
-    const T* dp = (const T*)p.dt.p + q.b * p.dt.batch + q.c;
-    const T* Bp = (const T*)p.bmat.p + q.b * p.bmat.batch + q.g * p.N + nn;
-    const float bias = p.dt_bias ? p.dt_bias[q.c] : 0.0f;
-    const size_t srow = ((size_t)q.b * p.D + q.c) * p.N + nn;
-    const size_t nt = (p.T + TS - 1) / TS;
-    f32x4* out = tiles + ((size_t)blockIdx.x * nt * W + q.wave) * 64 + q.lane;
-    float A[kStates], h[kStates];
-#pragma unroll
-    for (int n = 0; n < kStates; ++n) {
-        A[n] = p.a[(size_t)q.c * p.N + nn + n] * kLog2e;
-        h[n] = p.state ? p.state[srow + n] : 0.0f;
+// What passes 1 and 3 share of a workgroup's setting.  A wave's own steps of
+// a tile are own .. own + OWN - 1; with more waves than steps the waves behind
+// the last step own none (and read along with the last).
+template <typename T, int W> struct Walk {
+    static constexpr int TS = kTile, OWN = TS >= W ? TS / W : 1, NP = W * kStates;
+    static_assert(TS * 2 * NP == 64 * W, "one element of B and C to a thread and tile");
+    Place q;
+    int s0, s1, len, own, n0, ns;
+    bool mine;                       // this wave owns steps
+    int64_t nt;
+    const T *xp, *dp, *zp, *gp, *mp;
+    int64_t mr;
+    int ms;
+    bool mv;
+
+    __device__ __forceinline__ Walk(const ScanProblem& p, const Segments& sg, bool with_dy) : q(place(p, sg))
+    {
+        const int all = clamp_len(p.lengths, q.b, p.T);
+        s0 = q.seg * sg.len;
+        s1 = min(s0 + sg.len, p.T);
+        len = max(0, min(all, s1) - s0);
+        mine = q.wave * OWN < TS;
+        own = min(q.wave * OWN, TS - 1);
+        n0 = q.wave * kStates;
+        ns = min(kStates, p.N - n0);
+        nt = (p.T + TS - 1) / TS;
+        xp = (const T*)p.x.p + q.b * p.x.batch + s0 * p.x.row;
+        dp = (const T*)p.dt.p + q.b * p.dt.batch + s0 * p.dt.row;
+        zp = p.z.p ? (const T*)p.z.p + q.b * p.z.batch + s0 * p.z.row : nullptr;
+        gp = with_dy ? (const T*)p.dy.p + q.b * p.dy.batch + s0 * p.dy.row : nullptr;
+        // this thread's element of a tile's B and C: step, matrix, state in that order
+        const int e = threadIdx.x, n = e % NP;
+        const Rows& m = e / NP % 2 ? p.cmat : p.bmat;
+        mv = n < p.N;
+        ms = e / NP / 2;
+        mr = m.row;
+        mp = (const T*)m.p + q.b * m.batch + s0 * m.row + q.g * p.N + min(n, p.N - 1);
     }
-    for (int t0 = 0; t0 < len; t0 += TS) {
-        const int cnt = min(TS, len - t0);
-        out[(size_t)(t0 / TS) * W * 64] = f32x4{h[0], h[1], h[2], h[3]};
-        __syncthreads();
-        for (int s = q.wave; s < cnt; s += W) {
-            const float xv = to_float(xp[(t0 + s) * p.x.row]);
-            const float u = to_float(dp[(t0 + s) * p.dt.row]) + bias;
-            const float d = p.softplus ? softplus_t<T>(u) : u;
-            du[s][q.lane] = f32x2{d, d * xv};
-        }
-        __syncthreads();
-        for (int s = 0; s < cnt; ++s) {
-            const f32x2 v = du[s][q.lane];
-            Uniform4<T> Bv;
-            Bv.load(Bp + (t0 + s) * p.bmat.row);
+    // row t of the segment, the last one for rows behind the end: no branch stands around a load
+    __device__ __forceinline__ int64_t row(int t) const { return min(t, len - 1); }
+    __device__ __forceinline__ size_t tile0() const   // first tile of the segment among the sequence's, per block
+    {
+        return (size_t)s0 / TS;
+    }
+};
+
+// Pass 1.  ADJ: also the adjoint handed on (more than one segment).
+template <typename T, int W, bool ADJ, bool GATED>
+__global__ __launch_bounds__(64 * W) void scan_tiles_kernel(ScanProblem p, Segments sg, Ws ws, int nblk)
+{
+    typedef Walk<T, W> K;
+    constexpr int TS = K::TS, OWN = K::OWN;
+    __shared__ f32x2 du[TS][64];
+    __shared__ float gy[ADJ ? TS : 1][64];
+    __shared__ f32x4 bc[TS][2][W];
+    const K k(p, sg, ADJ);
+    const Place& q = k.q;
+    const unsigned c = q.c;
+    const float bias = p.dt_bias ? p.dt_bias[c] : 0.0f;
+    const size_t blk = (size_t)q.b * nblk + q.blk;
+    f32x4* tiles = ws.tiles + ((blk * k.nt + k.tile0()) * W + q.wave) * 64 + q.lane;
+    float* cums = ws.cums + (blk * k.nt + k.tile0()) * 64 + q.lane;
+    float A[kStates], h[kStates], P[kStates], G[kStates], cum = 0.0f;
+    {
+        const f32x4 av = load_states(p.a + (size_t)c * p.N + k.n0, k.ns);
+        const f32x4 hv = sg.nseg == 1 && p.state ? load_states(p.state + ((size_t)q.b * p.D + c) * p.N + k.n0, k.ns)
+                                                 : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int n = 0; n < kStates; ++n) h[n] = exp2_fast(v[0] * A[n]) * h[n] + v[1] * Bv.get(n);
+        for (int n = 0; n < kStates; ++n) {
+            A[n] = av[n] * kLog2e;
+            h[n] = hv[n];
+            P[n] = 1.0f;
+            G[n] = 0.0f;
         }
+    }
+    struct Raw {
+        T x[OWN], dt[OWN], z[OWN], dy[OWN], m;
+    };
+    Raw raw[AHEAD];
+    auto fetch = [&](Raw& r, int t0) {
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+            const int64_t t = k.row(t0 + k.own + i);
+            r.x[i] = (k.xp + t * p.x.row)[c];
+            r.dt[i] = (k.dp + t * p.dt.row)[c];
+            if (ADJ) r.dy[i] = (k.gp + t * p.dy.row)[c];
+            if (ADJ && GATED) r.z[i] = (k.zp + t * p.z.row)[c];
+        }
+        r.m = k.mp[k.row(t0 + k.ms) * k.mr];
+    };
+    auto publish = [&](const Raw& r) {
+        if (k.mine) {
+#pragma unroll
+            for (int i = 0; i < OWN; ++i) {
+                const float u = to_float(r.dt[i]) + bias;
+                const float d = p.softplus ? softplus_t<T>(u) : u;
+                du[k.own + i][q.lane] = f32x2{d, d * to_float(r.x[i])};
+                if (ADJ) {
+                    float g = to_float(r.dy[i]);
+                    if (GATED) {
+                        const float z = to_float(r.z[i]);
+                        g *= z * sigmoid_t<T>(z);
+                    }
+                    gy[k.own + i][q.lane] = g;
+                }
+            }
+        }
+        ((float*)bc)[threadIdx.x] = k.mv ? to_float(r.m) : 0.0f;
+    };
+    auto step = [&](int s) {
+        const f32x2 v = du[s][q.lane];
+        const f32x4 Bv = bc[s][0][q.wave], Cv = bc[s][1][q.wave];
+        const float g = ADJ ? gy[s][q.lane] : 0.0f;
+        cum += v[0];
+#pragma unroll
+        for (int n = 0; n < kStates; ++n) {
+            const float a = exp2_fast(v[0] * A[n]);
+            h[n] = a * h[n] + v[1] * Bv[n];
+            if (ADJ) {
+                P[n] *= a;
+                G[n] += P[n] * (Cv[n] * g);
+            }
+        }
+    };
+    __builtin_amdgcn_s_waitcnt(kVm0);   // see scan.hip
+    __builtin_amdgcn_sched_barrier(0);
+    if (k.len > 0) {
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) fetch(raw[a], a * TS);
+        publish(raw[0]);
+    }
+    auto tile = [&](int t0, Raw& r, const Raw& next) {
+        const int cnt = min(TS, k.len - t0);
+        fetch(r, t0 + AHEAD * TS);
+        tiles[(size_t)(t0 / TS) * W * 64] = f32x4{h[0], h[1], h[2], h[3]};
+        if (ADJ && q.wave == 0) cums[(size_t)(t0 / TS) * 64] = cum;
+        __syncthreads();
+        if (cnt == TS) {
+#pragma unroll
+            for (int s = 0; s < TS; ++s) {
+                step(s);
+                if (s & 1) __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
+            for (int s = 0; s < cnt; ++s) step(s);
+        }
+        __syncthreads();
+        publish(next);
+    };
+    for (int t0 = 0; t0 < k.len; t0 += AHEAD * TS) {
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+            if (t0 + a * TS < k.len) tile(t0 + a * TS, raw[a], raw[(a + 1) % AHEAD]);
+    }
+    if (ADJ && q.live) {
+        const size_t e = ((size_t)q.b * sg.nseg + q.seg) * p.D + c;
+        store_states(ws.ends + e * p.N + k.n0, k.ns, f32x4{h[0], h[1], h[2], h[3]});
+        store_states(ws.adj + e * p.N + k.n0, k.ns, f32x4{G[0], G[1], G[2], G[3]});
+        if (q.wave == 0) ws.sums[e] = cum;
+    }
+}
+
+// Pass 2.
+__global__ __launch_bounds__(256) void scan_links_kernel(ScanProblem p, Segments sg, Ws ws)
+{
+    const int64_t DN = (int64_t)p.D * p.N;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= p.B * DN) return;
+    const int64_t b = i / DN, k = i % DN;
+    const float A = p.a[k] * kLog2e;
+    float* e = ws.ends + b * sg.nseg * DN + k;
+    float* g = ws.adj + b * sg.nseg * DN + k;
+    const float* s = ws.sums + b * sg.nseg * p.D + k / p.N;
+    float h = p.state ? p.state[i] : 0.0f;
+    for (int j = 0; j < sg.nseg; ++j) {
+        const float next = exp2_fast(s[(int64_t)j * p.D] * A) * h + e[j * DN];
+        e[j * DN] = h;
+        h = next;
+    }
+    float in = p.dstate_out ? p.dstate_out[i] : 0.0f;
+    for (int j = sg.nseg - 1; j >= 0; --j) {
+        const float next = exp2_fast(s[(int64_t)j * p.D] * A) * in + g[j * DN];
+        g[j * DN] = in;
+        in = next;
     }
 }
 
@@ -113,8 +289,8 @@ __device__ __forceinline__ float dpp_add(float v)
     return v + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
 }
 
-// v0 + v1 where each half (rows, lane pairs ...) afterwards holds one of the
-// two values' partial sums: 32 lanes apart, 16 lanes apart.
+// Two values' sums over pairs of lanes 32 (16) apart: the lower half (even
+// rows) of the result belongs to a, the upper half (odd rows) to b.
 __device__ __forceinline__ float fold32(float a, float b)
 {
     const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, a), __builtin_bit_cast(unsigned, b), false, false);
@@ -124,7 +300,7 @@ __device__ __forceinline__ float fold32(float a, float b)
 __device__ __forceinline__ float fold16(float a, float b)
 {
     const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, a), __builtin_bit_cast(unsigned, b), false, false);
-    const unsigned lo = r[0], hi = r[1];   // a bit cast of a vector's element itself would take element 0
+    const unsigned lo = r[0], hi = r[1];
     return __builtin_bit_cast(float, lo) + __builtin_bit_cast(float, hi);
 }
 
@@ -142,125 +318,110 @@ __device__ __forceinline__ float sum8(const float (&v)[8], int lane)
     return c;
 }
 
-// Pass 2.
-template <typename T, int W>
-__global__ __launch_bounds__(64 * W) void scan_bwd_kernel(ScanProblem p, Ws ws)
+// Pass 3.
+template <typename T, int W, bool GATED>
+__global__ __launch_bounds__(64 * W) void scan_bwd_kernel(ScanProblem p, Segments sg, Ws ws, int nblk)
 {
-    constexpr int TS = tile_steps(W);
-    constexpr int OWN = TS / W > 0 ? TS / W : 1;
-    __shared__ f32x4 in[TS][64];              // delta, delta x, dy after the gate
-    __shared__ float part[W][3][TS][64];      // sum_n g B, sum_n w A, sum_n C h
-    const Place q = place(p, Segments{p.T, 1});
-    const int len = clamp_len(p.lengths, q.b, p.T);
-    const int n0 = q.wave * kStates;
-    const bool has = n0 < p.N;
-    const int nn = has ? n0 : 0;
-    const T* xp = (const T*)p.x.p + q.b * p.x.batch + q.c;
-    const T* dp = (const T*)p.dt.p + q.b * p.dt.batch + q.c;
-    const T* zp = p.z.p ? (const T*)p.z.p + q.b * p.z.batch + q.c : nullptr;
-    const T* gp = (const T*)p.dy.p + q.b * p.dy.batch + q.c;
-    T* dxp = (T*)p.dx.p + q.b * p.dx.batch + q.c;
-    T* ddp = (T*)p.ddt.p + q.b * p.ddt.batch + q.c;
-    T* dzp = p.z.p ? (T*)p.dz.p + q.b * p.dz.batch + q.c : nullptr;
-    const T* Bp = (const T*)p.bmat.p + q.b * p.bmat.batch + q.g * p.N + nn;
-    const T* Cp = (const T*)p.cmat.p + q.b * p.cmat.batch + q.g * p.N + nn;
-    const float skip = p.skip ? p.skip[q.c] : 0.0f;
-    const float bias = p.dt_bias ? p.dt_bias[q.c] : 0.0f;
-    const size_t srow = ((size_t)q.b * p.D + q.c) * p.N + nn;
-    const size_t nt = (p.T + TS - 1) / TS;
-    const f32x4* starts = ws.tiles + ((size_t)blockIdx.x * nt * W + q.wave) * 64 + q.lane;
-    // which of a step's eight sums this lane stores, and for which of eight steps
+    typedef Walk<T, W> K;
+    constexpr int TS = K::TS, OWN = K::OWN, NS = GATED ? 3 : 2;
+    static_assert(TS == 8, "the sums of eight steps leave together");
+    __shared__ f32x2 du[TS][64];              // delta, delta x
+    __shared__ float gy[TS][64];              // dy after the gate
+    __shared__ f32x4 bc[TS][2][W];
+    __shared__ float part[W][NS][TS][64];     // sum_n g B, sum_n w A, sum_n C h
+    const K k(p, sg, true);
+    const Place& q = k.q;
+    const unsigned c = q.c;
+    T* dxp = (T*)p.dx.p + q.b * p.dx.batch + k.s0 * p.dx.row;
+    T* ddp = (T*)p.ddt.p + q.b * p.ddt.batch + k.s0 * p.ddt.row;
+    T* dzp = GATED ? (T*)p.dz.p + q.b * p.dz.batch + k.s0 * p.dz.row : nullptr;
+    const float skip = p.skip ? p.skip[c] : 0.0f;
+    const float bias = p.dt_bias ? p.dt_bias[c] : 0.0f;
+    const size_t blk = (size_t)q.b * nblk + q.blk;
+    const f32x4* tiles = ws.tiles + ((blk * k.nt + k.tile0()) * W + q.wave) * 64 + q.lane;
+    const float* cums = ws.cums + (blk * k.nt + k.tile0()) * 64 + q.lane;
+    const size_t erow = (((size_t)q.b * sg.nseg + q.seg) * p.D + c) * p.N + k.n0;
+    const size_t srow = ((size_t)q.b * p.D + c) * p.N + k.n0;
+    const bool linked = sg.nseg > 1;
+    // which of a step's eight sums this lane stores, and for which of the tile's steps
     const int vi = 4 * ((q.lane >> 3) & 1) + 2 * ((q.lane >> 4) & 1) + (q.lane >> 5), vs = q.lane & 7;
+    const bool stores = (vi & 3) < k.ns;
     float* sums = (vi >= 4 ? ws.pc : ws.pb) +
-                  (((size_t)q.cb * p.B + q.b) * p.T * p.G + q.g) * p.N + nn + (vi & 3);
+                  ((((size_t)q.cb * p.B + q.b) * p.T + k.s0 + vs) * p.G + q.g) * p.N + k.n0 + (vi & 3);
 
-    float A[kStates], ag[kStates], dA[kStates];
+    float A[kStates], ag[kStates], dA[kStates], hs[kStates];
+    {
+        const f32x4 av = load_states(p.a + (size_t)c * p.N + k.n0, k.ns);
+        f32x4 gv = {0.0f, 0.0f, 0.0f, 0.0f}, sv = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (linked) {
+            gv = load_states(ws.adj + erow, k.ns);
+            sv = load_states(ws.ends + erow, k.ns);
+        } else if (p.dstate_out) {
+            gv = load_states(p.dstate_out + srow, k.ns);
+        }
 #pragma unroll
-    for (int n = 0; n < kStates; ++n) {
-        A[n] = p.a[(size_t)q.c * p.N + nn + n] * kLog2e;
-        ag[n] = p.dstate_out ? p.dstate_out[srow + n] : 0.0f;
-        dA[n] = 0.0f;
+        for (int n = 0; n < kStates; ++n) {
+            A[n] = av[n] * kLog2e;
+            ag[n] = q.live ? gv[n] : 0.0f;
+            hs[n] = sv[n];
+            dA[n] = 0.0f;
+        }
     }
     float dskip = 0.0f, dbias = 0.0f;
-    for (int t0 = (len - 1) / TS * TS; t0 >= 0 && len > 0; t0 -= TS) {
-        const int cnt = min(TS, len - t0);
-        float xv[OWN], dv[OWN], sl[OWN], gv[OWN], dzv[OWN], ge[OWN];
+    struct Raw {
+        T x[OWN], dt[OWN], z[OWN], dy[OWN], m;
+        f32x4 h0;
+        float cum;
+    };
+    Raw raw[AHEAD];
+    float xv[OWN], dv[OWN], sl[OWN], ge[OWN], zf[OWN];   // the current tile's own steps, for their finish
+    auto fetch = [&](Raw& r, int t0) {                   // behind the first tile: the first
+        t0 = max(t0, 0);
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
-            const int s = q.wave + i * W;
-            if (s < cnt) {
-                xv[i] = q.live ? to_float(xp[(t0 + s) * p.x.row]) : 0.0f;
-                const float u = to_float(dp[(t0 + s) * p.dt.row]) + bias;
-                dv[i] = p.softplus ? softplus_t<T>(u) : u;
-                sl[i] = p.softplus ? sigmoid_t<T>(u) : 1.0f;
-                gv[i] = q.live ? to_float(gp[(t0 + s) * p.dy.row]) : 0.0f;
-                ge[i] = gv[i];
-                if (zp) {
-                    const float z = to_float(zp[(t0 + s) * p.z.row]);
-                    const float sg = sigmoid_t<T>(z);
-                    ge[i] = gv[i] * z * sg;
-                    dzv[i] = gv[i] * sg * (1.0f + z * (1.0f - sg));
-                }
-                in[s][q.lane] = f32x4{dv[i], dv[i] * xv[i], ge[i], 0.0f};
-            }
+            const int64_t t = k.row(t0 + k.own + i);
+            r.x[i] = (k.xp + t * p.x.row)[c];
+            r.dt[i] = (k.dp + t * p.dt.row)[c];
+            r.dy[i] = (k.gp + t * p.dy.row)[c];
+            if (GATED) r.z[i] = (k.zp + t * p.z.row)[c];
         }
-        __syncthreads();
-        if (has) {
-            const f32x4 h0 = starts[(size_t)(t0 / TS) * W * 64];
-            float h[TS][kStates], a[TS][kStates];
-#pragma unroll
-            for (int s = 0; s < TS; ++s) {
-                if (s < cnt) {
-                    const f32x4 v = in[s][q.lane];
-                    Uniform4<T> Bv, Cv;
-                    Bv.load(Bp + (t0 + s) * p.bmat.row);
-                    Cv.load(Cp + (t0 + s) * p.cmat.row);
-                    float o = 0.0f;
-#pragma unroll
-                    for (int n = 0; n < kStates; ++n) {
-                        a[s][n] = exp2_fast(v[0] * A[n]);
-                        h[s][n] = a[s][n] * (s ? h[s ? s - 1 : 0][n] : h0[n]) + v[1] * Bv.get(n);
-                        o += Cv.get(n) * h[s][n];
-                    }
-                    if (zp) part[q.wave][2][s][q.lane] = o;
-                }
-            }
-            float mine = 0.0f;
-#pragma unroll
-            for (int s = TS - 1; s >= 0; --s) {
-                if (s < cnt) {
-                    const f32x4 v = in[s][q.lane];
-                    Uniform4<T> Bv, Cv;
-                    Bv.load(Bp + (t0 + s) * p.bmat.row);
-                    Cv.load(Cp + (t0 + s) * p.cmat.row);
-                    float s1 = 0.0f, s2 = 0.0f, sum[8];
-#pragma unroll
-                    for (int n = 0; n < kStates; ++n) {
-                        const float gn = Cv.get(n) * v[2] + ag[n];
-                        sum[n] = gn * v[1];
-                        sum[4 + n] = v[2] * h[s][n];
-                        s1 += gn * Bv.get(n);
-                        ag[n] = gn * a[s][n];
-                        const float wn = ag[n] * (s ? h[s ? s - 1 : 0][n] : h0[n]);
-                        s2 += wn * A[n];
-                        dA[n] += wn * v[0];
-                    }
-                    part[q.wave][0][s][q.lane] = s1;
-                    part[q.wave][1][s][q.lane] = s2;
-                    const float r = sum8(sum, q.lane);
-                    mine = vs == (s & 7) ? r : mine;
-                }
-                if ((s & 7) == 0 && s < cnt && s + vs < cnt) sums[(size_t)(t0 + s + vs) * p.G * p.N] = mine;
-            }
-        } else {
-            for (int s = 0; s < cnt; ++s)
-                for (int k = 0; k < 3; ++k) part[q.wave][k][s][q.lane] = 0.0f;
-        }
-        __syncthreads();
+        r.m = k.mp[k.row(t0 + k.ms) * k.mr];
+        r.h0 = tiles[(size_t)(t0 / TS) * W * 64];
+        r.cum = linked ? cums[(size_t)(t0 / TS) * 64] : 0.0f;
+    };
+    auto publish = [&](const Raw& r) {
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
-            const int s = q.wave + i * W;
-            if (s < cnt) {
+            // a lane without a channel adds nothing to the sums over channels
+            xv[i] = q.live ? to_float(r.x[i]) : 0.0f;
+            const float u = to_float(r.dt[i]) + bias;
+            dv[i] = u;
+            sl[i] = 1.0f;
+            if (p.softplus) {   // and its slope, sigmoid(u), from the same e^{-|u|}
+                const float y = sizeof(T) == 2 ? exp2_fast(fabsf(u) * -kLog2e) : exp_f(-fabsf(u));
+                dv[i] = softplus_of(u, y);
+                sl[i] = __builtin_amdgcn_rcpf(1.0f + y) * (u < 0.0f ? y : 1.0f);
+            }
+            float g = q.live ? to_float(r.dy[i]) : 0.0f;
+            if (GATED) {
+                const float z = to_float(r.z[i]), sg = sigmoid_t<T>(z), zs = z * sg;
+                zf[i] = g * (sg + zs * (1.0f - sg));
+                g = q.live ? g * zs : 0.0f;
+            }
+            ge[i] = g;
+            if (k.mine) {
+                du[k.own + i][q.lane] = f32x2{dv[i], dv[i] * xv[i]};
+                gy[k.own + i][q.lane] = g;
+            }
+        }
+        ((float*)bc)[threadIdx.x] = k.mv ? to_float(r.m) : 0.0f;
+    };
+    auto finish = [&](int t0) {
+        const int n = k.mine ? k.len - t0 - k.own : 0;
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+            if (i < n) {
+                const int s = k.own + i;
                 float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
@@ -270,31 +431,123 @@ __global__ __launch_bounds__(64 * W) void scan_bwd_kernel(ScanProblem p, Ws ws)
                 const float dd = (xv[i] * s1 + s2 * kLn2) * sl[i];
                 dskip += ge[i] * xv[i];
                 dbias += dd;
-                if (q.live) {
-                    dxp[(t0 + s) * p.dx.row] = from_float<T>(dv[i] * s1 + skip * ge[i]);
-                    ddp[(t0 + s) * p.ddt.row] = from_float<T>(dd);
-                }
-                if (zp) {
-                    float o = skip * xv[i];
+                const int64_t t = t0 + s;
+                float o = skip * xv[i];
+                if (GATED) {
 #pragma unroll
-                    for (int w = 0; w < W; ++w) o += part[w][2][s][q.lane];
-                    if (q.live) dzp[(t0 + s) * p.dz.row] = from_float<T>(dzv[i] * o);
+                    for (int w = 0; w < W; ++w) o += part[w][NS - 1][s][q.lane];
+                }
+                if (q.live) {
+                    (dxp + t * p.dx.row)[c] = from_float<T>(dv[i] * s1 + skip * ge[i]);
+                    (ddp + t * p.ddt.row)[c] = from_float<T>(dd);
+                    if (GATED) (dzp + t * p.dz.row)[c] = from_float<T>(zf[i] * o);
                 }
             }
         }
-    }
-    for (int t = len + q.wave; t < p.T; t += W)
-        if (q.live) {
-            dxp[t * p.dx.row] = from_float<T>(0.0f);
-            ddp[t * p.ddt.row] = from_float<T>(0.0f);
-            if (zp) dzp[t * p.dz.row] = from_float<T>(0.0f);
-        }
-    if (has && q.live) {
+    };
+    // cnt steps of the tile (ALL: all of them, known when compiled)
+    auto walk = [&](auto ALL, int cnt, int t0, f32x4 h0, float cum) {
+        constexpr bool all = decltype(ALL)::value;
+        if (linked) {
 #pragma unroll
-        for (int n = 0; n < kStates; ++n) {
-            if (p.dstate) p.dstate[srow + n] = ag[n];
-            ws.pa[srow + n] = dA[n];
+            for (int n = 0; n < kStates; ++n) h0[n] += exp2_fast(cum * A[n]) * hs[n];
         }
+        // The published values of the next step are read while the current one is computed; the scheduler is
+        // kept from reading further ahead, which costs registers and with them waves on a SIMD.
+        struct In {
+            f32x2 v;
+            f32x4 B, C;
+            float g;
+        } in[2];
+        auto load = [&](In& r, int s, bool c4, bool g1) {
+            r.v = du[s][q.lane];
+            r.B = bc[s][0][q.wave];
+            if (c4) r.C = bc[s][1][q.wave];
+            if (g1) r.g = gy[s][q.lane];
+        };
+        float h[TS][kStates], a[TS][kStates];
+        load(in[0], 0, GATED, false);
+#pragma unroll
+        for (int s = 0; s < TS; ++s) {
+            if (s + 1 < TS) load(in[(s + 1) & 1], s + 1, GATED, false);
+            __builtin_amdgcn_sched_barrier(0);
+            if (all || s < cnt) {
+                const In& r = in[s & 1];
+#pragma unroll
+                for (int n = 0; n < kStates; ++n) {
+                    a[s][n] = exp2_fast(r.v[0] * A[n]);
+                    h[s][n] = a[s][n] * (s ? h[s ? s - 1 : 0][n] : h0[n]) + r.v[1] * r.B[n];
+                }
+                if (GATED) {
+                    float o = 0.0f;
+#pragma unroll
+                    for (int n = 0; n < kStates; ++n) o += r.C[n] * h[s][n];
+                    part[q.wave][NS - 1][s][q.lane] = o;
+                }
+            }
+        }
+        float mine = 0.0f;
+        load(in[(TS - 1) & 1], TS - 1, true, true);
+#pragma unroll
+        for (int s = TS - 1; s >= 0; --s) {
+            if (s > 0) load(in[(s - 1) & 1], s - 1, true, true);
+            __builtin_amdgcn_sched_barrier(0);
+            if (all || s < cnt) {
+                const In& r = in[s & 1];
+                float s1 = 0.0f, s2 = 0.0f, sum[8];
+#pragma unroll
+                for (int n = 0; n < kStates; ++n) {
+                    const float gn = r.C[n] * r.g + ag[n];
+                    sum[n] = gn * r.v[1];
+                    sum[4 + n] = r.g * h[s][n];
+                    s1 += gn * r.B[n];
+                    ag[n] = gn * a[s][n];
+                    const float wn = ag[n] * (s ? h[s ? s - 1 : 0][n] : h0[n]);
+                    s2 += wn * A[n];
+                    dA[n] += wn * r.v[0];
+                }
+                part[q.wave][0][s][q.lane] = s1;
+                part[q.wave][1][s][q.lane] = s2;
+                const float t = sum8(sum, q.lane);
+                mine = vs == s ? t : mine;
+            }
+        }
+        if (stores && vs < cnt) sums[(size_t)t0 * p.G * p.N] = mine;
+    };
+    const int last = (k.len - 1) / TS * TS;
+    __builtin_amdgcn_s_waitcnt(kVm0);   // see scan.hip
+    __builtin_amdgcn_sched_barrier(0);
+    if (k.len > 0) {
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) fetch(raw[a], last - a * TS);
+        publish(raw[0]);
+    }
+    auto tile = [&](int t0, Raw& r, const Raw& next) {
+        const int cnt = min(TS, k.len - t0);
+        const f32x4 h0 = r.h0;
+        const float cum = r.cum;
+        fetch(r, t0 - AHEAD * TS);
+        __syncthreads();
+        if (cnt == TS) walk(std::true_type{}, TS, t0, h0, cum);
+        else walk(std::false_type{}, cnt, t0, h0, cum);
+        __syncthreads();
+        finish(t0);
+        publish(next);
+    };
+    for (int t0 = last; t0 >= 0 && k.len > 0; t0 -= AHEAD * TS) {
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+            if (t0 - a * TS >= 0) tile(t0 - a * TS, raw[a], raw[(a + 1) % AHEAD]);
+    }
+    for (int t = k.len + q.wave; t < k.s1 - k.s0; t += W)
+        if (q.live) {
+            (dxp + t * p.dx.row)[c] = from_float<T>(0.0f);
+            (ddp + t * p.ddt.row)[c] = from_float<T>(0.0f);
+            if (GATED) (dzp + t * p.dz.row)[c] = from_float<T>(0.0f);
+        }
+    if (q.live) {
+        if (p.dstate && q.seg == 0) store_states(p.dstate + srow, k.ns, f32x4{ag[0], ag[1], ag[2], ag[3]});
+        store_states(ws.pa + erow, k.ns, f32x4{dA[0], dA[1], dA[2], dA[3]});
     }
     __syncthreads();
     part[q.wave][0][0][q.lane] = dskip;
@@ -306,15 +559,16 @@ __global__ __launch_bounds__(64 * W) void scan_bwd_kernel(ScanProblem p, Ws ws)
             s1 += part[w][0][0][q.lane];
             s2 += part[w][1][0][q.lane];
         }
-        ws.pskip[(size_t)q.b * p.D + q.c] = s1;
-        ws.pbias[(size_t)q.b * p.D + q.c] = s2;
+        const size_t e = ((size_t)q.b * sg.nseg + q.seg) * p.D + c;
+        ws.pskip[e] = s1;
+        ws.pbias[e] = s2;
     }
 }
 
-// Pass 3: dB and dC over the blocks of channels (rows behind a sequence are
-// 0), dA, dskip and ddt_bias over the sequences.
+// Pass 4: dB and dC over the blocks of channels (rows behind a sequence are
+// 0), dA, dskip and ddt_bias over segments and sequences.
 template <typename T>
-__global__ __launch_bounds__(256) void scan_sums_kernel(ScanProblem p, Ws ws, int ncb)
+__global__ __launch_bounds__(256) void scan_sums_kernel(ScanProblem p, Ws ws, int ncb, int parts)
 {
     const int64_t GN = (int64_t)p.G * p.N, rows = (int64_t)p.B * p.T;
     const int64_t nbc = rows * GN, na = (int64_t)p.D * p.N;
@@ -336,35 +590,45 @@ __global__ __launch_bounds__(256) void scan_sums_kernel(ScanProblem p, Ws ws, in
     i -= 2 * nbc;
     if (i < na) {
         float s = 0.0f;
-        for (int b = 0; b < p.B; ++b) s += ws.pa[b * na + i];
+        for (int r = 0; r < parts; ++r) s += ws.pa[r * na + i];
         p.da[i] = s;
         return;
     }
     i -= na;
     if (i < p.D) {
-        float s = 0.0f, r = 0.0f;
-        for (int b = 0; b < p.B; ++b) {
-            s += ws.pskip[(int64_t)b * p.D + i];
-            r += ws.pbias[(int64_t)b * p.D + i];
+        float s = 0.0f, u = 0.0f;
+        for (int r = 0; r < parts; ++r) {
+            s += ws.pskip[(int64_t)r * p.D + i];
+            u += ws.pbias[(int64_t)r * p.D + i];
         }
         if (p.dskip) p.dskip[i] = s;
-        if (p.ddt_bias) p.ddt_bias[i] = r;
+        if (p.ddt_bias) p.ddt_bias[i] = u;
     }
 }
 
 template <typename T, int W>
 hipError_t bwd_w(const ScanProblem& p, hipStream_t stream)
 {
-    const int ncb = (p.D / p.G + 63) / 64;
-    const unsigned blocks = (unsigned)p.B * p.G * ncb;
-    const Ws ws = layout(p, p.ws);
-    scan_tiles_kernel<T, W><<<blocks, 64 * W, 0, stream>>>(p, ws.tiles);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    scan_bwd_kernel<T, W><<<blocks, 64 * W, 0, stream>>>(p, ws);
+    const Segments sg = segments_of(p);
+    const int nblk = channel_blocks(p);
+    const unsigned blocks = (unsigned)p.B * sg.nseg * nblk;
+    const Ws ws = layout(p, sg, p.ws);
+    hipError_t e;
+    if (sg.nseg > 1) {
+        if (p.z.p) scan_tiles_kernel<T, W, true, true><<<blocks, 64 * W, 0, stream>>>(p, sg, ws, nblk);
+        else scan_tiles_kernel<T, W, true, false><<<blocks, 64 * W, 0, stream>>>(p, sg, ws, nblk);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        const int64_t n = (int64_t)p.B * p.D * p.N;
+        scan_links_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(p, sg, ws);
+    } else {
+        scan_tiles_kernel<T, W, false, false><<<blocks, 64 * W, 0, stream>>>(p, sg, ws, nblk);
+    }
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (p.z.p) scan_bwd_kernel<T, W, true><<<blocks, 64 * W, 0, stream>>>(p, sg, ws, nblk);
+    else scan_bwd_kernel<T, W, false><<<blocks, 64 * W, 0, stream>>>(p, sg, ws, nblk);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const int64_t n = 2 * (int64_t)p.B * p.T * p.G * p.N + (int64_t)p.D * p.N + p.D;
-    scan_sums_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(p, ws, ncb);
+    scan_sums_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(p, ws, (p.D / p.G + 63) / 64, p.B * sg.nseg);
     return hipGetLastError();
 }
 
@@ -382,7 +646,7 @@ hipError_t bwd_t(const ScanProblem& p, hipStream_t stream)
 
 }  // namespace
 
-size_t scan_bwd_workspace(const ScanProblem& p) { return layout(p, nullptr).bytes; }
+size_t scan_bwd_workspace(const ScanProblem& p) { return layout(p, segments_of(p), nullptr).bytes; }
 
 hipError_t launch_scan_bwd(const ScanProblem& p, hipStream_t stream)
 {

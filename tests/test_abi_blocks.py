@@ -136,10 +136,10 @@ def scan_args(**kw):
 
 SCAN_BOTH = [
     ({"B": 0}, INVALID), ({"T": -1}, INVALID), ({"D": 0}, INVALID), ({"G": 0}, INVALID), ({"G": 3}, INVALID),
-    ({"N": 0}, INVALID), ({"N": 6}, UNSUPPORTED), ({"N": 68}, UNSUPPORTED), ({"flags": 0x200}, INVALID),
+    ({"N": 0}, INVALID), ({"N": 65}, UNSUPPORTED), ({"N": 1 << 20}, UNSUPPORTED), ({"flags": 0x200}, INVALID),
     ({"B": 1 << 16, "T": 1 << 15}, UNSUPPORTED), ({"D": 1 << 26}, UNSUPPORTED),
     ({"x.data": None}, INVALID), ({"dt.data": None}, INVALID), ({"bmat.data": None}, INVALID), ({"a": None}, INVALID),
-    ({"bmat.data": at(5) + 2}, INVALID), ({"cmat.row": 33}, INVALID), ({"bmat.batch": 9601}, INVALID),
+    ({"bmat.data": at(5) + 1}, INVALID), ({"cmat.row": -2}, INVALID), ({"bmat.batch": 1 << 55}, INVALID),
     ({"a": at(12) + 2}, INVALID), ({"state": at(15) + 1}, INVALID), ({"z.row": -1}, INVALID), ({"dt.batch": 1 << 60}, INVALID),
 ]
 
@@ -168,7 +168,7 @@ def test_scan_workspace():
     L = tfla.lib()
     n = L.tfla_scan_bwd_workspace_bytes(2, 300, 128, 16, 2, BF16)
     assert n > 0
-    for bad in ((2, 300, 128, 6, 2, BF16), (2, 300, 128, 16, 3, BF16), (0, 300, 128, 16, 2, BF16), (2, 300, 128, 16, 2, 1)):
+    for bad in ((2, 300, 128, 65, 2, BF16), (2, 300, 128, 16, 3, BF16), (0, 300, 128, 16, 2, BF16), (2, 300, 128, 16, 2, 1)):
         assert L.tfla_scan_bwd_workspace_bytes(*bad) == 0 and L.tfla_scan_workspace_bytes(*bad) == 0
     a = scan_args()
     n = L.tfla_scan_bwd_workspace_bytes(2, 300, 128, 16, 2, a.flags)
