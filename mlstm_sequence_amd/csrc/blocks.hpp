@@ -16,6 +16,17 @@ int fail(int code, const std::string& msg);
 // Whether a test asked the library's own allocations to fail.
 bool inject_alloc_fault();
 
+// A grid of `blocks` workgroups in two dimensions (one holds fewer than 2^32
+// threads); a kernel takes its number from block_id() and leaves when that
+// is behind the last.
+inline dim3 grid_of(int64_t blocks)
+{
+    const int64_t x = blocks < (1 << 21) ? blocks : (1 << 21);
+    return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
+}
+
+__device__ __forceinline__ int64_t block_id() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 // Rows of a [B,T,width] tensor: element (b,t,c) at p[b * batch + t * row + c].
 struct Rows {
     void* p = nullptr;

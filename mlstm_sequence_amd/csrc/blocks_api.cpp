@@ -232,9 +232,6 @@ int check_conv_sizes(int B, int T, int D, int K, int flags)
     if (K > 8) return fail(TFLA_ERR_UNSUPPORTED, "K must be 1 to 8, got " + std::to_string(K));
     if ((int64_t)B * T > kMaxRows) return fail(TFLA_ERR_UNSUPPORTED, "B*T must be <= 2^30");
     if (D > (1 << 24)) return fail(TFLA_ERR_UNSUPPORTED, "D must be <= 2^24");
-    // one launch covers the rows in runs of at least 8
-    if ((int64_t)B * ((T + 7) / 8) * D / 256 >= (int64_t(1) << 31) - 1)
-        return fail(TFLA_ERR_UNSUPPORTED, "problem too large for one launch grid");
     return TFLA_OK;
 }
 
@@ -323,9 +320,9 @@ int check_scan_sizes(int B, int T, int D, int N, int G, int flags, tfla::ScanPro
     if (N > 64) return fail(TFLA_ERR_UNSUPPORTED, "N must be 1 to 64, got " + std::to_string(N));
     if ((int64_t)B * T > kMaxRows) return fail(TFLA_ERR_UNSUPPORTED, "B*T must be <= 2^30");
     if (D > (1 << 24)) return fail(TFLA_ERR_UNSUPPORTED, "D must be <= 2^24");
-    const int64_t lim = (int64_t(1) << 31) - 1;
-    if ((int64_t)B * G * ((D / G + 63) / 64) > lim || (int64_t)B * T * G * N / 128 + (int64_t)D * N / 256 + D > lim)
-        return fail(TFLA_ERR_UNSUPPORTED, "problem too large for one launch grid");
+    // workgroups of up to 1024 threads, a grid below 2^32 of them
+    if ((int64_t)B * G * ((D / G + 63) / 64) >= (1 << 21))
+        return fail(TFLA_ERR_UNSUPPORTED, "B*D too large: at most 2^21 blocks of 64 channels of a group");
     *p = tfla::ScanProblem{};
     p->B = B;
     p->T = T;
@@ -450,8 +447,6 @@ int check_norm_sizes(int B, int T, int G, int C, int flags, tfla::NormProblem* p
     if (B < 1 || T < 1 || G < 1 || C < 1) return fail(TFLA_ERR_INVALID_ARG, "B, T, G and C must be >= 1");
     if ((int64_t)B * T > kMaxRows) return fail(TFLA_ERR_UNSUPPORTED, "B*T must be <= 2^30");
     if ((int64_t)G * C > (1 << 24)) return fail(TFLA_ERR_UNSUPPORTED, "G*C must be <= 2^24");
-    if ((int64_t)B * T * G >= (int64_t(1) << 32) || (int64_t)B * T * G * C / 256 >= (int64_t(1) << 31) - 1)
-        return fail(TFLA_ERR_UNSUPPORTED, "problem too large for one launch grid");
     *p = tfla::NormProblem{};
     p->B = B;
     p->T = T;

@@ -3,91 +3,138 @@
 //   u_t = bias + sum_{j<K} w_j X_{t-K+1+j},  y_t = u_t or SiLU(u_t)
 //
 // X is the carried state's K-1 rows, then x.  A thread owns VEC neighbouring
-// channels and a run of rows: the K-1 rows before it in registers, each row
-// of x loaded once.  2 K flops an element against 2 elements moved: bound by
-// memory.
+// channels and a run of rows, loads each row of its run once, kRows at a time
+// and one such group ahead, and keeps the K-1 rows before a group in
+// registers, so what is read twice is K-1 rows a run (from the caches).
+// 2 K + 6 flops an element against 2 elements moved: bound by memory.
+//
+// VEC is 16 bytes (8 in the backward pass, whose sums take the registers)
+// where the number of channels, the addresses and the strides allow it, else 1.
 #include "act.hpp"
 #include "blocks.hpp"
 
 namespace tfla {
 namespace {
 
+constexpr int kRows = 4;   // rows loaded together
+
 __device__ __forceinline__ int clamp_len(const int* lengths, int b, int T)
 {
     return lengths ? min(max(lengths[b], 0), T) : T;
 }
 
-struct ConvGeom {
-    int B, T, D, nv;      // nv: vectors of VEC channels in a row
-    int run, nrun;        // rows of a run, runs of a sequence
+// VEC elements as they lie in memory
+template <typename T, int VEC> struct Pack {
+    typedef T vec __attribute__((ext_vector_type(VEC)));
+    vec v;
+    __device__ __forceinline__ void load(const T* p) { v = *(const vec*)p; }
+    __device__ __forceinline__ void store(T* p) const { *(vec*)p = v; }
+    __device__ __forceinline__ float get(int i) const { return to_float((T)v[i]); }
+    __device__ __forceinline__ void set(int i, float x) { v[i] = from_float<T>(x); }
+};
+template <typename T> struct Pack<T, 1> {
+    T v;
+    __device__ __forceinline__ void load(const T* p) { v = *p; }
+    __device__ __forceinline__ void store(T* p) const { *p = v; }
+    __device__ __forceinline__ float get(int) const { return to_float(v); }
+    __device__ __forceinline__ void set(int, float x) { v = from_float<T>(x); }
 };
 
-// One thread: channels c0 .. c0+VEC-1, rows t0 .. t0+run-1 of sequence b.
-template <typename T, int VEC, int K>
-__global__ __launch_bounds__(256) void conv_fwd_kernel(ConvGeom g, const T* __restrict__ x, int64_t xb, int64_t xr,
-                                                       const float* __restrict__ w, const float* __restrict__ bias,
-                                                       const T* state, const int* __restrict__ lengths,
-                                                       T* __restrict__ y, int64_t yb, int64_t yr, T* state_out,
-                                                       int silu)
-{
-    const int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (item >= (int64_t)g.B * g.nrun * g.nv) return;
-    const int c0 = (int)(item % g.nv) * VEC;
-    const int64_t rb = item / g.nv;
-    const int r = (int)(rb % g.nrun), b = (int)(rb / g.nrun);
-    const int t0 = r * g.run, t1 = min(t0 + g.run, g.T);
-    const int len = clamp_len(lengths, b, g.T);
-    x += b * xb + c0;
-    y += b * yb + c0;
-    const size_t srow = ((size_t)b * (K - 1)) * g.D + c0;
+struct ConvGeom {
+    int nv;               // vectors of VEC channels in a row
+    int run, nrun;        // rows of a run, runs of a sequence
+    int cx;               // backward: vectors of a workgroup (a power of two), 256 / cx runs
+    int ncb;              // workgroups across a row
+    int64_t groups;       // and down the runs
+};
 
-    float wk[K][VEC], bs[VEC], win[K][VEC];   // win[j]: X[t-K+1+j]
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-        bs[v] = bias ? bias[c0 + v] : 0.0f;
-#pragma unroll
-        for (int j = 0; j < K; ++j) wk[j][v] = w[(size_t)(c0 + v) * K + j];
-    }
+// The K-1 rows before row t0 (r > 0: none of them from the state).
+template <typename T, int VEC, int K>
+__device__ __forceinline__ void history(float (*xr)[VEC], const T* x, int64_t row, int t0, int len, const T* state, int D)
+{
 #pragma unroll
     for (int j = 0; j + 1 < K; ++j) {
         const int p = t0 - (K - 1) + j;
+        Pack<T, VEC> v;
+        v.load(x + max(min(p, len - 1), 0) * row);
+        const bool in = p >= 0 && p < len;
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            float s = 0.0f;
-            if (p < 0) s = state ? to_float(state[srow + (size_t)(p + K - 1) * g.D + v]) : 0.0f;
-            else if (p < len) s = to_float(x[p * xr + v]);
-            win[j][v] = s;
+        for (int i = 0; i < VEC; ++i) xr[j][i] = in ? v.get(i) : 0.0f;
+        if (p < 0 && state) {
+            v.load(state + (size_t)(p + K - 1) * D);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) xr[j][i] = v.get(i);
         }
     }
-    for (int t = t0; t < t1; ++t) {
+}
+
+template <typename T, int VEC, int K, bool SILU>
+__global__ __launch_bounds__(256) void conv_fwd_kernel(ConvProblem p, ConvGeom g)
+{
+    const int64_t item = block_id() * 256 + threadIdx.x;
+    if (item >= (int64_t)p.B * g.nrun * g.nv) return;
+    const int c0 = (int)(item % g.nv) * VEC;
+    const int64_t rb = item / g.nv;
+    const int r = (int)(rb % g.nrun), b = (int)(rb / g.nrun);
+    const int t0 = r * g.run, t1 = min(t0 + g.run, p.T);
+    const int len = clamp_len(p.lengths, b, p.T);
+    const T* x = (const T*)p.x.p + b * p.x.batch + c0;
+    T* y = (T*)p.y.p + b * p.y.batch + c0;
+    const size_t srow = ((size_t)b * (K - 1)) * p.D + c0;
+    const T* state = p.state ? (const T*)p.state + srow : nullptr;
+
+    Pack<T, VEC> raw[kRows];
+    // rows behind the end are read as the last (or first) one and not used: no branch stands around a load
+    auto fetch = [&](int t) {
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            float o = 0.0f;
-            if (t < len) {
-                win[K - 1][v] = to_float(x[t * xr + v]);
+        for (int k = 0; k < kRows; ++k) raw[k].load(x + max(min(t + k, len - 1), 0) * p.x.row);
+    };
+    fetch(t0);
+    float wk[K][VEC], bs[VEC], xr[K - 1 + kRows][VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        bs[v] = p.bias ? p.bias[c0 + v] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < K; ++j) wk[j][v] = p.weight[(size_t)(c0 + v) * K + j];
+    }
+    history<T, VEC, K>(xr, x, p.x.row, t0, len, state, p.D);
+    for (int t = t0; t < t1; t += kRows) {
+#pragma unroll
+        for (int k = 0; k < kRows; ++k)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) xr[K - 1 + k][v] = raw[k].get(v);
+        fetch(t + kRows);
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            Pack<T, VEC> o;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
                 float u = bs[v];
 #pragma unroll
-                for (int j = 0; j < K; ++j) u += wk[j][v] * win[j][v];
-                o = silu ? u * sigmoid_f(u) : u;
-#pragma unroll
-                for (int j = 0; j + 1 < K; ++j) win[j][v] = win[j + 1][v];
+                for (int j = 0; j < K; ++j) u += wk[j][v] * xr[k + j][v];
+                if (SILU) u *= sigmoid_t<T>(u);
+                o.set(v, t + k < len ? u : 0.0f);
             }
-            y[t * yr + v] = from_float<T>(o);
+            if (t + k < t1) o.store(y + (t + k) * p.y.row);
         }
+#pragma unroll
+        for (int j = 0; j + 1 < K; ++j)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) xr[j][v] = xr[j + kRows][v];
     }
     // The thread that read the state's rows also writes the new ones, in
     // ascending order from rows at or after the one written: in place is safe.
-    if (state_out && r == 0) {
+    if (p.state_out && r == 0) {
+        T* out = (T*)p.state_out + srow;
 #pragma unroll
         for (int i = 0; i + 1 < K; ++i) {
-            const int p = len - (K - 1) + i;
+            const int q = len - (K - 1) + i;
+            Pack<T, VEC> s;
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                T s = from_float<T>(0.0f);
-                if (p >= 0) s = x[p * xr + v];
-                else if (state) s = state[srow + (size_t)(p + K - 1) * g.D + v];
-                state_out[srow + (size_t)i * g.D + v] = s;
-            }
+            for (int v = 0; v < VEC; ++v) s.set(v, 0.0f);
+            if (q >= 0) s.load(x + q * p.x.row);
+            else if (state) s.load(state + (size_t)(q + K - 1) * p.D);
+            s.store(out + (size_t)i * p.D);
         }
     }
 }
@@ -95,173 +142,266 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvGeom g, const T* __re
 // Backward.  du_t = dy_t act'(u_t); dX_p = sum_i w_{K-1-i} du_{p+i};
 // dw_j = sum_t du_t X_{t-K+1+j}.  A thread walks t over its run and the K-1
 // rows behind it (whose du it recomputes), so dX_p is complete at
-// t = p+K-1; run 0 also yields the rows of the carried state.  Weight
-// gradients of the run's own rows go to `part`, one row of sums for each
-// block row, and are summed over the runs in a fixed order afterwards.
-template <typename T, int VEC, int K>
-__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvGeom g, const T* __restrict__ x, int64_t xb, int64_t xr,
-                                                       const float* __restrict__ w, const float* __restrict__ bias,
-                                                       const T* state, const int* __restrict__ lengths,
-                                                       const T* __restrict__ dy, int64_t gb, int64_t gr,
-                                                       const T* dso, T* __restrict__ dx, int64_t db, int64_t dr,
-                                                       T* dstate, float* __restrict__ part, int silu)
+// t = p+K-1; run 0 also yields the rows of the carried state.  The weight
+// gradients of a workgroup's runs (each thread its own run's rows only) meet
+// in LDS and go to `part`; the workgroups' sums are added in a fixed order
+// afterwards.
+template <typename T, int VEC, int K, bool SILU>
+__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, ConvGeom g)
 {
-    const int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (item >= (int64_t)g.B * g.nrun * g.nv) return;
-    const int c0 = (int)(item % g.nv) * VEC;
-    const int64_t rb = item / g.nv;
-    const int r = (int)(rb % g.nrun), b = (int)(rb / g.nrun);
-    const int t0 = r * g.run, t1 = min(t0 + g.run, g.T);
-    const int len = clamp_len(lengths, b, g.T);
-    x += b * xb + c0;
-    dy += b * gb + c0;
-    dx += b * db + c0;
-    const size_t srow = ((size_t)b * (K - 1)) * g.D + c0;
+    __shared__ float red[256 * VEC];
+    const int cx = threadIdx.x & (g.cx - 1), ry = threadIdx.x / g.cx, nry = 256 / g.cx;
+    const int64_t group = block_id() / g.ncb, rb = group * nry + ry;
+    if (group >= g.groups) return;
+    const int cb = (int)(block_id() % g.ncb), cv = cb * g.cx + cx;
+    const bool live = cv < g.nv && rb < (int64_t)p.B * g.nrun;
+    float dw[K + 1][VEC];
+#pragma unroll
+    for (int j = 0; j <= K; ++j)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) dw[j][v] = 0.0f;
+    const int c0 = min(cv, g.nv - 1) * VEC;
+    if (live) {
+        const int r = (int)(rb % g.nrun), b = (int)(rb / g.nrun);
+        const int t0 = r * g.run, t1 = min(t0 + g.run, p.T);
+        const int len = clamp_len(p.lengths, b, p.T);
+        const T* x = (const T*)p.x.p + b * p.x.batch + c0;
+        const T* dy = (const T*)p.dy.p + b * p.dy.batch + c0;
+        T* dx = (T*)p.dx.p + b * p.dx.batch + c0;
+        const size_t srow = ((size_t)b * (K - 1)) * p.D + c0;
+        const T* state = p.state ? (const T*)p.state + srow : nullptr;
+        const T* dso = p.dstate_out ? (const T*)p.dstate_out + srow : nullptr;
+        T* dst = p.dstate ? (T*)p.dstate + srow : nullptr;
 
-    float wk[K][VEC], bs[VEC], win[K][VEC], dw[K + 1][VEC];
-    float du[K][VEC];                         // du[i]: du_{t-K+1+i}
+        Pack<T, VEC> rx[kRows], rd[kRows];
+        auto fetch = [&](int t) {
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-        bs[v] = bias ? bias[c0 + v] : 0.0f;
-        dw[K][v] = 0.0f;
+            for (int k = 0; k < kRows; ++k) {
+                const int64_t q = max(min(t + k, len - 1), 0);
+                rx[k].load(x + q * p.x.row);
+                rd[k].load(dy + q * p.dy.row);
+            }
+        };
+        fetch(t0);
+        float wk[K][VEC], bs[VEC], xr[K - 1 + kRows][VEC], du[K - 1 + kRows][VEC];
 #pragma unroll
-        for (int j = 0; j < K; ++j) {
-            wk[j][v] = w[(size_t)(c0 + v) * K + j];
-            dw[j][v] = 0.0f;
-            du[j][v] = 0.0f;
+        for (int v = 0; v < VEC; ++v) {
+            bs[v] = p.bias ? p.bias[c0 + v] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < K; ++j) wk[j][v] = p.weight[(size_t)(c0 + v) * K + j];
+#pragma unroll
+            for (int j = 0; j + 1 < K; ++j) du[j][v] = 0.0f;
+        }
+        history<T, VEC, K>(xr, x, p.x.row, t0, len, state, p.D);
+        const int first = r == 0 ? -(K - 1) : t0;   // rows of X this thread writes: first .. t1-1
+        for (int t = t0; t < t1 + K - 1; t += kRows) {
+#pragma unroll
+            for (int k = 0; k < kRows; ++k)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    xr[K - 1 + k][v] = t + k < len ? rx[k].get(v) : 0.0f;
+                    du[K - 1 + k][v] = t + k < len ? rd[k].get(v) : 0.0f;
+                }
+            fetch(t + kRows);
+#pragma unroll
+            for (int k = 0; k < kRows; ++k) {
+                const int q = t + k - (K - 1);              // the row of X completed here
+                const bool own = t + k < t1;
+                Pack<T, VEC> o;
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    float d = du[K - 1 + k][v];
+                    if (SILU) {
+                        float u = bs[v];
+#pragma unroll
+                        for (int j = 0; j < K; ++j) u += wk[j][v] * xr[k + j][v];
+                        const float sg = sigmoid_t<T>(u);
+                        const float us = u * sg;
+                        // behind the end d is 0, and 0 times a slope that overflowed must stay 0
+                        d = t + k < len ? d * (sg + us * (1.0f - sg)) : 0.0f;
+                        du[K - 1 + k][v] = d;
+                    }
+                    const float e = own ? d : 0.0f;
+#pragma unroll
+                    for (int j = 0; j < K; ++j) dw[j][v] += e * xr[k + j][v];
+                    dw[K][v] += e;
+                    float s = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < K; ++i) s += wk[K - 1 - i][v] * du[k + i][v];
+                    o.set(v, q < len ? s : 0.0f);
+                }
+                if (q >= first && q < t1) {
+                    const int e = q - (len - (K - 1));      // the row of state_out that is X_q
+                    if (dso && e >= 0 && q < len) {
+                        Pack<T, VEC> a;
+                        a.load(dso + (size_t)e * p.D);
+#pragma unroll
+                        for (int v = 0; v < VEC; ++v) {
+                            float s = a.get(v);             // once more: the sum is rounded once
+#pragma unroll
+                            for (int i = 0; i < K; ++i) s += wk[K - 1 - i][v] * du[k + i][v];
+                            o.set(v, s);
+                        }
+                    }
+                    if (q >= 0) o.store(dx + q * p.dx.row);
+                    else if (dst) o.store(dst + (size_t)(q + K - 1) * p.D);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j + 1 < K; ++j)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    xr[j][v] = xr[j + kRows][v];
+                    du[j][v] = du[j + kRows][v];
+                }
         }
     }
 #pragma unroll
-    for (int j = 0; j + 1 < K; ++j) {
-        const int p = t0 - (K - 1) + j;
+    for (int j = 0; j <= K; ++j) {
+        __syncthreads();
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
+        for (int v = 0; v < VEC; ++v) red[v * 256 + threadIdx.x] = dw[j][v];
+        __syncthreads();
+        for (int i = threadIdx.x; i < g.cx * VEC; i += 256) {
+            const int c = i & (g.cx - 1), v = i / g.cx, cc = cb * g.cx + c;
             float s = 0.0f;
-            if (p < 0) s = state ? to_float(state[srow + (size_t)(p + K - 1) * g.D + v]) : 0.0f;
-            else if (p < len) s = to_float(x[p * xr + v]);
-            win[j][v] = s;
+            for (int k = 0; k < nry; ++k) s += red[v * 256 + k * g.cx + c];
+            if (cc < g.nv) p.part[((size_t)group * (K + 1) + j) * p.D + (size_t)cc * VEC + v] = s;
         }
     }
-    const int first = r == 0 ? -(K - 1) : t0;   // rows of X this thread writes: first .. t1-1
-    for (int t = t0; t < t1 + K - 1; ++t) {
-        const bool live = t < len, own = t < t1;
-        const int p = t - (K - 1);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            float d = 0.0f;
-            if (live) {
-                win[K - 1][v] = to_float(x[t * xr + v]);
-                d = to_float(dy[t * gr + v]);
-                if (silu) {
-                    float u = bs[v];
-#pragma unroll
-                    for (int j = 0; j < K; ++j) u += wk[j][v] * win[j][v];
-                    const float sg = sigmoid_f(u);
-                    d *= sg * (1.0f + u * (1.0f - sg));
-                }
-                if (own) {
-#pragma unroll
-                    for (int j = 0; j < K; ++j) dw[j][v] += d * win[j][v];
-                    dw[K][v] += d;
-                }
-#pragma unroll
-                for (int j = 0; j + 1 < K; ++j) win[j][v] = win[j + 1][v];
-            }
-            du[K - 1][v] = d;
-            if (p >= first && p < t1) {
-                float o = 0.0f;
-                if (p < len) {
-#pragma unroll
-                    for (int i = 0; i < K; ++i) o += wk[K - 1 - i][v] * du[i][v];
-                    const int q = p - (len - (K - 1));   // row of state_out that is X_p
-                    if (dso && q >= 0) o += to_float(dso[srow + (size_t)q * g.D + v]);
-                }
-                if (p >= 0) dx[p * dr + v] = from_float<T>(o);
-                else if (dstate) dstate[srow + (size_t)(p + K - 1) * g.D + v] = from_float<T>(o);
-            }
-#pragma unroll
-            for (int i = 0; i + 1 < K; ++i) du[i][v] = du[i + 1][v];
-        }
-    }
-#pragma unroll
-    for (int v = 0; v < VEC; ++v)
-#pragma unroll
-        for (int j = 0; j <= K; ++j) part[((size_t)rb * (K + 1) + j) * g.D + c0 + v] = dw[j][v];
 }
 
-// dweight [D,K] and dbias [D] from the runs' sums [parts][K+1][D]
+// dweight [D,K] and dbias [D] from the workgroups' sums [parts][K+1][D]: 64
+// columns and 4 slices of the parts to a workgroup.
 __global__ __launch_bounds__(256) void conv_params_kernel(const float* __restrict__ part, int parts, int D, int K,
                                                           float* __restrict__ dweight, float* __restrict__ dbias)
 {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (int64_t)(K + 1) * D) return;
-    const int j = (int)(i / D), c = (int)(i % D);
+    __shared__ float red[4][64];
+    const int64_t n = (int64_t)(K + 1) * D, i = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+    const int slice = threadIdx.x >> 6;
     float s = 0.0f;
-    for (int r = 0; r < parts; ++r) s += part[(size_t)r * (K + 1) * D + i];
+    if (i < n) {
+#pragma unroll 8
+        for (int r = slice; r < parts; r += 4) s += part[r * n + i];
+    }
+    red[slice][threadIdx.x & 63] = s;
+    __syncthreads();
+    if (slice || i >= n) return;
+    s = (red[0][threadIdx.x] + red[1][threadIdx.x]) + (red[2][threadIdx.x] + red[3][threadIdx.x]);
+    const int j = (int)(i / D), c = (int)(i % D);
     if (j < K) dweight[(size_t)c * K + j] = s;
     else if (dbias) dbias[c] = s;
 }
 
-int run_rows(int B, int T, int D)
+bool fits(const void* p, int64_t batch, int64_t row, const ConvProblem& c, size_t bytes)
 {
-    (void)B;
-    (void)D;
-    return T < 64 ? T : 64;
+    const size_t e = c.bf16 ? 2 : 4;
+    return (uintptr_t)p % bytes == 0 && (c.B == 1 || batch * e % bytes == 0) && (c.T == 1 || row * e % bytes == 0);
 }
 
-template <typename T, int K>
-hipError_t fwd_t(const ConvProblem& p, hipStream_t stream)
+// Elements of a vector: `bytes` of them where the rows, states and widths allow it, else 1.
+int vec_of(const ConvProblem& p, size_t bytes, bool bwd)
 {
-    ConvGeom g{p.B, p.T, p.D, p.D, run_rows(p.B, p.T, p.D), 0};
+    const size_t e = p.bf16 ? 2 : 4;
+    const int v = (int)(bytes / e);
+    bool ok = p.D % v == 0 && fits(p.x.p, p.x.batch, p.x.row, p, bytes) && (uintptr_t)p.state % bytes == 0;
+    if (bwd) ok = ok && fits(p.dy.p, p.dy.batch, p.dy.row, p, bytes) && fits(p.dx.p, p.dx.batch, p.dx.row, p, bytes) &&
+                  (uintptr_t)p.dstate_out % bytes == 0 && (uintptr_t)p.dstate % bytes == 0;
+    else ok = ok && fits(p.y.p, p.y.batch, p.y.row, p, bytes) && (uintptr_t)p.state_out % bytes == 0;
+    return ok ? v : 1;
+}
+
+// Rows of a run, 8 at least (no run but the first then reaches into the state): as long as about `threads` threads
+// remain, up to `most`.
+int run_rows(int64_t rows, int T, int64_t nv, int64_t threads, int most)
+{
+    int run = 8;
+    while (run < most && rows * nv / (2 * run) >= threads) run *= 2;
+    return run < T ? run : T;
+}
+
+ConvGeom geom(const ConvProblem& p, int vec, bool bwd)
+{
+    ConvGeom g;
+    g.nv = p.D / vec;
+    g.run = run_rows((int64_t)p.B * p.T, p.T, g.nv, 1 << 17, bwd ? 64 : 32);
     g.nrun = (p.T + g.run - 1) / g.run;
-    const int64_t items = (int64_t)p.B * g.nrun * g.nv;
-    conv_fwd_kernel<T, 1, K><<<dim3((unsigned)((items + 255) / 256)), 256, 0, stream>>>(
-        g, (const T*)p.x.p, p.x.batch, p.x.row, p.weight, p.bias, (const T*)p.state, p.lengths, (T*)p.y.p, p.y.batch,
-        p.y.row, (T*)p.state_out, p.silu);
+    g.cx = 1;
+    while (g.cx < 64 && g.cx < g.nv) g.cx *= 2;
+    g.ncb = (g.nv + g.cx - 1) / g.cx;
+    const int nry = 256 / g.cx;
+    g.groups = ((int64_t)p.B * g.nrun + nry - 1) / nry;
+    return g;
+}
+
+template <typename T, int VEC, int K>
+hipError_t fwd_v(const ConvProblem& p, hipStream_t stream)
+{
+    const ConvGeom g = geom(p, VEC, false);
+    const dim3 blocks = grid_of(((int64_t)p.B * g.nrun * g.nv + 255) / 256);
+    if (p.silu) conv_fwd_kernel<T, VEC, K, true><<<blocks, 256, 0, stream>>>(p, g);
+    else conv_fwd_kernel<T, VEC, K, false><<<blocks, 256, 0, stream>>>(p, g);
     return hipGetLastError();
 }
 
-template <typename T, int K>
-hipError_t bwd_t(const ConvProblem& p, hipStream_t stream)
+template <typename T, int VEC, int K>
+hipError_t bwd_v(const ConvProblem& p, hipStream_t stream)
 {
-    ConvGeom g{p.B, p.T, p.D, p.D, run_rows(p.B, p.T, p.D), 0};
-    g.nrun = (p.T + g.run - 1) / g.run;
-    const int64_t items = (int64_t)p.B * g.nrun * g.nv;
-    conv_bwd_kernel<T, 1, K><<<dim3((unsigned)((items + 255) / 256)), 256, 0, stream>>>(
-        g, (const T*)p.x.p, p.x.batch, p.x.row, p.weight, p.bias, (const T*)p.state, p.lengths, (const T*)p.dy.p,
-        p.dy.batch, p.dy.row, (const T*)p.dstate_out, (T*)p.dx.p, p.dx.batch, p.dx.row, (T*)p.dstate, p.part, p.silu);
+    const ConvGeom g = geom(p, VEC, true);
+    const dim3 blocks = grid_of(g.groups * g.ncb);
+    if (p.silu) conv_bwd_kernel<T, VEC, K, true><<<blocks, 256, 0, stream>>>(p, g);
+    else conv_bwd_kernel<T, VEC, K, false><<<blocks, 256, 0, stream>>>(p, g);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t n = (int64_t)(K + 1) * p.D;
-    conv_params_kernel<<<dim3((unsigned)((n + 255) / 256)), 256, 0, stream>>>(p.part, p.B * g.nrun, p.D, K, p.dweight,
-                                                                             p.dbias);
+    conv_params_kernel<<<(unsigned)((n + 63) / 64), 256, 0, stream>>>(p.part, (int)g.groups, p.D, K, p.dweight, p.dbias);
     return hipGetLastError();
+}
+
+constexpr size_t kFwdBytes = 8, kBwdBytes = 4;
+
+template <typename T, int K, bool BWD>
+hipError_t by_width(const ConvProblem& p, hipStream_t stream)
+{
+    constexpr int V = (int)((BWD ? kBwdBytes : kFwdBytes) / sizeof(T));
+    const bool wide = vec_of(p, BWD ? kBwdBytes : kFwdBytes, BWD) == V;
+    if constexpr (BWD) return wide ? bwd_v<T, V, K>(p, stream) : bwd_v<T, 1, K>(p, stream);
+    else return wide ? fwd_v<T, V, K>(p, stream) : fwd_v<T, 1, K>(p, stream);
 }
 
 template <typename T, bool BWD>
 hipError_t by_taps(const ConvProblem& p, hipStream_t stream)
 {
     switch (p.K) {
-#define TFLA_TAPS(k) case k: return BWD ? bwd_t<T, k>(p, stream) : fwd_t<T, k>(p, stream)
-    TFLA_TAPS(1);
-    TFLA_TAPS(2);
-    TFLA_TAPS(3);
-    TFLA_TAPS(4);
-    TFLA_TAPS(5);
-    TFLA_TAPS(6);
-    TFLA_TAPS(7);
-    default: return BWD ? bwd_t<T, 8>(p, stream) : fwd_t<T, 8>(p, stream);
-#undef TFLA_TAPS
+    case 1: return by_width<T, 1, BWD>(p, stream);
+    case 2: return by_width<T, 2, BWD>(p, stream);
+    case 3: return by_width<T, 3, BWD>(p, stream);
+    case 4: return by_width<T, 4, BWD>(p, stream);
+    case 5: return by_width<T, 5, BWD>(p, stream);
+    case 6: return by_width<T, 6, BWD>(p, stream);
+    case 7: return by_width<T, 7, BWD>(p, stream);
+    default: return by_width<T, 8, BWD>(p, stream);
     }
 }
 
 }  // namespace
 
+// For whichever width the call's addresses allow.
 size_t conv_bwd_workspace(int B, int T, int D, int K, bool bf16)
 {
-    (void)bf16;
-    const int run = run_rows(B, T, D);
-    return (size_t)B * ((T + run - 1) / run) * (K + 1) * D * sizeof(float);
+    ConvProblem p{};
+    p.B = B;
+    p.T = T;
+    p.D = D;
+    p.K = K;
+    p.bf16 = bf16;
+    size_t most = 0;
+    for (const int v : {1, (int)(kBwdBytes / (bf16 ? 2 : 4))}) {
+        if (D % v) continue;
+        const size_t n = (size_t)geom(p, v, true).groups * (K + 1) * D * sizeof(float);
+        if (n > most) most = n;
+    }
+    return most;
 }
 
 hipError_t launch_conv_fwd(const ConvProblem& p, hipStream_t stream)

@@ -228,7 +228,7 @@ __global__ __launch_bounds__(256) void scan_starts_kernel(ScanProblem p, Segment
                                                           const float* __restrict__ sums)
 {
     const int64_t DN = (int64_t)p.D * p.N;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t i = block_id() * 256 + threadIdx.x;
     if (i >= p.B * DN) return;
     const int64_t b = i / DN, k = i % DN;
     const int c = (int)(k / p.N);
@@ -278,8 +278,9 @@ SegWs seg_ws(const ScanProblem& p, const Segments& sg, char* base, size_t* bytes
 template <typename T, int L>
 __global__ __launch_bounds__(256) void scan_step_kernel(ScanProblem p, int per_seq)
 {
-    const int b = blockIdx.x / per_seq;
-    const int i = (blockIdx.x % per_seq) * 256 + threadIdx.x;
+    const int64_t blk = block_id();
+    if (blk >= (int64_t)p.B * per_seq) return;
+    const int b = (int)(blk / per_seq), i = (int)(blk % per_seq) * 256 + threadIdx.x;
     const int c = min(i / L, p.D - 1), n0 = (i % L) * kStates;
     const bool live = i / L < p.D;
     const int ns = min(kStates, p.N - n0);
@@ -329,7 +330,7 @@ template <typename T, int L>
 hipError_t step_l(const ScanProblem& p, hipStream_t stream)
 {
     const int per_seq = (int)(((int64_t)p.D * L + 255) / 256);
-    scan_step_kernel<T, L><<<(unsigned)p.B * per_seq, 256, 0, stream>>>(p, per_seq);
+    scan_step_kernel<T, L><<<grid_of((int64_t)p.B * per_seq), 256, 0, stream>>>(p, per_seq);
     return hipGetLastError();
 }
 
@@ -348,7 +349,7 @@ hipError_t fwd_w(const ScanProblem& p, hipStream_t stream)
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         const int64_t n = (int64_t)p.B * p.D * p.N;
-        scan_starts_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(p, sg, ws.ends, ws.sums);
+        scan_starts_kernel<<<grid_of((n + 255) / 256), 256, 0, stream>>>(p, sg, ws.ends, ws.sums);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (p.z.p) scan_fwd_kernel<T, W, true, true><<<blocks, 64 * W, 0, stream>>>(p, sg, ws);

@@ -258,7 +258,7 @@ __global__ __launch_bounds__(64 * W) void scan_tiles_kernel(ScanProblem p, Segme
 __global__ __launch_bounds__(256) void scan_links_kernel(ScanProblem p, Segments sg, Ws ws)
 {
     const int64_t DN = (int64_t)p.D * p.N;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t i = block_id() * 256 + threadIdx.x;
     if (i >= p.B * DN) return;
     const int64_t b = i / DN, k = i % DN;
     const float A = p.a[k] * kLog2e;
@@ -572,7 +572,7 @@ __global__ __launch_bounds__(256) void scan_sums_kernel(ScanProblem p, Ws ws, in
 {
     const int64_t GN = (int64_t)p.G * p.N, rows = (int64_t)p.B * p.T;
     const int64_t nbc = rows * GN, na = (int64_t)p.D * p.N;
-    int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    int64_t i = block_id() * 256 + threadIdx.x;
     if (i < 2 * nbc) {
         const bool isc = i >= nbc;
         if (isc) i -= nbc;
@@ -619,7 +619,7 @@ hipError_t bwd_w(const ScanProblem& p, hipStream_t stream)
         else scan_tiles_kernel<T, W, true, false><<<blocks, 64 * W, 0, stream>>>(p, sg, ws, nblk);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         const int64_t n = (int64_t)p.B * p.D * p.N;
-        scan_links_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(p, sg, ws);
+        scan_links_kernel<<<grid_of((n + 255) / 256), 256, 0, stream>>>(p, sg, ws);
     } else {
         scan_tiles_kernel<T, W, false, false><<<blocks, 64 * W, 0, stream>>>(p, sg, ws, nblk);
     }
@@ -628,7 +628,7 @@ hipError_t bwd_w(const ScanProblem& p, hipStream_t stream)
     else scan_bwd_kernel<T, W, false><<<blocks, 64 * W, 0, stream>>>(p, sg, ws, nblk);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const int64_t n = 2 * (int64_t)p.B * p.T * p.G * p.N + (int64_t)p.D * p.N + p.D;
-    scan_sums_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(p, ws, (p.D / p.G + 63) / 64, p.B * sg.nseg);
+    scan_sums_kernel<T><<<grid_of((n + 255) / 256), 256, 0, stream>>>(p, ws, (p.D / p.G + 63) / 64, p.B * sg.nseg);
     return hipGetLastError();
 }
 
