@@ -6,12 +6,19 @@
 // channels and a run of rows, loads each row of its run once, kRows at a time
 // and one such group ahead, and keeps the K-1 rows before a group in
 // registers, so what is read twice is K-1 rows a run (from the caches).
-// 2 K + 6 flops an element against 2 elements moved: bound by memory.
+// 2 K + 6 flops an element against 2 elements moved: bound by memory forward
+// (B=4 T=4096 D=4096 bf16, K=4: 268 MB in 48 us, 5.6 TB/s, where a copy moves
+// 5.1); backward the 28 instructions an element come close to it (403 MB in
+// 93 us).
 //
-// VEC is 16 bytes (8 in the backward pass, whose sums take the registers)
-// where the number of channels, the addresses and the strides allow it, else 1.
+// VEC is 8 bytes (4 in the backward pass, whose sums take the registers)
+// where the number of channels, the addresses and the strides allow it, else
+// 1 element.  16 bytes leave too few waves for short calls (padded prompts,
+// B=6 T=1531 D=2048: 23 us against 17) and gain nothing on long ones.
 #include "act.hpp"
 #include "blocks.hpp"
+
+#include <type_traits>
 
 namespace tfla {
 namespace {
@@ -40,12 +47,29 @@ template <typename T> struct Pack<T, 1> {
     __device__ __forceinline__ void set(int, float x) { v = from_float<T>(x); }
 };
 
+// A wave owns 64 vectors of channels and a run of rows (so all that depends on
+// the row alone is scalar), a workgroup four runs of the same channels.
 struct ConvGeom {
     int nv;               // vectors of VEC channels in a row
     int run, nrun;        // rows of a run, runs of a sequence
-    int cx;               // backward: vectors of a workgroup (a power of two), 256 / cx runs
     int ncb;              // workgroups across a row
     int64_t groups;       // and down the runs
+};
+
+// The wave's run and the lane's channels; false: none.
+struct ConvPlace {
+    int64_t group, rb;
+    int cb, cv, lane, wave;
+    __device__ __forceinline__ bool set(const ConvProblem& p, const ConvGeom& g)
+    {
+        group = block_id() / g.ncb;
+        cb = (int)(block_id() % g.ncb);
+        lane = threadIdx.x & 63;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        cv = cb * 64 + lane;
+        rb = group * 4 + wave;
+        return cv < g.nv && rb < (int64_t)p.B * g.nrun;
+    }
 };
 
 // The K-1 rows before row t0 (r > 0: none of them from the state).
@@ -71,11 +95,10 @@ __device__ __forceinline__ void history(float (*xr)[VEC], const T* x, int64_t ro
 template <typename T, int VEC, int K, bool SILU>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvProblem p, ConvGeom g)
 {
-    const int64_t item = block_id() * 256 + threadIdx.x;
-    if (item >= (int64_t)p.B * g.nrun * g.nv) return;
-    const int c0 = (int)(item % g.nv) * VEC;
-    const int64_t rb = item / g.nv;
-    const int r = (int)(rb % g.nrun), b = (int)(rb / g.nrun);
+    ConvPlace q;
+    if (!q.set(p, g)) return;
+    const int c0 = q.cv * VEC;
+    const int r = (int)(q.rb % g.nrun), b = (int)(q.rb / g.nrun);
     const int t0 = r * g.run, t1 = min(t0 + g.run, p.T);
     const int len = clamp_len(p.lengths, b, p.T);
     const T* x = (const T*)p.x.p + b * p.x.batch + c0;
@@ -98,7 +121,9 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvProblem p, ConvGeom g
         for (int j = 0; j < K; ++j) wk[j][v] = p.weight[(size_t)(c0 + v) * K + j];
     }
     history<T, VEC, K>(xr, x, p.x.row, t0, len, state, p.D);
-    for (int t = t0; t < t1; t += kRows) {
+    // ALL: every row of the group is one of the run's, before the end
+    auto rows = [&](auto ALL, int t) {
+        constexpr bool all = decltype(ALL)::value;
 #pragma unroll
         for (int k = 0; k < kRows; ++k)
 #pragma unroll
@@ -113,14 +138,18 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvProblem p, ConvGeom g
 #pragma unroll
                 for (int j = 0; j < K; ++j) u += wk[j][v] * xr[k + j][v];
                 if (SILU) u *= sigmoid_t<T>(u);
-                o.set(v, t + k < len ? u : 0.0f);
+                o.set(v, all || t + k < len ? u : 0.0f);
             }
-            if (t + k < t1) o.store(y + (t + k) * p.y.row);
+            if (all || t + k < t1) o.store(y + (t + k) * p.y.row);
         }
 #pragma unroll
         for (int j = 0; j + 1 < K; ++j)
 #pragma unroll
             for (int v = 0; v < VEC; ++v) xr[j][v] = xr[j + kRows][v];
+    };
+    for (int t = t0; t < t1; t += kRows) {
+        if (t + kRows <= min(t1, len)) rows(std::true_type{}, t);
+        else rows(std::false_type{}, t);
     }
     // The thread that read the state's rows also writes the new ones, in
     // ascending order from rows at or after the one written: in place is safe.
@@ -150,19 +179,17 @@ template <typename T, int VEC, int K, bool SILU>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, ConvGeom g)
 {
     __shared__ float red[256 * VEC];
-    const int cx = threadIdx.x & (g.cx - 1), ry = threadIdx.x / g.cx, nry = 256 / g.cx;
-    const int64_t group = block_id() / g.ncb, rb = group * nry + ry;
-    if (group >= g.groups) return;
-    const int cb = (int)(block_id() % g.ncb), cv = cb * g.cx + cx;
-    const bool live = cv < g.nv && rb < (int64_t)p.B * g.nrun;
+    ConvPlace q;
+    const bool live = q.set(p, g);
+    if (q.group >= g.groups) return;
     float dw[K + 1][VEC];
 #pragma unroll
     for (int j = 0; j <= K; ++j)
 #pragma unroll
         for (int v = 0; v < VEC; ++v) dw[j][v] = 0.0f;
-    const int c0 = min(cv, g.nv - 1) * VEC;
+    const int c0 = min(q.cv, g.nv - 1) * VEC;
     if (live) {
-        const int r = (int)(rb % g.nrun), b = (int)(rb / g.nrun);
+        const int r = (int)(q.rb % g.nrun), b = (int)(q.rb / g.nrun);
         const int t0 = r * g.run, t1 = min(t0 + g.run, p.T);
         const int len = clamp_len(p.lengths, b, p.T);
         const T* x = (const T*)p.x.p + b * p.x.batch + c0;
@@ -177,9 +204,9 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, ConvGeom g
         auto fetch = [&](int t) {
 #pragma unroll
             for (int k = 0; k < kRows; ++k) {
-                const int64_t q = max(min(t + k, len - 1), 0);
-                rx[k].load(x + q * p.x.row);
-                rd[k].load(dy + q * p.dy.row);
+                const int64_t s = max(min(t + k, len - 1), 0);
+                rx[k].load(x + s * p.x.row);
+                rd[k].load(dy + s * p.dy.row);
             }
         };
         fetch(t0);
@@ -194,20 +221,22 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, ConvGeom g
         }
         history<T, VEC, K>(xr, x, p.x.row, t0, len, state, p.D);
         const int first = r == 0 ? -(K - 1) : t0;   // rows of X this thread writes: first .. t1-1
-        for (int t = t0; t < t1 + K - 1; t += kRows) {
+        // ALL: every row of the group is one of the run's, before the end, and completes one that it writes to dx
+        // without a part of dstate_out
+        auto rows = [&](auto ALL, int t) {
+            constexpr bool all = decltype(ALL)::value;
 #pragma unroll
             for (int k = 0; k < kRows; ++k)
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
-                    xr[K - 1 + k][v] = t + k < len ? rx[k].get(v) : 0.0f;
-                    du[K - 1 + k][v] = t + k < len ? rd[k].get(v) : 0.0f;
+                    xr[K - 1 + k][v] = all || t + k < len ? rx[k].get(v) : 0.0f;
+                    du[K - 1 + k][v] = all || t + k < len ? rd[k].get(v) : 0.0f;
                 }
             fetch(t + kRows);
 #pragma unroll
             for (int k = 0; k < kRows; ++k) {
-                const int q = t + k - (K - 1);              // the row of X completed here
-                const bool own = t + k < t1;
-                Pack<T, VEC> o;
+                const int s = t + k - (K - 1);              // the row of X completed here
+                float o[VEC];
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
                     float d = du[K - 1 + k][v];
@@ -216,35 +245,34 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, ConvGeom g
 #pragma unroll
                         for (int j = 0; j < K; ++j) u += wk[j][v] * xr[k + j][v];
                         const float sg = sigmoid_t<T>(u);
-                        const float us = u * sg;
+                        d *= sg + u * sg * (1.0f - sg);
                         // behind the end d is 0, and 0 times a slope that overflowed must stay 0
-                        d = t + k < len ? d * (sg + us * (1.0f - sg)) : 0.0f;
+                        if (!all && t + k >= len) d = 0.0f;
                         du[K - 1 + k][v] = d;
                     }
-                    const float e = own ? d : 0.0f;
+                    const float e = all || t + k < t1 ? d : 0.0f;
 #pragma unroll
                     for (int j = 0; j < K; ++j) dw[j][v] += e * xr[k + j][v];
                     dw[K][v] += e;
-                    float s = 0.0f;
+                    o[v] = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < K; ++i) s += wk[K - 1 - i][v] * du[k + i][v];
-                    o.set(v, q < len ? s : 0.0f);
+                    for (int i = 0; i < K; ++i) o[v] += wk[K - 1 - i][v] * du[k + i][v];
                 }
-                if (q >= first && q < t1) {
-                    const int e = q - (len - (K - 1));      // the row of state_out that is X_q
-                    if (dso && e >= 0 && q < len) {
-                        Pack<T, VEC> a;
-                        a.load(dso + (size_t)e * p.D);
+                Pack<T, VEC> w;
+                if (all) {
 #pragma unroll
-                        for (int v = 0; v < VEC; ++v) {
-                            float s = a.get(v);             // once more: the sum is rounded once
+                    for (int v = 0; v < VEC; ++v) w.set(v, o[v]);
+                    w.store(dx + s * p.dx.row);
+                } else if (s >= first && s < t1) {
+                    const int e = s - (len - (K - 1));      // the row of state_out that is X_s
+                    Pack<T, VEC> a;
 #pragma unroll
-                            for (int i = 0; i < K; ++i) s += wk[K - 1 - i][v] * du[k + i][v];
-                            o.set(v, s);
-                        }
-                    }
-                    if (q >= 0) o.store(dx + q * p.dx.row);
-                    else if (dst) o.store(dst + (size_t)(q + K - 1) * p.D);
+                    for (int v = 0; v < VEC; ++v) a.set(v, 0.0f);
+                    if (dso && e >= 0 && s < len) a.load(dso + (size_t)e * p.D);
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) w.set(v, s < len ? o[v] + a.get(v) : 0.0f);
+                    if (s >= 0) w.store(dx + s * p.dx.row);
+                    else if (dst) w.store(dst + (size_t)(s + K - 1) * p.D);
                 }
             }
 #pragma unroll
@@ -254,19 +282,23 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, ConvGeom g
                     xr[j][v] = xr[j + kRows][v];
                     du[j][v] = du[j + kRows][v];
                 }
+        };
+        for (int t = t0; t < t1 + K - 1; t += kRows) {
+            // rows t-K+1 .. t+kRows-K of X are completed
+            if (t > t0 && t - (K - 1) >= t0 && t + kRows <= t1 && t + kRows - K < len - (K - 1)) rows(std::true_type{}, t);
+            else rows(std::false_type{}, t);
         }
     }
 #pragma unroll
     for (int j = 0; j <= K; ++j) {
         __syncthreads();
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) red[v * 256 + threadIdx.x] = dw[j][v];
+        for (int v = 0; v < VEC; ++v) red[(q.wave * VEC + v) * 64 + q.lane] = dw[j][v];
         __syncthreads();
-        for (int i = threadIdx.x; i < g.cx * VEC; i += 256) {
-            const int c = i & (g.cx - 1), v = i / g.cx, cc = cb * g.cx + c;
-            float s = 0.0f;
-            for (int k = 0; k < nry; ++k) s += red[v * 256 + k * g.cx + c];
-            if (cc < g.nv) p.part[((size_t)group * (K + 1) + j) * p.D + (size_t)cc * VEC + v] = s;
+        for (int i = threadIdx.x; i < VEC * 64; i += 256) {
+            const int c = q.cb * 64 + (i & 63), v = i >> 6;
+            const float s = (red[i] + red[i + VEC * 64]) + (red[i + 2 * VEC * 64] + red[i + 3 * VEC * 64]);
+            if (c < g.nv) p.part[((size_t)q.group * (K + 1) + j) * p.D + (size_t)c * VEC + v] = s;
         }
     }
 }
@@ -299,12 +331,12 @@ bool fits(const void* p, int64_t batch, int64_t row, const ConvProblem& c, size_
     return (uintptr_t)p % bytes == 0 && (c.B == 1 || batch * e % bytes == 0) && (c.T == 1 || row * e % bytes == 0);
 }
 
-// Elements of a vector: `bytes` of them where the rows, states and widths allow it, else 1.
+// Elements of a vector: `bytes` of them where the rows, states and widths allow it and fill a wave, else 1.
 int vec_of(const ConvProblem& p, size_t bytes, bool bwd)
 {
     const size_t e = p.bf16 ? 2 : 4;
     const int v = (int)(bytes / e);
-    bool ok = p.D % v == 0 && fits(p.x.p, p.x.batch, p.x.row, p, bytes) && (uintptr_t)p.state % bytes == 0;
+    bool ok = p.D % v == 0 && p.D >= 64 * v && fits(p.x.p, p.x.batch, p.x.row, p, bytes) && (uintptr_t)p.state % bytes == 0;
     if (bwd) ok = ok && fits(p.dy.p, p.dy.batch, p.dy.row, p, bytes) && fits(p.dx.p, p.dx.batch, p.dx.row, p, bytes) &&
                   (uintptr_t)p.dstate_out % bytes == 0 && (uintptr_t)p.dstate % bytes == 0;
     else ok = ok && fits(p.y.p, p.y.batch, p.y.row, p, bytes) && (uintptr_t)p.state_out % bytes == 0;
@@ -324,13 +356,10 @@ ConvGeom geom(const ConvProblem& p, int vec, bool bwd)
 {
     ConvGeom g;
     g.nv = p.D / vec;
-    g.run = run_rows((int64_t)p.B * p.T, p.T, g.nv, 1 << 17, bwd ? 64 : 32);
+    g.run = run_rows((int64_t)p.B * p.T, p.T, g.nv, bwd ? 1 << 17 : 1 << 18, bwd ? 128 : 32);
     g.nrun = (p.T + g.run - 1) / g.run;
-    g.cx = 1;
-    while (g.cx < 64 && g.cx < g.nv) g.cx *= 2;
-    g.ncb = (g.nv + g.cx - 1) / g.cx;
-    const int nry = 256 / g.cx;
-    g.groups = ((int64_t)p.B * g.nrun + nry - 1) / nry;
+    g.ncb = (g.nv + 63) / 64;
+    g.groups = ((int64_t)p.B * g.nrun + 3) / 4;
     return g;
 }
 
@@ -338,7 +367,7 @@ template <typename T, int VEC, int K>
 hipError_t fwd_v(const ConvProblem& p, hipStream_t stream)
 {
     const ConvGeom g = geom(p, VEC, false);
-    const dim3 blocks = grid_of(((int64_t)p.B * g.nrun * g.nv + 255) / 256);
+    const dim3 blocks = grid_of(g.groups * g.ncb);
     if (p.silu) conv_fwd_kernel<T, VEC, K, true><<<blocks, 256, 0, stream>>>(p, g);
     else conv_fwd_kernel<T, VEC, K, false><<<blocks, 256, 0, stream>>>(p, g);
     return hipGetLastError();

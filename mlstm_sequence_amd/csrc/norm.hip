@@ -1,224 +1,189 @@
-// norm.hip -- group norm over [B,T,G,C] with channels last, and the
-// activation or gate behind it.
+// norm.hip -- group norm per token, forward (norm_impl.hpp).
 //
-//   xh = (x - mean) rstd,  u = xh w + bias,  y = act(u) or u act(gate)
-//   v = du w,  dx = rstd (v - mean(v) - xh mean(v xh))
-//
-// A set is what shares one mean: the C channels of a token's group, or the
-// T x C values of a sequence's group.
-#include "act.hpp"
-#include "blocks.hpp"
+// Bound by memory: x and the gate are read once, y written once.  A row lives
+// in the registers of L lanes, so mean and variance take two passes over
+// registers and 2 log2 L lane steps; the next row's loads are under way
+// meanwhile.  Rows too long for that are walked by a workgroup each, from
+// memory.
+#include "norm_impl.hpp"
 
 namespace tfla {
 namespace {
 
-__device__ __forceinline__ float act_f(float u, int act)
-{
-    if (act == kActNone) return u;
-    const float s = sigmoid_f(u);
-    return act == kActSilu ? u * s : s;
-}
+using namespace norm;
 
-__device__ __forceinline__ float act_grad(float u, int act)
+template <typename T, int VEC, int V, bool GATED, bool ACTIVE>
+__global__ __launch_bounds__(256) void norm_fwd_kernel(NormProblem p, TokenMap m)
 {
-    if (act == kActNone) return 1.0f;
-    const float s = sigmoid_f(u);
-    return act == kActSilu ? s * (1.0f + u * (1.0f - s)) : s * (1.0f - s);
-}
-
-__device__ __forceinline__ int64_t at(const Heads& h, int b, int t, int g, int c)
-{
-    return b * h.batch + t * h.row + g * h.group + c;
-}
-
-__device__ __forceinline__ float block_sum(float v)
-{
-    __shared__ float s[4];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t id = block_id() * 4 + wave;
+    if (id >= m.chunks * m.ng) return;
+    const int set = (int)(id % m.ng);
+    const int64_t i0 = id / m.ng * m.per * m.step, i1 = min(i0 + m.per * m.step, m.tokens);
+    const int slot = lane / m.L, lv = lane & (m.L - 1);
+    const int g = m.by_group ? set * m.slots + slot : set;
+    const int off = m.by_group ? 0 : slot;            // of the lane's token in a step
+    const bool silu = p.act == kActSilu;
+    const T* xp = (const T*)p.x.p + g * p.x.group;
+    const T* zp = GATED ? (const T*)p.gate.p + g * p.gate.group : nullptr;
+    T* yp = (T*)p.y.p + g * p.y.group;
+    int c[V];
+    bool in[V];
+    float w[V][VEC], bs[V][VEC];
 #pragma unroll
-    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
-    __syncthreads();
-    return (s[0] + s[1]) + (s[2] + s[3]);
-}
-
-struct Set {
-    int b, t0, t1, g;
-    int64_t id;
-};
-
-// Block -> set: token sets [B,T,G], sequence sets [B,G].
-__device__ __forceinline__ Set set_of(const NormProblem& p)
-{
-    Set s;
-    int64_t i = blockIdx.x;
-    s.id = i;
-    s.g = (int)(i % p.G);
-    i /= p.G;
-    if (p.sequence) {
-        s.b = (int)i;
-        s.t0 = 0;
-        s.t1 = p.T;
-    } else {
-        s.b = (int)(i / p.T);
-        s.t0 = (int)(i % p.T);
-        s.t1 = s.t0 + 1;
+    for (int k = 0; k < V; ++k) {
+        in[k] = lv + k * m.L < m.nv;
+        c[k] = min(lv + k * m.L, m.nv - 1) * VEC;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            w[k][v] = p.weight ? p.weight[g * p.C + c[k] + v] : 1.0f;
+            bs[k][v] = p.bias ? p.bias[g * p.C + c[k] + v] : 0.0f;
+        }
     }
-    return s;
+    const float inv = 1.0f / (float)p.C;
+
+    Pack<T, VEC> rx[V], rz[V];
+    auto fetch = [&](int64_t i) {                     // behind the last token: the last
+        i = min(i + off, m.tokens - 1);
+        const int b = (int)(i / p.T), t = (int)(i % p.T);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            rx[k].load(xp + b * p.x.batch + t * p.x.row + c[k]);
+            if (GATED) rz[k].load(zp + b * p.gate.batch + t * p.gate.row + c[k]);
+        }
+    };
+    fetch(i0);
+    for (int64_t i = i0; i < i1; i += m.step) {
+        float x[V][VEC], z[V][VEC], s = 0.0f, q = 0.0f;
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                x[k][v] = rx[k].get(v);
+                if (GATED) z[k][v] = rz[k].get(v);
+            }
+        fetch(i + m.step);
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) s += in[k] ? x[k][v] : 0.0f;
+        const float mean = lane_sum(s, m.L) * inv;
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                x[k][v] -= mean;
+                q += in[k] ? x[k][v] * x[k][v] : 0.0f;
+            }
+        const float rstd = 1.0f / sqrtf(lane_sum(q, m.L) * inv + p.eps);
+        const int64_t tok = i + off;
+        if (tok >= i1) continue;
+        const int b = (int)(tok / p.T), t = (int)(tok % p.T);
+        if (lv == 0) {
+            if (p.mean) p.mean[tok * p.G + g] = mean;
+            if (p.rstd) p.rstd[tok * p.G + g] = rstd;
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            Pack<T, VEC> o;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const float u = x[k][v] * rstd * w[k][v] + bs[k][v];
+                o.set(v, GATED ? u * act_f<T, ACTIVE>(z[k][v], silu) : act_f<T, ACTIVE>(u, silu));
+            }
+            if (in[k]) o.store(yp + b * p.y.batch + t * p.y.row + c[k]);
+        }
+    }
 }
 
+// A workgroup to a row of any length.
 template <typename T>
-__global__ __launch_bounds__(256) void norm_fwd_kernel(NormProblem p)
+__global__ __launch_bounds__(256) void norm_fwd_long_kernel(NormProblem p)
 {
-    const Set s = set_of(p);
-    const T* x = (const T*)p.x.p;
-    const T* z = (const T*)p.gate.p;
-    T* y = (T*)p.y.p;
-    const int64_t n = (int64_t)(s.t1 - s.t0) * p.C;
-    float m = 0.0f;
-    for (int64_t i = threadIdx.x; i < n; i += 256) m += to_float(x[at(p.x, s.b, s.t0 + (int)(i / p.C), s.g, (int)(i % p.C))]);
-    m = block_sum(m) / (float)n;
-    float q = 0.0f;
-    for (int64_t i = threadIdx.x; i < n; i += 256) {
-        const float d = to_float(x[at(p.x, s.b, s.t0 + (int)(i / p.C), s.g, (int)(i % p.C))]) - m;
+    __shared__ float red[4];
+    const int64_t id = block_id();
+    if (id >= (int64_t)p.B * p.T * p.G) return;
+    const int g = (int)(id % p.G);
+    const int64_t tok = id / p.G;
+    const int b = (int)(tok / p.T), t = (int)(tok % p.T);
+    auto sum = [&](float v) {
+        v = lane_sum(v, 64);
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        return (red[0] + red[1]) + (red[2] + red[3]);
+    };
+    const T* x = (const T*)p.x.p + at(p.x, b, t, g, 0);
+    const T* z = p.gate.p ? (const T*)p.gate.p + at(p.gate, b, t, g, 0) : nullptr;
+    T* y = (T*)p.y.p + at(p.y, b, t, g, 0);
+    const float* w = p.weight ? p.weight + (int64_t)g * p.C : nullptr;
+    const float* bs = p.bias ? p.bias + (int64_t)g * p.C : nullptr;
+    float s = 0.0f, q = 0.0f;
+    for (int c = threadIdx.x; c < p.C; c += 256) s += to_float(x[c]);
+    const float mean = sum(s) / (float)p.C;
+    for (int c = threadIdx.x; c < p.C; c += 256) {
+        const float d = to_float(x[c]) - mean;
         q += d * d;
     }
-    const float r = 1.0f / sqrtf(block_sum(q) / (float)n + p.eps);
+    const float rstd = 1.0f / sqrtf(sum(q) / (float)p.C + p.eps);
     if (threadIdx.x == 0) {
-        if (p.mean) p.mean[s.id] = m;
-        if (p.rstd) p.rstd[s.id] = r;
+        if (p.mean) p.mean[id] = mean;
+        if (p.rstd) p.rstd[id] = rstd;
     }
-    for (int64_t i = threadIdx.x; i < n; i += 256) {
-        const int t = s.t0 + (int)(i / p.C), c = (int)(i % p.C);
-        const float w = p.weight ? p.weight[s.g * p.C + c] : 1.0f, bs = p.bias ? p.bias[s.g * p.C + c] : 0.0f;
-        const float u = (to_float(x[at(p.x, s.b, t, s.g, c)]) - m) * r * w + bs;
-        const float o = z ? u * act_f(to_float(z[at(p.gate, s.b, t, s.g, c)]), p.act) : act_f(u, p.act);
-        y[at(p.y, s.b, t, s.g, c)] = from_float<T>(o);
+    const bool active = p.act != kActNone, silu = p.act == kActSilu;
+    for (int c = threadIdx.x; c < p.C; c += 256) {
+        const float u = (to_float(x[c]) - mean) * rstd * (w ? w[c] : 1.0f) + (bs ? bs[c] : 0.0f);
+        const float in = z ? to_float(z[c]) : u;
+        const float f = active ? act_f<T, true>(in, silu) : in;
+        y[c] = from_float<T>(z ? u * f : f);
     }
 }
 
-// xh, u, du and dgate's factor of one element
-struct Elem1 {
-    float xh, u, du, dz;
-};
-template <typename T>
-__device__ __forceinline__ Elem1 elem(const NormProblem& p, float m, float r, int b, int t, int g, int c)
+template <typename T, int VEC, int V>
+hipError_t fwd_v(const NormProblem& p, const TokenMap& m, hipStream_t stream)
 {
-    Elem1 e;
-    const float w = p.weight ? p.weight[g * p.C + c] : 1.0f, bs = p.bias ? p.bias[g * p.C + c] : 0.0f;
-    e.xh = (to_float(((const T*)p.x.p)[at(p.x, b, t, g, c)]) - m) * r;
-    e.u = e.xh * w + bs;
-    const float dy = to_float(((const T*)p.dy.p)[at(p.dy, b, t, g, c)]);
+    const dim3 blocks = grid_of((m.chunks * m.ng + 3) / 4);
+    const bool a = p.act != kActNone;
     if (p.gate.p) {
-        const float z = to_float(((const T*)p.gate.p)[at(p.gate, b, t, g, c)]);
-        e.du = dy * act_f(z, p.act);
-        e.dz = dy * e.u * act_grad(z, p.act);
+        if (a) norm_fwd_kernel<T, VEC, V, true, true><<<blocks, 256, 0, stream>>>(p, m);
+        else norm_fwd_kernel<T, VEC, V, true, false><<<blocks, 256, 0, stream>>>(p, m);
     } else {
-        e.du = dy * act_grad(e.u, p.act);
-        e.dz = 0.0f;
+        if (a) norm_fwd_kernel<T, VEC, V, false, true><<<blocks, 256, 0, stream>>>(p, m);
+        else norm_fwd_kernel<T, VEC, V, false, false><<<blocks, 256, 0, stream>>>(p, m);
     }
-    return e;
-}
-
-template <typename T>
-__global__ __launch_bounds__(256) void norm_bwd_kernel(NormProblem p)
-{
-    const Set s = set_of(p);
-    const int64_t n = (int64_t)(s.t1 - s.t0) * p.C;
-    const float m = p.mean[s.id], r = p.rstd[s.id];
-    float s1 = 0.0f, s2 = 0.0f;
-    for (int64_t i = threadIdx.x; i < n; i += 256) {
-        const int t = s.t0 + (int)(i / p.C), c = (int)(i % p.C);
-        const Elem1 e = elem<T>(p, m, r, s.b, t, s.g, c);
-        const float v = e.du * (p.weight ? p.weight[s.g * p.C + c] : 1.0f);
-        s1 += v;
-        s2 += v * e.xh;
-    }
-    s1 = block_sum(s1) / (float)n;
-    s2 = block_sum(s2) / (float)n;
-    for (int64_t i = threadIdx.x; i < n; i += 256) {
-        const int t = s.t0 + (int)(i / p.C), c = (int)(i % p.C);
-        const Elem1 e = elem<T>(p, m, r, s.b, t, s.g, c);
-        const float v = e.du * (p.weight ? p.weight[s.g * p.C + c] : 1.0f);
-        ((T*)p.dx.p)[at(p.dx, s.b, t, s.g, c)] = from_float<T>(r * (v - s1 - e.xh * s2));
-        if (p.dgate.p) ((T*)p.dgate.p)[at(p.dgate, s.b, t, s.g, c)] = from_float<T>(e.dz);
-    }
-}
-
-// dweight, dbias: sums of a run of rows into ws [parts][2][G C], then over the parts
-constexpr int kRun = 64;
-
-template <typename T>
-__global__ __launch_bounds__(256) void norm_params_kernel(NormProblem p)
-{
-    const int W = p.G * p.C, nb = (W + 255) / 256;
-    const int64_t part = blockIdx.x / nb;
-    const int i = (int)(blockIdx.x % nb) * 256 + threadIdx.x;
-    if (i >= W) return;
-    const int g = i / p.C, c = i % p.C;
-    float s1 = 0.0f, s2 = 0.0f;
-    const int64_t r1 = min((part + 1) * kRun, (int64_t)p.B * p.T);
-    for (int64_t r = part * kRun; r < r1; ++r) {
-        const int b = (int)(r / p.T), t = (int)(r % p.T);
-        const int64_t id = (p.sequence ? b : r) * p.G + g;
-        const Elem1 e = elem<T>(p, p.mean[id], p.rstd[id], b, t, g, c);
-        s1 += e.du * e.xh;
-        s2 += e.du;
-    }
-    float* o = (float*)p.ws + part * 2 * W;
-    o[i] = s1;
-    o[W + i] = s2;
-}
-
-__global__ __launch_bounds__(256) void norm_sums_kernel(NormProblem p, int64_t parts)
-{
-    const int W = p.G * p.C;
-    const int i = blockIdx.x * 256 + threadIdx.x;
-    if (i >= 2 * W) return;
-    const float* src = (const float*)p.ws;
-    float s = 0.0f;
-    for (int64_t r = 0; r < parts; ++r) s += src[r * 2 * W + i];
-    if (i < W) {
-        if (p.dweight) p.dweight[i] = s;
-    } else if (p.dbias) {
-        p.dbias[i - W] = s;
-    }
-}
-
-int64_t parts_of(const NormProblem& p) { return ((int64_t)p.B * p.T + kRun - 1) / kRun; }
-
-template <typename T>
-hipError_t bwd_t(const NormProblem& p, hipStream_t stream)
-{
-    const unsigned sets = (unsigned)p.B * (p.sequence ? 1 : p.T) * p.G;
-    norm_bwd_kernel<T><<<sets, 256, 0, stream>>>(p);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || (!p.dweight && !p.dbias)) return e;
-    const int W = p.G * p.C;
-    const int64_t parts = parts_of(p);
-    norm_params_kernel<T><<<(unsigned)(parts * ((W + 255) / 256)), 256, 0, stream>>>(p);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    norm_sums_kernel<<<(2 * W + 255) / 256, 256, 0, stream>>>(p, parts);
     return hipGetLastError();
+}
+
+template <typename T, int VEC>
+hipError_t fwd_vec(const NormProblem& p, hipStream_t stream)
+{
+    const TokenMap m = token_map(p, VEC, 16384, 16);
+    switch (lane_vectors(m, 8)) {
+    case 1: return fwd_v<T, VEC, 1>(p, m, stream);
+    case 2: return fwd_v<T, VEC, 2>(p, m, stream);
+    case 4: return fwd_v<T, VEC, 4>(p, m, stream);
+    case 8: return fwd_v<T, VEC, 8>(p, m, stream);
+    default:
+        norm_fwd_long_kernel<T><<<grid_of((int64_t)p.B * p.T * p.G), 256, 0, stream>>>(p);
+        return hipGetLastError();
+    }
+}
+
+template <typename T>
+hipError_t fwd_t(const NormProblem& p, hipStream_t stream)
+{
+    constexpr int wide = 16 / sizeof(T);
+    return vec_of(p, false) == wide ? fwd_vec<T, wide>(p, stream) : fwd_vec<T, 1>(p, stream);
 }
 
 }  // namespace
 
-size_t norm_workspace(const NormProblem&) { return 0; }
+size_t norm_workspace(const NormProblem& p) { return p.sequence ? seq_workspace(p) : 0; }
 
 hipError_t launch_norm_fwd(const NormProblem& p, hipStream_t stream)
 {
-    const unsigned sets = (unsigned)p.B * (p.sequence ? 1 : p.T) * p.G;
-    if (p.bf16) norm_fwd_kernel<bf16><<<sets, 256, 0, stream>>>(p);
-    else norm_fwd_kernel<float><<<sets, 256, 0, stream>>>(p);
-    return hipGetLastError();
-}
-
-size_t norm_bwd_workspace(const NormProblem& p) { return (size_t)parts_of(p) * 2 * p.G * p.C * 4; }
-
-hipError_t launch_norm_bwd(const NormProblem& p, hipStream_t stream)
-{
-    return p.bf16 ? bwd_t<bf16>(p, stream) : bwd_t<float>(p, stream);
+    if (p.sequence) return launch_seq_fwd(p, stream);
+    return p.bf16 ? fwd_t<bf16>(p, stream) : fwd_t<float>(p, stream);
 }
 
 }  // namespace tfla
