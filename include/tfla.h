@@ -492,7 +492,7 @@ int tfla_conv_bwd(const tfla_conv_args* args, void* workspace, size_t workspace_
  * the last row and may be `state` itself (updated in place), so the same call
  * serves prompts and single tokens (T = 1).  States are fp32 throughout.
  *
- *   B, T, D >= 1, B T <= 2^30; G divides D; N 1 to 64
+ *   B, T, D >= 1, B T <= 2^30, B D < 2^27; G divides D; N 1 to 64
  *   x, dt, z, y   [B,T,D], z.data NULL for no gate; dt is x's type
  *   bmat, cmat    [B,T,G,N], the last two dimensions contiguous
  *   a [D,N], skip [D] or NULL, dt_bias [D] or NULL, state, state_out [B,D,N] or NULL: fp32
@@ -546,7 +546,8 @@ int tfla_scan_bwd(const tfla_scan_args* args, void* workspace, size_t workspace_
  * var is the biased variance.  x may be the head-major output [B,H,T,d_hv] of
  * tfla_fwd seen as [B,T,H,d_hv] (group stride T d_hv, row stride d_hv).
  *
- *   B, T, G, C >= 1, B T <= 2^30, G C <= 2^24; act any tfla_act
+ *   B, T, G, C >= 1, B T <= 2^30, G C <= 2^24, B T G < 2^31 (with TFLA_NORM_SEQUENCE also
+ *   B G <= 2^20, T C < 2^35); act any tfla_act
  *   x, gate, y   [B,T,G,C], gate.data NULL for no gate
  *   weight, bias fp32 [G,C] or NULL (1 and 0); eps > 0
  *   mean, rstd   fp32 [B,T,G] ([B,G] with TFLA_NORM_SEQUENCE): outputs of the forward pass

@@ -447,6 +447,10 @@ int check_norm_sizes(int B, int T, int G, int C, int flags, tfla::NormProblem* p
     if (B < 1 || T < 1 || G < 1 || C < 1) return fail(TFLA_ERR_INVALID_ARG, "B, T, G and C must be >= 1");
     if ((int64_t)B * T > kMaxRows) return fail(TFLA_ERR_UNSUPPORTED, "B*T must be <= 2^30");
     if ((int64_t)G * C > (1 << 24)) return fail(TFLA_ERR_UNSUPPORTED, "G*C must be <= 2^24");
+    if ((int64_t)B * T * G >= (int64_t(1) << 31)) return fail(TFLA_ERR_UNSUPPORTED, "B*T*G must be below 2^31");
+    // the sequence's statistics: a workgroup to a set, partial sums counted in 32 bits
+    if ((flags & TFLA_NORM_SEQUENCE) && ((int64_t)B * G > (1 << 20) || (int64_t)(T / 16 + 1) * C >= (int64_t(1) << 31)))
+        return fail(TFLA_ERR_UNSUPPORTED, "TFLA_NORM_SEQUENCE: B*G must be <= 2^20 and T*C/16 below 2^31");
     *p = tfla::NormProblem{};
     p->B = B;
     p->T = T;

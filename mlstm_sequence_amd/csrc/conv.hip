@@ -304,22 +304,25 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, ConvGeom g
 }
 
 // dweight [D,K] and dbias [D] from the workgroups' sums [parts][K+1][D]: 64
-// columns and 4 slices of the parts to a workgroup.
-__global__ __launch_bounds__(256) void conv_params_kernel(const float* __restrict__ part, int parts, int D, int K,
-                                                          float* __restrict__ dweight, float* __restrict__ dbias)
+// columns and 16 slices of the parts to a workgroup.
+__global__ __launch_bounds__(1024) void conv_params_kernel(const float* __restrict__ part, int64_t parts, int D, int K,
+                                                           float* __restrict__ dweight, float* __restrict__ dbias)
 {
-    __shared__ float red[4][64];
+    __shared__ float red[16][64];
     const int64_t n = (int64_t)(K + 1) * D, i = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
     const int slice = threadIdx.x >> 6;
     float s = 0.0f;
     if (i < n) {
-#pragma unroll 8
-        for (int r = slice; r < parts; r += 4) s += part[r * n + i];
+#pragma unroll 4
+        for (int64_t r = slice; r < parts; r += 16) s += part[r * n + i];
     }
     red[slice][threadIdx.x & 63] = s;
-    __syncthreads();
+    for (int k = 8; k; k >>= 1) {
+        __syncthreads();
+        if (slice < k) red[slice][threadIdx.x & 63] += red[slice + k][threadIdx.x & 63];
+    }
     if (slice || i >= n) return;
-    s = (red[0][threadIdx.x] + red[1][threadIdx.x]) + (red[2][threadIdx.x] + red[3][threadIdx.x]);
+    s = red[0][threadIdx.x];
     const int j = (int)(i / D), c = (int)(i % D);
     if (j < K) dweight[(size_t)c * K + j] = s;
     else if (dbias) dbias[c] = s;
@@ -383,7 +386,7 @@ hipError_t bwd_v(const ConvProblem& p, hipStream_t stream)
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t n = (int64_t)(K + 1) * p.D;
-    conv_params_kernel<<<(unsigned)((n + 63) / 64), 256, 0, stream>>>(p.part, (int)g.groups, p.D, K, p.dweight, p.dbias);
+    conv_params_kernel<<<(unsigned)((n + 63) / 64), 1024, 0, stream>>>(p.part, g.groups, p.D, K, p.dweight, p.dbias);
     return hipGetLastError();
 }
 

@@ -3,8 +3,8 @@
 // Bound by memory: x and the gate are read once, y written once.  A row lives
 // in the registers of L lanes, so mean and variance take two passes over
 // registers and 2 log2 L lane steps; the next row's loads are under way
-// meanwhile.  Rows too long for that are walked by a workgroup each, from
-// memory.
+// meanwhile.  Rows too long for that (8192 channels in vectors, 1024 single
+// ones) are walked by a workgroup each, from memory.
 #include "norm_impl.hpp"
 
 namespace tfla {
@@ -12,14 +12,16 @@ namespace {
 
 using namespace norm;
 
-template <typename T, int VEC, int V, bool GATED, bool ACTIVE>
+template <typename T, int VEC, int V, bool GATED, bool ACTIVE, bool BLOCK>
 __global__ __launch_bounds__(256) void norm_fwd_kernel(NormProblem p, TokenMap m)
 {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t id = block_id() * 4 + wave;
-    if (id >= m.chunks * m.ng) return;
-    const int set = (int)(id % m.ng);
-    const int64_t i0 = id / m.ng * m.per * m.step, i1 = min(i0 + m.per * m.step, m.tokens);
+    __shared__ float red[4];
+    const int lane = BLOCK ? threadIdx.x : threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const unsigned id = BLOCK ? (unsigned)block_id() : (unsigned)block_id() * 4 + wave;
+    if (id >= m.chunks * (unsigned)m.ng) return;
+    const int set = (int)(id % (unsigned)m.ng);
+    const unsigned i0 = id / (unsigned)m.ng * m.per * m.step, i1 = min(i0 + m.per * m.step, m.tokens);
     const int slot = lane / m.L, lv = lane & (m.L - 1);
     const int g = m.by_group ? set * m.slots + slot : set;
     const int off = m.by_group ? 0 : slot;            // of the lane's token in a step
@@ -43,9 +45,9 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormProblem p, TokenMap m
     const float inv = 1.0f / (float)p.C;
 
     Pack<T, VEC> rx[V], rz[V];
-    auto fetch = [&](int64_t i) {                     // behind the last token: the last
+    auto fetch = [&](unsigned i) {                    // behind the last token: the last
         i = min(i + off, m.tokens - 1);
-        const int b = (int)(i / p.T), t = (int)(i % p.T);
+        const int b = (int)(i / (unsigned)p.T), t = (int)(i % (unsigned)p.T);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             rx[k].load(xp + b * p.x.batch + t * p.x.row + c[k]);
@@ -53,7 +55,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormProblem p, TokenMap m
         }
     };
     fetch(i0);
-    for (int64_t i = i0; i < i1; i += m.step) {
+    for (unsigned i = i0; i < i1; i += m.step) {
         float x[V][VEC], z[V][VEC], s = 0.0f, q = 0.0f;
 #pragma unroll
         for (int k = 0; k < V; ++k)
@@ -67,7 +69,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormProblem p, TokenMap m
         for (int k = 0; k < V; ++k)
 #pragma unroll
             for (int v = 0; v < VEC; ++v) s += in[k] ? x[k][v] : 0.0f;
-        const float mean = lane_sum(s, m.L) * inv;
+        const float mean = row_sum<BLOCK>(s, m.L, red) * inv;
 #pragma unroll
         for (int k = 0; k < V; ++k)
 #pragma unroll
@@ -75,13 +77,13 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormProblem p, TokenMap m
                 x[k][v] -= mean;
                 q += in[k] ? x[k][v] * x[k][v] : 0.0f;
             }
-        const float rstd = 1.0f / sqrtf(lane_sum(q, m.L) * inv + p.eps);
-        const int64_t tok = i + off;
-        if (tok >= i1) continue;
-        const int b = (int)(tok / p.T), t = (int)(tok % p.T);
+        const float rstd = 1.0f / sqrtf(row_sum<BLOCK>(q, m.L, red) * inv + p.eps);
+        const unsigned tok = i + off;
+        if (tok >= i1) continue;                      // never for a workgroup's row
+        const int b = (int)(tok / (unsigned)p.T), t = (int)(tok % (unsigned)p.T);
         if (lv == 0) {
-            if (p.mean) p.mean[tok * p.G + g] = mean;
-            if (p.rstd) p.rstd[tok * p.G + g] = rstd;
+            if (p.mean) p.mean[(int64_t)tok * p.G + g] = mean;
+            if (p.rstd) p.rstd[(int64_t)tok * p.G + g] = rstd;
         }
 #pragma unroll
         for (int k = 0; k < V; ++k) {
@@ -106,13 +108,7 @@ __global__ __launch_bounds__(256) void norm_fwd_long_kernel(NormProblem p)
     const int g = (int)(id % p.G);
     const int64_t tok = id / p.G;
     const int b = (int)(tok / p.T), t = (int)(tok % p.T);
-    auto sum = [&](float v) {
-        v = lane_sum(v, 64);
-        __syncthreads();
-        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-        __syncthreads();
-        return (red[0] + red[1]) + (red[2] + red[3]);
-    };
+    auto sum = [&](float v) { return row_sum<true>(v, 256, red); };
     const T* x = (const T*)p.x.p + at(p.x, b, t, g, 0);
     const T* z = p.gate.p ? (const T*)p.gate.p + at(p.gate, b, t, g, 0) : nullptr;
     T* y = (T*)p.y.p + at(p.y, b, t, g, 0);
@@ -139,17 +135,18 @@ __global__ __launch_bounds__(256) void norm_fwd_long_kernel(NormProblem p)
     }
 }
 
-template <typename T, int VEC, int V>
+template <typename T, int VEC, int V, bool BLOCK>
 hipError_t fwd_v(const NormProblem& p, const TokenMap& m, hipStream_t stream)
 {
-    const dim3 blocks = grid_of((m.chunks * m.ng + 3) / 4);
+    const int64_t n = (int64_t)m.chunks * m.ng;
+    const dim3 blocks = grid_of(BLOCK ? n : (n + 3) / 4);
     const bool a = p.act != kActNone;
     if (p.gate.p) {
-        if (a) norm_fwd_kernel<T, VEC, V, true, true><<<blocks, 256, 0, stream>>>(p, m);
-        else norm_fwd_kernel<T, VEC, V, true, false><<<blocks, 256, 0, stream>>>(p, m);
+        if (a) norm_fwd_kernel<T, VEC, V, true, true, BLOCK><<<blocks, 256, 0, stream>>>(p, m);
+        else norm_fwd_kernel<T, VEC, V, true, false, BLOCK><<<blocks, 256, 0, stream>>>(p, m);
     } else {
-        if (a) norm_fwd_kernel<T, VEC, V, false, true><<<blocks, 256, 0, stream>>>(p, m);
-        else norm_fwd_kernel<T, VEC, V, false, false><<<blocks, 256, 0, stream>>>(p, m);
+        if (a) norm_fwd_kernel<T, VEC, V, false, true, BLOCK><<<blocks, 256, 0, stream>>>(p, m);
+        else norm_fwd_kernel<T, VEC, V, false, false, BLOCK><<<blocks, 256, 0, stream>>>(p, m);
     }
     return hipGetLastError();
 }
@@ -158,11 +155,11 @@ template <typename T, int VEC>
 hipError_t fwd_vec(const NormProblem& p, hipStream_t stream)
 {
     const TokenMap m = token_map(p, VEC, 16384, 16);
-    switch (lane_vectors(m, 8)) {
-    case 1: return fwd_v<T, VEC, 1>(p, m, stream);
-    case 2: return fwd_v<T, VEC, 2>(p, m, stream);
-    case 4: return fwd_v<T, VEC, 4>(p, m, stream);
-    case 8: return fwd_v<T, VEC, 8>(p, m, stream);
+    if (!m.block) return fwd_v<T, VEC, 1, false>(p, m, stream);
+    switch (lane_vectors(m)) {
+    case 1: return fwd_v<T, VEC, 1, true>(p, m, stream);
+    case 2: return fwd_v<T, VEC, 2, true>(p, m, stream);
+    case 4: return fwd_v<T, VEC, 4, true>(p, m, stream);
     default:
         norm_fwd_long_kernel<T><<<grid_of((int64_t)p.B * p.T * p.G), 256, 0, stream>>>(p);
         return hipGetLastError();

@@ -13,15 +13,17 @@ namespace {
 
 using namespace norm;
 
-template <typename T, int VEC, int V, bool GATED, bool ACTIVE>
+template <typename T, int VEC, int V, bool GATED, bool ACTIVE, bool BLOCK>
 __global__ __launch_bounds__(256) void norm_bwd_kernel(NormProblem p, TokenMap m)
 {
-    __shared__ float red[4][2][64 * VEC];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t group = block_id() / m.ng, chunk = group * 4 + wave;
-    const int set = (int)(block_id() % m.ng);
-    if (group * 4 >= m.chunks) return;
-    const int64_t i0 = chunk * m.per * m.step, i1 = min(i0 + m.per * m.step, m.tokens);   // none behind the last chunk
+    __shared__ float red[BLOCK ? 1 : 4][2][BLOCK ? 4 : 64 * VEC];
+    const int lane = BLOCK ? threadIdx.x : threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const unsigned id = (unsigned)block_id(), group = id / (unsigned)m.ng, chunk = BLOCK ? group : group * 4 + wave;
+    const int set = (int)(id % (unsigned)m.ng);
+    if ((BLOCK ? group : group * 4) >= m.chunks) return;
+    const unsigned i0 = min(chunk, m.chunks) * m.per * m.step;
+    const unsigned i1 = chunk < m.chunks ? min(i0 + m.per * m.step, m.tokens) : i0;   // none behind the last chunk
     const int slot = lane / m.L, lv = lane & (m.L - 1);
     const int g = m.by_group ? set * m.slots + slot : set;
     const int off = m.by_group ? 0 : slot;
@@ -49,11 +51,11 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormProblem p, TokenMap m
 
     Pack<T, VEC> rx[V], rg[V], rz[V];
     float rm, rr;
-    auto fetch = [&](int64_t i) {
+    auto fetch = [&](unsigned i) {
         i = min(i + off, m.tokens - 1);
-        const int b = (int)(i / p.T), t = (int)(i % p.T);
-        rm = p.mean[i * p.G + g];
-        rr = p.rstd[i * p.G + g];
+        const int b = (int)(i / (unsigned)p.T), t = (int)(i % (unsigned)p.T);
+        rm = p.mean[(int64_t)i * p.G + g];
+        rr = p.rstd[(int64_t)i * p.G + g];
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             rx[k].load(xp + b * p.x.batch + t * p.x.row + c[k]);
@@ -61,11 +63,11 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormProblem p, TokenMap m
             if (GATED) rz[k].load(zp + b * p.gate.batch + t * p.gate.row + c[k]);
         }
     };
-    if (i0 < i1) fetch(i0);
-    for (int64_t i = i0; i < i1; i += m.step) {
+    fetch(i0);
+    for (unsigned i = i0; i < i1; i += m.step) {
         const float mean = rm, rstd = rr;
         float xh[V][VEC], du[V][VEC], dz[V][VEC], s1 = 0.0f, s2 = 0.0f;
-        const int64_t tok = i + off;
+        const unsigned tok = i + off;
         const bool live = tok < i1;
 #pragma unroll
         for (int k = 0; k < V; ++k)
@@ -92,10 +94,10 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormProblem p, TokenMap m
                 s1 += in[k] ? du[k][v] : 0.0f;
                 s2 += in[k] ? du[k][v] * xh[k][v] : 0.0f;
             }
-        s1 = lane_sum(s1, m.L) * inv;
-        s2 = lane_sum(s2, m.L) * inv;
-        if (!live) continue;
-        const int b = (int)(tok / p.T), t = (int)(tok % p.T);
+        s1 = row_sum<BLOCK>(s1, m.L, red[0][0]) * inv;
+        s2 = row_sum<BLOCK>(s2, m.L, red[0][1]) * inv;
+        if (!live) continue;                          // never for a workgroup's row
+        const int b = (int)(tok / (unsigned)p.T), t = (int)(tok % (unsigned)p.T);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             Pack<T, VEC> o, oz;
@@ -111,7 +113,19 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormProblem p, TokenMap m
         }
     }
     if (!p.dweight && !p.dbias) return;
-    float* part = (float*)p.ws + group * 2 * p.G * p.C;
+    const int64_t W = (int64_t)p.G * p.C;
+    float* part = (float*)p.ws + group * 2 * W;
+    if (BLOCK) {
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v)
+                if (in[k]) {
+                    part[(int64_t)g * p.C + c[k] + v] = dw[k][v];
+                    part[W + (int64_t)g * p.C + c[k] + v] = db[k][v];
+                }
+        return;
+    }
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         __syncthreads();
@@ -130,7 +144,7 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormProblem p, TokenMap m
                 for (int u = 0; u < 4; ++u) s += red[u][which][a * cols + q];
             const int l = q / VEC, cv = (l & (m.L - 1)) + k * m.L;
             const int gg = m.by_group ? set * m.slots + l / m.L : set;
-            if (cv < m.nv) part[(int64_t)which * p.G * p.C + (int64_t)gg * p.C + cv * VEC + q % VEC] = s;
+            if (cv < m.nv) part[which * W + (int64_t)gg * p.C + cv * VEC + q % VEC] = s;
         }
     }
 }
@@ -167,13 +181,7 @@ __global__ __launch_bounds__(256) void norm_bwd_long_kernel(NormProblem p)
     const int g = (int)(id % p.G);
     const int64_t tok = id / p.G;
     const int b = (int)(tok / p.T), t = (int)(tok % p.T);
-    auto sum = [&](float v) {
-        v = lane_sum(v, 64);
-        __syncthreads();
-        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-        __syncthreads();
-        return (red[0] + red[1]) + (red[2] + red[3]);
-    };
+    auto sum = [&](float v) { return row_sum<true>(v, 256, red); };
     const float mean = p.mean[id], rstd = p.rstd[id];
     float s1 = 0.0f, s2 = 0.0f;
     for (int c = threadIdx.x; c < p.C; c += 256) {
@@ -213,59 +221,56 @@ __global__ __launch_bounds__(256) void norm_long_params_kernel(NormProblem p)
     o[W + i] = s2;
 }
 
-// 64 columns and 4 slices of the parts to a workgroup.
-__global__ __launch_bounds__(256) void param_sums_kernel(const float* __restrict__ part, int64_t parts, size_t stride,
-                                                         int64_t n, float* __restrict__ out0, float* __restrict__ out1)
+// dweight and dbias from the workgroups' sums [parts][2][G C]
+__global__ __launch_bounds__(1024) void norm_params_kernel(NormProblem p, int64_t parts)
 {
-    __shared__ float red[4][64];
-    const int64_t i = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
-    const int slice = threadIdx.x >> 6;
-    float s = 0.0f;
-    if (i < 2 * n) {
-#pragma unroll 8
-        for (int64_t r = slice; r < parts; r += 4) s += part[r * stride + i];
+    __shared__ float red[16][64];
+    const int64_t W = (int64_t)p.G * p.C, i = (int64_t)blockIdx.x * 64 + threadIdx.x;
+    const float s = part_sum((const float*)p.ws, parts, 2 * W, 2 * W, blockIdx.x, red);
+    if (threadIdx.x >= 64 || i >= 2 * W) return;
+    if (i < W) {
+        if (p.dweight) p.dweight[i] = s;
+    } else if (p.dbias) {
+        p.dbias[i - W] = s;
     }
-    red[slice][threadIdx.x & 63] = s;
-    __syncthreads();
-    if (slice || i >= 2 * n) return;
-    s = (red[0][threadIdx.x] + red[1][threadIdx.x]) + (red[2][threadIdx.x] + red[3][threadIdx.x]);
-    if (i < n) {
-        if (out0) out0[i] = s;
-    } else if (out1) {
-        out1[i - n] = s;
-    }
+}
+
+hipError_t params(const NormProblem& p, int64_t parts, hipStream_t stream)
+{
+    const int64_t W = (int64_t)p.G * p.C;
+    norm_params_kernel<<<(unsigned)((2 * W + 63) / 64), 1024, 0, stream>>>(p, parts);
+    return hipGetLastError();
 }
 
 constexpr int64_t kWaves = 8192;
 constexpr int kMostSteps = 32;
 
-template <typename T, int VEC, int V>
+template <typename T, int VEC, int V, bool BLOCK>
 hipError_t bwd_v(const NormProblem& p, const TokenMap& m, hipStream_t stream)
 {
-    const int64_t groups = (m.chunks + 3) / 4;
+    const int64_t groups = BLOCK ? m.chunks : (m.chunks + 3) / 4;
     const dim3 blocks = grid_of(groups * m.ng);
     const bool a = p.act != kActNone;
     if (p.gate.p) {
-        if (a) norm_bwd_kernel<T, VEC, V, true, true><<<blocks, 256, 0, stream>>>(p, m);
-        else norm_bwd_kernel<T, VEC, V, true, false><<<blocks, 256, 0, stream>>>(p, m);
+        if (a) norm_bwd_kernel<T, VEC, V, true, true, BLOCK><<<blocks, 256, 0, stream>>>(p, m);
+        else norm_bwd_kernel<T, VEC, V, true, false, BLOCK><<<blocks, 256, 0, stream>>>(p, m);
     } else {
-        if (a) norm_bwd_kernel<T, VEC, V, false, true><<<blocks, 256, 0, stream>>>(p, m);
-        else norm_bwd_kernel<T, VEC, V, false, false><<<blocks, 256, 0, stream>>>(p, m);
+        if (a) norm_bwd_kernel<T, VEC, V, false, true, BLOCK><<<blocks, 256, 0, stream>>>(p, m);
+        else norm_bwd_kernel<T, VEC, V, false, false, BLOCK><<<blocks, 256, 0, stream>>>(p, m);
     }
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || (!p.dweight && !p.dbias)) return e;
-    const int64_t W = (int64_t)p.G * p.C;
-    return launch_param_sums((const float*)p.ws, groups, 2 * W, W, p.dweight, p.dbias, stream);
+    return e != hipSuccess || (!p.dweight && !p.dbias) ? e : params(p, groups, stream);
 }
 
 template <typename T, int VEC>
 hipError_t bwd_vec(const NormProblem& p, hipStream_t stream)
 {
     const TokenMap m = token_map(p, VEC, kWaves, kMostSteps);
-    switch (lane_vectors(m, 4)) {
-    case 1: return bwd_v<T, VEC, 1>(p, m, stream);
-    case 2: return bwd_v<T, VEC, 2>(p, m, stream);
-    case 4: return bwd_v<T, VEC, 4>(p, m, stream);
+    if (!m.block) return bwd_v<T, VEC, 1, false>(p, m, stream);
+    switch (lane_vectors(m)) {
+    case 1: return bwd_v<T, VEC, 1, true>(p, m, stream);
+    case 2: return bwd_v<T, VEC, 2, true>(p, m, stream);
+    case 4: return bwd_v<T, VEC, 4, true>(p, m, stream);
     default: break;
     }
     norm_bwd_long_kernel<T><<<grid_of((int64_t)p.B * p.T * p.G), 256, 0, stream>>>(p);
@@ -274,7 +279,7 @@ hipError_t bwd_vec(const NormProblem& p, hipStream_t stream)
     const int64_t W = (int64_t)p.G * p.C, parts = ((int64_t)p.B * p.T + kLongRun - 1) / kLongRun;
     norm_long_params_kernel<T><<<grid_of(parts * ((W + 255) / 256)), 256, 0, stream>>>(p);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    return launch_param_sums((const float*)p.ws, parts, 2 * W, W, p.dweight, p.dbias, stream);
+    return params(p, parts, stream);
 }
 
 template <typename T>
@@ -286,17 +291,6 @@ hipError_t bwd_t(const NormProblem& p, hipStream_t stream)
 
 }  // namespace
 
-namespace norm {
-
-hipError_t launch_param_sums(const float* part, int64_t parts, size_t stride, int64_t n, float* out0, float* out1,
-                             hipStream_t stream)
-{
-    param_sums_kernel<<<(unsigned)((2 * n + 63) / 64), 256, 0, stream>>>(part, parts, stride, n, out0, out1);
-    return hipGetLastError();
-}
-
-}  // namespace norm
-
 // For whichever width the call's addresses allow.
 size_t norm_bwd_workspace(const NormProblem& p)
 {
@@ -304,7 +298,8 @@ size_t norm_bwd_workspace(const NormProblem& p)
     int64_t most = ((int64_t)p.B * p.T + kLongRun - 1) / kLongRun;
     for (const int v : {1, p.bf16 ? 8 : 4}) {
         if (p.C % v) continue;
-        const int64_t n = (token_map(p, v, kWaves, kMostSteps).chunks + 3) / 4;
+        const TokenMap m = token_map(p, v, kWaves, kMostSteps);
+        const int64_t n = m.block ? m.chunks : (m.chunks + 3) / 4;
         if (n > most) most = n;
     }
     return (size_t)most * 2 * p.G * p.C * sizeof(float);

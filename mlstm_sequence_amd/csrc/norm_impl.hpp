@@ -85,35 +85,38 @@ __device__ __forceinline__ float lane_sum(float v, int L)
     return v;
 }
 
-// How the rows [B,T,G] of token sets fall to waves.  L lanes hold a row (V
-// vectors each), so a wave holds 64 / L: consecutive groups of a token where
-// those divide G (`by_group`), else consecutive tokens of a group.  A wave
-// keeps its groups and walks `per` token steps, so its weights stay in
-// registers.
+// How the rows [B,T,G] of token sets fall to waves.  L lanes hold a row, one
+// vector each, so a wave holds 64 / L: consecutive groups of a token where
+// those divide G (`by_group`), else consecutive tokens of a group.  A row of
+// more than 64 vectors falls to a whole workgroup (L = 256), up to 4 vectors
+// a lane.  A wave (workgroup) keeps its groups and walks `per` token steps, so
+// its weights stay in registers.  Rows are counted in 32 bits: a division
+// by T in 64 costs more than a row of 512 channels.
 struct TokenMap {
     int L, slots, ng, step;     // rows of a wave; sets of groups; tokens of a step
-    bool by_group;
+    bool by_group, block;
     int nv;                     // vectors of a row
-    int64_t tokens, per, chunks;
+    unsigned tokens, per, chunks;
 };
 
 inline TokenMap token_map(const NormProblem& p, int vec, int64_t waves, int most)
 {
     TokenMap m;
     m.nv = p.C / vec;
-    m.L = 1;
+    m.block = m.nv > 64;
+    m.L = m.block ? 256 : 1;
     while (m.L < 64 && m.L < m.nv) m.L *= 2;
-    m.slots = 64 / m.L;
+    m.slots = m.block ? 1 : 64 / m.L;
     m.by_group = p.G % m.slots == 0;
     m.ng = m.by_group ? p.G / m.slots : p.G;
     m.step = m.by_group ? 1 : m.slots;
-    m.tokens = (int64_t)p.B * p.T;
-    const int64_t steps = (m.tokens + m.step - 1) / m.step;
-    int64_t per = steps * m.ng / waves;
+    m.tokens = (unsigned)p.B * (unsigned)p.T;
+    const int64_t steps = ((int64_t)m.tokens + m.step - 1) / m.step;
+    int64_t per = steps * m.ng / (m.block ? waves / 4 : waves);
     if (per < 1) per = 1;
     if (per > most) per = most;
-    m.per = per;
-    m.chunks = (steps + per - 1) / per;
+    m.per = (unsigned)per;
+    m.chunks = (unsigned)((steps + per - 1) / per);
     return m;
 }
 
@@ -135,11 +138,21 @@ inline int vec_of(const NormProblem& p, bool bwd)
 }
 
 // Vectors that a lane holds of a row (rounded to what is built), or 0: too many.
-inline int lane_vectors(const TokenMap& m, int most)
+inline int lane_vectors(const TokenMap& m)
 {
     const int v = (m.nv + m.L - 1) / m.L;
-    const int r = v <= 1 ? 1 : v <= 2 ? 2 : v <= 4 ? 4 : 8;
-    return v <= most ? r : 0;
+    return v <= 1 ? 1 : v <= 2 ? 2 : v <= 4 ? 4 : 0;
+}
+
+// Sum over the lanes of a row; for a workgroup's row through LDS (two barriers; `red` of 4 floats).
+template <bool BLOCK> __device__ __forceinline__ float row_sum(float v, int L, float* red)
+{
+    if (!BLOCK) return lane_sum(v, L);
+    v = lane_sum(v, 64);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return (red[0] + red[1]) + (red[2] + red[3]);
 }
 
 // Sequence sets (norm_seq.hip)
@@ -148,10 +161,25 @@ hipError_t launch_seq_bwd(const NormProblem& p, hipStream_t stream);
 size_t seq_workspace(const NormProblem& p);
 size_t seq_bwd_workspace(const NormProblem& p);
 
-// Sums of parts: out0[i] (i < n) and out1[i - n] (n <= i < 2 n) of part[r * stride + i] over r < parts, in a fixed
-// order; NULL: not wanted (norm_bwd.hip).
-hipError_t launch_param_sums(const float* part, int64_t parts, size_t stride, int64_t n, float* out0, float* out1,
-                             hipStream_t stream);
+// Sums of parts, for a workgroup of 1024 threads: columns block * 64 .. + 63 of part[r * stride + i], i < n, over
+// r < parts in a fixed order, 16 slices of the parts side by side.  Returns a column's sum in the threads below 64.
+__device__ __forceinline__ float part_sum(const float* __restrict__ part, int64_t parts, int64_t stride, int64_t n,
+                                          int64_t block, float (*red)[64])
+{
+    const int64_t i = block * 64 + (threadIdx.x & 63);
+    const int slice = threadIdx.x >> 6;
+    float s = 0.0f;
+    if (i < n) {
+#pragma unroll 4
+        for (int64_t r = slice; r < parts; r += 16) s += part[r * stride + i];
+    }
+    red[slice][threadIdx.x & 63] = s;
+    for (int k = 8; k; k >>= 1) {
+        __syncthreads();
+        if (slice < k) red[slice][threadIdx.x & 63] += red[slice + k][threadIdx.x & 63];
+    }
+    return red[0][threadIdx.x & 63];
+}
 
 }  // namespace norm
 }  // namespace tfla

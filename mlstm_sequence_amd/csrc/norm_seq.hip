@@ -10,8 +10,6 @@
 // the weights' gradients and, weighted, the set's two means; then the values
 // once more.  Bound by memory: two readings and a writing (what fits the
 // last-level cache is read from there the second time).
-#include <type_traits>
-
 #include "norm_impl.hpp"
 
 namespace tfla {
@@ -32,7 +30,7 @@ SeqMap seq_map(const NormProblem& p, int vec)
     m.nv = p.G * p.C / vec;
     m.ncs = (m.nv + 63) / 64;
     m.run = 16;            // rows of each wave: a quarter
-    while (m.run < 256 && (int64_t)p.B * m.ncs * ((p.T + 2 * m.run - 1) / (2 * m.run)) >= 2048) m.run *= 2;
+    while (m.run < 256 && (int64_t)p.B * m.ncs * ((p.T + 2 * m.run - 1) / (2 * m.run)) >= 384) m.run *= 2;
     m.nrun = (p.T + m.run - 1) / m.run;
     return m;
 }
@@ -145,7 +143,7 @@ __global__ __launch_bounds__(256) void seq_join_kernel(NormProblem p, SeqMap m, 
     const int64_t W = (int64_t)p.G * p.C;
     const float* part = (const float*)p.ws + (int64_t)b * m.nrun * 2 * W + (int64_t)g * p.C;
     float n = 0.0f, mean = 0.0f, m2 = 0.0f;
-    for (int64_t i = threadIdx.x; i < (int64_t)m.nrun * p.C; i += 256) {
+    for (unsigned i = threadIdx.x; i < (unsigned)m.nrun * p.C; i += 256) {
         const int run = (int)(i / p.C), c = (int)(i % p.C);
         const float* s = part + run * 2 * W + c;
         join(n, mean, m2, (float)min(m.run, p.T - run * m.run), s[0], s[W]);
@@ -292,15 +290,27 @@ __global__ __launch_bounds__(256) void seq_grad_kernel(NormProblem p, SeqMap m, 
     }
 }
 
-// One workgroup to a set: mean(v) and mean(v xh).
-__global__ __launch_bounds__(256) void seq_means_kernel(NormProblem p, SeqMap m, float* __restrict__ means)
+// The first B G workgroups, one to a set: mean(v) and mean(v xh); the others, 64 columns each: dweight and dbias.
+__global__ __launch_bounds__(1024) void seq_means_kernel(NormProblem p, SeqMap m, float* __restrict__ means)
 {
-    __shared__ float red[2][4];
-    const int b = (int)(blockIdx.x / p.G), g = (int)(blockIdx.x % p.G);
+    __shared__ float red[16][64];
     const int64_t W = (int64_t)p.G * p.C;
+    const unsigned sets = (unsigned)p.B * p.G;
+    if (blockIdx.x >= sets) {
+        const int64_t i = (int64_t)(blockIdx.x - sets) * 64 + threadIdx.x;
+        const float s = part_sum((const float*)p.ws, (int64_t)p.B * m.nrun, 2 * W, 2 * W, blockIdx.x - sets, red);
+        if (threadIdx.x >= 64 || i >= 2 * W) return;
+        if (i < W) {
+            if (p.dweight) p.dweight[i] = s;
+        } else if (p.dbias) {
+            p.dbias[i - W] = s;
+        }
+        return;
+    }
+    const int b = (int)(blockIdx.x / p.G), g = (int)(blockIdx.x % p.G);
     const float* part = (const float*)p.ws + (int64_t)b * m.nrun * 2 * W + (int64_t)g * p.C;
     float s1 = 0.0f, s2 = 0.0f;
-    for (int64_t i = threadIdx.x; i < (int64_t)m.nrun * p.C; i += 256) {
+    for (int64_t i = threadIdx.x; i < (int64_t)m.nrun * p.C; i += 1024) {
         const int run = (int)(i / p.C), c = (int)(i % p.C);
         const float w = p.weight ? p.weight[(int64_t)g * p.C + c] : 1.0f;
         s1 += w * part[run * 2 * W + W + c];
@@ -314,8 +324,9 @@ __global__ __launch_bounds__(256) void seq_means_kernel(NormProblem p, SeqMap m,
     }
     __syncthreads();
     if (threadIdx.x < 2) {
-        const float* r = red[threadIdx.x];
-        means[2 * (int64_t)blockIdx.x + threadIdx.x] = ((r[0] + r[1]) + (r[2] + r[3])) / ((float)p.T * (float)p.C);
+        float s = 0.0f;
+        for (int u = 0; u < 16; ++u) s += red[threadIdx.x][u];
+        means[2 * (int64_t)blockIdx.x + threadIdx.x] = s / ((float)p.T * (float)p.C);
     }
 }
 
@@ -357,12 +368,12 @@ hipError_t bwd_g(const NormProblem& p, hipStream_t stream)
     seq_grad_kernel<T, VEC, GATED, ACTIVE, false><<<blocks, 256, 0, stream>>>(p, m, nullptr);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    seq_means_kernel<<<(unsigned)(p.B * p.G), 256, 0, stream>>>(p, m, means);
+    const int64_t W = (int64_t)p.G * p.C;
+    const int64_t params = p.dweight || p.dbias ? (2 * W + 63) / 64 : 0;
+    seq_means_kernel<<<(unsigned)((int64_t)p.B * p.G + params), 1024, 0, stream>>>(p, m, means);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     seq_grad_kernel<T, VEC, GATED, ACTIVE, true><<<blocks, 256, 0, stream>>>(p, m, means);
-    if ((e = hipGetLastError()) != hipSuccess || (!p.dweight && !p.dbias)) return e;
-    const int64_t W = (int64_t)p.G * p.C;
-    return launch_param_sums((const float*)p.ws, (int64_t)p.B * m.nrun, 2 * W, W, p.dweight, p.dbias, stream);
+    return hipGetLastError();
 }
 
 template <typename T, int VEC>
