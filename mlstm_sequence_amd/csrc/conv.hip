@@ -6,10 +6,10 @@
 // channels and a run of rows, loads each row of its run once, kRows at a time
 // and one such group ahead, and keeps the K-1 rows before a group in
 // registers, so what is read twice is K-1 rows a run (from the caches).
-// 2 K + 6 flops an element against 2 elements moved: bound by memory forward
-// (B=4 T=4096 D=4096 bf16, K=4: 268 MB in 48 us, 5.6 TB/s, where a copy moves
-// 5.1); backward the 28 instructions an element come close to it (403 MB in
-// 93 us).
+// 2 K + 6 flops an element against 2 elements moved: bound by memory
+// (B=4 T=4096 D=4096 bf16, K=4: forward 268 MB in 48 us, 5.6 TB/s, where a copy
+// moves 5.1; backward 403 MB in 81 us, whose 28 instructions an element come
+// close to it).
 //
 // VEC is 8 bytes (4 in the backward pass, whose sums take the registers)
 // where the number of channels, the addresses and the strides allow it, else
@@ -35,7 +35,9 @@ template <typename T, int VEC> struct Pack {
     typedef T vec __attribute__((ext_vector_type(VEC)));
     vec v;
     __device__ __forceinline__ void load(const T* p) { v = *(const vec*)p; }
-    __device__ __forceinline__ void store(T* p) const { *(vec*)p = v; }
+    // non-temporal: this launch does not read it again (B=4 T=4096 D=4096 backward: 94 us with plain stores, 81 so;
+    // padded prompts 17.8 and 15.9)
+    __device__ __forceinline__ void store(T* p) const { __builtin_nontemporal_store(v, (vec*)p); }
     __device__ __forceinline__ float get(int i) const { return to_float((T)v[i]); }
     __device__ __forceinline__ void set(int i, float x) { v[i] = from_float<T>(x); }
 };

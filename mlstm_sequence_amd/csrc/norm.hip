@@ -12,7 +12,7 @@ namespace {
 
 using namespace norm;
 
-template <typename T, int VEC, int V, bool GATED, bool ACTIVE, bool BLOCK>
+template <typename T, int VEC, int V, bool GATED, bool ACTIVE, bool BLOCK, bool NT>
 __global__ __launch_bounds__(256) void norm_fwd_kernel(NormProblem p, TokenMap m)
 {
     __shared__ float red[4];
@@ -50,8 +50,8 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormProblem p, TokenMap m
         const int b = (int)(i / (unsigned)p.T), t = (int)(i % (unsigned)p.T);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            rx[k].load(xp + b * p.x.batch + t * p.x.row + c[k]);
-            if (GATED) rz[k].load(zp + b * p.gate.batch + t * p.gate.row + c[k]);
+            rx[k].template load_t<NT>(xp + b * p.x.batch + t * p.x.row + c[k]);
+            if (GATED) rz[k].template load_t<NT>(zp + b * p.gate.batch + t * p.gate.row + c[k]);
         }
     };
     fetch(i0);
@@ -135,18 +135,18 @@ __global__ __launch_bounds__(256) void norm_fwd_long_kernel(NormProblem p)
     }
 }
 
-template <typename T, int VEC, int V, bool BLOCK>
+template <typename T, int VEC, int V, bool BLOCK, bool NT>
 hipError_t fwd_v(const NormProblem& p, const TokenMap& m, hipStream_t stream)
 {
     const int64_t n = (int64_t)m.chunks * m.ng;
     const dim3 blocks = grid_of(BLOCK ? n : (n + 3) / 4);
     const bool a = p.act != kActNone;
     if (p.gate.p) {
-        if (a) norm_fwd_kernel<T, VEC, V, true, true, BLOCK><<<blocks, 256, 0, stream>>>(p, m);
-        else norm_fwd_kernel<T, VEC, V, true, false, BLOCK><<<blocks, 256, 0, stream>>>(p, m);
+        if (a) norm_fwd_kernel<T, VEC, V, true, true, BLOCK, NT><<<blocks, BLOCK ? m.L : 256, 0, stream>>>(p, m);
+        else norm_fwd_kernel<T, VEC, V, true, false, BLOCK, NT><<<blocks, BLOCK ? m.L : 256, 0, stream>>>(p, m);
     } else {
-        if (a) norm_fwd_kernel<T, VEC, V, false, true, BLOCK><<<blocks, 256, 0, stream>>>(p, m);
-        else norm_fwd_kernel<T, VEC, V, false, false, BLOCK><<<blocks, 256, 0, stream>>>(p, m);
+        if (a) norm_fwd_kernel<T, VEC, V, false, true, BLOCK, NT><<<blocks, BLOCK ? m.L : 256, 0, stream>>>(p, m);
+        else norm_fwd_kernel<T, VEC, V, false, false, BLOCK, NT><<<blocks, BLOCK ? m.L : 256, 0, stream>>>(p, m);
     }
     return hipGetLastError();
 }
@@ -154,12 +154,13 @@ hipError_t fwd_v(const NormProblem& p, const TokenMap& m, hipStream_t stream)
 template <typename T, int VEC>
 hipError_t fwd_vec(const NormProblem& p, hipStream_t stream)
 {
-    const TokenMap m = token_map(p, VEC, 16384, 16);
-    if (!m.block) return fwd_v<T, VEC, 1, false>(p, m, stream);
+    const TokenMap m = token_map(p, VEC, 4096, 32);
+    const bool nt = VEC > 1 && streams(p, p.gate.p ? 3 : 2);
+    if (!m.block) return nt ? fwd_v<T, VEC, 1, false, (VEC > 1)>(p, m, stream) : fwd_v<T, VEC, 1, false, false>(p, m, stream);
     switch (lane_vectors(m)) {
-    case 1: return fwd_v<T, VEC, 1, true>(p, m, stream);
-    case 2: return fwd_v<T, VEC, 2, true>(p, m, stream);
-    case 4: return fwd_v<T, VEC, 4, true>(p, m, stream);
+    case 1: return fwd_v<T, VEC, 1, true, false>(p, m, stream);
+    case 2: return fwd_v<T, VEC, 2, true, false>(p, m, stream);
+    case 4: return fwd_v<T, VEC, 4, true, false>(p, m, stream);
     default:
         norm_fwd_long_kernel<T><<<grid_of((int64_t)p.B * p.T * p.G), 256, 0, stream>>>(p);
         return hipGetLastError();

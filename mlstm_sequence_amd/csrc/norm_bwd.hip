@@ -13,7 +13,7 @@ namespace {
 
 using namespace norm;
 
-template <typename T, int VEC, int V, bool GATED, bool ACTIVE, bool BLOCK>
+template <typename T, int VEC, int V, bool GATED, bool ACTIVE, bool BLOCK, bool NT>
 __global__ __launch_bounds__(256) void norm_bwd_kernel(NormProblem p, TokenMap m)
 {
     __shared__ float red[BLOCK ? 1 : 4][2][BLOCK ? 4 : 64 * VEC];
@@ -58,9 +58,9 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormProblem p, TokenMap m
         rr = p.rstd[(int64_t)i * p.G + g];
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            rx[k].load(xp + b * p.x.batch + t * p.x.row + c[k]);
-            rg[k].load(gp + b * p.dy.batch + t * p.dy.row + c[k]);
-            if (GATED) rz[k].load(zp + b * p.gate.batch + t * p.gate.row + c[k]);
+            rx[k].template load_t<NT>(xp + b * p.x.batch + t * p.x.row + c[k]);
+            rg[k].template load_t<NT>(gp + b * p.dy.batch + t * p.dy.row + c[k]);
+            if (GATED) rz[k].template load_t<NT>(zp + b * p.gate.batch + t * p.gate.row + c[k]);
         }
     };
     fetch(i0);
@@ -107,8 +107,8 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormProblem p, TokenMap m
                 if (GATED) oz.set(v, dz[k][v]);
             }
             if (in[k]) {
-                o.store(dxp + b * p.dx.batch + t * p.dx.row + c[k]);
-                if (GATED) oz.store(dzp + b * p.dgate.batch + t * p.dgate.row + c[k]);
+                o.template store_t<NT>(dxp + b * p.dx.batch + t * p.dx.row + c[k]);
+                if (GATED) oz.template store_t<NT>(dzp + b * p.dgate.batch + t * p.dgate.row + c[k]);
             }
         }
     }
@@ -242,21 +242,21 @@ hipError_t params(const NormProblem& p, int64_t parts, hipStream_t stream)
     return hipGetLastError();
 }
 
-constexpr int64_t kWaves = 8192;
+constexpr int64_t kWaves = 4096;
 constexpr int kMostSteps = 32;
 
-template <typename T, int VEC, int V, bool BLOCK>
+template <typename T, int VEC, int V, bool BLOCK, bool NT>
 hipError_t bwd_v(const NormProblem& p, const TokenMap& m, hipStream_t stream)
 {
     const int64_t groups = BLOCK ? m.chunks : (m.chunks + 3) / 4;
     const dim3 blocks = grid_of(groups * m.ng);
     const bool a = p.act != kActNone;
     if (p.gate.p) {
-        if (a) norm_bwd_kernel<T, VEC, V, true, true, BLOCK><<<blocks, 256, 0, stream>>>(p, m);
-        else norm_bwd_kernel<T, VEC, V, true, false, BLOCK><<<blocks, 256, 0, stream>>>(p, m);
+        if (a) norm_bwd_kernel<T, VEC, V, true, true, BLOCK, NT><<<blocks, BLOCK ? m.L : 256, 0, stream>>>(p, m);
+        else norm_bwd_kernel<T, VEC, V, true, false, BLOCK, NT><<<blocks, BLOCK ? m.L : 256, 0, stream>>>(p, m);
     } else {
-        if (a) norm_bwd_kernel<T, VEC, V, false, true, BLOCK><<<blocks, 256, 0, stream>>>(p, m);
-        else norm_bwd_kernel<T, VEC, V, false, false, BLOCK><<<blocks, 256, 0, stream>>>(p, m);
+        if (a) norm_bwd_kernel<T, VEC, V, false, true, BLOCK, NT><<<blocks, BLOCK ? m.L : 256, 0, stream>>>(p, m);
+        else norm_bwd_kernel<T, VEC, V, false, false, BLOCK, NT><<<blocks, BLOCK ? m.L : 256, 0, stream>>>(p, m);
     }
     hipError_t e = hipGetLastError();
     return e != hipSuccess || (!p.dweight && !p.dbias) ? e : params(p, groups, stream);
@@ -266,11 +266,12 @@ template <typename T, int VEC>
 hipError_t bwd_vec(const NormProblem& p, hipStream_t stream)
 {
     const TokenMap m = token_map(p, VEC, kWaves, kMostSteps);
-    if (!m.block) return bwd_v<T, VEC, 1, false>(p, m, stream);
+    const bool nt = VEC > 1 && streams(p, p.gate.p ? 5 : 3);
+    if (!m.block) return nt ? bwd_v<T, VEC, 1, false, (VEC > 1)>(p, m, stream) : bwd_v<T, VEC, 1, false, false>(p, m, stream);
     switch (lane_vectors(m)) {
-    case 1: return bwd_v<T, VEC, 1, true>(p, m, stream);
-    case 2: return bwd_v<T, VEC, 2, true>(p, m, stream);
-    case 4: return bwd_v<T, VEC, 4, true>(p, m, stream);
+    case 1: return bwd_v<T, VEC, 1, true, false>(p, m, stream);
+    case 2: return bwd_v<T, VEC, 2, true, false>(p, m, stream);
+    case 4: return bwd_v<T, VEC, 4, true, false>(p, m, stream);
     default: break;
     }
     norm_bwd_long_kernel<T><<<grid_of((int64_t)p.B * p.T * p.G), 256, 0, stream>>>(p);

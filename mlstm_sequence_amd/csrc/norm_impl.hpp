@@ -19,6 +19,16 @@ template <typename T, int VEC> struct Pack {
     vec v;
     __device__ __forceinline__ void load(const T* p) { v = *(const vec*)p; }
     __device__ __forceinline__ void store(T* p) const { *(vec*)p = v; }
+    template <bool NT> __device__ __forceinline__ void load_t(const T* p)
+    {
+        if (NT) v = __builtin_nontemporal_load((const vec*)p);
+        else load(p);
+    }
+    template <bool NT> __device__ __forceinline__ void store_t(T* p) const
+    {
+        if (NT) __builtin_nontemporal_store(v, (vec*)p);
+        else store(p);
+    }
     __device__ __forceinline__ float get(int i) const { return to_float((T)v[i]); }
     __device__ __forceinline__ void set(int i, float x) { v[i] = from_float<T>(x); }
 };
@@ -26,6 +36,8 @@ template <typename T> struct Pack<T, 1> {
     T v;
     __device__ __forceinline__ void load(const T* p) { v = *p; }
     __device__ __forceinline__ void store(T* p) const { *p = v; }
+    template <bool> __device__ __forceinline__ void load_t(const T* p) { load(p); }
+    template <bool> __device__ __forceinline__ void store_t(T* p) const { store(p); }
     __device__ __forceinline__ float get(int) const { return to_float(v); }
     __device__ __forceinline__ void set(int, float x) { v = from_float<T>(x); }
 };
@@ -88,8 +100,8 @@ __device__ __forceinline__ float lane_sum(float v, int L)
 // How the rows [B,T,G] of token sets fall to waves.  L lanes hold a row, one
 // vector each, so a wave holds 64 / L: consecutive groups of a token where
 // those divide G (`by_group`), else consecutive tokens of a group.  A row of
-// more than 64 vectors falls to a whole workgroup (L = 256), up to 4 vectors
-// a lane.  A wave (workgroup) keeps its groups and walks `per` token steps, so
+// more than 64 vectors falls to a whole workgroup (L = 128 or 256 threads), up
+// to 4 vectors a lane.  A wave (workgroup) keeps its groups and walks `per` token steps, so
 // its weights stay in registers.  Rows are counted in 32 bits: a division
 // by T in 64 costs more than a row of 512 channels.
 struct TokenMap {
@@ -104,7 +116,7 @@ inline TokenMap token_map(const NormProblem& p, int vec, int64_t waves, int most
     TokenMap m;
     m.nv = p.C / vec;
     m.block = m.nv > 64;
-    m.L = m.block ? 256 : 1;
+    m.L = !m.block ? 1 : m.nv > 128 ? 256 : 128;
     while (m.L < 64 && m.L < m.nv) m.L *= 2;
     m.slots = m.block ? 1 : 64 / m.L;
     m.by_group = p.G % m.slots == 0;
@@ -112,7 +124,7 @@ inline TokenMap token_map(const NormProblem& p, int vec, int64_t waves, int most
     m.step = m.by_group ? 1 : m.slots;
     m.tokens = (unsigned)p.B * (unsigned)p.T;
     const int64_t steps = ((int64_t)m.tokens + m.step - 1) / m.step;
-    int64_t per = steps * m.ng / (m.block ? waves / 4 : waves);
+    int64_t per = steps * m.ng / (m.block ? waves * 64 / m.L : waves);
     if (per < 1) per = 1;
     if (per > most) per = most;
     m.per = (unsigned)per;
@@ -137,6 +149,14 @@ inline int vec_of(const NormProblem& p, bool bwd)
     return ok ? v : 1;
 }
 
+// Whether a call moves far more than the last-level cache holds (256 MB): its loads (and, backward, its stores) are
+// then non-temporal.  Gated norm of [4,8192,8,512] bf16, 807 MB: 186 us without, 169 so; backward of
+// [8,4096,32,128], 1.3 GB: 289 and 278; but gated norm of [1,2000,8,512], 49 MB, 19.4 and 22.0.
+inline bool streams(const NormProblem& p, int tensors)
+{
+    return (int64_t)p.B * p.T * p.G * p.C * (p.bf16 ? 2 : 4) * tensors >= (int64_t(512) << 20);
+}
+
 // Vectors that a lane holds of a row (rounded to what is built), or 0: too many.
 inline int lane_vectors(const TokenMap& m)
 {
@@ -152,7 +172,8 @@ template <bool BLOCK> __device__ __forceinline__ float row_sum(float v, int L, f
     __syncthreads();
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
-    return (red[0] + red[1]) + (red[2] + red[3]);
+    const float s = red[0] + red[1];
+    return L > 128 ? s + (red[2] + red[3]) : s;
 }
 
 // Sequence sets (norm_seq.hip)

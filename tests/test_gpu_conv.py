@@ -198,3 +198,22 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         assert torch.equal(y, wy) and torch.equal(end, wend)
         assert all(torch.equal(p, q) for p, q in zip(g, wg))
+
+
+def test_offsets_beyond_32_bits():
+    """Batches 2^32 elements apart in one buffer."""
+    T, D, K = 9, 128, 4
+    far = (1 << 32) + 128
+    view, out = (torch.as_strided(torch.empty(far + T * D, dtype=BF, device="cuda"), (2, T, D), (far, D, 1)) for _ in range(2))
+    x, w = torch.randn(2, T, D, device="cuda").to(BF), torch.randn(D, K, device="cuda")
+    view.copy_(x)
+    assert torch.equal(tfla.conv_forward(view, w, y=out)[0], tfla.conv_forward(x, w)[0])
+    got, want = tfla.conv_backward(view, w, view, dx=out), tfla.conv_backward(x, w, x)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    torch.cuda.synchronize()
+
+
+def test_many_short_sequences():
+    """More sequences than a run of rows is long, one and two rows each."""
+    for T in (1, 2):
+        check(BF, 700, T, 72, 4, lengths=[T * (i % 3 > 0) for i in range(700)])

@@ -261,3 +261,46 @@ def test_captured_replayed_streams_and_workspaces(over):
         want = both()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(out, want))
+
+
+def test_a_large_call_equals_its_halves():
+    """Calls that move more than the caches hold load past them; rows are
+    independent, so the two halves of the batch give the same bits."""
+    B, T, G, C = 2, 8192, 32, 256
+    x, dy = (torch.randn(B, T, G, C, device="cuda", dtype=BF) for _ in range(2))
+    z = torch.randn(B, T, G, C, device="cuda", dtype=BF)
+    w, b = torch.randn(G, C, device="cuda"), torch.randn(G, C, device="cuda")
+    kw = dict(act=tfla.ACT_SILU)
+    y, mean, rstd = tfla.norm_forward(x, w, b, gate=z, **kw)
+    dx, dz, dw, db = tfla.norm_backward(x, dy, mean, rstd, w, b, gate=z, **kw)
+    sums = [torch.zeros(G, C, dtype=torch.float64, device="cuda") for _ in range(2)]
+    for i in range(2):
+        h = slice(i, i + 1)
+        yh, mh, rh = tfla.norm_forward(x[h], w, b, gate=z[h], **kw)
+        gh = tfla.norm_backward(x[h], dy[h], mh, rh, w, b, gate=z[h], **kw)
+        assert torch.equal(yh, y[h]) and torch.equal(mh, mean[h]) and torch.equal(rh, rstd[h])
+        assert torch.equal(gh[0], dx[h]) and torch.equal(gh[1], dz[h])
+        sums[0] += gh[2].double()
+        sums[1] += gh[3].double()
+    # du xh and du summed over 2^14 rows twice, in other orders: each within (n + 1) U of their magnitudes, which
+    # are below 64 sqrt(n) here only on average, so bounded by the values' own: |dy| <= 7, |act| <= 7, |xh| <= 7
+    tol = 2 * (B * T + 1) * U * B * T * 7.0 ** 3
+    assert float((sums[0] - dw).abs().max()) <= tol and float((sums[1] - db).abs().max()) <= tol
+
+
+def test_offsets_beyond_32_bits():
+    """Batches 2^32 elements apart in one buffer."""
+    T, G, C = 3, 4, 64
+    far = (1 << 32) + 64
+    buf = torch.empty(far + T * G * C, dtype=BF, device="cuda")
+    view = torch.as_strided(buf, (2, T, G, C), (far, G * C, C, 1))
+    out = torch.as_strided(torch.empty_like(buf), (2, T, G, C), (far, G * C, C, 1))
+    x = torch.randn(2, T, G, C, device="cuda").to(BF)
+    view.copy_(x)
+    for over in (tfla.NORM_TOKEN, tfla.NORM_SEQUENCE):
+        want, m, r = tfla.norm_forward(x, act=tfla.ACT_SILU, over=over)
+        got, _, _ = tfla.norm_forward(view, act=tfla.ACT_SILU, over=over, y=out)
+        assert torch.equal(got, want)
+        g = tfla.norm_backward(x, x, m, r, act=tfla.ACT_SILU, over=over)[0]
+        assert torch.equal(tfla.norm_backward(view, view, m, r, act=tfla.ACT_SILU, over=over, dx=out)[0], g)
+    torch.cuda.synchronize()

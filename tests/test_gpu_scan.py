@@ -264,3 +264,30 @@ def test_captured_and_replayed():
         wg = tfla.scan_backward(*args, dy, z=z, state=s)
         torch.cuda.synchronize()
         assert grads_equal(f, wf) and grads_equal(g, wg)
+
+
+def test_offsets_beyond_32_bits():
+    """Batches 2^32 elements apart in one buffer."""
+    T, D, N = 70, 64, 16
+    far = (1 << 32) + 64
+    dev, _ = make(BF, 2, T, D, N, state=False)
+    x, dt, a, b, c, dy = (dev[k].cuda() for k in ("x", "dt", "a", "bmat", "cmat", "dy"))
+    view, out = (torch.as_strided(torch.empty(far + T * D, dtype=BF, device="cuda"), (2, T, D), (far, D, 1)) for _ in range(2))
+    view.copy_(x)
+    want = tfla.scan_forward(x, dt, a, b, c)[0]
+    assert torch.equal(tfla.scan_forward(view, dt, a, b, c, y=out)[0], want)
+    assert torch.equal(tfla.scan_forward(view[:, :1], dt[:, :1], a, b[:, :1], c[:, :1], y=out[:, :1])[0], want[:, :1])
+    g = tfla.scan_backward(x, dt, a, b, c, dy)
+    assert grads_equal(tfla.scan_backward(view, dt, a, b, c, dy, dx=out), g)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("T", [1, 3, 4, 5])
+def test_many_short_sequences(T):
+    check(BF, 300, T, 40, 12, lengths=[min(T, i % 6) for i in range(300)])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_every_segment_of_a_padded_batch(dtype):
+    """Sequences that end in the first, a middle and the last of many segments, one of them empty."""
+    check(dtype, 4, 1030, 33, 16, lengths=[1030, 0, 65, 500])
