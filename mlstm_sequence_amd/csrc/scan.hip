@@ -236,10 +236,20 @@ __global__ __launch_bounds__(256) void scan_starts_kernel(ScanProblem p, Segment
     float h = p.state ? p.state[i] : 0.0f;
     float* e = ends + b * sg.nseg * DN + k;
     const float* s = sums + b * sg.nseg * p.D + c;
-    for (int j = 0; j < sg.nseg; ++j) {
-        const float next = exp2_fast(s[(int64_t)j * p.D] * A) * h + e[j * DN];
-        e[j * DN] = h;
-        h = next;
+    constexpr int LINKS = 8;                          // in batches, whose loads are under way together
+    for (int j0 = 0; j0 < sg.nseg; j0 += LINKS) {
+        float d[LINKS], v[LINKS];
+#pragma unroll
+        for (int k = 0; k < LINKS; ++k) {
+            const int64_t j = min(j0 + k, sg.nseg - 1);
+            d[k] = s[j * p.D];
+            v[k] = e[j * DN];
+        }
+#pragma unroll
+        for (int k = 0; k < LINKS; ++k) {
+            if (j0 + k < sg.nseg) e[(j0 + k) * DN] = h;
+            h = exp2_fast(d[k] * A) * h + v[k];
+        }
     }
 }
 

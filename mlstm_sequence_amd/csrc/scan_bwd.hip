@@ -36,7 +36,9 @@ using namespace scan;
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kVm0 = 0x0f70;   // s_waitcnt: no vector load outstanding
-constexpr int AHEAD = 2;       // tiles whose inputs are under way
+// Tiles whose inputs are under way: two, but one where the registers are short (16 waves: 128 each; one wave: a whole
+// tile's steps to prepare), N=64 288 against 278 us, N=4 135 against 103.
+constexpr int ahead(int W) { return W == 1 || W == 16 ? 1 : 2; }
 constexpr int kTile = 8;       // steps of a tile: its states and decays take 16 registers a step pair
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -52,12 +54,14 @@ struct Ws {
     size_t bytes;
 };
 
-// Segments of whole tiles, 64 steps at least, enough for 8192 waves.
+// Segments of whole tiles, 64 steps at least.  Two waves of pass 3 fit a SIMD (registers): from there on (2048) one
+// segment, which saves pass 1 its adjoint (B=8 T=2048 D=4096 N=16: 1169 us against 1189 with four), below it enough
+// for 4096 waves.
 Segments segments_of(const ScanProblem& p)
 {
     const int64_t waves = (int64_t)p.B * channel_blocks(p) * waves_of(p.N);
     const int tiles = (p.T + kTile - 1) / kTile;
-    int64_t n = waves >= 4096 ? 1 : 8192 / waves;
+    int64_t n = waves >= 2048 ? 1 : 4096 / waves;
     if (n > p.T / 64) n = p.T / 64;
     if (n < 1) n = 1;
     const int per = (int)((tiles + n - 1) / n);
@@ -170,6 +174,7 @@ __global__ __launch_bounds__(64 * W) void scan_tiles_kernel(ScanProblem p, Segme
     struct Raw {
         T x[OWN], dt[OWN], z[OWN], dy[OWN], m;
     };
+    constexpr int AHEAD = ahead(W);
     Raw raw[AHEAD];
     auto fetch = [&](Raw& r, int t0) {
 #pragma unroll
@@ -265,17 +270,37 @@ __global__ __launch_bounds__(256) void scan_links_kernel(ScanProblem p, Segments
     float* e = ws.ends + b * sg.nseg * DN + k;
     float* g = ws.adj + b * sg.nseg * DN + k;
     const float* s = ws.sums + b * sg.nseg * p.D + k / p.N;
+    // in batches, whose loads are under way together
+    constexpr int LINKS = 8;
     float h = p.state ? p.state[i] : 0.0f;
-    for (int j = 0; j < sg.nseg; ++j) {
-        const float next = exp2_fast(s[(int64_t)j * p.D] * A) * h + e[j * DN];
-        e[j * DN] = h;
-        h = next;
+    for (int j0 = 0; j0 < sg.nseg; j0 += LINKS) {
+        float a[LINKS], v[LINKS];
+#pragma unroll
+        for (int k = 0; k < LINKS; ++k) {
+            const int64_t j = min(j0 + k, sg.nseg - 1);
+            a[k] = s[j * p.D];
+            v[k] = e[j * DN];
+        }
+#pragma unroll
+        for (int k = 0; k < LINKS; ++k) {
+            if (j0 + k < sg.nseg) e[(j0 + k) * DN] = h;
+            h = exp2_fast(a[k] * A) * h + v[k];
+        }
     }
     float in = p.dstate_out ? p.dstate_out[i] : 0.0f;
-    for (int j = sg.nseg - 1; j >= 0; --j) {
-        const float next = exp2_fast(s[(int64_t)j * p.D] * A) * in + g[j * DN];
-        g[j * DN] = in;
-        in = next;
+    for (int j0 = sg.nseg - 1; j0 >= 0; j0 -= LINKS) {
+        float a[LINKS], v[LINKS];
+#pragma unroll
+        for (int k = 0; k < LINKS; ++k) {
+            const int64_t j = max(j0 - k, 0);
+            a[k] = s[j * p.D];
+            v[k] = g[j * DN];
+        }
+#pragma unroll
+        for (int k = 0; k < LINKS; ++k) {
+            if (j0 - k >= 0) g[(j0 - k) * DN] = in;
+            in = exp2_fast(a[k] * A) * in + v[k];
+        }
     }
 }
 
@@ -373,6 +398,7 @@ __global__ __launch_bounds__(64 * W) void scan_bwd_kernel(ScanProblem p, Segment
         f32x4 h0;
         float cum;
     };
+    constexpr int AHEAD = ahead(W);
     Raw raw[AHEAD];
     float xv[OWN], dv[OWN], sl[OWN], ge[OWN], zf[OWN];   // the current tile's own steps, for their finish
     auto fetch = [&](Raw& r, int t0) {                   // behind the first tile: the first
@@ -581,6 +607,7 @@ __global__ __launch_bounds__(256) void scan_sums_kernel(ScanProblem p, Ws ws, in
         float s = 0.0f;
         if (t < clamp_len(p.lengths, b, p.T)) {
             const float* src = (isc ? ws.pc : ws.pb) + i;
+#pragma unroll 8
             for (int cb = 0; cb < ncb; ++cb) s += src[cb * nbc];
         }
         const Rows& o = isc ? p.dcmat : p.dbmat;
@@ -590,6 +617,7 @@ __global__ __launch_bounds__(256) void scan_sums_kernel(ScanProblem p, Ws ws, in
     i -= 2 * nbc;
     if (i < na) {
         float s = 0.0f;
+#pragma unroll 8
         for (int r = 0; r < parts; ++r) s += ws.pa[r * na + i];
         p.da[i] = s;
         return;
