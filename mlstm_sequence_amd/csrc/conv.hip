@@ -17,6 +17,7 @@
 // B=6 T=1531 D=2048: 23 us against 17) and gain nothing on long ones.
 #include "act.hpp"
 #include "blocks.hpp"
+#include "sums.hpp"
 
 #include <type_traits>
 
@@ -305,26 +306,14 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvProblem p, ConvGeom g
     }
 }
 
-// dweight [D,K] and dbias [D] from the workgroups' sums [parts][K+1][D]: 64
-// columns and 16 slices of the parts to a workgroup.
+// dweight [D,K] and dbias [D] from the workgroups' sums [parts][K+1][D]
 __global__ __launch_bounds__(1024) void conv_params_kernel(const float* __restrict__ part, int64_t parts, int D, int K,
                                                            float* __restrict__ dweight, float* __restrict__ dbias)
 {
     __shared__ float red[16][64];
-    const int64_t n = (int64_t)(K + 1) * D, i = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
-    const int slice = threadIdx.x >> 6;
-    float s = 0.0f;
-    if (i < n) {
-#pragma unroll 4
-        for (int64_t r = slice; r < parts; r += 16) s += part[r * n + i];
-    }
-    red[slice][threadIdx.x & 63] = s;
-    for (int k = 8; k; k >>= 1) {
-        __syncthreads();
-        if (slice < k) red[slice][threadIdx.x & 63] += red[slice + k][threadIdx.x & 63];
-    }
-    if (slice || i >= n) return;
-    s = red[0][threadIdx.x];
+    const int64_t n = (int64_t)(K + 1) * D, i = (int64_t)blockIdx.x * 64 + threadIdx.x;
+    const float s = part_sum(part, parts, n, n, blockIdx.x, red);
+    if (threadIdx.x >= 64 || i >= n) return;
     const int j = (int)(i / D), c = (int)(i % D);
     if (j < K) dweight[(size_t)c * K + j] = s;
     else if (dbias) dbias[c] = s;

@@ -26,6 +26,7 @@
 // the channels.  Segments cost it next to nothing, so there are enough of
 // them to fill the chip.
 #include "scan_impl.hpp"
+#include "sums.hpp"
 
 #include <type_traits>
 
@@ -54,15 +55,16 @@ struct Ws {
     size_t bytes;
 };
 
-// Segments of whole tiles, 64 steps at least.  Two waves of pass 3 fit a SIMD (registers): from there on (2048) one
-// segment, which saves pass 1 its adjoint (B=8 T=2048 D=4096 N=16: 1169 us against 1189 with four), below it enough
-// for 4096 waves.
+// Segments of whole tiles, 32 steps at least (B=3 T=619 D=1000 G=2 N=8: 63 us; 64 at least: 75).  Two waves of pass 3
+// fit a SIMD (registers): from there on (2048) one segment, which saves pass 1 its adjoint (B=8 T=2048 D=4096 N=16:
+// 1169 us against 1189 with four), below it enough for 4096 waves; 2048 where a wave is alone in its workgroup and
+// fills a SIMD's registers (B=4 T=1024 D=2048 N=4: 101 us, with 4096 waves 128).
 Segments segments_of(const ScanProblem& p)
 {
     const int64_t waves = (int64_t)p.B * channel_blocks(p) * waves_of(p.N);
     const int tiles = (p.T + kTile - 1) / kTile;
-    int64_t n = waves >= 2048 ? 1 : 4096 / waves;
-    if (n > p.T / 64) n = p.T / 64;
+    int64_t n = waves >= 2048 ? 1 : (waves_of(p.N) == 1 ? 2048 : 4096) / waves;
+    if (n > p.T / 32) n = p.T / 32;
     if (n < 1) n = 1;
     const int per = (int)((tiles + n - 1) / n);
     return Segments{per * kTile, (tiles + per - 1) / per};
@@ -592,46 +594,47 @@ __global__ __launch_bounds__(64 * W) void scan_bwd_kernel(ScanProblem p, Segment
 }
 
 // Pass 4: dB and dC over the blocks of channels (rows behind a sequence are
-// 0), dA, dskip and ddt_bias over segments and sequences.
-template <typename T>
-__global__ __launch_bounds__(256) void scan_sums_kernel(ScanProblem p, Ws ws, int ncb, int parts)
+// 0), a thread an element; dA, dskip and ddt_bias over segments and
+// sequences, 64 columns to a workgroup.  I: the type that counts dB's and dC's
+// elements (a division in 64 bits costs more than the sum).
+template <typename T, typename I>
+__global__ __launch_bounds__(1024) void scan_sums_kernel(ScanProblem p, Ws ws, int ncb, int parts)
 {
-    const int64_t GN = (int64_t)p.G * p.N, rows = (int64_t)p.B * p.T;
-    const int64_t nbc = rows * GN, na = (int64_t)p.D * p.N;
-    int64_t i = block_id() * 256 + threadIdx.x;
-    if (i < 2 * nbc) {
+    __shared__ float red[16][64];
+    const I GN = (I)(p.G * p.N), nbc = (I)p.B * (I)p.T * GN;
+    const int64_t na = (int64_t)p.D * p.N, first = (2 * (int64_t)nbc + 1023) / 1024, da = (na + 63) / 64, dd = (p.D + 63) / 64;
+    int64_t blk = block_id();
+    if (blk < first) {
+        I i = (I)blk * 1024 + threadIdx.x;
+        if (i >= 2 * nbc) return;
         const bool isc = i >= nbc;
         if (isc) i -= nbc;
-        const int64_t r = i / GN, k = i % GN;
-        const int b = (int)(r / p.T), t = (int)(r % p.T);
+        const I r = i / GN;
+        const int k = (int)(i % GN), b = (int)(r / (I)p.T), t = (int)(r % (I)p.T);
         float s = 0.0f;
         if (t < clamp_len(p.lengths, b, p.T)) {
             const float* src = (isc ? ws.pc : ws.pb) + i;
 #pragma unroll 8
-            for (int cb = 0; cb < ncb; ++cb) s += src[cb * nbc];
+            for (int cb = 0; cb < ncb; ++cb) s += src[(size_t)cb * nbc];
         }
         const Rows& o = isc ? p.dcmat : p.dbmat;
         ((T*)o.p)[b * o.batch + t * o.row + k] = from_float<T>(s);
         return;
     }
-    i -= 2 * nbc;
-    if (i < na) {
-        float s = 0.0f;
-#pragma unroll 8
-        for (int r = 0; r < parts; ++r) s += ws.pa[r * na + i];
-        p.da[i] = s;
-        return;
+    blk -= first;
+    const float* part = ws.pa;
+    float* out = p.da;
+    int64_t n = na;
+    if (blk >= da) {
+        blk -= da;
+        n = p.D;
+        part = blk < dd ? ws.pskip : ws.pbias;
+        out = blk < dd ? p.dskip : p.ddt_bias;
+        if (blk >= dd) blk -= dd;
+        if (blk >= dd) return;   // behind the last workgroup
     }
-    i -= na;
-    if (i < p.D) {
-        float s = 0.0f, u = 0.0f;
-        for (int r = 0; r < parts; ++r) {
-            s += ws.pskip[(int64_t)r * p.D + i];
-            u += ws.pbias[(int64_t)r * p.D + i];
-        }
-        if (p.dskip) p.dskip[i] = s;
-        if (p.ddt_bias) p.ddt_bias[i] = u;
-    }
+    const float s = part_sum(part, parts, n, n, blk, red);
+    if (threadIdx.x < 64 && out && blk * 64 + threadIdx.x < n) out[blk * 64 + threadIdx.x] = s;
 }
 
 template <typename T, int W>
@@ -655,8 +658,11 @@ hipError_t bwd_w(const ScanProblem& p, hipStream_t stream)
     if (p.z.p) scan_bwd_kernel<T, W, true><<<blocks, 64 * W, 0, stream>>>(p, sg, ws, nblk);
     else scan_bwd_kernel<T, W, false><<<blocks, 64 * W, 0, stream>>>(p, sg, ws, nblk);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    const int64_t n = 2 * (int64_t)p.B * p.T * p.G * p.N + (int64_t)p.D * p.N + p.D;
-    scan_sums_kernel<T><<<grid_of((n + 255) / 256), 256, 0, stream>>>(p, ws, (p.D / p.G + 63) / 64, p.B * sg.nseg);
+    const int64_t nbc = (int64_t)p.B * p.T * p.G * p.N;
+    const dim3 grid = grid_of((2 * nbc + 1023) / 1024 + ((int64_t)p.D * p.N + 63) / 64 + 2 * ((p.D + 63) / 64));
+    const int ncb = (p.D / p.G + 63) / 64, parts = p.B * sg.nseg;
+    if (nbc < (int64_t(1) << 30)) scan_sums_kernel<T, uint32_t><<<grid, 1024, 0, stream>>>(p, ws, ncb, parts);
+    else scan_sums_kernel<T, uint64_t><<<grid, 1024, 0, stream>>>(p, ws, ncb, parts);
     return hipGetLastError();
 }
 
