@@ -419,7 +419,10 @@ int tfla_dbg_set_knob(int knob, int value);
  * 0, states are those after the last row, a sequence of length 0 keeps its
  * state.
  *
- * All calls are deterministic: the same arguments give the same bits.
+ * The conventions at the top of this file hold (streams, errors, no pointer
+ * kept; the tensors' device must be current), except that alignment is as
+ * said here.  All calls are deterministic: the same arguments give the same
+ * bits, whatever else runs; two calls at once need workspaces of their own.
  */
 typedef struct tfla_rows {
     void* data;
@@ -553,6 +556,9 @@ int tfla_scan_bwd(const tfla_scan_args* args, void* workspace, size_t workspace_
  *   mean, rstd   fp32 [B,T,G] ([B,G] with TFLA_NORM_SEQUENCE): outputs of the forward pass
  *                (or NULL), inputs of the backward pass
  *   flags        TFLA_IO_BF16 and/or TFLA_NORM_SEQUENCE
+ *
+ * There are no lengths here: every row counts, and where rows are padding
+ * their dy should be 0 (and finite gates leave their gradients 0).
  *
  * Backward: from dy and the saved mean and rstd the gradients dx, dgate
  * (given exactly when gate is), dweight and dbias (given exactly when weight

@@ -1,5 +1,6 @@
 """libtfla: chunkwise-parallel gated linear attention forward (mLSTMsig,
-fixed per-head decay, per-key-channel gate) on AMD gfx950.
+fixed per-head decay, per-key-channel gate) on AMD gfx950, and the operators
+around it: causal convolution, selective scan, group norm with a gate.
 
 The compute path is the C-ABI library ``libtfla.so`` built from ``csrc/``;
 :mod:`mlstm_sequence_amd.tfla` is its ctypes binding.
