@@ -4,14 +4,13 @@
 //   delta_t = softplus(dt_t + dt_bias),   a_t = exp(delta_t A[c,n])
 //   h_t = a_t h_{t-1} + delta_t x_t B_t[n],   y_t = sum_n C_t[n] h_t + skip x_t
 //
-// Lanes are channels: a workgroup owns 64 channels of one group and one
-// sequence, and its W waves split the N states, kStates to a wave, held in
-// fp32 registers along the whole walk.  B_t and C_t are then the same for
-// every lane of a wave: they are read by scalar loads and enter the products
-// as scalar operands, at no cost in vector registers or vector loads.  What
-// belongs to a channel and a step alone (softplus, the gate, their gradients)
-// is done once, by the wave that owns the step in the tile, and handed to the
-// others through LDS.
+// Lanes are channels: a workgroup owns 64 channels of one group and a segment
+// of one sequence, and its W waves split the N states, kStates to a wave, held
+// in fp32 registers along the whole walk.  B_t and C_t are then the same for
+// every lane of a wave: one LDS read of four values serves 64 x 4 states.
+// What belongs to a channel and a step alone (softplus, the gate, their
+// gradients) is done once, by the wave that owns the step in the tile, and
+// handed to the others through LDS.
 #pragma once
 
 #include "act.hpp"
@@ -22,39 +21,7 @@ namespace scan {
 
 constexpr int kStates = 4;    // states of a wave
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef f32x4 f32x4u __attribute__((aligned(4)));   // four states of the caller's arrays
-
-// kStates values of B or C at a wave-uniform address: scalar loads (the data
-// is read-only during the launch), unpacked by the scalar unit.
-template <typename T> struct Uniform4;
-template <> struct Uniform4<bf16> {
-    u32x2 r;
-    __device__ __forceinline__ void load(const bf16* p)
-    {
-        typedef const u32x2 __attribute__((address_space(4), aligned(4))) cvec;
-        r = *(cvec*)(uintptr_t)p;
-    }
-    __device__ __forceinline__ float get(int n) const
-    {
-        const uint32_t w = n < 2 ? r[0] : r[1];
-        return __builtin_bit_cast(float, (n & 1) ? w & 0xffff0000u : w << 16);
-    }
-};
-template <> struct Uniform4<float> {
-    u32x4 r;
-    __device__ __forceinline__ void load(const float* p)
-    {
-        typedef const u32x4 __attribute__((address_space(4), aligned(4))) cvec;
-        r = *(cvec*)(uintptr_t)p;
-    }
-    __device__ __forceinline__ float get(int n) const
-    {
-        const uint32_t w = r[n];
-        return __builtin_bit_cast(float, w);
-    }
-};
 
 // ns <= kStates states of a channel, the rest 0 (ns <= 0: none).
 __device__ __forceinline__ f32x4 load_states(const float* p, int ns)
