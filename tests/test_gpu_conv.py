@@ -217,3 +217,7 @@ def test_many_short_sequences():
     """More sequences than a run of rows is long, one and two rows each."""
     for T in (1, 2):
         check(BF, 700, T, 72, 4, lengths=[T * (i % 3 > 0) for i in range(700)])
+
+
+def test_a_very_long_sequence():
+    check(F32, 1, 30000, 3, 4)

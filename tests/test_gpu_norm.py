@@ -304,3 +304,8 @@ def test_offsets_beyond_32_bits():
         g = tfla.norm_backward(x, x, m, r, act=tfla.ACT_SILU, over=over)[0]
         assert torch.equal(tfla.norm_backward(view, view, m, r, act=tfla.ACT_SILU, over=over, dx=out)[0], g)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_very_long_sequence(dtype):
+    check(dtype, 1, 100000, 2, 8, sequence=True)

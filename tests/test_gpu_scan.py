@@ -291,3 +291,7 @@ def test_many_short_sequences(T):
 def test_every_segment_of_a_padded_batch(dtype):
     """Sequences that end in the first, a middle and the last of many segments, one of them empty."""
     check(dtype, 4, 1030, 33, 16, lengths=[1030, 0, 65, 500])
+
+
+def test_a_very_long_sequence():
+    check(F32, 1, 20000, 5, 3)
