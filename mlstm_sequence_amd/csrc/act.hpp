@@ -31,7 +31,8 @@ __device__ __forceinline__ float softplus_of(float u, float y)
 {
     constexpr float kLn2 = 0.6931471805599453f;
     const float v = 1.0f + y;
-    return fmaxf(u, 0.0f) + fmaf(__builtin_amdgcn_logf(v), kLn2, y - (v - 1.0f));
+    // the median of u, 0 and infinity is max(u, 0) in one instruction; a NaN comes back through y
+    return __builtin_amdgcn_fmed3f(u, 0.0f, __builtin_inff()) + fmaf(__builtin_amdgcn_logf(v), kLn2, y - (v - 1.0f));
 }
 __device__ __forceinline__ float softplus_f(float u) { return softplus_of(u, exp_f(-fabsf(u))); }
 

@@ -38,8 +38,10 @@ struct SegWs {
 };
 
 // OUT: the outputs; else the end state and the sum of the steps.  GATED: y times z sigmoid(z).
+// Four waves to a SIMD are asked for (16 waves fill it as they are): left alone, the gated kernel takes 166
+// registers and three fit.
 template <typename T, int W, bool OUT, bool GATED>
-__global__ __launch_bounds__(64 * W) void scan_fwd_kernel(ScanProblem p, Segments sg, SegWs ws)
+__global__ __launch_bounds__(64 * W, W == 16 ? 1 : 4) void scan_fwd_kernel(ScanProblem p, Segments sg, SegWs ws)
 {
     constexpr int TS = tile_steps(W), OWN = TS / W;                       // steps of a tile that a wave prepares and finishes
     constexpr int NP = W * kStates, BC = OUT ? 2 : 1;  // states with padding; B alone, or B and C
@@ -60,19 +62,15 @@ __global__ __launch_bounds__(64 * W) void scan_fwd_kernel(ScanProblem p, Segment
     const unsigned c = q.c;
     const int own = q.wave * OWN;                     // the wave's steps of a tile: own .. own + OWN - 1
     // this thread's elements of the tile's B and C: element e of the tile is step, matrix, state in that order
-    const T* mp[PER];
-    int64_t mr[PER];
-    int ms[PER];
+    MatCursor<T> mat[PER];
     bool mv[PER];                                     // padding is 0
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
         const int e = threadIdx.x + k * 64 * W, n = e % NP, isc = e / NP % BC;
-        const Rows& m = isc ? p.cmat : p.bmat;
         mv[k] = n < p.N;
-        ms[k] = min(e / NP / BC, TS - 1);
-        mr[k] = m.row;
-        mp[k] = (const T*)m.p + q.b * m.batch + s0 * m.row + q.g * p.N + min(n, p.N - 1);
+        mat[k].set(isc ? p.cmat : p.bmat, q.b, s0, q.g * p.N + min(n, p.N - 1), min(e / NP / BC, TS - 1), 0, TS, len);
     }
+    const int softplus = __builtin_amdgcn_readfirstlane(p.softplus);
     const float skip = OUT && p.skip ? p.skip[q.c] : 0.0f;
     const float bias = p.dt_bias ? p.dt_bias[q.c] : 0.0f;
     const size_t srow = ((size_t)q.b * p.D + q.c) * p.N + n0;
@@ -110,13 +108,13 @@ __global__ __launch_bounds__(64 * W) void scan_fwd_kernel(ScanProblem p, Segment
             if (GATED) r.z[i] = (zp + t * p.z.row)[c];
         }
 #pragma unroll
-        for (int k = 0; k < PER; ++k) r.m[k] = mp[k][min(t0 + ms[k], len - 1) * mr[k]];
+        for (int k = 0; k < PER; ++k) r.m[k] = mat[k].next(t0, len);
     };
     auto publish = [&](const Raw& r, int t0, int buf) {
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
             const float u = to_float(r.dt[i]) + bias;
-            const float d = p.softplus ? softplus_t<T>(u) : u;
+            const float d = softplus ? softplus_t<T>(u) : u;
             du[buf][own + i][q.lane] = f32x2{d, d * to_float(r.x[i])};   // behind the end: never read
             if (!OUT && t0 + own + i < len) dsum += d;
         }

@@ -136,6 +136,14 @@ template <typename T, int W> struct Walk {
         mr = m.row;
         mp = (const T*)m.p + q.b * m.batch + s0 * m.row + q.g * p.N + min(n, p.N - 1);
     }
+    // the same, for tiles from t0 on, `tile` steps apart
+    __device__ __forceinline__ MatCursor<T> matrices(const ScanProblem& p, int t0, int tile) const
+    {
+        const int e = threadIdx.x, n = e % NP;
+        MatCursor<T> c;
+        c.set(e / NP % 2 ? p.cmat : p.bmat, q.b, s0, q.g * p.N + min(n, p.N - 1), e / NP / 2, t0, tile, len);
+        return c;
+    }
     // row t of the segment, the last one for rows behind the end: no branch stands around a load
     __device__ __forceinline__ int64_t row(int t) const { return min(t, len - 1); }
     __device__ __forceinline__ size_t tile0() const   // first tile of the segment among the sequence's, per block
@@ -178,6 +186,8 @@ __global__ __launch_bounds__(64 * W) void scan_tiles_kernel(ScanProblem p, Segme
     };
     constexpr int AHEAD = ahead(W);
     Raw raw[AHEAD];
+    MatCursor<T> mat = k.matrices(p, 0, TS);
+    const int softplus = __builtin_amdgcn_readfirstlane(p.softplus);
     auto fetch = [&](Raw& r, int t0) {
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
@@ -187,14 +197,14 @@ __global__ __launch_bounds__(64 * W) void scan_tiles_kernel(ScanProblem p, Segme
             if (ADJ) r.dy[i] = (k.gp + t * p.dy.row)[c];
             if (ADJ && GATED) r.z[i] = (k.zp + t * p.z.row)[c];
         }
-        r.m = k.mp[k.row(t0 + k.ms) * k.mr];
+        r.m = mat.next(t0, k.len);
     };
     auto publish = [&](const Raw& r) {
         if (k.mine) {
 #pragma unroll
             for (int i = 0; i < OWN; ++i) {
                 const float u = to_float(r.dt[i]) + bias;
-                const float d = p.softplus ? softplus_t<T>(u) : u;
+                const float d = softplus ? softplus_t<T>(u) : u;
                 du[k.own + i][q.lane] = f32x2{d, d * to_float(r.x[i])};
                 if (ADJ) {
                     float g = to_float(r.dy[i]);

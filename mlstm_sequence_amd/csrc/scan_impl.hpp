@@ -46,6 +46,30 @@ __device__ __forceinline__ int clamp_len(const int* lengths, int b, int T)
     return lengths ? min(max(lengths[b], 0), T) : T;
 }
 
+// A lane's element of each tile's B or C, tile after tile: `at` its row of the tile fetched next, `last` the
+// segment's last row, read in the place of rows behind it.  Stepping the pointer costs a quarter of the 64-bit
+// product that a row number would need in every tile.
+template <typename T> struct MatCursor {
+    const T *at, *last;
+    int64_t step;      // elements from tile to tile
+    int s;             // the element's step within a tile
+    // element (b, first + t0 + s, column): `first` the segment's first row, tiles from t0 on, `tile` steps apart
+    __device__ __forceinline__ void set(const Rows& m, int b, int first, int column, int step_of, int t0, int tile, int len)
+    {
+        const T* base = (const T*)m.p + b * m.batch + first * m.row + column;
+        s = step_of;
+        at = base + (int64_t)(t0 + s) * m.row;
+        last = base + (int64_t)max(len - 1, 0) * m.row;
+        step = tile * m.row;
+    }
+    __device__ __forceinline__ T next(int t0, int len)
+    {
+        const T v = *(t0 + s < len ? at : last);
+        at += step;
+        return v;
+    }
+};
+
 // How a sequence is cut: nseg segments of len steps (a multiple of the tile),
 // walked by workgroups of their own.
 struct Segments {
