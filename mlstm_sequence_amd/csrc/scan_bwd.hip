@@ -21,9 +21,11 @@
 // its own sums, and pass 4 adds blocks, segments and sequences in a fixed
 // order.
 //
-// The arithmetic bounds pass 3: of about 100 issue slots that a wave spends
-// on a step of its four states, 20 recompute, 32 run the adjoint, 18 sum over
-// the channels.  Segments cost it next to nothing, so there are enough of
+// The arithmetic bounds pass 3: of 106 issue slots that a wave spends on a
+// step of its four states, about 20 recompute, 32 run the adjoint and 18 sum
+// over the channels.  B=4 T=2048 D=4096 N=16 bf16 with a gate: 611 to 616 us
+// for the call; profiled apart pass 1 takes 186 us with 88 % of the issue
+// slots taken, pass 3 498 with 82 %.  Segments cost it next to nothing, so there are enough of
 // them to fill the chip.
 #include "scan_impl.hpp"
 #include "sums.hpp"
@@ -38,7 +40,8 @@ using namespace scan;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kVm0 = 0x0f70;   // s_waitcnt: no vector load outstanding
 // Tiles whose inputs are under way: two, but one where the registers are short (16 waves: 128 each; one wave: a whole
-// tile's steps to prepare), N=64 288 against 278 us, N=4 135 against 103.
+// tile's steps to prepare), N=64 (B=2 T=1024 D=1024) 287 us with two against 253, N=4 (B=4 T=1024
+// D=2048) 121 against 88.
 constexpr int ahead(int W) { return W == 1 || W == 16 ? 1 : 2; }
 constexpr int kTile = 8;       // steps of a tile: its states and decays take 16 registers a step pair
 
@@ -55,10 +58,10 @@ struct Ws {
     size_t bytes;
 };
 
-// Segments of whole tiles, 32 steps at least (B=3 T=619 D=1000 G=2 N=8: 63 us; 64 at least: 75).  Two waves of pass 3
+// Segments of whole tiles, 32 steps at least (B=3 T=619 D=1000 G=2 N=8: 50 us; 64 at least: 67).  Two waves of pass 3
 // fit a SIMD (registers): from there on (2048) one segment, which saves pass 1 its adjoint (B=8 T=2048 D=4096 N=16:
-// 1169 us against 1189 with four), below it enough for 4096 waves; 2048 where a wave is alone in its workgroup and
-// fills a SIMD's registers (B=4 T=1024 D=2048 N=4: 101 us, with 4096 waves 128).
+// 1164 us against 1172 with four), below it enough for 4096 waves; 2048 where a wave is alone in its workgroup and
+// fills a SIMD's registers (B=4 T=1024 D=2048 N=4: 88 us, with 4096 waves 93).
 Segments segments_of(const ScanProblem& p)
 {
     const int64_t waves = (int64_t)p.B * channel_blocks(p) * waves_of(p.N);
