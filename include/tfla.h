@@ -495,7 +495,8 @@ int tfla_conv_bwd(const tfla_conv_args* args, void* workspace, size_t workspace_
  * the last row and may be `state` itself (updated in place), so the same call
  * serves prompts and single tokens (T = 1).  States are fp32 throughout.
  *
- *   B, T, D >= 1, B T <= 2^30, B D < 2^27; G divides D; N 1 to 64
+ *   B, T, D >= 1, B T <= 2^30; G divides D; N 1 to 64; B G ceil(D / G / 64) < 2^21, the blocks of
+ *   64 channels of a group (B D < 2^27 where groups are whole blocks)
  *   x, dt, z, y   [B,T,D], z.data NULL for no gate; dt is x's type
  *   bmat, cmat    [B,T,G,N], the last two dimensions contiguous
  *   a [D,N], skip [D] or NULL, dt_bias [D] or NULL, state, state_out [B,D,N] or NULL: fp32

@@ -322,7 +322,7 @@ int check_scan_sizes(int B, int T, int D, int N, int G, int flags, tfla::ScanPro
     if (D > (1 << 24)) return fail(TFLA_ERR_UNSUPPORTED, "D must be <= 2^24");
     // workgroups of up to 1024 threads, a grid below 2^32 of them
     if ((int64_t)B * G * ((D / G + 63) / 64) >= (1 << 21))
-        return fail(TFLA_ERR_UNSUPPORTED, "B*D too large: at most 2^21 blocks of 64 channels of a group");
+        return fail(TFLA_ERR_UNSUPPORTED, "B*D too large: blocks of 64 channels of a group must be below 2^21");
     *p = tfla::ScanProblem{};
     p->B = B;
     p->T = T;

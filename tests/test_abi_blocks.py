@@ -164,6 +164,18 @@ def test_scan_bwd_refuses(kw, code):
     assert tfla.tfla_last_error()
 
 
+@pytest.mark.parametrize("B,D,G,fits", [
+    (1, (1 << 24), 1, True), (8, (1 << 24), 1, False), (7, (1 << 24), 1, True),
+    (1, (1 << 21) - 1, (1 << 21) - 1, True), (1, 1 << 21, 1 << 21, False),   # one channel a group: a block each
+    (4, 65 << 13, 1 << 13, True), (128, 65 << 13, 1 << 13, False),           # 65 channels a group: two blocks each
+])
+def test_scan_blocks_of_channels(B, D, G, fits):
+    L = tfla.lib()
+    assert (L.tfla_scan_bwd_workspace_bytes(B, 64, D, 4, G, BF16) > 0) == fits
+    if not fits:
+        assert L.tfla_scan_fwd(ctypes.byref(scan_args(B=B, D=D, G=G)), None, 0, None) == UNSUPPORTED
+
+
 def test_scan_workspace():
     L = tfla.lib()
     n = L.tfla_scan_bwd_workspace_bytes(2, 300, 128, 16, 2, BF16)
