@@ -58,10 +58,11 @@ struct Ws {
     size_t bytes;
 };
 
-// Segments of whole tiles, 32 steps at least (B=3 T=619 D=1000 G=2 N=8: 50 us; 64 at least: 67).  Two waves of pass 3
-// fit a SIMD (registers): from there on (2048) one segment, which saves pass 1 its adjoint (B=8 T=2048 D=4096 N=16:
-// 1164 us against 1172 with four), below it enough for 4096 waves; 2048 where a wave is alone in its workgroup and
-// fills a SIMD's registers (B=4 T=1024 D=2048 N=4: 88 us, with 4096 waves 93).
+// Segments of whole tiles, 32 steps at least (B=3 T=619 D=1000 G=2 N=8: 51 us; 64 at least: 67, 16 at least: 47, but
+// B=1 T=512 D=2048 N=16 52 for 47).  Two waves of pass 3 fit a SIMD (registers): from there on (2048) one segment,
+// which saves pass 1 its adjoint (B=8 T=2048 D=4096 N=16: 1164 us against 1172 with four), below it enough for 4096
+// waves (B=1 T=2048 D=2048 N=16: 107 us, for 8192 116, though B=4 T=2048 D=4096 gains, 608 for 617); 2048 where a
+// wave is alone in its workgroup and fills a SIMD's registers (B=4 T=1024 D=2048 N=4: 88 us, with 4096 waves 93).
 Segments segments_of(const ScanProblem& p)
 {
     const int64_t waves = (int64_t)p.B * channel_blocks(p) * waves_of(p.N);
