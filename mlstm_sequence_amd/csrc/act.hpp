@@ -7,18 +7,19 @@
 
 namespace tfla {
 
-// e^x.  The product x log2(e) is carried in two parts, so the result keeps
-// its relative accuracy (about 3 half-steps) at any size of x; without the
-// low part the error would grow with |x|.  Infinities and NaN go through.
+// e^x.  The product x log2(e) is carried in two parts, so every normal
+// result keeps its relative accuracy (about 3 half-steps); without the low
+// part the error would grow with |x|.  The low part is used where 2^p is
+// finite and not 0 only: an infinity times it, or times 0, would be NaN.
+// Beyond stand infinity (x above 88.7), 0 and NaN as they come.
 __device__ __forceinline__ float exp_f(float x)
 {
     constexpr float kLn2 = 0.6931471805599453f;
     constexpr float kLog2eLow = 1.9259629911266175e-08f;   // log2(e) - (float)log2(e)
     const float p = x * kLog2e;
-    float lo = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -p));
-    lo = fabsf(p) < 256.0f ? lo * kLn2 : 0.0f;
+    const float lo = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -p)) * kLn2;
     const float e = exp2_fast(p);
-    return fmaf(e, lo, e);
+    return fabsf(p) < 128.0f ? fmaf(e, lo, e) : e;
 }
 
 __device__ __forceinline__ float sigmoid_f(float u) { return __builtin_amdgcn_rcpf(1.0f + exp_f(-u)); }
