@@ -3,13 +3,16 @@ causal depthwise convolution, selective state space scan, and group norm with
 an activation or a gate; :mod:`mlstm_sequence_amd.tfla` offers the same names.
 
 Argument checks, output allocation and marshalling only; the work runs in the
-library's HIP kernels on torch's current stream of the tensors' device (or the
-given one).  Activations are [B,T,...] with contiguous channels and any batch
-and row strides, so views of projections need no copy; a tensor that does not
-fit is refused, never copied.
+library's HIP kernels on torch's current stream of the tensors' device, or with
+``stream`` as under ``torch.cuda.stream(stream)``: outputs and workspaces are
+allocated there, and the caller orders what other streams do with the tensors
+(and records those streams on them).  Activations are [B,T,...] with contiguous
+channels and any batch and row strides, so views of projections need no copy; a
+tensor that does not fit is refused, never copied.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import struct
 from typing import NamedTuple, Optional
@@ -153,14 +156,41 @@ def _rows(t, name, shape, dtype, dev):
     return t.data_ptr(), st[0], st[1]
 
 
-def _call(name, packed, dev, stream, nbytes=None, workspace=None):
-    """Calls entry point ``name`` on ``stream`` (None: the device's current
-    one) with the tensors' device current; ``nbytes``: the workspace it needs."""
+# the current stream's handle without a Stream object around it, where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+_HERE = contextlib.nullcontext()
+
+
+def _current(stream, x):
+    """Context with ``stream`` (a torch stream, a raw handle, or None for the
+    current one) as the current stream of the device of ``x``, for all that a
+    call allocates: memory of another stream could still be in use by that
+    stream's pending work when a kernel writes it, and be handed out there
+    again before the kernel is done."""
+    if stream is None or not getattr(x, "is_cuda", False):   # tensors elsewhere are refused by the checks
+        return _HERE
+    dev = x.get_device()
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device_index != dev:
+            raise ValueError(f"stream is on {stream.device}, tensors on cuda:{dev}")
+    elif handle <= 1:   # the null stream's two names
+        stream = torch.cuda.default_stream(dev)
+        handle = stream.cuda_stream
+    else:
+        stream = torch.cuda.ExternalStream(handle, device=dev)
+    return _HERE if handle == _raw_stream(dev) else torch.cuda.stream(stream)
+
+
+def _call(name, packed, dev, nbytes=None, workspace=None):
+    """Calls entry point ``name`` on the current stream of the tensors' device
+    with that device current; ``nbytes``: the workspace it needs."""
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return _call(name, packed, dev, stream, nbytes, workspace)
-    current = _raw_stream(dev)
-    s = current if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
+            return _call(name, packed, dev, nbytes, workspace)
+    s = _raw_stream(dev)
     if nbytes is None:
         rc = _fn[name](packed, s)
     else:
@@ -169,18 +199,13 @@ def _call(name, packed, dev, stream, nbytes=None, workspace=None):
             from . import tfla
             tfla._check_workspace(workspace, nbytes, torch.device("cuda", dev))
             at, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        elif nbytes and s == current:   # else the library allocates, in that stream's order
+        elif nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
             at, size = workspace.data_ptr(), nbytes
         rc = _fn[name](packed, at, size, s)
     if rc:
         from . import tfla
         tfla._check(rc, name)
-
-
-# the current stream's handle without a Stream object around it, where torch offers that
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 # ---- causal convolution --------------------------------------------------------
@@ -210,17 +235,18 @@ def conv_forward(x, weight, bias=None, act: int = ACT_SILU, state=None, lengths=
     receives the last K-1 inputs, what the next call continues from.
     ``lengths`` int32 [B]: valid rows of each sequence of a padded batch."""
     _entry("tfla_conv_fwd")
-    a, dev, K = _conv_args(x, weight, bias, act, state, lengths)
-    shape, dtype = x.shape, x.dtype
-    B, _, D = shape
-    if y is None:
-        y = x.new_empty(shape)
-    if state_out is None and want_state:
-        state_out = x.new_empty((B, K - 1, D))
-    packed = _CONV.pack(*a, *_rows(y, "y", shape, dtype, dev),
-                        _flat(state_out, "state_out", (B, K - 1, D), dtype, dev), *_NO_ROWS, 0, *_NO_ROWS, 0, 0, 0)
-    _call("tfla_conv_fwd", packed, dev, stream)
-    return y, state_out
+    with _current(stream, x):
+        a, dev, K = _conv_args(x, weight, bias, act, state, lengths)
+        shape, dtype = x.shape, x.dtype
+        B, _, D = shape
+        if y is None:
+            y = x.new_empty(shape)
+        if state_out is None and want_state:
+            state_out = x.new_empty((B, K - 1, D))
+        packed = _CONV.pack(*a, *_rows(y, "y", shape, dtype, dev),
+                            _flat(state_out, "state_out", (B, K - 1, D), dtype, dev), *_NO_ROWS, 0, *_NO_ROWS, 0, 0, 0)
+        _call("tfla_conv_fwd", packed, dev)
+        return y, state_out
 
 
 def conv_backward(x, weight, dy, bias=None, act: int = ACT_SILU, state=None, lengths=None, dstate_out=None, dx=None,
@@ -229,19 +255,20 @@ def conv_backward(x, weight, dy, bias=None, act: int = ACT_SILU, state=None, len
     ``dstate_out``; returns ``(dx, dweight, dbias, dstate)``, dbias None
     without bias, dstate None without state."""
     need = _entry("tfla_conv_bwd_workspace_bytes")
-    a, dev, K = _conv_args(x, weight, bias, act, state, lengths)
-    shape, dtype = x.shape, x.dtype
-    B, T, D = shape
-    if dx is None:
-        dx = x.new_empty(shape)
-    dweight = torch.empty_like(weight)
-    dbias = None if bias is None else torch.empty_like(bias)
-    dstate = None if state is None else torch.empty_like(state)
-    packed = _CONV.pack(*a, *_NO_ROWS, 0, *_rows(dy, "dy", shape, dtype, dev),
-                        _flat(dstate_out, "dstate_out", (B, K - 1, D), dtype, dev),
-                        *_rows(dx, "dx", shape, dtype, dev), *map(_ptr, (dweight, dbias, dstate)))
-    _call("tfla_conv_bwd", packed, dev, stream, need(B, T, D, K, _IO[dtype]), workspace)
-    return dx, dweight, dbias, dstate
+    with _current(stream, x):
+        a, dev, K = _conv_args(x, weight, bias, act, state, lengths)
+        shape, dtype = x.shape, x.dtype
+        B, T, D = shape
+        if dx is None:
+            dx = x.new_empty(shape)
+        dweight = torch.empty_like(weight)
+        dbias = None if bias is None else torch.empty_like(bias)
+        dstate = None if state is None else torch.empty_like(state)
+        packed = _CONV.pack(*a, *_NO_ROWS, 0, *_rows(dy, "dy", shape, dtype, dev),
+                            _flat(dstate_out, "dstate_out", (B, K - 1, D), dtype, dev),
+                            *_rows(dx, "dx", shape, dtype, dev), *map(_ptr, (dweight, dbias, dstate)))
+        _call("tfla_conv_bwd", packed, dev, need(B, T, D, K, _IO[dtype]), workspace)
+        return dx, dweight, dbias, dstate
 
 
 def _ptr(t):
@@ -301,16 +328,18 @@ def scan_forward(x, dt, a, bmat, cmat, skip=None, z=None, dt_bias=None, softplus
     ``state_out`` (allocated with ``want_state``, may be ``state`` itself) the
     one after the last.  ``lengths`` int32 [B]: valid rows of a padded batch."""
     need = _entry("tfla_scan_workspace_bytes")
-    fields, sizes, dev = _scan_args(x, dt, a, bmat, cmat, skip, z, dt_bias, softplus, state, lengths)
-    B, T, D, N = sizes[:4]
-    if y is None:
-        y = x.new_empty(x.shape)
-    if state_out is None and want_state:
-        state_out = a.new_empty((B, D, N))
-    packed = _SCAN.pack(*fields, *_rows(y, "y", x.shape, x.dtype, dev),
-                        _flat(state_out, "state_out", (B, D, N), torch.float32, dev), *_NO_ROWS, 0, *_NO_ROWS * 5, 0, 0, 0, 0)
-    _call("tfla_scan_fwd", packed, dev, stream, need(*sizes), workspace)
-    return y, state_out
+    with _current(stream, x):
+        fields, sizes, dev = _scan_args(x, dt, a, bmat, cmat, skip, z, dt_bias, softplus, state, lengths)
+        B, T, D, N = sizes[:4]
+        if y is None:
+            y = x.new_empty(x.shape)
+        if state_out is None and want_state:
+            state_out = a.new_empty((B, D, N))
+        packed = _SCAN.pack(*fields, *_rows(y, "y", x.shape, x.dtype, dev),
+                            _flat(state_out, "state_out", (B, D, N), torch.float32, dev), *_NO_ROWS, 0,
+                            *_NO_ROWS * 5, 0, 0, 0, 0)
+        _call("tfla_scan_fwd", packed, dev, need(*sizes), workspace)
+        return y, state_out
 
 
 def scan_backward(x, dt, a, bmat, cmat, dy, skip=None, z=None, dt_bias=None, softplus: bool = True, state=None,
@@ -320,24 +349,25 @@ def scan_backward(x, dt, a, bmat, cmat, dy, skip=None, z=None, dt_bias=None, sof
     ``dstate_out``.  dx, ddt, dz, dbmat and dcmat may be given, as parts of
     a projection's gradient for instance."""
     need = _entry("tfla_scan_bwd_workspace_bytes")
-    fields, sizes, dev = _scan_args(x, dt, a, bmat, cmat, skip, z, dt_bias, softplus, state, lengths)
-    shape, dtype, bc = x.shape, x.dtype, bmat.shape
-    B, T, D, N = sizes[:4]
-    dx, ddt = (x.new_empty(shape) if t is None else t for t in (dx, ddt))
-    dbmat, dcmat = (x.new_empty(bc) if t is None else t for t in (dbmat, dcmat))
-    dz = None if z is None else x.new_empty(shape) if dz is None else dz
-    da = torch.empty_like(a)
-    dskip = None if skip is None else torch.empty_like(skip)
-    ddt_bias = None if dt_bias is None else torch.empty_like(dt_bias)
-    dstate = None if state is None else torch.empty_like(state)
-    packed = _SCAN.pack(*fields, *_NO_ROWS, 0, *_rows(dy, "dy", shape, dtype, dev),
-                        _flat(dstate_out, "dstate_out", (B, D, N), torch.float32, dev),
-                        *_rows(dx, "dx", shape, dtype, dev), *_rows(ddt, "ddt", shape, dtype, dev),
-                        *(_NO_ROWS if z is None else _rows(dz, "dz", shape, dtype, dev)),
-                        *_group_rows(dbmat, "dbmat", bc, dtype, dev), *_group_rows(dcmat, "dcmat", bc, dtype, dev),
-                        *map(_ptr, (da, dskip, ddt_bias, dstate)))
-    _call("tfla_scan_bwd", packed, dev, stream, need(*sizes), workspace)
-    return ScanGrads(dx, ddt, da, dbmat, dcmat, dskip, dz, ddt_bias, dstate)
+    with _current(stream, x):
+        fields, sizes, dev = _scan_args(x, dt, a, bmat, cmat, skip, z, dt_bias, softplus, state, lengths)
+        shape, dtype, bc = x.shape, x.dtype, bmat.shape
+        B, T, D, N = sizes[:4]
+        dx, ddt = (x.new_empty(shape) if t is None else t for t in (dx, ddt))
+        dbmat, dcmat = (x.new_empty(bc) if t is None else t for t in (dbmat, dcmat))
+        dz = None if z is None else x.new_empty(shape) if dz is None else dz
+        da = torch.empty_like(a)
+        dskip = None if skip is None else torch.empty_like(skip)
+        ddt_bias = None if dt_bias is None else torch.empty_like(dt_bias)
+        dstate = None if state is None else torch.empty_like(state)
+        packed = _SCAN.pack(*fields, *_NO_ROWS, 0, *_rows(dy, "dy", shape, dtype, dev),
+                            _flat(dstate_out, "dstate_out", (B, D, N), torch.float32, dev),
+                            *_rows(dx, "dx", shape, dtype, dev), *_rows(ddt, "ddt", shape, dtype, dev),
+                            *(_NO_ROWS if z is None else _rows(dz, "dz", shape, dtype, dev)),
+                            *_group_rows(dbmat, "dbmat", bc, dtype, dev), *_group_rows(dcmat, "dcmat", bc, dtype, dev),
+                            *map(_ptr, (da, dskip, ddt_bias, dstate)))
+        _call("tfla_scan_bwd", packed, dev, need(*sizes), workspace)
+        return ScanGrads(dx, ddt, da, dbmat, dcmat, dskip, dz, ddt_bias, dstate)
 
 
 # ---- group norm --------------------------------------------------------------------------
@@ -377,17 +407,18 @@ def norm_forward(x, weight=None, bias=None, eps: float = 1e-5, act: int = ACT_NO
     recurrences' head-major output h [B,H,T,d] goes in as
     ``h.transpose(1, 2)``; y is contiguous [B,T,G,C] unless given."""
     need = _entry("tfla_norm_workspace_bytes")
-    fields, sizes, dev = _norm_args(x, weight, bias, act, gate, over, eps)
-    B, T, G, C = shape = x.shape
-    if y is None:
-        y = x.new_empty(shape)
-    stats = (B, G) if over else (B, T, G)
-    mean = torch.empty(stats, dtype=torch.float32, device=x.device)
-    rstd = torch.empty_like(mean)
-    packed = _NORM.pack(*fields, mean.data_ptr(), rstd.data_ptr(), *_heads(y, "y", shape, x.dtype, dev),
-                        *_NO_HEADS * 3, 0, 0)
-    _call("tfla_norm_fwd", packed, dev, stream, need(*sizes), workspace)
-    return y, mean, rstd
+    with _current(stream, x):
+        fields, sizes, dev = _norm_args(x, weight, bias, act, gate, over, eps)
+        B, T, G, C = shape = x.shape
+        if y is None:
+            y = x.new_empty(shape)
+        stats = (B, G) if over else (B, T, G)
+        mean = torch.empty(stats, dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+        packed = _NORM.pack(*fields, mean.data_ptr(), rstd.data_ptr(), *_heads(y, "y", shape, x.dtype, dev),
+                            *_NO_HEADS * 3, 0, 0)
+        _call("tfla_norm_fwd", packed, dev, need(*sizes), workspace)
+        return y, mean, rstd
 
 
 def norm_backward(x, dy, mean, rstd, weight=None, bias=None, act: int = ACT_NONE, gate=None, over: int = NORM_TOKEN,
@@ -395,19 +426,20 @@ def norm_backward(x, dy, mean, rstd, weight=None, bias=None, act: int = ACT_NONE
     """Gradients of :func:`norm_forward` for ``dy`` from its mean and rstd;
     returns ``(dx, dgate, dweight, dbias)``, None where the input was None."""
     need = _entry("tfla_norm_bwd_workspace_bytes")
-    fields, sizes, dev = _norm_args(x, weight, bias, act, gate, over, 0.0)
-    B, T, G, C = shape = x.shape
-    dtype = x.dtype
-    if dx is None:
-        dx = x.new_empty(shape)
-    dgate = None if gate is None else x.new_empty(shape) if dgate is None else dgate
-    dweight = None if weight is None else torch.empty_like(weight)
-    dbias = None if bias is None else torch.empty_like(bias)
-    stats = (B, G) if over else (B, T, G)
-    packed = _NORM.pack(*fields, _flat(mean, "mean", stats, torch.float32, dev),
-                        _flat(rstd, "rstd", stats, torch.float32, dev), *_NO_HEADS,
-                        *_heads(dy, "dy", shape, dtype, dev), *_heads(dx, "dx", shape, dtype, dev),
-                        *(_NO_HEADS if gate is None else _heads(dgate, "dgate", shape, dtype, dev)),
-                        _ptr(dweight), _ptr(dbias))
-    _call("tfla_norm_bwd", packed, dev, stream, need(*sizes), workspace)
-    return dx, dgate, dweight, dbias
+    with _current(stream, x):
+        fields, sizes, dev = _norm_args(x, weight, bias, act, gate, over, 0.0)
+        B, T, G, C = shape = x.shape
+        dtype = x.dtype
+        if dx is None:
+            dx = x.new_empty(shape)
+        dgate = None if gate is None else x.new_empty(shape) if dgate is None else dgate
+        dweight = None if weight is None else torch.empty_like(weight)
+        dbias = None if bias is None else torch.empty_like(bias)
+        stats = (B, G) if over else (B, T, G)
+        packed = _NORM.pack(*fields, _flat(mean, "mean", stats, torch.float32, dev),
+                            _flat(rstd, "rstd", stats, torch.float32, dev), *_NO_HEADS,
+                            *_heads(dy, "dy", shape, dtype, dev), *_heads(dx, "dx", shape, dtype, dev),
+                            *(_NO_HEADS if gate is None else _heads(dgate, "dgate", shape, dtype, dev)),
+                            _ptr(dweight), _ptr(dbias))
+        _call("tfla_norm_bwd", packed, dev, need(*sizes), workspace)
+        return dx, dgate, dweight, dbias

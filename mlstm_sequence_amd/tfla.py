@@ -453,7 +453,8 @@ def forward(q, k, v, igate_pre, fgate_pre, gate: int, L: int, h=None, workspace=
     B, H, T, d_qk, d_hv = _dims(q, v)
     var = variant_of(gate, q.dtype)
     if h is None:
-        h = torch.empty((B, H, T, d_hv), dtype=q.dtype, device=q.device)
+        with _blocks._current(stream, q):   # of the stream that writes it
+            h = torch.empty((B, H, T, d_hv), dtype=q.dtype, device=q.device)
     if workspace is None:
         tfla_fwd(q, k, v, igate_pre, fgate_pre, h, B, H, T, d_qk, d_hv, L, var, stream)
     else:
@@ -467,9 +468,10 @@ def backward(q, k, v, igate_pre, fgate_pre, dh, gate: int, L: int, workspace=Non
     returns (dq, dk, dv, dig, dfg), dig None unless mLSTMsig."""
     B, H, T, d_qk, d_hv = _dims(q, v)
     var = variant_of(gate, q.dtype)
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    dig = torch.empty_like(igate_pre) if igate_pre is not None else None
-    dfg = torch.empty_like(fgate_pre)
+    with _blocks._current(stream, q):   # of the stream that writes them
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        dig = torch.empty_like(igate_pre) if igate_pre is not None else None
+        dfg = torch.empty_like(fgate_pre)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     tfla_bwd(q, k, v, igate_pre, fgate_pre, dh, dq, dk, dv, dig, dfg, B, H, T, d_qk, d_hv, L, var,
              workspace, nbytes, stream)

@@ -288,3 +288,42 @@ def test_packed_arguments_match_the_structures():
         raw = packed.pack(*values)
         for v, (off, kind) in zip(values, flat):
             assert kind.from_buffer_copy(raw, off).value == v
+
+
+class _OnGpu:
+    """What the stream rule asks of a tensor."""
+    is_cuda = True
+
+    def get_device(self):
+        return 0
+
+
+def test_a_given_stream_becomes_the_current_one(monkeypatch):
+    """All that a call allocates and launches follows: see tests/test_gpu_streams.py for the memory itself."""
+    import contextlib
+    entered = []
+
+    @contextlib.contextmanager
+    def on(s):
+        entered.append(s)
+        yield
+
+    class Stream:
+        def __init__(self, handle, device_index=0):
+            self.cuda_stream, self.device_index, self.device = handle, device_index, f"cuda:{device_index}"
+
+    monkeypatch.setattr(blocks, "_raw_stream", lambda dev: 0x50)
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda dev: Stream(0))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: Stream(handle, device))
+    x, side = _OnGpu(), Stream(0x90)
+    for given, handle in ((None, None), (0x50, None), (Stream(0x50), None), (side, 0x90), (0x90, 0x90), (0, 0), (1, 0)):
+        with blocks._current(given, x):
+            assert [s.cuda_stream for s in entered] == ([] if handle is None else [handle])
+        entered.clear()
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        blocks._current(Stream(0x90, 1), x)
+    with pytest.raises(ValueError, match="GPU memory"):
+        tfla.conv_forward(torch.zeros(2, 5, 8), torch.zeros(8, 4), stream=side)
+    assert not entered
