@@ -67,8 +67,11 @@ _fn = {}   # this module's entry points, once the library is loaded
 
 
 def bind(L):
-    """Argument types of this module's entry points."""
+    """Argument types of this module's entry points, which are offered all at
+    once: another thread may be on its first call."""
+    global _fn
     vp, sz = ctypes.c_void_p, ctypes.c_size_t
+    fn = {}
     for name, args, res in (
             ("tfla_conv_fwd", [vp, vp], _i),
             ("tfla_conv_bwd_workspace_bytes", [_i] * 5, sz),
@@ -83,7 +86,8 @@ def bind(L):
             ("tfla_norm_bwd", [vp, vp, sz, vp], _i)):
         f = getattr(L, name)
         f.argtypes, f.restype = args, res
-        _fn[name] = f
+        fn[name] = f
+    _fn = fn
 
 
 def _entry(name):

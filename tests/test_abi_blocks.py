@@ -327,3 +327,29 @@ def test_a_given_stream_becomes_the_current_one(monkeypatch):
     with pytest.raises(ValueError, match="GPU memory"):
         tfla.conv_forward(torch.zeros(2, 5, 8), torch.zeros(8, 4), stream=side)
     assert not entered
+
+
+def test_first_use_from_two_threads(monkeypatch):
+    """A thread that comes while another is still filling in the entry points finds none, or all."""
+    import threading
+    real, half, go = tfla.lib(), threading.Event(), threading.Event()
+
+    class Slow:
+        def __getattr__(self, name):
+            if name == "tfla_scan_bwd":
+                half.set()
+                go.wait(20)
+            return getattr(real, name)
+
+    monkeypatch.setattr(blocks, "_fn", {})
+    monkeypatch.setattr(tfla, "_lib", None)
+    first = threading.Thread(target=blocks.bind, args=(Slow(),))
+    first.start()
+    try:
+        assert half.wait(20)
+        assert blocks._entry("tfla_norm_bwd").restype is ctypes.c_int
+        assert blocks._fn["tfla_norm_fwd"] and blocks._fn["tfla_conv_fwd"]
+    finally:
+        go.set()
+        first.join()
+    assert len(blocks._fn) == 11
