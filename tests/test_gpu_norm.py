@@ -309,3 +309,65 @@ def test_offsets_beyond_32_bits():
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_a_very_long_sequence(dtype):
     check(dtype, 1, 100000, 2, 8, sequence=True)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_parameter_gradients_of_a_large_call(gated):
+    """dweight and dbias of a call whose loads go past the caches, against sums in 64 bits; bounds as in check()."""
+    B, T, G, C = 2, 8192, 32, 256
+    x, dy = (torch.randn(B, T, G, C, device="cuda", dtype=BF) for _ in range(2))
+    z = torch.randn(B, T, G, C, device="cuda", dtype=BF) if gated else None
+    w, b = torch.randn(G, C, device="cuda"), torch.randn(G, C, device="cuda")
+    kw = dict(act=tfla.ACT_SILU, gate=z)
+    _, mean, rstd = tfla.norm_forward(x, w, b, eps=EPS, **kw)
+    got = tfla.norm_backward(x, dy, mean, rstd, w, b, **kw)[2:]
+    want, off = (torch.zeros(2, G, C, dtype=torch.float64, device="cuda") for _ in range(2))
+    N, rows = (C + 60) * U, (B * T + 60) * U
+    W, bias = w.double(), b.double()
+    for i in range(B):
+        v, g = x[i].double(), dy[i].double()
+        m = v.mean(-1, keepdim=True)
+        var = ((v - m) ** 2).mean(-1, keepdim=True)
+        r = 1.0 / (var + EPS).sqrt()
+        xh = (v - m) * r
+        em = N * v.abs().mean(-1, keepdim=True)
+        er = 0.5 * (2 * N * var + 4 * var.sqrt() * em + em ** 2) / (var + EPS) + 4 * U
+        exh = r * (2 * U * (v.abs() + m.abs()) + em) + xh.abs() * er
+        u = xh * W + bias
+        at = z[i].double() if gated else u
+        s = torch.sigmoid(at)
+        if gated:
+            du = g * at * s
+            edu = 13 * U * du.abs()
+        else:
+            du = g * s * (1 + at * (1 - s))
+            edu = g.abs() * (0.5 * (W.abs() * exh + 3 * U * ((xh * W).abs() + bias.abs())) + 12 * U)
+        want[0] += (du * xh).sum(0)
+        want[1] += du.sum(0)
+        off[0] += (edu * xh.abs() + du.abs() * exh + rows * (du * xh).abs()).sum(0)
+        off[1] += (edu + rows * du.abs()).sum(0)
+    torch.cuda.synchronize()
+    for name, p, q, tol in zip(("dweight", "dbias"), got, want, off):
+        assert float(tol.max()) < 0.1 * float(q.abs().max()), name   # the bound tells a wrong sum from a right one
+        within(name, p, q.cpu().numpy(), tol.cpu().numpy())
+
+
+# rows of more than 1024 vectors, or single elements, go through memory; their weights' gradients in runs of 64 tokens
+@pytest.mark.parametrize("dtype,C", [(BF, 1025), (BF, 1031), (BF, 8200), (F32, 1031), (F32, 4100)])
+@pytest.mark.parametrize("kind,gated", [("none", False), ("sigmoid", False), ("silu", True), ("sigmoid", True), ("none", True)])
+@pytest.mark.parametrize("B,T", [(1, 64), (1, 65), (2, 65)])
+def test_rows_walked_from_memory(dtype, C, kind, gated, B, T):
+    check(dtype, B, T, 2, C, kind=kind, gated=gated)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("C", [1024, 1032, 2048])
+@pytest.mark.parametrize("gated", [False, True])
+def test_wide_rows_without_wide_alignment(dtype, C, gated):
+    """Single elements where rows are one element longer: a workgroup's registers up to 1024, memory beyond."""
+    check(dtype, 2, 33, 2, C, gated=gated, layout="odd")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_walked_from_memory_without_weights(dtype):
+    check(dtype, 2, 40, 1, 8200, affine=False, gated=dtype == BF)
