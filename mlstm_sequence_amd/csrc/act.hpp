@@ -38,7 +38,9 @@ __device__ __forceinline__ float softplus_of(float u, float y)
 __device__ __forceinline__ float softplus_f(float u) { return softplus_of(u, exp_f(-fabsf(u))); }
 
 // The same for bf16 data, whose own half step (2^-8) is far above the
-// exponential's error of |x| 2^-24 without the product's low part.
+// exponential's error of |x| 2^-24 without the product's low part.  fp32
+// results of bf16 data (weights' gradients, states) carry that error too,
+// below what the data's half steps leave in them.
 __device__ __forceinline__ float sigmoid_fast(float u)
 {
     return __builtin_amdgcn_rcpf(1.0f + exp2_fast(u * -kLog2e));

@@ -150,8 +150,10 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormProblem p, TokenMap m
     }
 }
 
-// Rows of any length: dx and dgate by a workgroup to a row, the weights' gradients by a thread to a column and a
-// run of tokens.
+// Rows of any length: dx and dgate by a workgroup to a row in two readings, the weights' gradients by a thread to a
+// column and a run of tokens in a third.  Gated, bf16 [4092,8200] 332 us, where [4096,8192] takes 143 in registers
+// (2.3 TB/s: four vectors a lane take all of them, one wave to a SIMD; [8192,4096] 95); fp32 [8184,4100] 454,
+// [8192,4096] 159.
 constexpr int kLongRun = 64;
 
 template <typename T> struct Elem1 {

@@ -140,7 +140,8 @@ inline bool fits(const Heads& h, const NormProblem& p, size_t bytes)
                     (p.T == 1 || h.row * e % bytes == 0) && (p.G == 1 || h.group * e % bytes == 0));
 }
 
-// Elements of a vector: 16 bytes where channels, addresses and strides allow, else 1.
+// Elements of a vector: 16 bytes where channels, addresses and strides allow, else 1 (gated [4,8192,8,512] with rows
+// an element longer, aligned rows after the comma: bf16 264, 160 us, backward 365, 272; fp32 352, 342 and 593, 570).
 inline int vec_of(const NormProblem& p, bool bwd)
 {
     const int v = p.bf16 ? 8 : 4;

@@ -26,7 +26,11 @@
 // over the channels.  B=4 T=2048 D=4096 N=16 bf16 with a gate: 611 to 616 us
 // for the call; profiled apart pass 1 takes 186 us with 88 % of the issue
 // slots taken, pass 3 498 with 82 %.  Segments cost it next to nothing, so there are enough of
-// them to fill the chip.
+// them to fill the chip.  N above 32 takes 16 waves, which leaves each 128
+// registers, 64 of them for a tile's states and decays: 44 to 53 values go to
+// scratch within the walk, and the call takes 1.87 ps a state and step (B=2
+// T=1024 D=1024 N=64: 251 us) where it takes 1.17 at N=32 (B=2 T=2048 D=2048:
+// 315) and 1.14 at N=16.
 #include "scan_impl.hpp"
 #include "sums.hpp"
 
@@ -427,7 +431,7 @@ __global__ __launch_bounds__(64 * W) void scan_bwd_kernel(ScanProblem p, Segment
             r.dy[i] = (k.gp + t * p.dy.row)[c];
             if (GATED) r.z[i] = (k.zp + t * p.z.row)[c];
         }
-        r.m = k.mp[k.row(t0 + k.ms) * k.mr];
+        r.m = k.mp[k.row(t0 + k.ms) * k.mr];   // a product a tile: the cursor steps forwards only
         r.h0 = tiles[(size_t)(t0 / TS) * W * 64];
         r.cum = linked ? cums[(size_t)(t0 / TS) * 64] : 0.0f;
     };
