@@ -400,8 +400,10 @@ int tfla_dbg_set_knob(int knob, int value);
  *
  * What stands before and after a gated linear recurrence in a model, and the
  * recurrence with a diagonal state per channel: a short causal convolution
- * (tfla_conv_*), a selective state space scan (tfla_scan_*) and a group norm
- * with an activation or a gate (tfla_norm_*).  Tensors have their channels
+ * (tfla_conv_*), a selective state space scan (tfla_scan_*), a group norm
+ * with an activation or a gate (tfla_norm_*), rotary positions of queries and
+ * keys (tfla_rotary_*), a gated linear recurrence of channels (tfla_diag_*)
+ * and a residual sum with a norm (tfla_addnorm_*).  Tensors have their channels
  * last, [B,T,D]; the element type of the activations is bf16 with
  * TFLA_IO_BF16 in `flags`, else fp32, and parameters are fp32.
  *
@@ -409,7 +411,7 @@ int tfla_dbg_set_knob(int knob, int value);
  * batch and row strides in elements, the channels being contiguous (x as one
  * half of a projection's output, say).  Strides are >= 0; those of an output
  * must keep its rows apart.  Outputs must not overlap inputs or each other,
- * except where a state is named as updated in place; views of one buffer
+ * except where one is named as updated in place; views of one buffer
  * that interleave without sharing an element are fine.  Data needs the
  * alignment of its element type; wider alignment is faster.
  *
@@ -592,6 +594,145 @@ size_t tfla_norm_workspace_bytes(int B, int T, int G, int C, int flags);
 int tfla_norm_fwd(const tfla_norm_args* args, void* workspace, size_t workspace_bytes, void* stream);
 size_t tfla_norm_bwd_workspace_bytes(int B, int T, int G, int C, int flags);
 int tfla_norm_bwd(const tfla_norm_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Rotary positions of queries and keys: the pair j < R/2 of a head's first R
+ * channels, (a, b) = (x[j], x[j + R/2]) or, with TFLA_ROTARY_INTERLEAVED,
+ * (x[2j], x[2j+1]), turns by an angle of its row's position,
+ *
+ *     th = pos[b,t] freqs[j],   a' = scale (a cos th - b sin th),   b' = scale (b cos th + a sin th)
+ *
+ * and the channels from R on pass as they are.  pos is positions[b,t], else
+ * start[b] + t, else t.  Angles are formed in 64 bits.
+ *
+ *   B, T, H >= 1, Hk >= 0, B T <= 2^30, C 1 to 1024, R even, 0 to C, (H + Hk) C <= 2^24
+ *   q, q_out  [B,T,H,C];  k, k_out [B,T,Hk,C], not looked at when Hk is 0; any strides over contiguous
+ *             channels (head-major [B,H,T,C] seen as [B,T,H,C] as for tfla_norm_*).  An output may be its
+ *             own input (rotated in place).
+ *   freqs     fp64 [R/2], device memory (may be NULL when R is 0)
+ *   positions int32, row b at positions + b positions_batch (0: the same for every sequence), or NULL
+ *   start     int32 [B] or NULL; not together with positions
+ *   lengths   as above: rows behind a sequence's end come out 0
+ *   flags     TFLA_IO_BF16 and/or TFLA_ROTARY_INTERLEAVED
+ *
+ * Backward: q and k hold the gradients of the outputs, q_out and k_out receive
+ * those of the inputs: the turn by -th, times scale.
+ */
+#define TFLA_ROTARY_INTERLEAVED 0x4000
+typedef struct tfla_rotary_args {
+    int B, T, H, Hk, C, R, flags;
+    float scale;
+    const double* freqs;
+    const int* positions;
+    long long positions_batch;
+    const int* start;
+    const int* lengths;
+    tfla_heads q, k, q_out, k_out;
+} tfla_rotary_args;
+
+int tfla_rotary_fwd(const tfla_rotary_args* args, void* stream);
+int tfla_rotary_bwd(const tfla_rotary_args* args, void* stream);
+
+/*
+ * Gated linear recurrence of channels: one fp32 state a channel,
+ *
+ *     h_t = f_t h_{t-1} + i_t x_t,   y_t = h_t
+ *
+ * from h_{-1} = `state` (zeros when NULL), with s() the sigmoid and gates
+ *
+ *     TFLA_DIAG_COUPLED   f = s(fgate),                  i = 1 - f
+ *     TFLA_DIAG_SIGMOID   f = s(fgate),                  i = s(igate)
+ *     TFLA_DIAG_DECAY     f = exp(-decay[c] s(fgate)),   i = sqrt(1 - f^2) s(igate)
+ *
+ * state_out receives the state after the last row and may be `state` itself,
+ * so the same call serves prompts and single tokens (T = 1).  `starts`
+ * receives the states before rows 0, TFLA_DIAG_CHUNK, 2 TFLA_DIAG_CHUNK, ...:
+ * what the backward pass starts from.
+ *
+ *   B, T, D >= 1, B T <= 2^30, D <= 2^24
+ *   x, fgate, igate, y  [B,T,D]; igate only where the kind has it (not looked at else)
+ *   decay [D], >= 0, for TFLA_DIAG_DECAY (not looked at else); state, state_out [B,D] or NULL;
+ *   starts [B, ceil(T / TFLA_DIAG_CHUNK), D] or NULL: fp32
+ *   flags  TFLA_IO_BF16 or 0
+ *
+ * Backward: from starts (of the forward pass over the same inputs), dy and
+ * dstate_out (the gradient of state_out, or NULL) the gradients dx, dfgate,
+ * digate (where the kind has igate), ddecay (where it has decay) and dstate
+ * (or NULL).  Where 1 - f^2 is 0 the gradient through its root is taken as 0.
+ */
+#define TFLA_DIAG_CHUNK 128
+enum tfla_diag_kind { TFLA_DIAG_COUPLED = 0, TFLA_DIAG_SIGMOID = 1, TFLA_DIAG_DECAY = 2 };
+typedef struct tfla_diag_args {
+    int B, T, D, kind, flags;
+    tfla_rows x, fgate, igate;
+    const float* decay;
+    const int* lengths;
+    /* tfla_diag_fwd */
+    const float* state;
+    tfla_rows y;
+    float* state_out;
+    /* written by tfla_diag_fwd, read by tfla_diag_bwd */
+    float* starts;
+    /* tfla_diag_bwd */
+    tfla_rows dy;
+    const float* dstate_out;
+    tfla_rows dx, dfgate, digate;
+    float* ddecay;
+    float* dstate;
+} tfla_diag_args;
+
+/* Workspaces as for tfla_conv_bwd (sizes may be 0); they depend on B, T, D, kind, flags only. */
+size_t tfla_diag_workspace_bytes(int B, int T, int D, int kind, int flags);
+int tfla_diag_fwd(const tfla_diag_args* args, void* workspace, size_t workspace_bytes, void* stream);
+size_t tfla_diag_bwd_workspace_bytes(int B, int T, int D, int kind, int flags);
+int tfla_diag_bwd(const tfla_diag_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Residual sum with a layer norm or, with TFLA_ADDNORM_RMS, an RMS norm:
+ *
+ *     t = x + residual,   y = (t - mean(t)) rstd weight + bias,   rstd = 1 / sqrt(mean((t - mean(t))^2) + eps)
+ *
+ * (RMS: mean(t) is taken as 0).  `total` receives t, the residual stream that
+ * the next block adds to, and may be `residual` itself; y comes from t before
+ * it is rounded to the stream's type.  Without a residual (data NULL) t is x
+ * and total is not written (data NULL).
+ *
+ *   B, T, C >= 1, B T <= 2^30, C <= 2^24; eps > 0
+ *   x, y, dy, dx [B,T,C]: bf16 with TFLA_IO_BF16, else fp32
+ *   residual, total, dtotal, dresidual [B,T,C]: the same type, or fp32 with TFLA_ADDNORM_SUM_FP32
+ *   weight, bias fp32 [C] or NULL (1 and 0)
+ *
+ * Backward: from total (x where there was no residual), dy and dtotal (the
+ * gradient of total from behind, or NULL) the gradient of t,
+ *
+ *     v = dy weight,   rstd (v - mean(v) - th mean(v th)) + dtotal,   th = (t - mean(t)) rstd
+ *
+ * (RMS: no mean(v)), as dx and, with TFLA_ADDNORM_SUM_FP32 and where wanted,
+ * dresidual in the stream's type (else dx is the gradient of both and
+ * dresidual NULL); dweight and dbias where wanted (or NULL).  It forms the
+ * statistics again from total.
+ */
+#define TFLA_ADDNORM_RMS 0x8000
+#define TFLA_ADDNORM_SUM_FP32 0x10000
+typedef struct tfla_addnorm_args {
+    int B, T, C, flags;
+    float eps;
+    tfla_rows x, residual;
+    const float* weight;
+    const float* bias;
+    tfla_rows y;
+    /* written by tfla_addnorm_fwd, read by tfla_addnorm_bwd */
+    tfla_rows total;
+    /* tfla_addnorm_bwd */
+    tfla_rows dy, dtotal, dx, dresidual;
+    float* dweight;
+    float* dbias;
+} tfla_addnorm_args;
+
+int tfla_addnorm_fwd(const tfla_addnorm_args* args, void* stream);
+/* Workspace as for tfla_conv_bwd; the size depends on B, T, C, flags only. */
+size_t tfla_addnorm_bwd_workspace_bytes(int B, int T, int C, int flags);
+int tfla_addnorm_bwd(const tfla_addnorm_args* args, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static description of a status code. */
 const char* tfla_error_string(int code);

@@ -188,15 +188,17 @@ def _current(stream, x):
     return _HERE if handle == _raw_stream(dev) else torch.cuda.stream(stream)
 
 
-def _call(name, packed, dev, nbytes=None, workspace=None):
-    """Calls entry point ``name`` on the current stream of the tensors' device
-    with that device current; ``nbytes``: the workspace it needs."""
+def _call(name, packed, dev, nbytes=None, workspace=None, fn=None):
+    """Calls entry point ``name`` (of this module, or ``fn``) on the current
+    stream of the tensors' device with that device current; ``nbytes``: the
+    workspace it needs."""
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return _call(name, packed, dev, nbytes, workspace)
+            return _call(name, packed, dev, nbytes, workspace, fn)
+    fn = fn or _fn[name]
     s = _raw_stream(dev)
     if nbytes is None:
-        rc = _fn[name](packed, s)
+        rc = fn(packed, s)
     else:
         at = size = 0
         if workspace is not None:
@@ -206,7 +208,7 @@ def _call(name, packed, dev, nbytes=None, workspace=None):
         elif nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
             at, size = workspace.data_ptr(), nbytes
-        rc = _fn[name](packed, at, size, s)
+        rc = fn(packed, at, size, s)
     if rc:
         from . import tfla
         tfla._check(rc, name)

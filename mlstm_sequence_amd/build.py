@@ -16,7 +16,8 @@ OBJDIR = os.path.join(ROOT, "_build", "libtfla")
 LIB = os.path.join(_HERE, "libtfla.so")
 SOURCES = ["tfla_api.cpp", "gates.hip", "gates_exp.hip", "state.hip", "intra.hip", "intra_sweep.hip", "recurrent.hip", "grad.hip", "probe.hip",
            "intra_bwd_q.hip", "intra_bwd_k.hip", "intra_bwd_v.hip", "intra_bwd_p.hip",
-           "blocks_api.cpp", "conv.hip", "scan.hip", "scan_bwd.hip", "norm.hip", "norm_bwd.hip", "norm_seq.hip"]
+           "blocks_api.cpp", "conv.hip", "scan.hip", "scan_bwd.hip", "norm.hip", "norm_bwd.hip", "norm_seq.hip",
+           "edges_api.cpp", "rotary.hip", "diag.hip", "diag_bwd.hip", "addnorm.hip", "addnorm_bwd.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -1,6 +1,7 @@
 // blocks.hpp -- the operators around the recurrences (internal): problem
-// descriptions and launchers of the causal convolution, the selective scan
-// and the group norm.
+// descriptions and launchers of the causal convolution, the selective scan,
+// the group norm, rotary positions, the gated linear recurrence of channels
+// and the residual sum with a norm.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -97,5 +98,60 @@ size_t norm_workspace(const NormProblem& p);
 hipError_t launch_norm_fwd(const NormProblem& p, hipStream_t stream);
 size_t norm_bwd_workspace(const NormProblem& p);
 hipError_t launch_norm_bwd(const NormProblem& p, hipStream_t stream);
+
+// ---- rotary positions (rotary.hip) -------------------------------------------------------
+struct RotaryProblem {
+    int B, T, H, Hk, C, R;
+    bool bf16, interleaved, inverse;        // inverse: the turn by minus the angle (backward)
+    float scale;
+    const double* freqs;                    // [R/2]
+    const int* positions;                   // row b at positions + b * positions_batch, or NULL
+    int64_t positions_batch;
+    const int *start, *lengths;             // [B] or NULL
+    Heads q, k, q_out, k_out;
+};
+
+hipError_t launch_rotary(const RotaryProblem& p, hipStream_t stream);
+
+// ---- gated linear recurrence of channels (diag.hip, diag_bwd.hip) ------------------------
+enum DiagKind { kCoupled = 0, kSigmoid = 1, kDecay = 2 };
+
+struct DiagProblem {
+    int B, T, D, kind;
+    bool bf16;
+    Rows x, fgate, igate;                   // igate.p NULL: coupled
+    const float* decay;                     // [D], kDecay only
+    const int* lengths;
+    const float* state;                     // [B,D] or NULL
+    Rows y;
+    float *state_out, *starts;              // [B,D], [B,chunks,D] or NULL
+    // backward
+    Rows dy, dx, dfgate, digate;
+    const float* dstate_out;
+    float *ddecay, *dstate;
+    char* ws;
+};
+
+size_t diag_workspace(const DiagProblem& p);
+hipError_t launch_diag_fwd(const DiagProblem& p, hipStream_t stream);
+size_t diag_bwd_workspace(const DiagProblem& p);
+hipError_t launch_diag_bwd(const DiagProblem& p, hipStream_t stream);
+
+// ---- residual sum with a norm (addnorm.hip, addnorm_bwd.hip) -------------------------------
+struct AddNormProblem {
+    int B, T, C;
+    bool bf16, sum_fp32, rms;               // sum_fp32: the stream is fp32 beside bf16 activations
+    float eps;
+    Rows x, residual, y, total;             // residual.p, total.p NULL: no residual
+    const float *weight, *bias;             // [C] or NULL
+    // backward
+    Rows dy, dtotal, dx, dresidual;
+    float *dweight, *dbias;
+    char* ws;
+};
+
+hipError_t launch_addnorm_fwd(const AddNormProblem& p, hipStream_t stream);
+size_t addnorm_bwd_workspace(const AddNormProblem& p);
+hipError_t launch_addnorm_bwd(const AddNormProblem& p, hipStream_t stream);
 
 }  // namespace tfla

@@ -1,0 +1,362 @@
+"""The operators at a block's edges and beside the recurrences on torch tensors
+(include/tfla.h): rotary positions of queries and keys, the gated linear
+recurrence of channels, and the residual sum with a layer or RMS norm;
+:mod:`mlstm_sequence_amd.tfla` offers the same names.
+
+Argument checks, output allocation and marshalling only, in the manner of
+:mod:`mlstm_sequence_amd.blocks`: the work runs in the library's HIP kernels on
+torch's current stream of the tensors' device, or with ``stream`` as under
+``torch.cuda.stream(stream)``.  Channels are contiguous, other strides are
+free; a tensor that does not fit is refused, never copied.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+import struct
+from typing import NamedTuple, Optional
+
+import torch
+
+from .blocks import (
+    _HEADS, _IO, _NO_HEADS, _NO_ROWS, _ROWS, Heads, Rows, _bad, _call, _current, _first, _fits, _flat, _heads, _i,
+    _ll, _p, _ptr, _rows,
+)
+
+ROTARY_HALVES, ROTARY_INTERLEAVED = 0, 0x4000   # pairs: channels j and j + R/2, or 2j and 2j + 1
+DIAG_COUPLED, DIAG_SIGMOID, DIAG_DECAY = 0, 1, 2
+DIAG_CHUNK = 128   # rows between the states that diag_forward leaves for diag_backward
+_RMS, _SUM_FP32 = 0x8000, 0x10000
+
+_fn = {}   # this module's entry points, once the library is loaded
+
+
+def bind(L):
+    """Argument types of this module's entry points, offered all at once."""
+    global _fn
+    vp, sz = ctypes.c_void_p, ctypes.c_size_t
+    fn = {}
+    for name, args, res in (
+            ("tfla_rotary_fwd", [vp, vp], _i),
+            ("tfla_rotary_bwd", [vp, vp], _i),
+            ("tfla_diag_workspace_bytes", [_i] * 5, sz),
+            ("tfla_diag_fwd", [vp, vp, sz, vp], _i),
+            ("tfla_diag_bwd_workspace_bytes", [_i] * 5, sz),
+            ("tfla_diag_bwd", [vp, vp, sz, vp], _i),
+            ("tfla_addnorm_fwd", [vp, vp], _i),
+            ("tfla_addnorm_bwd_workspace_bytes", [_i] * 4, sz),
+            ("tfla_addnorm_bwd", [vp, vp, sz, vp], _i)):
+        f = getattr(L, name)
+        f.argtypes, f.restype = args, res
+        fn[name] = f
+    _fn = fn
+
+
+def _entry(name):
+    if not _fn:
+        from . import tfla
+        tfla.lib()
+    return _fn[name]
+
+
+class RotaryArgs(ctypes.Structure):
+    """tfla_rotary_args."""
+    _fields_ = [("B", _i), ("T", _i), ("H", _i), ("Hk", _i), ("C", _i), ("R", _i), ("flags", _i), ("scale", ctypes.c_float),
+                ("freqs", _p), ("positions", _p), ("positions_batch", _ll), ("start", _p), ("lengths", _p),
+                ("q", Heads), ("k", Heads), ("q_out", Heads), ("k_out", Heads)]
+
+
+class DiagArgs(ctypes.Structure):
+    """tfla_diag_args."""
+    _fields_ = [("B", _i), ("T", _i), ("D", _i), ("kind", _i), ("flags", _i),
+                ("x", Rows), ("fgate", Rows), ("igate", Rows), ("decay", _p), ("lengths", _p),
+                ("state", _p), ("y", Rows), ("state_out", _p), ("starts", _p),
+                ("dy", Rows), ("dstate_out", _p), ("dx", Rows), ("dfgate", Rows), ("digate", Rows), ("ddecay", _p),
+                ("dstate", _p)]
+
+
+class AddNormArgs(ctypes.Structure):
+    """tfla_addnorm_args."""
+    _fields_ = [("B", _i), ("T", _i), ("C", _i), ("flags", _i), ("eps", ctypes.c_float),
+                ("x", Rows), ("residual", Rows), ("weight", _p), ("bias", _p), ("y", Rows), ("total", Rows),
+                ("dy", Rows), ("dtotal", Rows), ("dx", Rows), ("dresidual", Rows), ("dweight", _p), ("dbias", _p)]
+
+
+_ROTARY = struct.Struct("@7if2Pq2P" + _HEADS * 4)
+_DIAG = struct.Struct("@5i" + _ROWS * 3 + "3P" + _ROWS + "2P" + _ROWS + "P" + _ROWS * 3 + "2P")
+_ADDNORM = struct.Struct("@4if" + _ROWS * 2 + "2P" + _ROWS * 6 + "2P")
+
+
+# ---- rotary positions ------------------------------------------------------------
+
+def rotary_frequencies(dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                       original_length: Optional[int] = None, slow: float = 1.0, fast: float = 32.0, device="cuda"):
+    """Frequencies of ``dim`` rotated channels, fp64 [dim/2] on ``device``, and
+    the factor of the rotated values: what :func:`rotary_forward` takes as
+    ``freqs`` and ``scale``.
+
+    ``base ** (-2 j / dim)``, for contexts ``factor`` times the trained length:
+    "linear" divides all by the factor; "ntk" stretches the base to
+    ``base factor ** (dim / (dim - 2))``, so the fastest stay and the slowest
+    are divided by the factor; "yarn" divides those with fewer than ``slow``
+    turns in ``original_length`` rows, keeps those with more than ``fast``,
+    goes over linearly between, and scales by ``0.1 ln(factor) + 1``."""
+    if dim < 0 or dim % 2:
+        raise ValueError(f"dim must be even and not negative, got {dim}")
+    if not (base > 0 and math.isfinite(base)):
+        raise ValueError(f"base must be positive and finite, got {base}")
+    if not (factor >= 1 and math.isfinite(factor)):
+        raise ValueError(f"factor must be finite and at least 1, got {factor}")
+    exponent = -2.0 * torch.arange(dim // 2, dtype=torch.float64) / max(dim, 1)
+    scale = 1.0
+    if scaling == "ntk" and dim > 2:
+        base = base * factor ** (dim / (dim - 2))
+    freqs = torch.pow(torch.tensor(float(base), dtype=torch.float64), exponent)
+    if scaling == "linear":
+        freqs = freqs / factor
+    elif scaling == "yarn":
+        if original_length is None or original_length < 1:
+            raise ValueError("yarn needs original_length, the trained length in rows")
+        if not fast > slow:
+            raise ValueError(f"fast must be above slow, got {fast} and {slow}")
+        keep = ((original_length * freqs / (2 * math.pi) - slow) / (fast - slow)).clamp(0.0, 1.0)
+        freqs = (1.0 - keep) * freqs / factor + keep * freqs
+        scale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in ("none", "ntk"):
+        raise ValueError(f'scaling must be "none", "linear", "ntk" or "yarn", got {scaling!r}')
+    return freqs.to(device), scale
+
+
+def _rotary(name, q, k, freqs, layout, scale, positions, start, lengths, q_out, k_out, head_major, stream):
+    fn = _entry(name)
+    with _current(stream, q):
+        dev = _first(q, "q", 4)
+        shape, dtype = q.shape, q.dtype
+        B, T, H, C = shape
+        if layout not in (ROTARY_HALVES, ROTARY_INTERLEAVED):
+            raise ValueError(f"layout must be ROTARY_HALVES or ROTARY_INTERLEAVED, got {layout}")
+        if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
+            raise ValueError("freqs must be a one-dimensional fp64 tensor")
+        if k is None and k_out is not None:
+            raise ValueError("k_out is given without k")
+        if k is not None and (not isinstance(k, torch.Tensor) or k.dim() != 4):
+            raise ValueError("k must be a [B,T,Hk,C] tensor")
+        Hk = 0 if k is None else k.shape[2]
+        kshape = (B, T, Hk, C)
+        at = stride = 0
+        if positions is not None:
+            if isinstance(positions, torch.Tensor) and positions.dim() == 1:
+                positions = positions.expand(B, T) if positions.shape == (T,) else positions
+            if not _fits(positions, (B, T), torch.int32, dev) or (T > 1 and positions.stride(1) != 1):
+                _bad(positions, "positions", (B, T), torch.int32, dev)
+            at, stride = positions.data_ptr(), positions.stride(0)
+
+        def out(t, like):
+            if t is not None or like is None:
+                return t
+            b, n, h, c = like.shape
+            return q.new_empty((b, h, n, c)).transpose(1, 2) if head_major else q.new_empty(like.shape)
+
+        q_out, k_out = out(q_out, q), out(k_out, k)
+        packed = _ROTARY.pack(B, T, H, Hk, C, 2 * freqs.shape[0], _IO[dtype] | layout, float(scale),
+                              _flat(freqs, "freqs", (freqs.shape[0],), torch.float64, dev), at, stride,
+                              _flat(start, "start", (B,), torch.int32, dev), _flat(lengths, "lengths", (B,), torch.int32, dev),
+                              *_heads(q, "q", shape, dtype, dev),
+                              *(_NO_HEADS if k is None else _heads(k, "k", kshape, dtype, dev)),
+                              *_heads(q_out, "q_out", shape, dtype, dev),
+                              *(_NO_HEADS if k is None else _heads(k_out, "k_out", kshape, dtype, dev)))
+        _call(name, packed, dev, fn=fn)
+        return q_out, k_out
+
+
+def rotary_forward(q, k, freqs, layout: int = ROTARY_HALVES, scale: float = 1.0, positions=None, start=None, lengths=None,
+                   q_out=None, k_out=None, head_major: bool = False, stream=None):
+    """Rotary positions of q [B,T,H,C] and k [B,T,Hk,C] (or None): the first
+    2 len(freqs) channels of each head turn by ``position * freqs``, times
+    ``scale``; the others pass.  Returns ``(q_out, k_out)``.
+
+    ``freqs`` fp64 [R/2] (:func:`rotary_frequencies`); positions are
+    ``positions`` int32 [B,T] or [T], else ``start`` int32 [B] plus the row,
+    else the row.  ``head_major`` allocates outputs whose memory is [B,H,T,C],
+    so that ``q_out.transpose(1, 2)`` is what :func:`forward` takes; ``q_out``
+    may be q itself.  ``lengths`` int32 [B]: valid rows of a padded batch."""
+    return _rotary("tfla_rotary_fwd", q, k, freqs, layout, scale, positions, start, lengths, q_out, k_out, head_major, stream)
+
+
+def rotary_backward(dq, dk, freqs, layout: int = ROTARY_HALVES, scale: float = 1.0, positions=None, start=None,
+                    lengths=None, q_out=None, k_out=None, head_major: bool = False, stream=None):
+    """Gradients of :func:`rotary_forward`'s q and k from those of its outputs
+    (dk None: of q alone), the other arguments being the forward pass's;
+    ``q_out`` and ``k_out`` receive them where given."""
+    return _rotary("tfla_rotary_bwd", dq, dk, freqs, layout, scale, positions, start, lengths, q_out, k_out, head_major, stream)
+
+
+# ---- gated linear recurrence of channels --------------------------------------------
+
+class DiagGrads(NamedTuple):
+    """Gradients of :func:`diag_forward`; None where the input was None."""
+    dx: torch.Tensor
+    dfgate: torch.Tensor
+    digate: Optional[torch.Tensor]
+    ddecay: Optional[torch.Tensor]
+    dstate: Optional[torch.Tensor]
+
+
+def _diag_args(x, fgate, igate, decay, kind, lengths):
+    """(fields shared by both directions, sizes of the workspace calls, device)"""
+    dev = _first(x, "x", 3)
+    shape, dtype = x.shape, x.dtype
+    B, T, D = shape
+    if kind not in (DIAG_COUPLED, DIAG_SIGMOID, DIAG_DECAY):
+        raise ValueError(f"kind must be DIAG_COUPLED, DIAG_SIGMOID or DIAG_DECAY, got {kind}")
+    if (igate is None) != (kind == DIAG_COUPLED):
+        raise ValueError("igate must be given exactly for DIAG_SIGMOID and DIAG_DECAY")
+    if (decay is None) != (kind != DIAG_DECAY):
+        raise ValueError("decay must be given exactly for DIAG_DECAY")
+    sizes = (B, T, D, kind, _IO[dtype])
+    return (*sizes, *_rows(x, "x", shape, dtype, dev), *_rows(fgate, "fgate", shape, dtype, dev),
+            *(_NO_ROWS if igate is None else _rows(igate, "igate", shape, dtype, dev)),
+            _flat(decay, "decay", (D,), torch.float32, dev), _flat(lengths, "lengths", (B,), torch.int32, dev)), sizes, dev
+
+
+def _chunks(x):
+    B, T, D = x.shape
+    return B, -(-T // DIAG_CHUNK), D
+
+
+def diag_forward(x, fgate, igate=None, decay=None, kind: int = DIAG_COUPLED, state=None, lengths=None,
+                 want_state: bool = False, want_starts: bool = False, y=None, state_out=None, starts=None, workspace=None,
+                 stream=None):
+    """Gated linear recurrence ``y = h = f h + i x`` of x [B,T,D], a state a
+    channel; returns ``(y, state_out, starts)``.
+
+    Gates from pre-activations [B,T,D]: DIAG_COUPLED ``f = sigmoid(fgate)``,
+    ``i = 1 - f``; DIAG_SIGMOID the same f and ``i = sigmoid(igate)``;
+    DIAG_DECAY ``f = exp(-decay sigmoid(fgate))``,
+    ``i = sqrt(1 - f^2) sigmoid(igate)`` with decay fp32 [D], not negative.
+    ``state`` fp32 [B,D] is the state before the first row; ``state_out``
+    (allocated with ``want_state``, may be ``state`` itself) the one after the
+    last; ``starts`` (allocated with ``want_starts``) fp32
+    [B, ceil(T / DIAG_CHUNK), D] the states that :func:`diag_backward` needs.
+    ``lengths`` int32 [B]: valid rows of a padded batch."""
+    need, fn = _entry("tfla_diag_workspace_bytes"), _entry("tfla_diag_fwd")
+    with _current(stream, x):
+        fields, sizes, dev = _diag_args(x, fgate, igate, decay, kind, lengths)
+        shape, dtype, f32 = x.shape, x.dtype, torch.float32
+        B, _, D = shape
+        if y is None:
+            y = x.new_empty(shape)
+        if state_out is None and want_state:
+            state_out = torch.empty((B, D), dtype=f32, device=x.device)
+        if starts is None and want_starts:
+            starts = torch.empty(_chunks(x), dtype=f32, device=x.device)
+        packed = _DIAG.pack(*fields, _flat(state, "state", (B, D), f32, dev), *_rows(y, "y", shape, dtype, dev),
+                            _flat(state_out, "state_out", (B, D), f32, dev), _flat(starts, "starts", _chunks(x), f32, dev),
+                            *_NO_ROWS, 0, *_NO_ROWS * 3, 0, 0)
+        _call("tfla_diag_fwd", packed, dev, need(*sizes), workspace, fn)
+        return y, state_out, starts
+
+
+def diag_backward(x, fgate, dy, starts, igate=None, decay=None, kind: int = DIAG_COUPLED, lengths=None, dstate_out=None,
+                  want_dstate: bool = False, dx=None, dfgate=None, digate=None, workspace=None, stream=None) -> DiagGrads:
+    """Gradients of :func:`diag_forward` for ``dy`` and (with carried states)
+    ``dstate_out``, from the ``starts`` it left; dx, dfgate and digate may be
+    given, as parts of a projection's gradient for instance.  The gradient of
+    the state before the first row comes with ``want_dstate``."""
+    need, fn = _entry("tfla_diag_bwd_workspace_bytes"), _entry("tfla_diag_bwd")
+    with _current(stream, x):
+        fields, sizes, dev = _diag_args(x, fgate, igate, decay, kind, lengths)
+        shape, dtype, f32 = x.shape, x.dtype, torch.float32
+        B, _, D = shape
+        if starts is None:
+            raise ValueError("starts is needed: the states that diag_forward leaves with want_starts")
+        if digate is not None and igate is None:
+            raise ValueError("digate is given without igate")
+        dx, dfgate = (x.new_empty(shape) if t is None else t for t in (dx, dfgate))
+        digate = None if igate is None else x.new_empty(shape) if digate is None else digate
+        ddecay = None if decay is None else torch.empty_like(decay)
+        dstate = torch.empty((B, D), dtype=f32, device=x.device) if want_dstate else None
+        packed = _DIAG.pack(*fields, 0, *_NO_ROWS, 0, _flat(starts, "starts", _chunks(x), f32, dev),
+                            *_rows(dy, "dy", shape, dtype, dev), _flat(dstate_out, "dstate_out", (B, D), f32, dev),
+                            *_rows(dx, "dx", shape, dtype, dev), *_rows(dfgate, "dfgate", shape, dtype, dev),
+                            *(_NO_ROWS if igate is None else _rows(digate, "digate", shape, dtype, dev)),
+                            _ptr(ddecay), _ptr(dstate))
+        _call("tfla_diag_bwd", packed, dev, need(*sizes), workspace, fn)
+        return DiagGrads(dx, dfgate, digate, ddecay, dstate)
+
+
+# ---- residual sum with a norm ---------------------------------------------------------
+
+def _stream_type(t, name, dtype):
+    """Type of a tensor of the residual stream: the activations' or fp32."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype not in (dtype, torch.float32):
+        raise TypeError(f"{name} must be {dtype} or torch.float32, got {t.dtype}")
+    return t.dtype
+
+
+def addnorm_forward(x, residual=None, weight=None, bias=None, eps: float = 1e-5, rms: bool = False, y=None, total=None,
+                    stream=None):
+    """Residual sum ``total = x + residual`` of [B,T,C] and its layer norm (or,
+    with ``rms``, RMS norm) ``y = norm(total) weight + bias``; returns
+    ``(y, total)``, total None without a residual.
+
+    residual and total are of x's type or fp32; ``total`` may be ``residual``
+    itself.  y comes from the sum before it is rounded to total's type.
+    weight, bias are fp32 [C]."""
+    fn = _entry("tfla_addnorm_fwd")
+    with _current(stream, x):
+        dev = _first(x, "x", 3)
+        shape, dtype, f32 = x.shape, x.dtype, torch.float32
+        C = shape[2]
+        if residual is None and total is not None:
+            raise ValueError("total is given without a residual")
+        st = dtype if residual is None else _stream_type(residual, "residual", dtype)
+        if y is None:
+            y = x.new_empty(shape)
+        if total is None and residual is not None:
+            total = torch.empty(shape, dtype=st, device=x.device)
+        flags = _IO[dtype] | (_RMS if rms else 0) | (_SUM_FP32 if st != dtype else 0)
+        packed = _ADDNORM.pack(*shape, flags, float(eps), *_rows(x, "x", shape, dtype, dev),
+                               *(_NO_ROWS if residual is None else _rows(residual, "residual", shape, st, dev)),
+                               _flat(weight, "weight", (C,), f32, dev), _flat(bias, "bias", (C,), f32, dev),
+                               *_rows(y, "y", shape, dtype, dev),
+                               *(_NO_ROWS if residual is None else _rows(total, "total", shape, st, dev)), *_NO_ROWS * 4, 0, 0)
+        _call("tfla_addnorm_fwd", packed, dev, fn=fn)
+        return y, total
+
+
+def addnorm_backward(total, dy, weight=None, bias: bool = False, eps: float = 1e-5, rms: bool = False, dtotal=None, dx=None,
+                     dresidual=None, workspace=None, stream=None):
+    """Gradients of :func:`addnorm_forward` from its ``total`` (x where there
+    was no residual), ``dy`` and ``dtotal``, the gradient of total from behind
+    (or None); returns ``(dx, dresidual, dweight, dbias)``.
+
+    The gradient of the sum, in dy's type and in total's: one tensor where
+    these are the same.  dweight comes where weight is given, dbias with
+    ``bias``."""
+    need, fn = _entry("tfla_addnorm_bwd_workspace_bytes"), _entry("tfla_addnorm_bwd")
+    with _current(stream, dy):
+        dev = _first(dy, "dy", 3)
+        shape, dtype, f32 = dy.shape, dy.dtype, torch.float32
+        B, T, C = shape
+        st = _stream_type(total, "total", dtype)
+        if dx is None:
+            dx = dy.new_empty(shape)
+        if st == dtype:
+            if dresidual is not None and dresidual is not dx:
+                raise ValueError("dresidual is dx where dy and total have one type")
+        elif dresidual is None:
+            dresidual = torch.empty(shape, dtype=st, device=dy.device)
+        dweight = None if weight is None else torch.empty_like(weight)
+        dbias = torch.empty((C,), dtype=f32, device=dy.device) if bias else None
+        flags = _IO[dtype] | (_RMS if rms else 0) | (_SUM_FP32 if st != dtype else 0)
+        packed = _ADDNORM.pack(B, T, C, flags, float(eps), *_NO_ROWS * 2, _flat(weight, "weight", (C,), f32, dev), 0,
+                               *_NO_ROWS, *_rows(total, "total", shape, st, dev), *_rows(dy, "dy", shape, dtype, dev),
+                               *(_NO_ROWS if dtotal is None else _rows(dtotal, "dtotal", shape, st, dev)),
+                               *_rows(dx, "dx", shape, dtype, dev),
+                               *(_NO_ROWS if st == dtype else _rows(dresidual, "dresidual", shape, st, dev)),
+                               _ptr(dweight), _ptr(dbias))
+        _call("tfla_addnorm_bwd", packed, dev, need(B, T, C, flags), workspace, fn)
+        return dx, dx if st == dtype else dresidual, dweight, dbias

@@ -13,9 +13,15 @@ import os
 import torch  # loaded first: libtfla then shares torch's HIP runtime (same SONAME)
 
 from . import blocks as _blocks
+from . import edges as _edges
 from .blocks import (  # noqa: F401
     ACT_NONE, ACT_SIGMOID, ACT_SILU, NORM_SEQUENCE, NORM_TOKEN, ConvArgs, Heads, NormArgs, Rows, ScanArgs, ScanGrads,
     conv_backward, conv_forward, norm_backward, norm_forward, scan_backward, scan_forward,
+)
+from .edges import (  # noqa: F401
+    DIAG_CHUNK, DIAG_COUPLED, DIAG_DECAY, DIAG_SIGMOID, ROTARY_HALVES, ROTARY_INTERLEAVED, AddNormArgs, DiagArgs, DiagGrads,
+    RotaryArgs, addnorm_backward, addnorm_forward, diag_backward, diag_forward, rotary_backward, rotary_forward,
+    rotary_frequencies,
 )
 
 MLSTM_SIG = 0
@@ -96,6 +102,7 @@ def lib():
         L.tfla_version.argtypes = []
         L.tfla_version.restype = i
         _blocks.bind(L)
+        _edges.bind(L)
         _lib = L
     return _lib
 
