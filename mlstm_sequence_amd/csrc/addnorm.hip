@@ -1,16 +1,106 @@
 // addnorm.hip -- residual sum with a layer or RMS norm, forward.
 //
 //   t = x + residual,  y = (t - mean) rstd weight + bias   (RMS: mean taken as 0)
+//
+// Bound by memory: x and the stream are read once, the stream and y written
+// once (addnorm_impl.hpp).  Mean and variance take two passes over registers.
 #include "gfx950.hpp"
 
-#include "norm_impl.hpp"
+#include "addnorm_impl.hpp"
 
 namespace tfla {
 namespace {
 
-// A workgroup to a row.  T: activations, S: the stream.
+using namespace addnorm;
+
+constexpr unsigned kBlocks = 2048;
+
+// T: activations, S: the stream.  NV vectors a lane.
+template <typename T, typename S, int VEC, int NV>
+__global__ __launch_bounds__(1024) void addnorm_fwd_kernel(AddNormProblem p, RowMap m)
+{
+    __shared__ float red[2][16][1];
+    const int slot = threadIdx.x / m.L, lv = threadIdx.x & (m.L - 1);
+    const bool sum = p.residual.p != nullptr, shift = !p.rms;
+    int c[NV];
+    bool in[NV];
+    float w[NV][VEC], bs[NV][VEC];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        in[k] = lv + k * m.L < m.nv;
+        c[k] = min(lv + k * m.L, m.nv - 1) * VEC;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            w[k][v] = p.weight ? p.weight[c[k] + v] : 1.0f;
+            bs[k][v] = p.bias ? p.bias[c[k] + v] : 0.0f;
+        }
+    }
+    const float inv = 1.0f / (float)p.C;
+    Pack<T, VEC> rx[NV];
+    Pack<S, VEC> rr[NV];
+    auto fetch = [&](unsigned i) {                    // behind the last row: the last
+        i = min(i, m.rows - 1);
+        const int64_t b = i / (unsigned)p.T, t = i % (unsigned)p.T;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            rx[k].load((const T*)p.x.p + b * p.x.batch + t * p.x.row + c[k]);
+            if (sum) rr[k].load((const S*)p.residual.p + b * p.residual.batch + t * p.residual.row + c[k]);
+        }
+    };
+    const unsigned step = gridDim.x * m.slots, first = blockIdx.x * m.slots;
+    fetch(first + slot);
+    int turn = 0;
+    for (unsigned i0 = first; i0 < m.rows; i0 += step) {
+        const unsigned i = i0 + slot;
+        float x[NV][VEC], s = 0.0f, q = 0.0f, mean = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                x[k][v] = rx[k].get(v);
+                if (sum) x[k][v] += rr[k].get(v);
+            }
+        fetch(i + step);
+        if (shift) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) s += in[k] ? x[k][v] : 0.0f;
+            row_sums<1>(&s, m.L, red, turn);
+            turn ^= 1;
+            mean = s * inv;
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const float d = x[k][v] - mean;
+                q += in[k] ? d * d : 0.0f;
+            }
+        row_sums<1>(&q, m.L, red, turn);
+        turn ^= 1;
+        const float rstd = 1.0f / sqrtf(q * inv + p.eps);
+        if (i >= m.rows) continue;
+        const int64_t b = i / (unsigned)p.T, t = i % (unsigned)p.T;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (!in[k]) continue;
+            Pack<T, VEC> o;
+            Pack<S, VEC> ot;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                o.set(v, (x[k][v] - mean) * rstd * w[k][v] + bs[k][v]);
+                ot.set(v, x[k][v]);
+            }
+            o.store((T*)p.y.p + b * p.y.batch + t * p.y.row + c[k]);
+            if (sum) ot.store((S*)p.total.p + b * p.total.batch + t * p.total.row + c[k]);
+        }
+    }
+}
+
+// A workgroup to a row of any length, walked from memory.
 template <typename T, typename S>
-__global__ __launch_bounds__(256) void addnorm_fwd_kernel(AddNormProblem p)
+__global__ __launch_bounds__(256) void addnorm_fwd_long_kernel(AddNormProblem p)
 {
     __shared__ float red[4];
     const int64_t id = block_id();
@@ -37,15 +127,32 @@ __global__ __launch_bounds__(256) void addnorm_fwd_kernel(AddNormProblem p)
     }
 }
 
+template <typename T, typename S, int VEC>
+hipError_t fwd_v(const AddNormProblem& p, hipStream_t stream)
+{
+    if (p.C / VEC > kMostVectors) {
+        addnorm_fwd_long_kernel<T, S><<<grid_of((int64_t)p.B * p.T), 256, 0, stream>>>(p);
+        return hipGetLastError();
+    }
+    const RowMap m = row_map(p, VEC, kBlocks);
+    if (m.nv <= m.L) addnorm_fwd_kernel<T, S, VEC, 1><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    else addnorm_fwd_kernel<T, S, VEC, 2><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    return hipGetLastError();
+}
+
+template <typename T, typename S>
+hipError_t fwd_t(const AddNormProblem& p, hipStream_t stream)
+{
+    constexpr int wide = 16 / sizeof(T);
+    return vec_of(p, {&p.x, &p.residual, &p.y, &p.total}) == wide ? fwd_v<T, S, wide>(p, stream) : fwd_v<T, S, 1>(p, stream);
+}
+
 }  // namespace
 
 hipError_t launch_addnorm_fwd(const AddNormProblem& p, hipStream_t stream)
 {
-    const dim3 grid = grid_of((int64_t)p.B * p.T);
-    if (!p.bf16) addnorm_fwd_kernel<float, float><<<grid, 256, 0, stream>>>(p);
-    else if (p.sum_fp32) addnorm_fwd_kernel<bf16, float><<<grid, 256, 0, stream>>>(p);
-    else addnorm_fwd_kernel<bf16, bf16><<<grid, 256, 0, stream>>>(p);
-    return hipGetLastError();
+    if (!p.bf16) return fwd_t<float, float>(p, stream);
+    return p.sum_fp32 ? fwd_t<bf16, float>(p, stream) : fwd_t<bf16, bf16>(p, stream);
 }
 
 }  // namespace tfla

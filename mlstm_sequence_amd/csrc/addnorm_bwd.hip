@@ -1,20 +1,159 @@
 // addnorm_bwd.hip -- residual sum with a layer or RMS norm, backward.
 //
-//   th = (t - mean) rstd,  v = dy weight
-//   dt = rstd (v - mean(v) - th mean(v th)) + dtotal,  dweight = sum dy th,  dbias = sum dy
+//   d = t - mean,  v = dy weight
+//   dt = rstd (v - mean(v) - d rstd^2 mean(v d)) + dtotal,  dweight = sum dy d rstd,  dbias = sum dy
+//
+// The layout of the forward pass (addnorm_impl.hpp), the statistics formed
+// again: two sums over a row, mean(t) and then three together.  The weights'
+// gradients add up in registers over the rows that a workgroup takes and
+// leave it once, to be added over the workgroups in a fixed order.  Bound by
+// memory: the stream, its gradient and dy are read once, dt written once.
 #include "gfx950.hpp"
 
-#include "norm_impl.hpp"
+#include "addnorm_impl.hpp"
 #include "sums.hpp"
 
 namespace tfla {
 namespace {
 
-constexpr int kRun = 64;   // rows of a part of the weights' gradients
+using namespace addnorm;
 
-// A workgroup to a row; its statistics go to the workspace.
+constexpr unsigned kBlocks = 768;   // also the parts of the weights' gradients
+
+// THREADS: the workgroup's size is at most that.
+template <typename T, typename S, int VEC, int NV, int THREADS>
+__global__ __launch_bounds__(THREADS) void addnorm_bwd_kernel(AddNormProblem p, RowMap m)
+{
+    constexpr bool TWO = sizeof(T) != sizeof(S);
+    __shared__ float red1[2][16][1], red3[2][16][3];
+    __shared__ float acc[THREADS > 256 ? 1 : 256 * NV * VEC];
+    const int slot = threadIdx.x / m.L, lv = threadIdx.x & (m.L - 1);
+    const bool shift = !p.rms, behind = p.dtotal.p != nullptr;
+    int c[NV];
+    bool in[NV];
+    float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        in[k] = lv + k * m.L < m.nv;
+        c[k] = min(lv + k * m.L, m.nv - 1) * VEC;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            w[k][v] = p.weight ? p.weight[c[k] + v] : 1.0f;
+            dw[k][v] = db[k][v] = 0.0f;
+        }
+    }
+    const float inv = 1.0f / (float)p.C;
+    Pack<S, VEC> rt[NV], re[NV];
+    Pack<T, VEC> rg[NV];
+    auto fetch = [&](unsigned i) {                    // behind the last row: the last
+        i = min(i, m.rows - 1);
+        const int64_t b = i / (unsigned)p.T, t = i % (unsigned)p.T;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            rt[k].load((const S*)p.total.p + b * p.total.batch + t * p.total.row + c[k]);
+            rg[k].load((const T*)p.dy.p + b * p.dy.batch + t * p.dy.row + c[k]);
+            if (behind) re[k].load((const S*)p.dtotal.p + b * p.dtotal.batch + t * p.dtotal.row + c[k]);
+        }
+    };
+    const unsigned step = gridDim.x * m.slots, first = blockIdx.x * m.slots;
+    fetch(first + slot);
+    int turn = 0;
+    for (unsigned i0 = first; i0 < m.rows; i0 += step, turn ^= 1) {
+        const unsigned i = i0 + slot;
+        const bool live = i < m.rows;
+        float d[NV][VEC], g[NV][VEC], s = 0.0f, mean = 0.0f;
+        Pack<S, VEC> e[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            e[k] = re[k];
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                d[k][v] = rt[k].get(v);
+                g[k][v] = rg[k].get(v);
+            }
+        }
+        fetch(i + step);
+        if (shift) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) s += in[k] ? d[k][v] : 0.0f;
+            row_sums<1>(&s, m.L, red1, turn);
+            mean = s * inv;
+        }
+        float q[3] = {0.0f, 0.0f, 0.0f};              // d^2, v, v d
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                d[k][v] -= mean;
+                const float u = g[k][v] * w[k][v];
+                q[0] += in[k] ? d[k][v] * d[k][v] : 0.0f;
+                q[1] += in[k] ? u : 0.0f;
+                q[2] += in[k] ? u * d[k][v] : 0.0f;
+            }
+        row_sums<3>(q, m.L, red3, turn);
+        const float rstd = 1.0f / sqrtf(q[0] * inv + p.eps);
+        if (!live) continue;
+        const float m1 = shift ? q[1] * inv : 0.0f, m2 = q[2] * inv * rstd * rstd;
+        const int64_t b = i / (unsigned)p.T, t = i % (unsigned)p.T;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (!in[k]) continue;
+            Pack<T, VEC> o;
+            Pack<S, VEC> o2;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                dw[k][v] += g[k][v] * (d[k][v] * rstd);
+                db[k][v] += g[k][v];
+                float x = rstd * (g[k][v] * w[k][v] - m1 - d[k][v] * m2);
+                if (behind) x += e[k].get(v);
+                o.set(v, x);
+                if (TWO) o2.set(v, x);
+            }
+            o.store((T*)p.dx.p + b * p.dx.batch + t * p.dx.row + c[k]);
+            if (TWO && p.dresidual.p) o2.store((S*)p.dresidual.p + b * p.dresidual.batch + t * p.dresidual.row + c[k]);
+        }
+    }
+    if (!p.dweight && !p.dbias) return;
+    float* part = (float*)p.ws + (int64_t)blockIdx.x * 2 * p.C;
+    if (m.slots == 1) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v)
+                if (in[k]) {
+                    part[c[k] + v] = dw[k][v];
+                    part[p.C + c[k] + v] = db[k][v];
+                }
+        return;
+    }
+    if constexpr (THREADS == 256) {
+        // the slots' sums in order
+        for (int which = 0; which < 2; ++which) {
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) acc[(k * 256 + threadIdx.x) * VEC + v] = which ? db[k][v] : dw[k][v];
+            __syncthreads();
+            const int cols = m.L * VEC;
+            for (int e = threadIdx.x; e < NV * cols; e += 256) {
+                const int k = e / cols, at = e % cols, col = k * cols + at;
+                float s = 0.0f;
+                for (int j = 0; j < m.slots; ++j) s += acc[k * 256 * VEC + j * cols + at];
+                if (col < p.C) part[which * p.C + col] = s;
+            }
+        }
+    }
+}
+
+// Rows of any length: dt by a workgroup to a row in two readings, the statistics left in the workspace, the weights'
+// gradients by a thread to a column and a run of rows in a third.
+constexpr int kRun = 64;
+
 template <typename T, typename S>
-__global__ __launch_bounds__(256) void addnorm_bwd_kernel(AddNormProblem p)
+__global__ __launch_bounds__(256) void addnorm_bwd_long_kernel(AddNormProblem p, f32x2* stats)
 {
     __shared__ float red[4];
     const int64_t id = block_id();
@@ -45,15 +184,11 @@ __global__ __launch_bounds__(256) void addnorm_bwd_kernel(AddNormProblem p)
         dx[c] = from_float<T>(o);
         if (dr) dr[c] = from_float<S>(o);
     }
-    if (threadIdx.x == 0 && p.ws) {
-        ((f32x2*)p.ws)[id] = f32x2{mean, rstd};
-    }
+    if (threadIdx.x == 0 && (p.dweight || p.dbias)) stats[id] = f32x2{mean, rstd};
 }
 
-size_t stats_bytes(const AddNormProblem& p) { return ((size_t)p.B * p.T * 8 + 255) & ~size_t(255); }
-
 template <typename T, typename S>
-__global__ __launch_bounds__(256) void addnorm_columns_kernel(AddNormProblem p, float* part)
+__global__ __launch_bounds__(256) void addnorm_columns_kernel(AddNormProblem p, const f32x2* stats)
 {
     const int nb = (p.C + 255) / 256;
     const int64_t run = block_id() / nb, rows = (int64_t)p.B * p.T;
@@ -62,20 +197,22 @@ __global__ __launch_bounds__(256) void addnorm_columns_kernel(AddNormProblem p, 
     float dw = 0.0f, db = 0.0f;
     for (int64_t i = run * kRun; i < min(rows, (run + 1) * kRun); ++i) {
         const int64_t b = i / p.T, t = i % p.T;
-        const f32x2 st = ((const f32x2*)p.ws)[i];
+        const f32x2 st = stats[i];
         const float g = to_float(((const T*)p.dy.p)[b * p.dy.batch + t * p.dy.row + c]);
         dw += g * ((to_float(((const S*)p.total.p)[b * p.total.batch + t * p.total.row + c]) - st[0]) * st[1]);
         db += g;
     }
-    part[run * 2 * p.C + c] = dw;
-    part[run * 2 * p.C + p.C + c] = db;
+    float* part = (float*)p.ws + run * 2 * p.C;
+    part[c] = dw;
+    part[p.C + c] = db;
 }
 
-__global__ __launch_bounds__(1024) void addnorm_params_kernel(AddNormProblem p, const float* part, int64_t parts)
+// dweight and dbias from the workgroups' sums [parts][2][C]
+__global__ __launch_bounds__(1024) void addnorm_params_kernel(AddNormProblem p, int64_t parts)
 {
     __shared__ float red[16][64];
     const int64_t W = p.C, i = (int64_t)blockIdx.x * 64 + threadIdx.x;
-    const float s = part_sum(part, parts, 2 * W, 2 * W, blockIdx.x, red);
+    const float s = part_sum((const float*)p.ws, parts, 2 * W, 2 * W, blockIdx.x, red);
     if (threadIdx.x >= 64 || i >= 2 * W) return;
     if (i < W) {
         if (p.dweight) p.dweight[i] = s;
@@ -84,26 +221,58 @@ __global__ __launch_bounds__(1024) void addnorm_params_kernel(AddNormProblem p, 
     }
 }
 
+hipError_t params(const AddNormProblem& p, int64_t parts, hipStream_t stream)
+{
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || (!p.dweight && !p.dbias)) return e;
+    addnorm_params_kernel<<<(unsigned)((2 * (int64_t)p.C + 63) / 64), 1024, 0, stream>>>(p, parts);
+    return hipGetLastError();
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+int64_t runs_of(const AddNormProblem& p) { return ((int64_t)p.B * p.T + kRun - 1) / kRun; }
+
+template <typename T, typename S, int VEC>
+hipError_t bwd_v(const AddNormProblem& p, hipStream_t stream)
+{
+    if (p.C / VEC > kMostVectors) {
+        f32x2* stats = (f32x2*)(p.ws + align256((size_t)runs_of(p) * 2 * p.C * sizeof(float)));
+        addnorm_bwd_long_kernel<T, S><<<grid_of((int64_t)p.B * p.T), 256, 0, stream>>>(p, stats);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess || (!p.dweight && !p.dbias)) return e;
+        addnorm_columns_kernel<T, S><<<grid_of(runs_of(p) * ((p.C + 255) / 256)), 256, 0, stream>>>(p, stats);
+        return params(p, runs_of(p), stream);
+    }
+    const RowMap m = row_map(p, VEC, kBlocks);
+    if (m.threads > 512) addnorm_bwd_kernel<T, S, VEC, 2, 1024><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    else if (m.threads > 256) addnorm_bwd_kernel<T, S, VEC, 2, 512><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    else if (m.nv <= m.L) addnorm_bwd_kernel<T, S, VEC, 1, 256><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    else addnorm_bwd_kernel<T, S, VEC, 2, 256><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    return params(p, m.blocks, stream);
+}
+
 template <typename T, typename S>
 hipError_t bwd_t(const AddNormProblem& p, hipStream_t stream)
 {
-    addnorm_bwd_kernel<T, S><<<grid_of((int64_t)p.B * p.T), 256, 0, stream>>>(p);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || (!p.dweight && !p.dbias)) return e;
-    float* part = (float*)(p.ws + stats_bytes(p));
-    const int64_t runs = ((int64_t)p.B * p.T + kRun - 1) / kRun;
-    addnorm_columns_kernel<T, S><<<grid_of(runs * ((p.C + 255) / 256)), 256, 0, stream>>>(p, part);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    addnorm_params_kernel<<<(unsigned)((2 * (int64_t)p.C + 63) / 64), 1024, 0, stream>>>(p, part, runs);
-    return hipGetLastError();
+    constexpr int wide = 16 / sizeof(T);
+    return vec_of(p, {&p.total, &p.dy, &p.dtotal, &p.dx, &p.dresidual}) == wide ? bwd_v<T, S, wide>(p, stream)
+                                                                                : bwd_v<T, S, 1>(p, stream);
 }
 
 }  // namespace
 
+// For whichever width the call's addresses allow.
 size_t addnorm_bwd_workspace(const AddNormProblem& p)
 {
-    const int64_t runs = ((int64_t)p.B * p.T + kRun - 1) / kRun;
-    return stats_bytes(p) + (size_t)runs * 2 * p.C * sizeof(float);
+    const size_t row = 2 * (size_t)p.C * sizeof(float);
+    size_t most = 0;
+    for (const int v : {1, p.bf16 ? 8 : 4}) {
+        if (p.C % v) continue;
+        const size_t n = p.C / v > kMostVectors ? align256((size_t)runs_of(p) * row) + (size_t)p.B * p.T * sizeof(f32x2)
+                                                : row_map(p, v, kBlocks).blocks * row;
+        if (n > most) most = n;
+    }
+    return most;
 }
 
 hipError_t launch_addnorm_bwd(const AddNormProblem& p, hipStream_t stream)
