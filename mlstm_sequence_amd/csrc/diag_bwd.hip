@@ -12,6 +12,9 @@
 // A long axis over few channels is cut into segments, whose adjoint maps are
 // formed first from fgate and dy alone.
 #include "diag_impl.hpp"
+
+#include <algorithm>
+
 #include "sums.hpp"
 
 namespace tfla {
@@ -19,12 +22,11 @@ namespace {
 
 using namespace diag;
 
-constexpr int kPer = 16, kTile = kWaves * kPer;
-static_assert(kTile == kChunk, "a tile starts where the forward pass left a state");
+constexpr int kGroup = 4;   // rows whose gates a lane forms together
 
 // The adjoint behind segment `seg`: dstate_out through the maps of the segments from the last on.
 template <int V>
-__device__ __forceinline__ void adjoint_behind(const DiagProblem& p, const Segments& sg, const Place& q, int cc,
+__device__ __forceinline__ void adjoint_behind(const DiagProblem& p, const Cut& sg, const Place& q, int cc,
                                                const f32x2* ends, float* a)
 {
 #pragma unroll
@@ -45,23 +47,27 @@ __device__ __forceinline__ void adjoint_behind(const DiagProblem& p, const Segme
     }
 }
 
-template <typename T, int KIND, int V, bool BUF>
-__global__ __launch_bounds__(64 * kWaves, 2) void diag_bwd_kernel(DiagProblem p, Segments sg, const f32x2* __restrict__ ends,
+template <typename T, int KIND, int CH, int V, bool BUF>
+__global__ __launch_bounds__(64 * kWaves, 2) void diag_bwd_kernel(DiagProblem p, Cut sg, const f32x2* __restrict__ ends,
                                                                    float* __restrict__ part)
 {
-    constexpr int R = kPer / V;
-    __shared__ f32x2 totf[2][kWaves][64];              // F, H
-    __shared__ float tota[2][kWaves][64];              // A
+    typedef Shape<CH, V> S;
+    constexpr int R = S::R, kTile = S::tile, LA = CH == 64 ? kStreamed : 0,
+                  SA = CH == 64 && (KIND != kCoupled || sizeof(T) == 4) ? kStreamed : 0;
+    __shared__ f32x2 totf[2][kWaves][CH];              // F, H
+    __shared__ float tota[2][kWaves][CH];              // A
     Place q;
     if (!place(p, sg, &q)) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    int half;
-    const Lane l = lane_of<V, kPer>(p, q, &half);
+    const Lane l = lane_of<CH, V>(p, q);
+    const bool first = lane < S::lanes;                // of the lanes that share channels
+    const int col = lane % S::lanes * V;
     const int s0 = q.seg * sg.len, all = min(sg.len, p.T - s0);
-    const int n = min(max(clamp_len(p.lengths, (int)q.b, p.T) - s0, 0), all);
+    const int n = __builtin_amdgcn_readfirstlane(min(max(clamp_len(p.lengths, (int)q.b, p.T) - s0, 0), all));
     const int cc = min(l.c, l.last);
     const int64_t nc = (p.T + kChunk - 1) / kChunk;
-    Walk<T, V, BUF> wx, wu, wv, wg, ox, ou, ov;
+    Walk<T, V, BUF, LA> wx, wu, wv, wg;
+    Walk<T, V, BUF, SA> ox, ou, ov;
     wx.open(p.x, q.b, s0, l);
     wu.open(p.fgate, q.b, s0, l);
     wg.open(p.dy, q.b, s0, l);
@@ -71,57 +77,88 @@ __global__ __launch_bounds__(64 * kWaves, 2) void diag_bwd_kernel(DiagProblem p,
         wv.open(p.igate, q.b, s0, l);
         ov.open(p.digate, q.b, s0, l);
     }
-    float decay[V], a0[V], dd[V];
+    Rate decay[V];
+    float a0[V], dd[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-        decay[k] = KIND == kDecay ? p.decay[cc + k] : 0.0f;
+        decay[k] = Rate(KIND == kDecay ? p.decay[cc + k] : 0.0f);
         dd[k] = 0.0f;
     }
     adjoint_behind<V>(p, sg, q, cc, ends, a0);
-    typename Walk<T, V, BUF>::raw rx[R], ru[R], rv[R], rg[R];
+    typename RawOf<sizeof(T) * V>::type rx[R], ru[R], rv[R], rg[R];
     float rh[V];
-    auto fetch = [&](int t0) {                         // t0 may be < 0: nothing that is used
-        const int rows = t0 < 0 ? 0 : min(n - t0, kTile), at = max(t0, 0);
-        wu.template load<R>(ru, at, rows, n, l);
-        if (KIND != kCoupled) wv.template load<R>(rv, at, rows, n, l);
-        wx.template load<R>(rx, at, rows, n, l);
-        wg.template load<R>(rg, at, rows, n, l);
-#pragma unroll
-        for (int k = 0; k < V; ++k) rh[k] = p.starts[(q.b * nc + (s0 + at) / kChunk) * p.D + cc + k];
-    };
-    ox.clear(n, all, q.cb * 64, p.D);
-    ou.clear(n, all, q.cb * 64, p.D);
-    if (KIND != kCoupled) ov.clear(n, all, q.cb * 64, p.D);
+    ox.template clear<CH>(n, all, q.cb * CH, p.D);
+    ou.template clear<CH>(n, all, q.cb * CH, p.D);
+    if (KIND != kCoupled) ov.template clear<CH>(n, all, q.cb * CH, p.D);
     const int last = (n - 1) / kTile * kTile;
-    if (n > 0) fetch(last);
-    int buf = 0;
-    for (int t0 = last; n > 0 && t0 >= 0; t0 -= kTile, buf ^= 1) {
-        const int rows = min(n - t0, kTile);
-        Gate g[R][V];
-        float x[R][V], dy[R][V], h[V];
+    auto start = [&](int t0) {                         // the state at a tile's start
+#pragma unroll
+        for (int k = 0; k < V; ++k) rh[k] = p.starts[(q.b * nc + (s0 + max(t0, 0)) / kChunk) * p.D + cc + k];
+    };
+    if (n > 0) {
+        const auto tu = wu.tile(last, n - last, n), tv = wv.tile(last, n - last, n), tx = wx.tile(last, n - last, n),
+                   tg = wg.tile(last, n - last, n);
+        start(last);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            float u[V], v[V];
-            decode<T, V>(ru[r], u);
-            if (KIND != kCoupled) decode<T, V>(rv[r], v);
-            decode<T, V>(rx[r], x[r]);
-            decode<T, V>(rg[r], dy[r]);
-#pragma unroll
-            for (int k = 0; k < V; ++k) g[r][k] = gate_of<T, KIND>(u[k], KIND != kCoupled ? v[k] : 0.0f, decay[k]);
+            ru[r] = wu.load(tu, r, l);
+            if (KIND != kCoupled) rv[r] = wv.load(tv, r, l);
+            rx[r] = wx.load(tx, r, l);
+            rg[r] = wg.load(tg, r, l);
         }
+    }
+    int buf = 0;
+    for (int t0 = last; n > 0 && t0 >= 0; t0 -= kTile, buf ^= 1) {
+        const int rows = min(n - t0, kTile), t1 = max(t0 - kTile, 0), rows1 = t0 ? kTile : 0;   // the next tile is whole, or none
+        const auto tu = wu.tile(t1, rows1, n), tv = wv.tile(t1, rows1, n), tx = wx.tile(t1, rows1, n), tg = wg.tile(t1, rows1, n);
+        Gate g[R][V];
+        typename RawOf<sizeof(T) * V>::type ax[R], ag[R];    // x and dy as they were loaded
+        float h[V];
 #pragma unroll
         for (int k = 0; k < V; ++k) h[k] = rh[k];
-        fetch(t0 - kTile);
-        if (rows < kTile)                              // rows behind the end change nothing
+        start(t1);
+#pragma unroll
+        for (int r0 = 0; r0 < R; r0 += kGroup) {
+            float u[kGroup][V], v[kGroup][V];
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i) {         // the next tile's rows into the registers of those taken
+                const int r = r0 + i;
+                decode<T, V>(ru[r], u[i]);
+                ru[r] = wu.load(tu, r, l);
+                if (KIND != kCoupled) {
+                    decode<T, V>(rv[r], v[i]);
+                    rv[r] = wv.load(tv, r, l);
+                }
+                ax[r] = rx[r];
+                rx[r] = wx.load(tx, r, l);
+                ag[r] = rg[r];
+                rg[r] = wg.load(tg, r, l);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i)
+#pragma unroll
+                for (int k = 0; k < V; ++k) g[r0 + i][k] = gate_of<T, KIND>(u[i][k], KIND != kCoupled ? v[i][k] : 0.0f, decay[k]);
+        }
+        if (rows < kTile) {                            // rows behind the end change nothing
+            const int end = (int)hidden((unsigned)rows);   // a branch, not selections in every tile
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int k = 0; k < V; ++k)
-                    if (l.row + r >= rows) {
+                    if (l.row + r >= end) {
                         g[r][k].f = 1.0f;
-                        g[r][k].i = x[r][k] = dy[r][k] = 0.0f;
+                        g[r][k].i = 0.0f;
+                        ax[r] = ag[r] = {};
                         if (KIND == kDecay) g[r][k].r = 0.0f;   // nothing for ddecay
                     }
+        }
+        float x[R][V], dy[R][V];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            decode<T, V>(ax[r], x[r]);
+            decode<T, V>(ag[r], dy[r]);
+        }
         float fl[V], hl[V], fa[V], aa[V];              // the state before the lane's rows, the adjoint behind them
 #pragma unroll
         for (int k = 0; k < V; ++k) {
@@ -135,25 +172,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void diag_bwd_kernel(DiagProblem p,
             for (int r = R - 1; r >= 0; --r) A = g[r][k].f * (dy[r][k] + A);
             fl[k] = fa[k] = 1.0f;
             hl[k] = aa[k] = 0.0f;
-            if (V == 2) {
-                float lf, uf, lh, uh, la, ua;
-                halves(F, &lf, &uf);
-                halves(H, &lh, &uh);
-                halves(A, &la, &ua);
-                if (half) {
-                    fl[k] = lf;
-                    hl[k] = lh;
-                } else {
-                    fa[k] = uf;
-                    aa[k] = ua;
-                }
-                F = lf * uf;
-                H = uf * lh + uh;
-                A = lf * ua + la;
-            }
-            if (half == 0) {
-                totf[buf][wave][lane * V + k] = f32x2{F, H};
-                tota[buf][wave][lane * V + k] = A;
+            join_both<S::lanes>(lane, &F, &H, &A, &fl[k], &hl[k], &fa[k], &aa[k]);
+            if (first) {
+                totf[buf][wave][col + k] = f32x2{F, H};
+                tota[buf][wave][col + k] = A;
             }
         }
         __syncthreads();
@@ -162,29 +184,27 @@ __global__ __launch_bounds__(64 * kWaves, 2) void diag_bwd_kernel(DiagProblem p,
         for (int w = kWaves - 1; w >= 0; --w)
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                const int c = lane % (64 / V) * V + k;
                 if (w == wave) a[k] = a0[k];
-                a0[k] = totf[buf][w][c][0] * a0[k] + tota[buf][w][c];
+                a0[k] = totf[buf][w][col + k][0] * a0[k] + tota[buf][w][col + k];
             }
         for (int w = 0; w < wave; ++w)
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                const f32x2 m = totf[buf][w][lane % (64 / V) * V + k];
+                const f32x2 m = totf[buf][w][col + k];
                 h[k] = m[0] * h[k] + m[1];
             }
         float before[R][V];
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            if (V == 2) {
-                h[k] = fl[k] * h[k] + hl[k];
-                a[k] = fa[k] * a[k] + aa[k];
-            }
+            h[k] = fl[k] * h[k] + hl[k];
+            a[k] = fa[k] * a[k] + aa[k];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 before[r][k] = h[k];
                 h[k] = g[r][k].f * h[k] + g[r][k].i * x[r][k];
             }
         }
+        const auto tdx = ox.tile(t0, rows, n), tdu = ou.tile(t0, rows, n), tdv = ov.tile(t0, rows, n);
 #pragma unroll
         for (int r = R - 1; r >= 0; --r) {
             float dx[V], du[V], dv[V];
@@ -198,87 +218,98 @@ __global__ __launch_bounds__(64 * kWaves, 2) void diag_bwd_kernel(DiagProblem p,
                 dv[k] = o.dv;
                 dd[k] += o.dd;
             }
-            ox.store(encode<T, V>(dx), r, t0, rows, l);
-            ou.store(encode<T, V>(du), r, t0, rows, l);
-            if (KIND != kCoupled) ov.store(encode<T, V>(dv), r, t0, rows, l);
+            ox.store(tdx, encode<T, V>(dx), r, l);
+            ou.store(tdu, encode<T, V>(du), r, l);
+            if (KIND != kCoupled) ov.store(tdv, encode<T, V>(dv), r, l);
         }
     }
-    if (p.dstate && q.seg == 0 && wave == 0 && half == 0 && l.live)
+    if (p.dstate && q.seg == 0 && wave == 0 && first && l.live)
 #pragma unroll
         for (int k = 0; k < V; ++k) p.dstate[q.b * p.D + l.c + k] = a0[k];
     if (KIND != kDecay) return;
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-        if (V == 2) {
-            float lo, hi;
-            halves(dd[k], &lo, &hi);
-            dd[k] = lo + hi;
-        }
-        if (half == 0) tota[0][wave][lane * V + k] = dd[k];
+        dd[k] = sum_groups<S::lanes>(lane, dd[k]);
+        if (first) tota[0][wave][col + k] = dd[k];
     }
     __syncthreads();
-    const int c = q.cb * 64 + lane;
-    if (wave != 0 || c >= p.D) return;
+    const int c = q.cb * CH + (int)threadIdx.x;
+    if (threadIdx.x >= CH || c >= p.D) return;
     float s = 0.0f;
-    for (int w = 0; w < kWaves; ++w) s += tota[0][w][lane];
+    for (int w = 0; w < kWaves; ++w) s += tota[0][w][threadIdx.x];
     part[(q.b * sg.nseg + q.seg) * p.D + c] = s;
 }
 
 // The adjoint maps of all segments but the first.
-template <typename T, int KIND, int V, bool BUF>
-__global__ __launch_bounds__(64 * kWaves, 2) void diag_adjoint_kernel(DiagProblem p, Segments sg, f32x2* __restrict__ ends)
+template <typename T, int KIND, int CH, int V, bool BUF>
+__global__ __launch_bounds__(64 * kWaves, 2) void diag_adjoint_kernel(DiagProblem p, Cut sg, f32x2* __restrict__ ends)
 {
-    constexpr int R = kPer / V;
-    __shared__ f32x2 tot[2][kWaves][64];
+    typedef Shape<CH, V> S;
+    constexpr int R = S::R, kTile = S::tile;
+    __shared__ f32x2 tot[2][kWaves][CH];
     Place q;
     if (!place(p, sg, &q) || q.seg == 0) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    int half;
-    const Lane l = lane_of<V, kPer>(p, q, &half);
+    const Lane l = lane_of<CH, V>(p, q);
+    const bool first = lane < S::lanes;                // of the lanes that share channels
+    const int col = lane % S::lanes * V;
     const int s0 = q.seg * sg.len, all = min(sg.len, p.T - s0);
-    const int n = min(max(clamp_len(p.lengths, (int)q.b, p.T) - s0, 0), all);
+    const int n = __builtin_amdgcn_readfirstlane(min(max(clamp_len(p.lengths, (int)q.b, p.T) - s0, 0), all));
     const int cc = min(l.c, l.last);
-    Walk<T, V, BUF> wu, wg;
+    Walk<T, V, BUF, 0> wu, wg;
     wu.open(p.fgate, q.b, s0, l);
     wg.open(p.dy, q.b, s0, l);
-    float decay[V], a0[V], f0[V];
+    Rate decay[V];
+    float a0[V], f0[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-        decay[k] = KIND == kDecay ? p.decay[cc + k] : 0.0f;
+        decay[k] = Rate(KIND == kDecay ? p.decay[cc + k] : 0.0f);
         a0[k] = 0.0f;
         f0[k] = 1.0f;
     }
-    typename Walk<T, V, BUF>::raw ru[R], rg[R];
-    auto fetch = [&](int t0) {
-        const int rows = t0 < 0 ? 0 : min(n - t0, kTile), at = max(t0, 0);
-        wu.template load<R>(ru, at, rows, n, l);
-        wg.template load<R>(rg, at, rows, n, l);
-    };
+    typename RawOf<sizeof(T) * V>::type ru[R], rg[R];
     const int last = (n - 1) / kTile * kTile;
-    if (n > 0) fetch(last);
-    int buf = 0;
-    for (int t0 = last; n > 0 && t0 >= 0; t0 -= kTile, buf ^= 1) {
-        const int rows = min(n - t0, kTile);
-        float f[R][V], dy[R][V];
+    if (n > 0) {
+        const auto tu = wu.tile(last, n - last, n), tg = wg.tile(last, n - last, n);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            float u[V];
-            decode<T, V>(ru[r], u);
-            decode<T, V>(rg[r], dy[r]);
-#pragma unroll
-            for (int k = 0; k < V; ++k) f[r][k] = forget_of<T, KIND>(u[k], decay[k]);
+            ru[r] = wu.load(tu, r, l);
+            rg[r] = wg.load(tg, r, l);
         }
-        fetch(t0 - kTile);
-        if (rows < kTile)
+    }
+    int buf = 0;
+    for (int t0 = last; n > 0 && t0 >= 0; t0 -= kTile, buf ^= 1) {
+        const int rows = min(n - t0, kTile), t1 = max(t0 - kTile, 0), rows1 = t0 ? kTile : 0;
+        const auto tu = wu.tile(t1, rows1, n), tg = wg.tile(t1, rows1, n);
+        float f[R][V], dy[R][V];
+#pragma unroll
+        for (int r0 = 0; r0 < R; r0 += kGroup) {
+            float u[kGroup][V];
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i) {
+                decode<T, V>(ru[r0 + i], u[i]);
+                ru[r0 + i] = wu.load(tu, r0 + i, l);
+                decode<T, V>(rg[r0 + i], dy[r0 + i]);
+                rg[r0 + i] = wg.load(tg, r0 + i, l);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i)
+#pragma unroll
+                for (int k = 0; k < V; ++k) f[r0 + i][k] = forget_of<T, KIND>(u[i][k], decay[k]);
+        }
+        if (rows < kTile) {
+            const int end = (int)hidden((unsigned)rows);
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int k = 0; k < V; ++k)
-                    if (l.row + r >= rows) {
+                    if (l.row + r >= end) {
                         f[r][k] = 1.0f;
                         dy[r][k] = 0.0f;
                     }
+        }
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             float F = 1.0f, A = 0.0f;
@@ -287,26 +318,20 @@ __global__ __launch_bounds__(64 * kWaves, 2) void diag_adjoint_kernel(DiagProble
                 A = f[r][k] * (dy[r][k] + A);
                 F *= f[r][k];
             }
-            if (V == 2) {
-                float lf, uf, la, ua;
-                halves(F, &lf, &uf);
-                halves(A, &la, &ua);
-                F = lf * uf;
-                A = lf * ua + la;
-            }
-            if (half == 0) tot[buf][wave][lane * V + k] = f32x2{F, A};
+            join_behind<S::lanes>(lane, &F, &A);
+            if (first) tot[buf][wave][col + k] = f32x2{F, A};
         }
         __syncthreads();
 #pragma unroll
         for (int w = kWaves - 1; w >= 0; --w)
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                const f32x2 m = tot[buf][w][lane % (64 / V) * V + k];
+                const f32x2 m = tot[buf][w][col + k];
                 a0[k] = m[0] * a0[k] + m[1];
                 f0[k] *= m[0];
             }
     }
-    if (wave == 0 && half == 0 && l.live)
+    if (wave == 0 && first && l.live)
 #pragma unroll
         for (int k = 0; k < V; ++k) ends[(q.b * sg.nseg + q.seg) * p.D + l.c + k] = f32x2{f0[k], a0[k]};
 }
@@ -319,35 +344,46 @@ __global__ __launch_bounds__(1024) void diag_params_kernel(DiagProblem p, const 
     if (threadIdx.x < 64 && i < p.D) p.ddecay[i] = s;
 }
 
-template <typename T, int KIND, int V, bool BUF>
-hipError_t bwd_v(const DiagProblem& p, hipStream_t stream)
+template <typename T, int KIND, int CH, int V, bool BUF>
+hipError_t bwd_v(const DiagProblem& p, const Cut& cut, hipStream_t stream)
 {
-    const Segments sg = segments_of(p, kTile);
     f32x2* ends = (f32x2*)p.ws;
-    const int64_t parts = (int64_t)p.B * sg.nseg;
-    float* part = parts == 1 ? p.ddecay : (float*)(p.ws + ends_bytes(p, sg));
-    const dim3 grid = grid_of(parts * sg.ncb);
+    const int64_t parts = (int64_t)p.B * cut.nseg;
+    float* part = parts == 1 ? p.ddecay : (float*)(p.ws + ends_bytes(p, cut));
     hipError_t e;
-    if (sg.nseg > 1) {
-        diag_adjoint_kernel<T, KIND, V, BUF><<<grid, 64 * kWaves, 0, stream>>>(p, sg, ends);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
+    if constexpr (CH == 16 || !BUF) {
+        if (cut.nseg > 1) {
+            diag_adjoint_kernel<T, KIND, CH, V, BUF><<<grid_of(cut.blocks), 64 * kWaves, 0, stream>>>(p, cut, ends);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
     }
-    diag_bwd_kernel<T, KIND, V, BUF><<<grid, 64 * kWaves, 0, stream>>>(p, sg, ends, part);
+    diag_bwd_kernel<T, KIND, CH, V, BUF><<<grid_of(cut.blocks), 64 * kWaves, 0, stream>>>(p, cut, ends, part);
     if ((e = hipGetLastError()) != hipSuccess || KIND != kDecay || parts == 1) return e;
     diag_params_kernel<<<(unsigned)((p.D + 63) / 64), 1024, 0, stream>>>(p, part, parts);
     return hipGetLastError();
 }
 
+template <typename T, int KIND, int V>
+hipError_t bwd_c(const DiagProblem& p, hipStream_t stream)
+{
+    const Cut cut = cut_of(p, false);
+    switch (cut.ch) {
+    case 64: return bwd_v<T, KIND, 64, V, true>(p, cut, stream);
+    case 32: return bwd_v<T, KIND, 32, V, true>(p, cut, stream);
+    default: return bwd_v<T, KIND, 16, V, true>(p, cut, stream);
+    }
+}
+
 template <typename T, int KIND>
 hipError_t bwd_k(const DiagProblem& p, hipStream_t stream)
 {
-    bool buf = true, two = p.D % 2 == 0;
+    bool buf = true, two = sizeof(T) == 2 && p.D % 2 == 0;
     for (const Rows* m : {&p.x, &p.fgate, &p.igate, &p.dy, (const Rows*)&p.dx, (const Rows*)&p.dfgate, (const Rows*)&p.digate}) {
-        buf = buf && walks(*m, p, kTile);
+        buf = buf && walks(*m, p);
         two = two && aligned(*m, p, 2 * sizeof(T));
     }
-    if (!buf) return bwd_v<T, KIND, 1, false>(p, stream);
-    return two ? bwd_v<T, KIND, 2, true>(p, stream) : bwd_v<T, KIND, 1, true>(p, stream);
+    if (!buf) return bwd_v<T, KIND, 64, 1, false>(p, cut_of(p, true), stream);
+    return two ? bwd_c<T, KIND, 2>(p, stream) : bwd_c<T, KIND, 1>(p, stream);
 }
 
 template <typename T>
@@ -362,11 +398,16 @@ hipError_t bwd_t(const DiagProblem& p, hipStream_t stream)
 
 }  // namespace
 
+// For whichever way the call's strides allow.
 size_t diag_bwd_workspace(const DiagProblem& p)
 {
-    const Segments sg = segments_of(p, kTile);
-    const int64_t parts = (int64_t)p.B * sg.nseg;
-    return ends_bytes(p, sg) + (p.kind == kDecay && parts > 1 ? (size_t)parts * p.D * sizeof(float) : 0);
+    size_t most = 0;
+    for (const bool wide : {false, true}) {
+        const Cut cut = cut_of(p, wide);
+        const int64_t parts = (int64_t)p.B * cut.nseg;
+        most = std::max(most, ends_bytes(p, cut) + (p.kind == kDecay && parts > 1 ? (size_t)parts * p.D * sizeof(float) : 0));
+    }
+    return most;
 }
 
 hipError_t launch_diag_bwd(const DiagProblem& p, hipStream_t stream)

@@ -24,18 +24,26 @@ __device__ __forceinline__ int clamp_len(const int* lengths, int b, int T)
 
 template <typename T> __device__ __forceinline__ float exp_t(float x) { return sizeof(T) == 2 ? exp2_fast(x * kLog2e) : exp_f(x); }
 
-// 1 - e^{-2w}: the series where the difference would cancel (w below 1/4; the first term left out is 2^-26 of it).
-__device__ __forceinline__ float one_minus_square(float w, float f)
+// 1 - f^2 = 1 - e^{-z}, z = 2 w: below 0.4, where the difference would cancel, z times a polynomial of degree 4 fitted
+// to (1 - e^{-z}) / z on [0, 0.4] (Chebyshev nodes; off by 0.9 half steps at most).
+__device__ __forceinline__ float one_minus_square(float z, float f)
 {
-    const float z = 2.0f * w;
-    float s = fmaf(z, -2.4801587e-5f, 1.9841270e-4f);
-    s = fmaf(z, -s, 1.3888889e-3f);
-    s = fmaf(z, -s, 8.3333333e-3f);
-    s = fmaf(z, -s, 4.1666667e-2f);
-    s = fmaf(z, -s, 1.6666667e-1f);
-    s = fmaf(z, -s, 0.5f);
-    s = fmaf(z, -s, 1.0f);
-    return z < 0.5f ? z * s : fmaf(-f, f, 1.0f);
+    float s = fmaf(z, 7.0668478e-3f, -4.1237194e-2f);
+    s = fmaf(z, s, 1.6660628e-1f);
+    s = fmaf(z, s, -4.9999702e-1f);
+    s = fmaf(z, s, 1.0f);
+    return z < 0.4f ? z * s : fmaf(-f, f, 1.0f);
+}
+
+// A channel's decay and what the steps need of it.
+struct Rate {
+    float decay, twice, log2;
+    __device__ __forceinline__ explicit Rate(float d = 0.0f) : decay(d), twice(2.0f * d), log2(-d * kLog2e) {}
+};
+
+template <typename T> __device__ __forceinline__ float decayed(float r, const Rate& d)
+{
+    return sizeof(T) == 2 ? exp2_fast(d.log2 * r) : exp_f(-(d.decay * r));
 }
 
 // The gates of a step; r = s(u), s = s(v) and m where the kind has them.
@@ -43,7 +51,7 @@ struct Gate {
     float f, i, r, s, m;
 };
 
-template <typename T, int KIND> __device__ __forceinline__ Gate gate_of(float u, float v, float decay)
+template <typename T, int KIND> __device__ __forceinline__ Gate gate_of(float u, float v, const Rate& d)
 {
     Gate g;
     if (KIND == kCoupled) {
@@ -57,9 +65,8 @@ template <typename T, int KIND> __device__ __forceinline__ Gate gate_of(float u,
             g.f = g.r;
             g.i = g.s;
         } else {
-            const float w = decay * g.r;
-            g.f = exp_t<T>(-w);
-            g.m = __builtin_amdgcn_sqrtf(one_minus_square(w, g.f));
+            g.f = decayed<T>(g.r, d);
+            g.m = __builtin_amdgcn_sqrtf(one_minus_square(d.twice * g.r, g.f));
             g.i = g.m * g.s;
         }
     }
@@ -67,11 +74,11 @@ template <typename T, int KIND> __device__ __forceinline__ Gate gate_of(float u,
 }
 
 // f alone.
-template <typename T, int KIND> __device__ __forceinline__ float forget_of(float u, float decay)
+template <typename T, int KIND> __device__ __forceinline__ float forget_of(float u, const Rate& d)
 {
     if (KIND == kCoupled) return __builtin_amdgcn_rcpf(1.0f + exp_t<T>(-u));
     const float r = sigmoid_t<T>(u);
-    return KIND == kSigmoid ? r : exp_t<T>(-(decay * r));
+    return KIND == kSigmoid ? r : decayed<T>(r, d);
 }
 
 struct GateGrads {
@@ -79,7 +86,7 @@ struct GateGrads {
 };
 
 // Gradients of a step from its gates, x, the state before it and g.
-template <int KIND> __device__ __forceinline__ GateGrads grads_of(const Gate& k, float x, float before, float g, float decay)
+template <int KIND> __device__ __forceinline__ GateGrads grads_of(const Gate& k, float x, float before, float g, const Rate& d)
 {
     GateGrads o;
     o.dx = k.i * g;
@@ -94,7 +101,7 @@ template <int KIND> __device__ __forceinline__ GateGrads grads_of(const Gate& k,
         const float dm = k.m > 0.0f ? k.f * k.f * __builtin_amdgcn_rcpf(k.m) : 0.0f;
         const float dw = di * k.s * dm - df * k.f;
         o.dd = dw * k.r;
-        o.du = o.dd * decay * (1.0f - k.r);
+        o.du = o.dd * d.decay * (1.0f - k.r);
         o.dv = di * k.i * (1.0f - k.s);
     }
     return o;
@@ -102,11 +109,26 @@ template <int KIND> __device__ __forceinline__ GateGrads grads_of(const Gate& k,
 
 // ---- tiles ---------------------------------------------------------------------------
 //
-// A workgroup owns 64 neighbouring channels of a sequence and walks their rows in
-// tiles of 8 waves times PER rows; a lane holds V neighbouring channels and
-// PER / V consecutive rows (64 / V lanes across a row).
+// A workgroup owns CH neighbouring channels of a sequence and walks their rows in
+// tiles; a lane holds V neighbouring channels of 16 / V consecutive rows, CH / V
+// lanes side by side make a row group, the wave's groups and the eight waves
+// follow each other in time.  CH is 64 (a row of 128 bytes in bf16) where that
+// makes workgroups enough, else 32 or 16, whose neighbours share lines: they are
+// put on one XCD, whose L2 reads a line once for them.
 
 constexpr int kWaves = 8;
+constexpr int kStreamed = 2;                              // of a buffer access: past the caches (nt)
+constexpr int kPer = 16;                                  // elements of a tensor that a lane holds
+
+template <int CH, int V> struct Shape {
+    static constexpr int lanes = CH / V;                  // of a row
+    static constexpr int groups = 64 / lanes;             // row groups of a wave
+    static constexpr int R = kPer / V;                    // rows of a lane
+    static constexpr int rows = groups * R;               // of a wave
+    static constexpr int tile = kWaves * rows;
+};
+static_assert(Shape<64, 2>::tile == kChunk && Shape<64, 1>::tile == kChunk && Shape<16, 2>::tile == 4 * kChunk,
+              "a tile starts where the forward pass leaves a state");
 
 template <int BYTES> struct RawOf;
 template <> struct RawOf<2> { typedef unsigned short type; };
@@ -158,63 +180,79 @@ __device__ __forceinline__ unsigned hidden(unsigned x)
 // The rows of a tensor that a workgroup walks.  BUF: by buffer instructions, whose bounds check makes rows behind the
 // tile's last valid one, and channels behind the last, read as 0 and never written, at one 32-bit addition a row;
 // else by 64-bit addresses held inside the tensor (rows further apart than a buffer spans, or sharing memory).
-template <typename T, int V, bool BUF> struct Walk {
+template <typename T, int V, bool BUF, int AUX> struct Walk {
     typedef typename RawOf<sizeof(T) * V>::type raw;
-    char* base;      // row 0 of the walk, channel 0
-    int64_t row;     // bytes
-    unsigned at;     // BUF: the lane's offset within a tile
+    char* base = nullptr;   // row 0 of the walk, channel 0
+    int64_t row = 0;        // bytes
+    unsigned at = 0;        // BUF: the lane's offset within a tile
     __device__ __forceinline__ void open(const Rows& m, int64_t b, int64_t first, const Lane& l)
     {
         row = m.row * (int64_t)sizeof(T);
         base = (char*)m.p + (b * m.batch + first * m.row) * (int64_t)sizeof(T);
         at = l.live ? (unsigned)(l.row * row) + (unsigned)l.c * (unsigned)sizeof(T) : 0x80000000u;
     }
-    // N rows of the tile at t0, of which `rows` are valid (may be <= 0); end: rows of the walk
-    template <int N> __device__ __forceinline__ void load(raw* o, int t0, int rows, int end, const Lane& l) const
+    // A tile of the walk: the rows from t0 on, of which `rows` are valid (may be <= 0); end: rows of the walk.
+    struct Tile {
+        decltype(__builtin_amdgcn_make_buffer_rsrc((void*)nullptr, 0, 0, 0)) rs;
+        char* at;
+        unsigned step;
+        int t0, rows, end;
+    };
+    __device__ __forceinline__ Tile tile(int t0, int rows, int end) const
+    {
+        Tile o;
+        if constexpr (BUF) {
+            // the clamp of a uniform value is done by a vector instruction; a descriptor in vector registers would make
+            // every load a loop over its lanes' descriptors
+            const int valid = __builtin_amdgcn_readfirstlane(max(rows, 0));
+            o.rs = __builtin_amdgcn_make_buffer_rsrc(base + t0 * row, 0, (int)(valid * row), 0x27000);
+            o.step = hidden((unsigned)row);
+        }
+        o.at = base;
+        o.t0 = t0;
+        o.rows = rows;
+        o.end = end;
+        return o;
+    }
+    __device__ __forceinline__ raw load(const Tile& t, int r, const Lane& l) const
     {
         if constexpr (BUF) {
-            const auto rs = __builtin_amdgcn_make_buffer_rsrc(base + t0 * row, 0, (int)(max(rows, 0) * row), 0x27000);
-            const unsigned step = hidden((unsigned)row);
-            unsigned v = at;
-#pragma unroll
-            for (int r = 0; r < N; ++r, v += step) {
-                if constexpr (sizeof(raw) == 2) o[r] = __builtin_amdgcn_raw_buffer_load_b16(rs, v, 0, 0);
-                else if constexpr (sizeof(raw) == 4) o[r] = __builtin_amdgcn_raw_buffer_load_b32(rs, v, 0, 0);
-                else o[r] = __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b64(rs, v, 0, 0));
-            }
+            const int v = (int)(at + r * t.step);
+            if constexpr (sizeof(raw) == 2) return __builtin_amdgcn_raw_buffer_load_b16(t.rs, v, 0, AUX);
+            else if constexpr (sizeof(raw) == 4) return __builtin_amdgcn_raw_buffer_load_b32(t.rs, v, 0, AUX);
+            else return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b64(t.rs, v, 0, AUX));
         } else {
-            const char* p = base + (int64_t)min(l.c, l.last) * (int64_t)sizeof(T);
-#pragma unroll
-            for (int r = 0; r < N; ++r) o[r] = *(const raw*)(p + min(t0 + l.row + r, end - 1) * row);
+            return *(const raw*)(t.at + (int64_t)min(l.c, l.last) * (int64_t)sizeof(T) + min(t.t0 + l.row + r, t.end - 1) * row);
         }
     }
-    __device__ __forceinline__ void store(raw v, int r, int t0, int rows, const Lane& l) const
+    __device__ __forceinline__ void store(const Tile& t, raw v, int r, const Lane& l) const
     {
         if constexpr (BUF) {
-            const auto rs = __builtin_amdgcn_make_buffer_rsrc(base + t0 * row, 0, (int)(rows * row), 0x27000);
-            const unsigned o = at + r * hidden((unsigned)row);
-            if constexpr (sizeof(raw) == 2) __builtin_amdgcn_raw_buffer_store_b16(v, rs, o, 0, 0);
-            else if constexpr (sizeof(raw) == 4) __builtin_amdgcn_raw_buffer_store_b32(v, rs, o, 0, 0);
+            const int o = (int)(at + r * t.step);
+            if constexpr (sizeof(raw) == 2) __builtin_amdgcn_raw_buffer_store_b16(v, t.rs, o, 0, AUX);
+            else if constexpr (sizeof(raw) == 4) __builtin_amdgcn_raw_buffer_store_b32(v, t.rs, o, 0, AUX);
             else {
                 typedef int i32x2 __attribute__((ext_vector_type(2)));
-                __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(i32x2, v), rs, o, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(i32x2, v), t.rs, o, 0, AUX);
             }
-        } else if (l.live && l.row + r < rows) {
-            *(raw*)(base + (t0 + l.row + r) * row + (int64_t)l.c * (int64_t)sizeof(T)) = v;
+        } else if (l.live && l.row + r < t.rows) {
+            *(raw*)(t.at + (t.t0 + l.row + r) * row + (int64_t)l.c * (int64_t)sizeof(T)) = v;
         }
     }
-    // Zeros in rows [from, to) of 64 channels from c0 on, by the whole workgroup.
-    __device__ __forceinline__ void clear(int from, int to, int c0, int D) const
+    // Zeros in rows [from, to) of CH channels from c0 on, by the whole workgroup.
+    template <int CH> __device__ __forceinline__ void clear(int from, int to, int c0, int D) const
     {
-        const int c = c0 + (threadIdx.x & 63);
+        const int c = c0 + (int)(threadIdx.x % CH);
         if (c >= D) return;
-        for (int64_t t = from + (int)(threadIdx.x >> 6); t < to; t += kWaves) *(T*)(base + t * row + c * (int64_t)sizeof(T)) = from_float<T>(0.0f);
+        for (int64_t t = from + (int)(threadIdx.x / CH); t < to; t += 64 * kWaves / CH)
+            *(T*)(base + t * row + c * (int64_t)sizeof(T)) = from_float<T>(0.0f);
     }
 };
 
-// Whether a tensor's rows can be walked by buffer instructions in tiles of `tile` rows, and lie at multiples of `bytes`.
-inline bool walks(const Rows& m, const DiagProblem& p, int tile)
+// Whether a tensor's rows can be walked by buffer instructions, and whether they lie at multiples of `bytes`.
+inline bool walks(const Rows& m, const DiagProblem& p)
 {
+    constexpr int tile = Shape<16, 1>::tile;           // the longest
     const int64_t row = m.row * (p.bf16 ? 2 : 4);
     return !m.p || (m.row >= p.D && row <= ((int64_t(1) << 31) - 1) / tile);
 }
@@ -224,67 +262,147 @@ inline bool aligned(const Rows& m, const DiagProblem& p, size_t bytes)
     return !m.p || ((uintptr_t)m.p % bytes == 0 && (p.B == 1 || m.batch * e % bytes == 0) && (p.T == 1 || m.row * e % bytes == 0));
 }
 
-// The value of the lower and of the upper half of the wave, in every lane.
-__device__ __forceinline__ void halves(float v, float* low, float* high)
+// The value of the lower and of the upper of the two lanes D apart (the one with bit D clear, and set), in both.
+template <int D> __device__ __forceinline__ void pair_of(float v, int lane, float* low, float* high)
 {
     const unsigned u = __builtin_bit_cast(unsigned, v);
-    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    const unsigned a = r[0], b = r[1];
-    *low = __builtin_bit_cast(float, a);
-    *high = __builtin_bit_cast(float, b);
+    if constexpr (D == 8) {
+        const float o = __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp((int)u, 0x128, 0xf, 0xf, true));   // rotated by 8 of 16
+        *low = lane & 8 ? o : v;
+        *high = lane & 8 ? v : o;
+    } else {
+        const auto r = D == 16 ? __builtin_amdgcn_permlane16_swap(u, u, false, false)
+                               : __builtin_amdgcn_permlane32_swap(u, u, false, false);
+        const unsigned x = r[0], y = r[1];
+        *low = __builtin_bit_cast(float, x);
+        *high = __builtin_bit_cast(float, y);
+    }
 }
 
-// How a sequence is cut: nseg segments of len rows (whole chunks), walked by workgroups of their own.
-struct Segments {
-    int len, nseg, ncb;
+// Joins the row groups of a wave, D lanes apart and more: F, H go from the map of a lane's group to the wave's, pf, ph
+// (1, 0 before) to the map of the groups before it.
+template <int D> __device__ __forceinline__ void join(int lane, float* F, float* H, float* pf, float* ph)
+{
+    if constexpr (D < 64) {
+        float lf, uf, lh, uh;
+        pair_of<D>(*F, lane, &lf, &uf);
+        pair_of<D>(*H, lane, &lh, &uh);
+        const bool upper = lane & D;
+        *ph += *pf * (upper ? lh : 0.0f);
+        *pf *= upper ? lf : 1.0f;
+        *F = lf * uf;
+        *H = uf * lh + uh;
+        join<2 * D>(lane, F, H, pf, ph);
+    }
+}
+// The same with the adjoint's map a -> F a + A, qf, qa the map of the groups behind.
+template <int D>
+__device__ __forceinline__ void join_both(int lane, float* F, float* H, float* A, float* pf, float* ph, float* qf, float* qa)
+{
+    if constexpr (D < 64) {
+        float lf, uf, lh, uh, la, ua;
+        pair_of<D>(*F, lane, &lf, &uf);
+        pair_of<D>(*H, lane, &lh, &uh);
+        pair_of<D>(*A, lane, &la, &ua);
+        const bool upper = lane & D;
+        *ph += *pf * (upper ? lh : 0.0f);
+        *pf *= upper ? lf : 1.0f;
+        *qa += *qf * (upper ? 0.0f : ua);
+        *qf *= upper ? 1.0f : uf;
+        *F = lf * uf;
+        *H = uf * lh + uh;
+        *A = lf * ua + la;
+        join_both<2 * D>(lane, F, H, A, pf, ph, qf, qa);
+    }
+}
+
+// F and A alone.
+template <int D> __device__ __forceinline__ void join_behind(int lane, float* F, float* A)
+{
+    if constexpr (D < 64) {
+        float lf, uf, la, ua;
+        pair_of<D>(*F, lane, &lf, &uf);
+        pair_of<D>(*A, lane, &la, &ua);
+        *F = lf * uf;
+        *A = lf * ua + la;
+        join_behind<2 * D>(lane, F, A);
+    }
+}
+// The sum over the row groups.
+template <int D> __device__ __forceinline__ float sum_groups(int lane, float v)
+{
+    if constexpr (D < 64) {
+        float a, b;
+        pair_of<D>(v, lane, &a, &b);
+        return sum_groups<2 * D>(lane, a + b);
+    }
+    return v;
+}
+
+// How the work is cut: ncb blocks of ch channels, nseg segments of len rows (whole tiles), each walked by a workgroup
+// of its own; `near` blocks share lines.
+struct Cut {
+    int ch, ncb, nseg, len, near;
+    int64_t blocks;
 };
 
 struct Place {
     int seg, cb;
     int64_t b;
 };
-__device__ __forceinline__ bool place(const DiagProblem& p, const Segments& sg, Place* q)
+// Workgroups go to the eight XCDs in turn; neighbouring channels go to one of them.
+__device__ __forceinline__ bool place(const DiagProblem& p, const Cut& cut, Place* q)
 {
-    int64_t i = block_id();
-    q->cb = (int)(i % sg.ncb);
-    i /= sg.ncb;
-    q->seg = (int)(i % sg.nseg);
-    q->b = i / sg.nseg;
+    const int64_t id = block_id(), k = id / 8;
+    int64_t i = (k / cut.near * 8 + id % 8) * cut.near + k % cut.near;
+    q->cb = (int)(i % cut.ncb);
+    i /= cut.ncb;
+    q->seg = (int)(i % cut.nseg);
+    q->b = i / cut.nseg;
     return q->b < p.B;
 }
 
-template <int V, int PER> __device__ __forceinline__ Lane lane_of(const DiagProblem& p, const Place& q, int* half)
+template <int CH, int V> __device__ __forceinline__ Lane lane_of(const DiagProblem& p, const Place& q)
 {
+    typedef Shape<CH, V> S;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    *half = lane / (64 / V);
     Lane l;
-    l.row = wave * PER + *half * (PER / V);
-    l.c = q.cb * 64 + lane % (64 / V) * V;
+    l.row = wave * S::rows + lane / S::lanes * S::R;
+    l.c = q.cb * CH + lane % S::lanes * V;
     l.live = l.c < p.D;
     l.last = p.D - V;
     return l;
 }
 
-inline Segments segments_of(const DiagProblem& p, int tile)
+inline int64_t blocks_of(const DiagProblem& p, int ch) { return (int64_t)p.B * ((p.D + ch - 1) / ch); }
+
+// wide: 64 channels to a workgroup whatever their number.
+inline Cut cut_of(const DiagProblem& p, bool wide)
 {
-    Segments s;
-    s.ncb = (p.D + 63) / 64;
-    const int64_t blocks = (int64_t)p.B * s.ncb;
+    Cut c;
+    c.ch = wide || blocks_of(p, 64) >= 256 ? 64 : blocks_of(p, 32) >= 256 ? 32 : 16;
+    c.ncb = (p.D + c.ch - 1) / c.ch;
+    c.near = 64 / c.ch;
+    const int tile = kWaves * kPer * 64 / c.ch;
     const int tiles = (p.T + tile - 1) / tile;
-    int64_t n = blocks >= 256 ? 1 : 512 / blocks;
+    const int64_t blocks = (int64_t)p.B * c.ncb;
+    int64_t n = blocks >= 128 || (c.ch == 64 && !wide) ? 1 : 256 / blocks;
     if (n > tiles) n = tiles;
+    if (n < 1) n = 1;
     const int per = (int)((tiles + n - 1) / n);
-    s.len = per * tile;
-    s.nseg = (tiles + per - 1) / per;
-    return s;
+    c.len = per * tile;
+    c.nseg = (tiles + per - 1) / per;
+    const int64_t g = 8 * c.near, all = blocks * c.nseg;
+    c.blocks = (all + g - 1) / g * g;
+    return c;
 }
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// The segments' sums, [B][nseg][D] pairs, at the start of the workspace.
-inline size_t ends_bytes(const DiagProblem& p, const Segments& s)
+// The segments' maps, [B][nseg][D] pairs, at the start of the workspace.
+inline size_t ends_bytes(const DiagProblem& p, const Cut& c)
 {
-    return s.nseg > 1 ? align256((size_t)p.B * s.nseg * p.D * sizeof(f32x2)) : 0;
+    return c.nseg > 1 ? align256((size_t)p.B * c.nseg * p.D * sizeof(f32x2)) : 0;
 }
 
 }  // namespace diag
