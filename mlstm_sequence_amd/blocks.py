@@ -164,6 +164,9 @@ def _rows(t, name, shape, dtype, dev):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
+# the current device, which tensors in GPU memory have initialised, without the checks around it
+_this_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
 _HERE = contextlib.nullcontext()
 
 
@@ -192,7 +195,7 @@ def _call(name, packed, dev, nbytes=None, workspace=None, fn=None):
     """Calls entry point ``name`` (of this module, or ``fn``) on the current
     stream of the tensors' device with that device current; ``nbytes``: the
     workspace it needs."""
-    if dev != torch.cuda.current_device():
+    if dev != _this_device():
         with torch.cuda.device(dev):
             return _call(name, packed, dev, nbytes, workspace, fn)
     fn = fn or _fn[name]

@@ -323,7 +323,9 @@ int tfla_addnorm_bwd(const tfla_addnorm_args* args, void* workspace, size_t work
         int rc = check_addnorm(args, true, &p, &w);
         if (rc) return rc;
         hipStream_t s = static_cast<hipStream_t>(stream);
-        return with_workspace(workspace, workspace_bytes, tfla::addnorm_bwd_workspace(p), w.v, w.n, s, [&](char* base) {
+        // the weights' gradients alone take memory
+        const size_t need = p.dweight || p.dbias ? tfla::addnorm_bwd_workspace(p) : 0;
+        return with_workspace(workspace, workspace_bytes, need, w.v, w.n, s, [&](char* base) {
             p.ws = base;
             return hip_status(tfla::launch_addnorm_bwd(p, s), "norm gradient kernel launch");
         });

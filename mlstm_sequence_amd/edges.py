@@ -18,10 +18,8 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .blocks import (
-    _HEADS, _IO, _NO_HEADS, _NO_ROWS, _ROWS, Heads, Rows, _bad, _call, _current, _first, _fits, _flat, _heads, _i,
-    _ll, _p, _ptr, _rows,
-)
+from . import blocks as _blocks
+from .blocks import _HEADS, _IO, _NO_HEADS, _NO_ROWS, _ROWS, Heads, Rows, _bad, _call, _current, _i, _ll, _p
 
 ROTARY_HALVES, ROTARY_INTERLEAVED = 0, 0x4000   # pairs: channels j and j + R/2, or 2j and 2j + 1
 DIAG_COUPLED, DIAG_SIGMOID, DIAG_DECAY = 0, 1, 2
@@ -87,6 +85,50 @@ _DIAG = struct.Struct("@5i" + _ROWS * 3 + "3P" + _ROWS + "2P" + _ROWS + "P" + _R
 _ADDNORM = struct.Struct("@4if" + _ROWS * 2 + "2P" + _ROWS * 6 + "2P")
 
 
+# ---- checks --------------------------------------------------------------------------
+#
+# As in blocks.py, each in one step: a call of single tokens spends most of its
+# time here.
+
+def _first(x, name, dims):
+    """Checks the tensor that sets type and device; returns the device's index."""
+    if isinstance(x, torch.Tensor) and x.dtype in _IO and x.dim() == dims and x.is_cuda and 0 < x.numel() <= 0x7FFFFFFF:
+        return x.get_device()
+    return _blocks._first(x, name, dims)   # says what does not fit, or that a large tensor does
+
+
+def _new(x):
+    """A contiguous tensor of the shape and type of ``x``."""
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+
+
+def _flat(t, name, shape, dtype, dev):
+    """Pointer of a contiguous tensor (None: NULL)."""
+    if t is None:
+        return 0
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _bad(t, name, shape, dtype, dev)
+
+
+def _rows(t, name, shape, dtype, dev):
+    """tfla_rows of a [B,T,D] tensor with contiguous channels."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        batch, row, one = t.stride()
+        if one == 1 or shape[2] <= 1:
+            return t.data_ptr(), batch, row
+    _bad(t, name, shape, dtype, dev)
+
+
+def _heads(t, name, shape, dtype, dev):
+    """tfla_heads of a [B,T,G,C] tensor with contiguous channels."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        batch, row, group, one = t.stride()
+        if one == 1 or shape[3] <= 1:
+            return t.data_ptr(), batch, row, group
+    _bad(t, name, shape, dtype, dev)
+
+
 # ---- rotary positions ------------------------------------------------------------
 
 def rotary_frequencies(dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -128,45 +170,46 @@ def rotary_frequencies(dim: int, base: float = 10000.0, scaling: str = "none", f
 
 
 def _rotary(name, q, k, freqs, layout, scale, positions, start, lengths, q_out, k_out, head_major, stream):
-    fn = _entry(name)
-    with _current(stream, q):
-        dev = _first(q, "q", 4)
-        shape, dtype = q.shape, q.dtype
-        B, T, H, C = shape
-        if layout not in (ROTARY_HALVES, ROTARY_INTERLEAVED):
-            raise ValueError(f"layout must be ROTARY_HALVES or ROTARY_INTERLEAVED, got {layout}")
-        if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
-            raise ValueError("freqs must be a one-dimensional fp64 tensor")
-        if k is None and k_out is not None:
-            raise ValueError("k_out is given without k")
-        if k is not None and (not isinstance(k, torch.Tensor) or k.dim() != 4):
+    if stream is not None:
+        with _current(stream, q):
+            return _rotary(name, q, k, freqs, layout, scale, positions, start, lengths, q_out, k_out, head_major, None)
+    fn = _fn.get(name) or _entry(name)
+    dev = _first(q, "q", 4)
+    shape, dtype = q.shape, q.dtype
+    B, T, H, C = shape
+    if layout not in (ROTARY_HALVES, ROTARY_INTERLEAVED):
+        raise ValueError(f"layout must be ROTARY_HALVES or ROTARY_INTERLEAVED, got {layout}")
+    if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
+        raise ValueError("freqs must be a one-dimensional fp64 tensor")
+    half = freqs.shape
+    if q_out is None:
+        q_out = q.new_empty((B, H, T, C)).transpose(1, 2) if head_major else _new(q)
+    Hk, keys, keys_out = 0, _NO_HEADS, _NO_HEADS
+    if k is not None:
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
             raise ValueError("k must be a [B,T,Hk,C] tensor")
-        Hk = 0 if k is None else k.shape[2]
+        Hk = k.shape[2]
         kshape = (B, T, Hk, C)
-        at = stride = 0
-        if positions is not None:
-            if isinstance(positions, torch.Tensor) and positions.dim() == 1:
-                positions = positions.expand(B, T) if positions.shape == (T,) else positions
-            if not _fits(positions, (B, T), torch.int32, dev) or (T > 1 and positions.stride(1) != 1):
-                _bad(positions, "positions", (B, T), torch.int32, dev)
-            at, stride = positions.data_ptr(), positions.stride(0)
-
-        def out(t, like):
-            if t is not None or like is None:
-                return t
-            b, n, h, c = like.shape
-            return q.new_empty((b, h, n, c)).transpose(1, 2) if head_major else q.new_empty(like.shape)
-
-        q_out, k_out = out(q_out, q), out(k_out, k)
-        packed = _ROTARY.pack(B, T, H, Hk, C, 2 * freqs.shape[0], _IO[dtype] | layout, float(scale),
-                              _flat(freqs, "freqs", (freqs.shape[0],), torch.float64, dev), at, stride,
-                              _flat(start, "start", (B,), torch.int32, dev), _flat(lengths, "lengths", (B,), torch.int32, dev),
-                              *_heads(q, "q", shape, dtype, dev),
-                              *(_NO_HEADS if k is None else _heads(k, "k", kshape, dtype, dev)),
-                              *_heads(q_out, "q_out", shape, dtype, dev),
-                              *(_NO_HEADS if k is None else _heads(k_out, "k_out", kshape, dtype, dev)))
-        _call(name, packed, dev, fn=fn)
-        return q_out, k_out
+        keys = _heads(k, "k", kshape, dtype, dev)
+        if k_out is None:
+            k_out = k.new_empty((B, Hk, T, C)).transpose(1, 2) if head_major else _new(k)
+        keys_out = _heads(k_out, "k_out", kshape, dtype, dev)
+    elif k_out is not None:
+        raise ValueError("k_out is given without k")
+    at = stride = 0
+    if positions is not None:
+        shared = isinstance(positions, torch.Tensor) and positions.dim() == 1
+        want = (T,) if shared else (B, T)
+        if not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int32 or positions.shape != want \
+                or positions.get_device() != dev or (T > 1 and positions.stride(-1) != 1):
+            _bad(positions, "positions", want, torch.int32, dev)
+        at, stride = positions.data_ptr(), 0 if shared else positions.stride(0)
+    packed = _ROTARY.pack(B, T, H, Hk, C, 2 * half[0], _IO[dtype] | layout, scale,
+                          _flat(freqs, "freqs", half, torch.float64, dev), at, stride,
+                          _flat(start, "start", (B,), torch.int32, dev), _flat(lengths, "lengths", (B,), torch.int32, dev),
+                          *_heads(q, "q", shape, dtype, dev), *keys, *_heads(q_out, "q_out", shape, dtype, dev), *keys_out)
+    _call(name, packed, dev, None, None, fn)
+    return q_out, k_out
 
 
 def rotary_forward(q, k, freqs, layout: int = ROTARY_HALVES, scale: float = 1.0, positions=None, start=None, lengths=None,
@@ -219,8 +262,8 @@ def _diag_args(x, fgate, igate, decay, kind, lengths):
             _flat(decay, "decay", (D,), torch.float32, dev), _flat(lengths, "lengths", (B,), torch.int32, dev)), sizes, dev
 
 
-def _chunks(x):
-    B, T, D = x.shape
+def _chunks(shape):
+    B, T, D = shape
     return B, -(-T // DIAG_CHUNK), D
 
 
@@ -239,22 +282,26 @@ def diag_forward(x, fgate, igate=None, decay=None, kind: int = DIAG_COUPLED, sta
     last; ``starts`` (allocated with ``want_starts``) fp32
     [B, ceil(T / DIAG_CHUNK), D] the states that :func:`diag_backward` needs.
     ``lengths`` int32 [B]: valid rows of a padded batch."""
-    need, fn = _entry("tfla_diag_workspace_bytes"), _entry("tfla_diag_fwd")
-    with _current(stream, x):
-        fields, sizes, dev = _diag_args(x, fgate, igate, decay, kind, lengths)
-        shape, dtype, f32 = x.shape, x.dtype, torch.float32
-        B, _, D = shape
-        if y is None:
-            y = x.new_empty(shape)
-        if state_out is None and want_state:
-            state_out = torch.empty((B, D), dtype=f32, device=x.device)
-        if starts is None and want_starts:
-            starts = torch.empty(_chunks(x), dtype=f32, device=x.device)
-        packed = _DIAG.pack(*fields, _flat(state, "state", (B, D), f32, dev), *_rows(y, "y", shape, dtype, dev),
-                            _flat(state_out, "state_out", (B, D), f32, dev), _flat(starts, "starts", _chunks(x), f32, dev),
-                            *_NO_ROWS, 0, *_NO_ROWS * 3, 0, 0)
-        _call("tfla_diag_fwd", packed, dev, need(*sizes), workspace, fn)
-        return y, state_out, starts
+    if stream is not None:
+        with _current(stream, x):
+            return diag_forward(x, fgate, igate, decay, kind, state, lengths, want_state, want_starts, y, state_out, starts,
+                                workspace)
+    need = _fn.get("tfla_diag_workspace_bytes") or _entry("tfla_diag_workspace_bytes")
+    fields, sizes, dev = _diag_args(x, fgate, igate, decay, kind, lengths)
+    shape, dtype, f32 = x.shape, x.dtype, torch.float32
+    bd = (shape[0], shape[2])
+    if y is None:
+        y = _new(x)
+    if state_out is None and want_state:
+        state_out = x.new_empty(bd, dtype=f32)
+    if starts is None and want_starts:
+        starts = x.new_empty(_chunks(shape), dtype=f32)
+    packed = _DIAG.pack(*fields, _flat(state, "state", bd, f32, dev), *_rows(y, "y", shape, dtype, dev),
+                        _flat(state_out, "state_out", bd, f32, dev),
+                        0 if starts is None else _flat(starts, "starts", _chunks(shape), f32, dev),
+                        *_NO_ROWS, 0, *_NO_ROWS * 3, 0, 0)
+    _call("tfla_diag_fwd", packed, dev, need(*sizes), workspace, _fn["tfla_diag_fwd"])
+    return y, state_out, starts
 
 
 def diag_backward(x, fgate, dy, starts, igate=None, decay=None, kind: int = DIAG_COUPLED, lengths=None, dstate_out=None,
@@ -263,26 +310,35 @@ def diag_backward(x, fgate, dy, starts, igate=None, decay=None, kind: int = DIAG
     ``dstate_out``, from the ``starts`` it left; dx, dfgate and digate may be
     given, as parts of a projection's gradient for instance.  The gradient of
     the state before the first row comes with ``want_dstate``."""
-    need, fn = _entry("tfla_diag_bwd_workspace_bytes"), _entry("tfla_diag_bwd")
-    with _current(stream, x):
-        fields, sizes, dev = _diag_args(x, fgate, igate, decay, kind, lengths)
-        shape, dtype, f32 = x.shape, x.dtype, torch.float32
-        B, _, D = shape
-        if starts is None:
-            raise ValueError("starts is needed: the states that diag_forward leaves with want_starts")
-        if digate is not None and igate is None:
-            raise ValueError("digate is given without igate")
-        dx, dfgate = (x.new_empty(shape) if t is None else t for t in (dx, dfgate))
-        digate = None if igate is None else x.new_empty(shape) if digate is None else digate
-        ddecay = None if decay is None else torch.empty_like(decay)
-        dstate = torch.empty((B, D), dtype=f32, device=x.device) if want_dstate else None
-        packed = _DIAG.pack(*fields, 0, *_NO_ROWS, 0, _flat(starts, "starts", _chunks(x), f32, dev),
-                            *_rows(dy, "dy", shape, dtype, dev), _flat(dstate_out, "dstate_out", (B, D), f32, dev),
-                            *_rows(dx, "dx", shape, dtype, dev), *_rows(dfgate, "dfgate", shape, dtype, dev),
-                            *(_NO_ROWS if igate is None else _rows(digate, "digate", shape, dtype, dev)),
-                            _ptr(ddecay), _ptr(dstate))
-        _call("tfla_diag_bwd", packed, dev, need(*sizes), workspace, fn)
-        return DiagGrads(dx, dfgate, digate, ddecay, dstate)
+    if stream is not None:
+        with _current(stream, x):
+            return diag_backward(x, fgate, dy, starts, igate, decay, kind, lengths, dstate_out, want_dstate, dx, dfgate,
+                                 digate, workspace)
+    need = _fn.get("tfla_diag_bwd_workspace_bytes") or _entry("tfla_diag_bwd_workspace_bytes")
+    fields, sizes, dev = _diag_args(x, fgate, igate, decay, kind, lengths)
+    shape, dtype, f32 = x.shape, x.dtype, torch.float32
+    bd = (shape[0], shape[2])
+    if starts is None:
+        raise ValueError("starts is needed: the states that diag_forward leaves with want_starts")
+    if dx is None:
+        dx = _new(x)
+    if dfgate is None:
+        dfgate = _new(x)
+    gate = _NO_ROWS
+    if igate is not None:
+        if digate is None:
+            digate = _new(x)
+        gate = _rows(digate, "digate", shape, dtype, dev)
+    elif digate is not None:
+        raise ValueError("digate is given without igate")
+    ddecay = None if decay is None else torch.empty_like(decay)
+    dstate = x.new_empty(bd, dtype=f32) if want_dstate else None
+    packed = _DIAG.pack(*fields, 0, *_NO_ROWS, 0, _flat(starts, "starts", _chunks(shape), f32, dev),
+                        *_rows(dy, "dy", shape, dtype, dev), _flat(dstate_out, "dstate_out", bd, f32, dev),
+                        *_rows(dx, "dx", shape, dtype, dev), *_rows(dfgate, "dfgate", shape, dtype, dev), *gate,
+                        0 if ddecay is None else ddecay.data_ptr(), 0 if dstate is None else dstate.data_ptr())
+    _call("tfla_diag_bwd", packed, dev, need(*sizes), workspace, _fn["tfla_diag_bwd"])
+    return DiagGrads(dx, dfgate, digate, ddecay, dstate)
 
 
 # ---- residual sum with a norm ---------------------------------------------------------
@@ -305,26 +361,31 @@ def addnorm_forward(x, residual=None, weight=None, bias=None, eps: float = 1e-5,
     residual and total are of x's type or fp32; ``total`` may be ``residual``
     itself.  y comes from the sum before it is rounded to total's type.
     weight, bias are fp32 [C]."""
-    fn = _entry("tfla_addnorm_fwd")
-    with _current(stream, x):
-        dev = _first(x, "x", 3)
-        shape, dtype, f32 = x.shape, x.dtype, torch.float32
-        C = shape[2]
-        if residual is None and total is not None:
-            raise ValueError("total is given without a residual")
-        st = dtype if residual is None else _stream_type(residual, "residual", dtype)
-        if y is None:
-            y = x.new_empty(shape)
-        if total is None and residual is not None:
-            total = torch.empty(shape, dtype=st, device=x.device)
-        flags = _IO[dtype] | (_RMS if rms else 0) | (_SUM_FP32 if st != dtype else 0)
-        packed = _ADDNORM.pack(*shape, flags, float(eps), *_rows(x, "x", shape, dtype, dev),
-                               *(_NO_ROWS if residual is None else _rows(residual, "residual", shape, st, dev)),
-                               _flat(weight, "weight", (C,), f32, dev), _flat(bias, "bias", (C,), f32, dev),
-                               *_rows(y, "y", shape, dtype, dev),
-                               *(_NO_ROWS if residual is None else _rows(total, "total", shape, st, dev)), *_NO_ROWS * 4, 0, 0)
-        _call("tfla_addnorm_fwd", packed, dev, fn=fn)
-        return y, total
+    if stream is not None:
+        with _current(stream, x):
+            return addnorm_forward(x, residual, weight, bias, eps, rms, y, total)
+    fn = _fn.get("tfla_addnorm_fwd") or _entry("tfla_addnorm_fwd")
+    dev = _first(x, "x", 3)
+    shape, dtype, f32 = x.shape, x.dtype, torch.float32
+    flags, c = _IO[dtype] | (_RMS if rms else 0), shape[2:]
+    res = tot = _NO_ROWS
+    if y is None:
+        y = _new(x)
+    if residual is not None:
+        st = _stream_type(residual, "residual", dtype)
+        if st is not dtype:
+            flags |= _SUM_FP32
+        res = _rows(residual, "residual", shape, st, dev)
+        if total is None:
+            total = _new(residual)
+        tot = _rows(total, "total", shape, st, dev)
+    elif total is not None:
+        raise ValueError("total is given without a residual")
+    packed = _ADDNORM.pack(*shape, flags, eps, *_rows(x, "x", shape, dtype, dev), *res,
+                           _flat(weight, "weight", c, f32, dev), _flat(bias, "bias", c, f32, dev),
+                           *_rows(y, "y", shape, dtype, dev), *tot, *_NO_ROWS * 4, 0, 0)
+    _call("tfla_addnorm_fwd", packed, dev, None, None, fn)
+    return y, total
 
 
 def addnorm_backward(total, dy, weight=None, bias: bool = False, eps: float = 1e-5, rms: bool = False, dtotal=None, dx=None,
@@ -336,27 +397,33 @@ def addnorm_backward(total, dy, weight=None, bias: bool = False, eps: float = 1e
     The gradient of the sum, in dy's type and in total's: one tensor where
     these are the same.  dweight comes where weight is given, dbias with
     ``bias``."""
-    need, fn = _entry("tfla_addnorm_bwd_workspace_bytes"), _entry("tfla_addnorm_bwd")
-    with _current(stream, dy):
-        dev = _first(dy, "dy", 3)
-        shape, dtype, f32 = dy.shape, dy.dtype, torch.float32
-        B, T, C = shape
-        st = _stream_type(total, "total", dtype)
-        if dx is None:
-            dx = dy.new_empty(shape)
-        if st == dtype:
-            if dresidual is not None and dresidual is not dx:
-                raise ValueError("dresidual is dx where dy and total have one type")
-        elif dresidual is None:
-            dresidual = torch.empty(shape, dtype=st, device=dy.device)
-        dweight = None if weight is None else torch.empty_like(weight)
-        dbias = torch.empty((C,), dtype=f32, device=dy.device) if bias else None
-        flags = _IO[dtype] | (_RMS if rms else 0) | (_SUM_FP32 if st != dtype else 0)
-        packed = _ADDNORM.pack(B, T, C, flags, float(eps), *_NO_ROWS * 2, _flat(weight, "weight", (C,), f32, dev), 0,
-                               *_NO_ROWS, *_rows(total, "total", shape, st, dev), *_rows(dy, "dy", shape, dtype, dev),
-                               *(_NO_ROWS if dtotal is None else _rows(dtotal, "dtotal", shape, st, dev)),
-                               *_rows(dx, "dx", shape, dtype, dev),
-                               *(_NO_ROWS if st == dtype else _rows(dresidual, "dresidual", shape, st, dev)),
-                               _ptr(dweight), _ptr(dbias))
-        _call("tfla_addnorm_bwd", packed, dev, need(B, T, C, flags), workspace, fn)
-        return dx, dx if st == dtype else dresidual, dweight, dbias
+    if stream is not None:
+        with _current(stream, dy):
+            return addnorm_backward(total, dy, weight, bias, eps, rms, dtotal, dx, dresidual, workspace)
+    need = _fn.get("tfla_addnorm_bwd_workspace_bytes") or _entry("tfla_addnorm_bwd_workspace_bytes")
+    dev = _first(dy, "dy", 3)
+    shape, dtype, f32 = dy.shape, dy.dtype, torch.float32
+    flags, c = _IO[dtype] | (_RMS if rms else 0), shape[2:]
+    st = _stream_type(total, "total", dtype)
+    res = _NO_ROWS
+    if dx is None:
+        dx = _new(dy)
+    if st is dtype:
+        if dresidual is not None and dresidual is not dx:
+            raise ValueError("dresidual is dx where dy and total have one type")
+        dresidual = dx
+    else:
+        flags |= _SUM_FP32
+        if dresidual is None:
+            dresidual = _new(total)
+        res = _rows(dresidual, "dresidual", shape, st, dev)
+    dweight = None if weight is None else torch.empty_like(weight)
+    dbias = dy.new_empty(c, dtype=f32) if bias else None
+    packed = _ADDNORM.pack(*shape, flags, eps, *_NO_ROWS * 2, _flat(weight, "weight", c, f32, dev), 0, *_NO_ROWS,
+                           *_rows(total, "total", shape, st, dev), *_rows(dy, "dy", shape, dtype, dev),
+                           *(_NO_ROWS if dtotal is None else _rows(dtotal, "dtotal", shape, st, dev)),
+                           *_rows(dx, "dx", shape, dtype, dev), *res,
+                           0 if dweight is None else dweight.data_ptr(), 0 if dbias is None else dbias.data_ptr())
+    wanted = need(*shape, flags) if weight is not None or bias else None
+    _call("tfla_addnorm_bwd", packed, dev, wanted or 0, workspace if wanted else None, _fn["tfla_addnorm_bwd"])
+    return dx, dresidual, dweight, dbias
