@@ -36,8 +36,8 @@ __global__ __launch_bounds__(1024) void addnorm_fwd_kernel(AddNormProblem p, Row
         }
     }
     const float inv = 1.0f / (float)p.C;
-    Pack<T, VEC> rx[NV];
-    Pack<S, VEC> rr[NV];
+    Pack<T, VEC, false> rx[NV];
+    Pack<S, VEC, false> rr[NV];
     auto fetch = [&](unsigned i) {                    // behind the last row: the last
         i = min(i, m.rows - 1);
         const int64_t b = i / (unsigned)p.T, t = i % (unsigned)p.T;
@@ -85,8 +85,8 @@ __global__ __launch_bounds__(1024) void addnorm_fwd_kernel(AddNormProblem p, Row
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             if (!in[k]) continue;
-            Pack<T, VEC> o;
-            Pack<S, VEC> ot;
+            Pack<T, VEC, false> o;
+            Pack<S, VEC, false> ot;
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
                 o.set(v, (x[k][v] - mean) * rstd * w[k][v] + bs[k][v]);
@@ -130,20 +130,22 @@ __global__ __launch_bounds__(256) void addnorm_fwd_long_kernel(AddNormProblem p)
 template <typename T, typename S, int VEC>
 hipError_t fwd_v(const AddNormProblem& p, hipStream_t stream)
 {
-    if (p.C / VEC > kMostVectors) {
+    if (!in_registers(p, VEC)) {
         addnorm_fwd_long_kernel<T, S><<<grid_of((int64_t)p.B * p.T), 256, 0, stream>>>(p);
         return hipGetLastError();
     }
-    const RowMap m = row_map(p, VEC, kBlocks);
-    if (m.nv <= m.L) addnorm_fwd_kernel<T, S, VEC, 1><<<m.blocks, m.threads, 0, stream>>>(p, m);
-    else addnorm_fwd_kernel<T, S, VEC, 2><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    const RowMap m = row_map(p, VEC, most_vectors(p, VEC), kBlocks);
+    const int v = (m.nv + m.L - 1) / m.L;
+    if (v == 1) addnorm_fwd_kernel<T, S, VEC, 1><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    else if (v == 2) addnorm_fwd_kernel<T, S, VEC, 2><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    else if constexpr (most_vectors<T, S, VEC>() == 4) addnorm_fwd_kernel<T, S, VEC, 4><<<m.blocks, m.threads, 0, stream>>>(p, m);
     return hipGetLastError();
 }
 
 template <typename T, typename S>
 hipError_t fwd_t(const AddNormProblem& p, hipStream_t stream)
 {
-    constexpr int wide = 16 / sizeof(T);
+    constexpr int wide = 16 / (sizeof(T) > sizeof(S) ? sizeof(T) : sizeof(S));
     return vec_of(p, {&p.x, &p.residual, &p.y, &p.total}) == wide ? fwd_v<T, S, wide>(p, stream) : fwd_v<T, S, 1>(p, stream);
 }
 

@@ -18,10 +18,27 @@ namespace {
 
 using namespace addnorm;
 
-constexpr unsigned kBlocks = 768;   // also the parts of the weights' gradients
+// How the rows fall to workgroups, and the parts of the weights' gradients: enough to fill the chip, of 16 rows or
+// more beyond that.  Rows of 512 to 1024 vectors take one vector a lane, as two leave room for one workgroup of 8 waves
+// on a CU.
+RowMap map_of(const AddNormProblem& p, int vec)
+{
+    const int nv = p.C / vec, most = nv > 512 && nv <= 1024 ? 1 : most_vectors(p, vec);
+    RowMap m = row_map(p, vec, most, 768);
+    const unsigned few = (m.rows + 16 * m.slots - 1) / (16 * m.slots);
+    if (m.blocks > few) m.blocks = few > 512 ? few : m.blocks < 512 ? m.blocks : 512;
+    return m;
+}
+
+// Whether a call moves more than the last-level cache holds (256 MB): its loads then go past it.
+bool streams(const AddNormProblem& p)
+{
+    const int64_t e = p.bf16 ? 2 : 4, es = p.sum_fp32 ? 4 : e;
+    return (int64_t)p.B * p.T * p.C * (2 * e + (p.dtotal.p ? 2 : 1) * es) >= (int64_t(256) << 20);
+}
 
 // THREADS: the workgroup's size is at most that.
-template <typename T, typename S, int VEC, int NV, int THREADS>
+template <typename T, typename S, int VEC, int NV, int THREADS, bool NT>
 __global__ __launch_bounds__(THREADS) void addnorm_bwd_kernel(AddNormProblem p, RowMap m)
 {
     constexpr bool TWO = sizeof(T) != sizeof(S);
@@ -43,8 +60,8 @@ __global__ __launch_bounds__(THREADS) void addnorm_bwd_kernel(AddNormProblem p, 
         }
     }
     const float inv = 1.0f / (float)p.C;
-    Pack<S, VEC> rt[NV], re[NV];
-    Pack<T, VEC> rg[NV];
+    Pack<S, VEC, NT> rt[NV], re[NV];
+    Pack<T, VEC, NT> rg[NV];
     auto fetch = [&](unsigned i) {                    // behind the last row: the last
         i = min(i, m.rows - 1);
         const int64_t b = i / (unsigned)p.T, t = i % (unsigned)p.T;
@@ -62,7 +79,7 @@ __global__ __launch_bounds__(THREADS) void addnorm_bwd_kernel(AddNormProblem p, 
         const unsigned i = i0 + slot;
         const bool live = i < m.rows;
         float d[NV][VEC], g[NV][VEC], s = 0.0f, mean = 0.0f;
-        Pack<S, VEC> e[NV];
+        Pack<S, VEC, NT> e[NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             e[k] = re[k];
@@ -100,8 +117,8 @@ __global__ __launch_bounds__(THREADS) void addnorm_bwd_kernel(AddNormProblem p, 
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             if (!in[k]) continue;
-            Pack<T, VEC> o;
-            Pack<S, VEC> o2;
+            Pack<T, VEC, false> o;
+            Pack<S, VEC, false> o2;
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
                 dw[k][v] += g[k][v] * (d[k][v] * rstd);
@@ -232,10 +249,24 @@ hipError_t params(const AddNormProblem& p, int64_t parts, hipStream_t stream)
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 int64_t runs_of(const AddNormProblem& p) { return ((int64_t)p.B * p.T + kRun - 1) / kRun; }
 
+template <typename T, typename S, int VEC, bool NT>
+hipError_t bwd_n(const AddNormProblem& p, const RowMap& m, hipStream_t stream)
+{
+    const int v = (m.nv + m.L - 1) / m.L;
+    constexpr int most = most_vectors<T, S, VEC>();
+    if (m.threads > 512 && v == 1) addnorm_bwd_kernel<T, S, VEC, 1, 1024, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    else if (m.threads > 512) addnorm_bwd_kernel<T, S, VEC, most, 1024, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    else if (m.threads > 256) addnorm_bwd_kernel<T, S, VEC, most, 512, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    else if (v == 1) addnorm_bwd_kernel<T, S, VEC, 1, 256, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    else if (v == 2) addnorm_bwd_kernel<T, S, VEC, 2, 256, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    else if constexpr (most == 4) addnorm_bwd_kernel<T, S, VEC, 4, 256, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    return params(p, m.blocks, stream);
+}
+
 template <typename T, typename S, int VEC>
 hipError_t bwd_v(const AddNormProblem& p, hipStream_t stream)
 {
-    if (p.C / VEC > kMostVectors) {
+    if (!in_registers(p, VEC)) {
         f32x2* stats = (f32x2*)(p.ws + align256((size_t)runs_of(p) * 2 * p.C * sizeof(float)));
         addnorm_bwd_long_kernel<T, S><<<grid_of((int64_t)p.B * p.T), 256, 0, stream>>>(p, stats);
         const hipError_t e = hipGetLastError();
@@ -243,18 +274,16 @@ hipError_t bwd_v(const AddNormProblem& p, hipStream_t stream)
         addnorm_columns_kernel<T, S><<<grid_of(runs_of(p) * ((p.C + 255) / 256)), 256, 0, stream>>>(p, stats);
         return params(p, runs_of(p), stream);
     }
-    const RowMap m = row_map(p, VEC, kBlocks);
-    if (m.threads > 512) addnorm_bwd_kernel<T, S, VEC, 2, 1024><<<m.blocks, m.threads, 0, stream>>>(p, m);
-    else if (m.threads > 256) addnorm_bwd_kernel<T, S, VEC, 2, 512><<<m.blocks, m.threads, 0, stream>>>(p, m);
-    else if (m.nv <= m.L) addnorm_bwd_kernel<T, S, VEC, 1, 256><<<m.blocks, m.threads, 0, stream>>>(p, m);
-    else addnorm_bwd_kernel<T, S, VEC, 2, 256><<<m.blocks, m.threads, 0, stream>>>(p, m);
-    return params(p, m.blocks, stream);
+    const RowMap m = map_of(p, VEC);
+    if constexpr (VEC > 1)
+        if (streams(p)) return bwd_n<T, S, VEC, true>(p, m, stream);
+    return bwd_n<T, S, VEC, false>(p, m, stream);
 }
 
 template <typename T, typename S>
 hipError_t bwd_t(const AddNormProblem& p, hipStream_t stream)
 {
-    constexpr int wide = 16 / sizeof(T);
+    constexpr int wide = 16 / (sizeof(T) > sizeof(S) ? sizeof(T) : sizeof(S));
     return vec_of(p, {&p.total, &p.dy, &p.dtotal, &p.dx, &p.dresidual}) == wide ? bwd_v<T, S, wide>(p, stream)
                                                                                 : bwd_v<T, S, 1>(p, stream);
 }
@@ -266,10 +295,10 @@ size_t addnorm_bwd_workspace(const AddNormProblem& p)
 {
     const size_t row = 2 * (size_t)p.C * sizeof(float);
     size_t most = 0;
-    for (const int v : {1, p.bf16 ? 8 : 4}) {
+    for (const int v : {1, p.bf16 && !p.sum_fp32 ? 8 : 4}) {
         if (p.C % v) continue;
-        const size_t n = p.C / v > kMostVectors ? align256((size_t)runs_of(p) * row) + (size_t)p.B * p.T * sizeof(f32x2)
-                                                : row_map(p, v, kBlocks).blocks * row;
+        const size_t n = !in_registers(p, v) ? align256((size_t)runs_of(p) * row) + (size_t)p.B * p.T * sizeof(f32x2)
+                                                : map_of(p, v).blocks * row;
         if (n > most) most = n;
     }
     return most;
