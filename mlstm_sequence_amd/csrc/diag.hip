@@ -224,7 +224,7 @@ template <typename T, int KIND, int CH, int V, bool BUF>
 hipError_t fwd_v(const DiagProblem& p, const Cut& cut, hipStream_t stream)
 {
     f32x2* ends = (f32x2*)p.ws;
-    if constexpr (CH == 16 || !BUF) {
+    if constexpr (CH == 64) {
         if (cut.nseg > 1) {
             diag_fwd_kernel<T, KIND, CH, V, BUF, false><<<grid_of(cut.blocks), 64 * kWaves, 0, stream>>>(p, cut, ends);
             const hipError_t e = hipGetLastError();
@@ -238,7 +238,7 @@ hipError_t fwd_v(const DiagProblem& p, const Cut& cut, hipStream_t stream)
 template <typename T, int KIND, int V>
 hipError_t fwd_c(const DiagProblem& p, hipStream_t stream)
 {
-    const Cut cut = cut_of(p, false);
+    const Cut cut = cut_of(p, true, false);
     switch (cut.ch) {
     case 64: return fwd_v<T, KIND, 64, V, true>(p, cut, stream);
     case 32: return fwd_v<T, KIND, 32, V, true>(p, cut, stream);
@@ -258,7 +258,7 @@ hipError_t fwd_k(const DiagProblem& p, hipStream_t stream)
         buf = buf && walks(*m, p);
         two = two && aligned(*m, p, 2 * sizeof(T));
     }
-    if (!buf) return fwd_v<T, KIND, 64, 1, false>(p, cut_of(p, true), stream);
+    if (!buf) return fwd_v<T, KIND, 64, 1, false>(p, cut_of(p, false, false), stream);
     return two ? fwd_c<T, KIND, 2>(p, stream) : fwd_c<T, KIND, 1>(p, stream);
 }
 
@@ -277,7 +277,7 @@ hipError_t fwd_t(const DiagProblem& p, hipStream_t stream)
 // For whichever way the call's strides allow.
 size_t diag_workspace(const DiagProblem& p)
 {
-    return p.T <= kStepRows ? 0 : std::max(ends_bytes(p, cut_of(p, false)), ends_bytes(p, cut_of(p, true)));
+    return p.T <= kStepRows ? 0 : std::max(ends_bytes(p, cut_of(p, true, false)), ends_bytes(p, cut_of(p, false, false)));
 }
 
 hipError_t launch_diag_fwd(const DiagProblem& p, hipStream_t stream)

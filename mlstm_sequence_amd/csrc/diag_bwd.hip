@@ -351,7 +351,7 @@ hipError_t bwd_v(const DiagProblem& p, const Cut& cut, hipStream_t stream)
     const int64_t parts = (int64_t)p.B * cut.nseg;
     float* part = parts == 1 ? p.ddecay : (float*)(p.ws + ends_bytes(p, cut));
     hipError_t e;
-    if constexpr (CH == 16 || !BUF) {
+    if constexpr (CH == 64) {
         if (cut.nseg > 1) {
             diag_adjoint_kernel<T, KIND, CH, V, BUF><<<grid_of(cut.blocks), 64 * kWaves, 0, stream>>>(p, cut, ends);
             if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -366,7 +366,7 @@ hipError_t bwd_v(const DiagProblem& p, const Cut& cut, hipStream_t stream)
 template <typename T, int KIND, int V>
 hipError_t bwd_c(const DiagProblem& p, hipStream_t stream)
 {
-    const Cut cut = cut_of(p, false);
+    const Cut cut = cut_of(p, true, true);
     switch (cut.ch) {
     case 64: return bwd_v<T, KIND, 64, V, true>(p, cut, stream);
     case 32: return bwd_v<T, KIND, 32, V, true>(p, cut, stream);
@@ -382,7 +382,7 @@ hipError_t bwd_k(const DiagProblem& p, hipStream_t stream)
         buf = buf && walks(*m, p);
         two = two && aligned(*m, p, 2 * sizeof(T));
     }
-    if (!buf) return bwd_v<T, KIND, 64, 1, false>(p, cut_of(p, true), stream);
+    if (!buf) return bwd_v<T, KIND, 64, 1, false>(p, cut_of(p, false, true), stream);
     return two ? bwd_c<T, KIND, 2>(p, stream) : bwd_c<T, KIND, 1>(p, stream);
 }
 
@@ -402,8 +402,8 @@ hipError_t bwd_t(const DiagProblem& p, hipStream_t stream)
 size_t diag_bwd_workspace(const DiagProblem& p)
 {
     size_t most = 0;
-    for (const bool wide : {false, true}) {
-        const Cut cut = cut_of(p, wide);
+    for (const bool buf : {true, false}) {
+        const Cut cut = cut_of(p, buf, true);
         const int64_t parts = (int64_t)p.B * cut.nseg;
         most = std::max(most, ends_bytes(p, cut) + (p.kind == kDecay && parts > 1 ? (size_t)parts * p.D * sizeof(float) : 0));
     }

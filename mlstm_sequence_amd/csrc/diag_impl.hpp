@@ -112,9 +112,9 @@ template <int KIND> __device__ __forceinline__ GateGrads grads_of(const Gate& k,
 // A workgroup owns CH neighbouring channels of a sequence and walks their rows in
 // tiles; a lane holds V neighbouring channels of 16 / V consecutive rows, CH / V
 // lanes side by side make a row group, the wave's groups and the eight waves
-// follow each other in time.  CH is 64 (a row of 128 bytes in bf16) where that
-// makes workgroups enough, else 32 or 16, whose neighbours share lines: they are
-// put on one XCD, whose L2 reads a line once for them.
+// follow each other in time.  CH is 64 (a row of 128 bytes in bf16), or 32 or 16
+// for more workgroups (cut_of), whose neighbours share lines: they are put on one
+// XCD, whose L2 reads a line once for them.
 
 constexpr int kWaves = 8;
 constexpr int kStreamed = 2;                              // of a buffer access: past the caches (nt)
@@ -376,19 +376,32 @@ template <int CH, int V> __device__ __forceinline__ Lane lane_of(const DiagProbl
 
 inline int64_t blocks_of(const DiagProblem& p, int ch) { return (int64_t)p.B * ((p.D + ch - 1) / ch); }
 
-// wide: 64 channels to a workgroup whatever their number.
-inline Cut cut_of(const DiagProblem& p, bool wide)
+// The cut of a call whose tensors are walked by buffer instructions (buf), else by segments of 64 channels always.
+//
+// 256 workgroups fill the chip.  64 channels to one where that gives as many, else 32 (B=8 T=1024 D=1024 bf16,
+// coupled, forward and backward: 14 and 19 us, in two segments of 64 channels 18 and 31); with fewer channels 16 where
+// the axis is short (T=512 D=2048: 5.3 and 6.8 us, segments 9.1 and 10.1; T=1500 D=768 forward 8.8 and 10.3, backward
+// 14.9 and 11.3) or, forward in fp32, where they are 4096 or more (T=8192 D=4096: 101 and 109 us); else segments of 64
+// (T=30000 D=1024 bf16: 64 and 88 us; 16 channels in four segments 119 and 166).  A segmented walk reads the inputs
+// twice, narrow blocks read lines that they share.
+inline Cut cut_of(const DiagProblem& p, bool buf, bool bwd)
 {
     Cut c;
-    c.ch = wide || blocks_of(p, 64) >= 256 ? 64 : blocks_of(p, 32) >= 256 ? 32 : 16;
+    c.ch = 64;
+    bool whole = blocks_of(p, 64) >= 256;
+    if (buf && !whole) {
+        if (blocks_of(p, 32) >= 256) c.ch = 32;
+        else if (p.T <= (bwd ? 768 : 2048) || (!bwd && !p.bf16 && blocks_of(p, 16) >= 256)) c.ch = 16;
+        whole = c.ch != 64;
+    }
     c.ncb = (p.D + c.ch - 1) / c.ch;
     c.near = 64 / c.ch;
     const int tile = kWaves * kPer * 64 / c.ch;
     const int tiles = (p.T + tile - 1) / tile;
     const int64_t blocks = (int64_t)p.B * c.ncb;
-    int64_t n = blocks >= 128 || (c.ch == 64 && !wide) ? 1 : 256 / blocks;
+    int64_t n = whole ? 1 : (256 + blocks - 1) / blocks;
+    if (n > 64) n = 64;                                // a segment's start folds the maps of those before it
     if (n > tiles) n = tiles;
-    if (n < 1) n = 1;
     const int per = (int)((tiles + n - 1) / n);
     c.len = per * tile;
     c.nseg = (tiles + per - 1) / per;
