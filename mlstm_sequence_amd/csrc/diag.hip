@@ -1,15 +1,18 @@
 // diag.hip -- gated linear recurrence of channels, forward (diag_impl.hpp).
 //
 // Rows of a tile are affine maps of the state, h -> F h + H, and maps compose:
-// a lane forms the map of its rows, the halves of a wave and the eight waves
-// join theirs (lane swaps, LDS, one barrier a tile), and each lane then runs
-// its rows again from the state before them, kept in registers all along.
-// The next tile's loads are under way meanwhile.  Each input is read once and
-// y written once: bound by memory.
+// a lane forms the map of its rows, the row groups of a wave and the eight
+// waves join theirs (lane swaps, LDS, one barrier a tile), and each lane then
+// runs its rows again from the state before them, the gates kept in registers
+// all along.  Two tiles' loads are under way meanwhile, a row's issued as the
+// row before it in the same register is taken.  Each input is read once and y
+// written once: bound by memory.  B=4 T=4096 D=4096 bf16, coupled gates 403 MB
+// in 80 us, two gates or a decay 537 MB in 109 and 111 (5.0 to 4.8 TB/s, where
+// a copy moves 5.1; 4.2 with loads through the caches); fp32 139, 194, 196.
 //
 // A long axis over few channels is cut into segments: their maps first (one
 // more reading of the inputs), then each from the state that the maps before
-// it give.
+// it give.  B=1 T=8192 D=4096 bf16: 74, 92 and 99 us.
 #include "diag_impl.hpp"
 
 #include <algorithm>
@@ -19,67 +22,58 @@ namespace {
 
 using namespace diag;
 
-constexpr int kGroup = 4;   // rows whose gates a lane forms together
 constexpr int kAhead = 2;   // tiles under way (even: two LDS buffers in turn)
 
-// OUT: outputs; else the segment's map.
-template <typename T, int KIND, int CH, int V, bool BUF, bool OUT>
-__global__ __launch_bounds__(64 * kWaves, 2) void diag_fwd_kernel(DiagProblem p, Cut sg, f32x2* __restrict__ ends)
+// OUT: outputs; else the segment's map.  The first reading of a segmented walk goes through the caches, for the second
+// (B=1 T=30000 D=1024 bf16, coupled: 63 us and 68 past them).
+template <typename T, int KIND, int CH, bool BUF, bool OUT>
+__global__ __launch_bounds__(64 * kWaves, 2) void diag_fwd_kernel(DiagProblem p, Cut cut, f32x2* __restrict__ ends)
 {
-    typedef Shape<CH, V> S;
-    constexpr int R = S::R, kTile = S::tile, LA = CH == 64 ? kStreamed : 0, SA = 0;
+    typedef Shape<CH> S;
+    typedef Walk<T, BUF, CH == 64 && OUT ? kStreamed : 0> In;
+    constexpr int kTile = S::tile;
     __shared__ f32x2 tot[2][kWaves][CH];
     Place q;
-    if (!place(p, sg, &q) || (!OUT && q.seg == sg.nseg - 1)) return;   // no segment starts from the last one's map
+    if (!place(p, cut, &q) || (!OUT && q.seg == cut.nseg - 1)) return;   // no segment starts from the last one's map
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const Lane l = lane_of<CH, V>(p, q);
-    const bool first = lane < S::lanes;                // of the lanes that share channels
-    const int col = lane % S::lanes * V;
-    const int s0 = q.seg * sg.len, all = min(sg.len, p.T - s0);
+    const Lane l = lane_of<CH>(p, q);
+    const int col = lane % CH, cc = min(l.c, p.D - 1);
+    const bool first = lane < CH;                      // of the lanes that share a channel
+    const int s0 = q.seg * cut.len, all = min(cut.len, p.T - s0);
     // rows of this segment; the same for all lanes, which the compiler cannot tell of a loaded value
     const int n = __builtin_amdgcn_readfirstlane(min(max(clamp_len(p.lengths, (int)q.b, p.T) - s0, 0), all));
-    const int cc = min(l.c, l.last);
-    Walk<T, V, BUF, LA> wx, wu, wv;
-    Walk<T, V, BUF, SA> wy;
-    wx.open(p.x, q.b, s0, l);
-    wu.open(p.fgate, q.b, s0, l);
-    if (KIND != kCoupled) wv.open(p.igate, q.b, s0, l);
-    if (OUT) wy.open(p.y, q.b, s0, l);
-    Rate decay[V];
-    float h0[V], f0[V];                                // the state before the tile; !OUT: the map so far
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-        decay[k] = Rate(KIND == kDecay ? p.decay[cc + k] : 0.0f);
-        h0[k] = OUT && p.state ? p.state[q.b * p.D + cc + k] : 0.0f;
-        f0[k] = 1.0f;
-    }
+    const int64_t nc = (p.T + kChunk - 1) / kChunk;
+    In wx, wu, wv;
+    Walk<T, BUF, 0> wy;
+    wx.open(p.x, q.b, s0, l, p.D);
+    wu.open(p.fgate, q.b, s0, l, p.D);
+    if (KIND != kCoupled) wv.open(p.igate, q.b, s0, l, p.D);
+    if (OUT) wy.open(p.y, q.b, s0, l, p.D);
+    const Rate decay(KIND == kDecay ? p.decay[cc] : 0.0f);
+    float h0 = OUT && p.state ? p.state[q.b * p.D + cc] : 0.0f, f0 = 1.0f;   // the state before the tile; !OUT: the map so far
     if (OUT) {
         constexpr int LINKS = 8;                       // in batches, whose loads are under way together
-        const f32x2* e = ends + q.b * sg.nseg * p.D + cc;
+        const f32x2* e = ends + q.b * cut.nseg * p.D + cc;
         for (int j0 = 0; j0 < q.seg; j0 += LINKS) {
-            f32x2 m[LINKS][V];
+            f32x2 m[LINKS];
+#pragma unroll
+            for (int j = 0; j < LINKS; ++j) m[j] = e[(int64_t)min(j0 + j, q.seg - 1) * p.D];
 #pragma unroll
             for (int j = 0; j < LINKS; ++j)
-#pragma unroll
-                for (int k = 0; k < V; ++k) m[j][k] = e[(int64_t)min(j0 + j, q.seg - 1) * p.D + k];
-#pragma unroll
-            for (int j = 0; j < LINKS; ++j)
-                if (j0 + j < q.seg)
-#pragma unroll
-                    for (int k = 0; k < V; ++k) h0[k] = m[j][k][0] * h0[k] + m[j][k][1];
+                if (j0 + j < q.seg) h0 = m[j][0] * h0 + m[j][1];
         }
     }
     struct Raw {
-        typename RawOf<sizeof(T) * V>::type x[R], u[R], v[R];
+        T x[kRows], u[kRows], v[kRows];
     };
-    Raw raw[kAhead];                                   // the tiles under way
+    Raw raw[kAhead];                                   // the tiles under way, as they were loaded
     if (n > 0)
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int t = i * kTile, rows = min(n - t, kTile);
             const auto tu = wu.tile(t, rows, n), tv = wv.tile(t, rows, n), tx = wx.tile(t, rows, n);
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
+            for (int r = 0; r < kRows; ++r) {
                 raw[i].u[r] = wu.load(tu, r, l);
                 if (KIND != kCoupled) raw[i].v[r] = wv.load(tv, r, l);
                 raw[i].x[r] = wx.load(tx, r, l);
@@ -88,85 +82,66 @@ __global__ __launch_bounds__(64 * kWaves, 2) void diag_fwd_kernel(DiagProblem p,
     auto tile = [&](int t0, int buf, Raw& raw) {
         const int rows = min(n - t0, kTile), t1 = t0 + kAhead * kTile, rows1 = min(n - t1, kTile);
         const auto tu = wu.tile(t1, rows1, n), tv = wv.tile(t1, rows1, n), tx = wx.tile(t1, rows1, n);
-        float f[R][V], b[R][V];
+        float f[kRows], b[kRows];
 #pragma unroll
-        for (int r0 = 0; r0 < R; r0 += kGroup) {
-            float u[kGroup][V], v[kGroup][V], x[kGroup][V];
+        for (int r0 = 0; r0 < kRows; r0 += kGroup) {
+            float u[kGroup], v[kGroup], x[kGroup];
 #pragma unroll
             for (int i = 0; i < kGroup; ++i) {         // a later tile's rows into the registers of those taken
-                decode<T, V>(raw.u[r0 + i], u[i]);
-                raw.u[r0 + i] = wu.load(tu, r0 + i, l);
+                const int r = r0 + i;
+                u[i] = to_float(raw.u[r]);
+                raw.u[r] = wu.load(tu, r, l);
                 if (KIND != kCoupled) {
-                    decode<T, V>(raw.v[r0 + i], v[i]);
-                    raw.v[r0 + i] = wv.load(tv, r0 + i, l);
+                    v[i] = to_float(raw.v[r]);
+                    raw.v[r] = wv.load(tv, r, l);
                 }
-                decode<T, V>(raw.x[r0 + i], x[i]);
-                raw.x[r0 + i] = wx.load(tx, r0 + i, l);
+                x[i] = to_float(raw.x[r]);
+                raw.x[r] = wx.load(tx, r, l);
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i = 0; i < kGroup; ++i)
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const Gate g = gate_of<T, KIND>(u[i][k], KIND != kCoupled ? v[i][k] : 0.0f, decay[k]);
-                    f[r0 + i][k] = g.f;
-                    b[r0 + i][k] = g.i * x[i][k];
-                }
+            for (int i = 0; i < kGroup; ++i) {
+                const Gate g = gate_of<T, KIND>(u[i], KIND != kCoupled ? v[i] : 0.0f, decay);
+                f[r0 + i] = g.f;
+                b[r0 + i] = g.i * x[i];
+            }
         }
         if (rows < kTile) {                            // rows behind the end change nothing
             const int end = (int)hidden((unsigned)rows);   // a branch, not selections in every tile
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int k = 0; k < V; ++k)
-                    if (l.row + r >= end) {
-                        f[r][k] = 1.0f;
-                        b[r][k] = 0.0f;
-                    }
+            for (int r = 0; r < kRows; ++r)
+                if (l.row + r >= end) {
+                    f[r] = 1.0f;
+                    b[r] = 0.0f;
+                }
         }
-        float F[V], H[V], fl[V], hl[V];                // the lane's map, then the wave's; the map before the lane's rows
+        float F = f[0], H = b[0], pf = 1.0f, ph = 0.0f;   // the lane's map, then the wave's; the map before the lane's rows
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            F[k] = f[0][k];
-            H[k] = b[0][k];
-#pragma unroll
-            for (int r = 1; r < R; ++r) {
-                H[k] = f[r][k] * H[k] + b[r][k];
-                F[k] *= f[r][k];
-            }
-            fl[k] = 1.0f;
-            hl[k] = 0.0f;
-            join<S::lanes>(lane, &F[k], &H[k], &fl[k], &hl[k]);
+        for (int r = 1; r < kRows; ++r) {
+            H = f[r] * H + b[r];
+            F *= f[r];
         }
-        if (first)
-#pragma unroll
-            for (int k = 0; k < V; ++k) tot[buf][wave][col + k] = f32x2{F[k], H[k]};
+        join<CH>(lane, &F, &H, &pf, &ph);
+        if (first) tot[buf][wave][col] = f32x2{F, H};
         __syncthreads();
-        float h[V];
+        float h;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w)
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const f32x2 m = tot[buf][w][col + k];
-                if (w == wave) h[k] = h0[k];
-                h0[k] = m[0] * h0[k] + m[1];
-                if (!OUT) f0[k] *= m[0];
-            }
-        if (!OUT) return;
-        if (p.starts && wave * S::rows % kChunk == 0 && first && l.live && t0 + wave * S::rows < all) {
-            const int64_t nc = (p.T + kChunk - 1) / kChunk;
-#pragma unroll
-            for (int k = 0; k < V; ++k)
-                p.starts[(q.b * nc + (s0 + t0 + wave * S::rows) / kChunk) * p.D + l.c + k] = h[k];
+        for (int w = 0; w < kWaves; ++w) {
+            const f32x2 m = tot[buf][w][col];
+            if (w == wave) h = h0;
+            h0 = m[0] * h0 + m[1];
+            if (!OUT) f0 *= m[0];
         }
-#pragma unroll
-        for (int k = 0; k < V; ++k) h[k] = fl[k] * h[k] + hl[k];
+        if (!OUT) return;
+        const int tw = t0 + wave * S::rows;            // the wave's first row
+        if (p.starts && wave * S::rows % kChunk == 0 && first && l.live && tw < all)
+            p.starts[(q.b * nc + (s0 + tw) / kChunk) * p.D + l.c] = h;
+        h = pf * h + ph;
         const auto ty = wy.tile(t0, rows, n);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-#pragma unroll
-            for (int k = 0; k < V; ++k) h[k] = f[r][k] * h[k] + b[r][k];
-            wy.store(ty, encode<T, V>(h), r, l);
+        for (int r = 0; r < kRows; ++r) {
+            h = f[r] * h + b[r];
+            wy.store(ty, h, r, l);
         }
     };
     for (int t0 = 0; t0 < n; t0 += kAhead * kTile)
@@ -174,25 +149,18 @@ __global__ __launch_bounds__(64 * kWaves, 2) void diag_fwd_kernel(DiagProblem p,
         for (int i = 0; i < kAhead; ++i)
             if (t0 + i * kTile < n) tile(t0 + i * kTile, i & 1, raw[i]);
     if (!OUT) {
-        if (wave == 0 && first && l.live)
-#pragma unroll
-            for (int k = 0; k < V; ++k) ends[(q.b * sg.nseg + q.seg) * p.D + l.c + k] = f32x2{f0[k], h0[k]};
+        if (wave == 0 && first && l.live) ends[(q.b * cut.nseg + q.seg) * p.D + l.c] = f32x2{f0, h0};
         return;
     }
     wy.template clear<CH>(n, all, q.cb * CH, p.D);
     if (wave != 0 || !first || !l.live) return;
-    if (p.starts) {                                    // of chunks behind the last tile
-        const int64_t nc = (p.T + kChunk - 1) / kChunk;
+    if (p.starts)                                      // of chunks behind the last tile
         for (int t = (n + kTile - 1) / kTile * kTile; t < all; t += kChunk)
-#pragma unroll
-            for (int k = 0; k < V; ++k) p.starts[(q.b * nc + (s0 + t) / kChunk) * p.D + l.c + k] = h0[k];
-    }
-    if (p.state_out && q.seg == sg.nseg - 1)
-#pragma unroll
-        for (int k = 0; k < V; ++k) p.state_out[q.b * p.D + l.c + k] = h0[k];
+            p.starts[(q.b * nc + (s0 + t) / kChunk) * p.D + l.c] = h0;
+    if (p.state_out && q.seg == cut.nseg - 1) p.state_out[q.b * p.D + l.c] = h0;
 }
 
-// Single tokens and very short calls: a thread to a channel.
+// Single tokens and very short calls: a thread to a channel.  B=64 T=1 D=4096: 3.3 us, the least that a launch takes.
 template <typename T, int KIND>
 __global__ __launch_bounds__(256) void diag_step_kernel(DiagProblem p)
 {
@@ -220,30 +188,19 @@ __global__ __launch_bounds__(256) void diag_step_kernel(DiagProblem p)
 // Calls of up to this many rows go to the step kernel.
 constexpr int kStepRows = 4;
 
-template <typename T, int KIND, int CH, int V, bool BUF>
-hipError_t fwd_v(const DiagProblem& p, const Cut& cut, hipStream_t stream)
+template <typename T, int KIND, int CH, bool BUF>
+hipError_t fwd_c(const DiagProblem& p, const Cut& cut, hipStream_t stream)
 {
     f32x2* ends = (f32x2*)p.ws;
     if constexpr (CH == 64) {
         if (cut.nseg > 1) {
-            diag_fwd_kernel<T, KIND, CH, V, BUF, false><<<grid_of(cut.blocks), 64 * kWaves, 0, stream>>>(p, cut, ends);
+            diag_fwd_kernel<T, KIND, CH, BUF, false><<<grid_of(cut.blocks), 64 * kWaves, 0, stream>>>(p, cut, ends);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
         }
     }
-    diag_fwd_kernel<T, KIND, CH, V, BUF, true><<<grid_of(cut.blocks), 64 * kWaves, 0, stream>>>(p, cut, ends);
+    diag_fwd_kernel<T, KIND, CH, BUF, true><<<grid_of(cut.blocks), 64 * kWaves, 0, stream>>>(p, cut, ends);
     return hipGetLastError();
-}
-
-template <typename T, int KIND, int V>
-hipError_t fwd_c(const DiagProblem& p, hipStream_t stream)
-{
-    const Cut cut = cut_of(p, true, false);
-    switch (cut.ch) {
-    case 64: return fwd_v<T, KIND, 64, V, true>(p, cut, stream);
-    case 32: return fwd_v<T, KIND, 32, V, true>(p, cut, stream);
-    default: return fwd_v<T, KIND, 16, V, true>(p, cut, stream);
-    }
 }
 
 template <typename T, int KIND>
@@ -253,13 +210,14 @@ hipError_t fwd_k(const DiagProblem& p, hipStream_t stream)
         diag_step_kernel<T, KIND><<<grid_of((int64_t)p.B * ((p.D + 255) / 256)), 256, 0, stream>>>(p);
         return hipGetLastError();
     }
-    bool buf = true, two = sizeof(T) == 2 && p.D % 2 == 0;
-    for (const Rows* m : {&p.x, &p.fgate, &p.igate, (const Rows*)&p.y}) {
-        buf = buf && walks(*m, p);
-        two = two && aligned(*m, p, 2 * sizeof(T));
+    const bool buf = walks(p.x, p) && walks(p.fgate, p) && walks(p.igate, p) && walks(p.y, p);
+    const Cut cut = cut_of(p, buf, false);
+    if (!buf) return fwd_c<T, KIND, 64, false>(p, cut, stream);
+    switch (cut.ch) {
+    case 64: return fwd_c<T, KIND, 64, true>(p, cut, stream);
+    case 32: return fwd_c<T, KIND, 32, true>(p, cut, stream);
+    default: return fwd_c<T, KIND, 16, true>(p, cut, stream);
     }
-    if (!buf) return fwd_v<T, KIND, 64, 1, false>(p, cut_of(p, false, false), stream);
-    return two ? fwd_c<T, KIND, 2>(p, stream) : fwd_c<T, KIND, 1>(p, stream);
 }
 
 template <typename T>

@@ -3,14 +3,17 @@
 // The walk of the forward pass from the end: with a_t = f_t g_t, what row t
 // hands to row t - 1, a tile's rows are a map of the state, h -> F h + H, and
 // one of the adjoint, a -> F a + A, with the same F.  A lane forms both maps of
-// its rows, halves and waves join theirs as in the forward pass, and each lane
-// then runs its rows forward from the state before them (the chunk's start,
-// which the forward pass left) and backward from the adjoint behind them.
-// Inputs and dy are read once, the gradients written once: bound by memory.
-// The gates stay in registers between the two.
+// its rows, row groups and waves join theirs as in the forward pass, and each
+// lane then runs its rows forward from the state before them (the chunk's
+// start, which the forward pass left) and backward from the adjoint behind
+// them, the gates kept in registers between the two; the next tile's loads are
+// under way meanwhile.  Inputs and dy are read once, the gradients written
+// once: bound by memory.  B=4 T=4096 D=4096 bf16, coupled gates 671 MB in 128 us,
+// two gates or a decay 940 MB in 198 and 206 (5.2 to 4.6 TB/s, where a copy
+// moves 5.1); fp32 250, 356, 362.
 //
 // A long axis over few channels is cut into segments, whose adjoint maps are
-// formed first from fgate and dy alone.
+// formed first from fgate and dy alone: B=1 T=8192 D=4096 bf16 96, 114, 126 us.
 #include "diag_impl.hpp"
 
 #include <algorithm>
@@ -22,85 +25,70 @@ namespace {
 
 using namespace diag;
 
-constexpr int kGroup = 4;   // rows whose gates a lane forms together
-
 // The adjoint behind segment `seg`: dstate_out through the maps of the segments from the last on.
-template <int V>
-__device__ __forceinline__ void adjoint_behind(const DiagProblem& p, const Cut& sg, const Place& q, int cc,
-                                               const f32x2* ends, float* a)
+__device__ __forceinline__ float adjoint_behind(const DiagProblem& p, const Cut& cut, const Place& q, int cc, const f32x2* ends)
 {
-#pragma unroll
-    for (int k = 0; k < V; ++k) a[k] = p.dstate_out ? p.dstate_out[q.b * p.D + cc + k] : 0.0f;
+    float a = p.dstate_out ? p.dstate_out[q.b * p.D + cc] : 0.0f;
     constexpr int LINKS = 8;                           // in batches, whose loads are under way together
-    const f32x2* e = ends + q.b * sg.nseg * p.D + cc;
-    for (int j0 = sg.nseg - 1; j0 > q.seg; j0 -= LINKS) {
-        f32x2 m[LINKS][V];
+    const f32x2* e = ends + q.b * cut.nseg * p.D + cc;
+    for (int j0 = cut.nseg - 1; j0 > q.seg; j0 -= LINKS) {
+        f32x2 m[LINKS];
+#pragma unroll
+        for (int j = 0; j < LINKS; ++j) m[j] = e[(int64_t)max(j0 - j, q.seg + 1) * p.D];
 #pragma unroll
         for (int j = 0; j < LINKS; ++j)
-#pragma unroll
-            for (int k = 0; k < V; ++k) m[j][k] = e[(int64_t)max(j0 - j, q.seg + 1) * p.D + k];
-#pragma unroll
-        for (int j = 0; j < LINKS; ++j)
-            if (j0 - j > q.seg)
-#pragma unroll
-                for (int k = 0; k < V; ++k) a[k] = m[j][k][0] * a[k] + m[j][k][1];
+            if (j0 - j > q.seg) a = m[j][0] * a + m[j][1];
     }
+    return a;
 }
 
-template <typename T, int KIND, int CH, int V, bool BUF>
-__global__ __launch_bounds__(64 * kWaves, 2) void diag_bwd_kernel(DiagProblem p, Cut sg, const f32x2* __restrict__ ends,
+// Loads and stores of full width go past the caches (B=4 T=4096 D=4096 bf16 with a decay: 219 us, neither so 226), but
+// not the stores of bf16 gradients of coupled gates (133 us, 150 so).
+template <typename T, int KIND, int CH, bool BUF>
+__global__ __launch_bounds__(64 * kWaves, 2) void diag_bwd_kernel(DiagProblem p, Cut cut, const f32x2* __restrict__ ends,
                                                                    float* __restrict__ part)
 {
-    typedef Shape<CH, V> S;
-    constexpr int R = S::R, kTile = S::tile, LA = CH == 64 ? kStreamed : 0,
-                  SA = CH == 64 && (KIND != kCoupled || sizeof(T) == 4) ? kStreamed : 0;
+    typedef Shape<CH> S;
+    typedef Walk<T, BUF, CH == 64 ? kStreamed : 0> In;
+    typedef Walk<T, BUF, CH == 64 && (KIND != kCoupled || sizeof(T) == 4) ? kStreamed : 0> Out;
+    constexpr int kTile = S::tile;
     __shared__ f32x2 totf[2][kWaves][CH];              // F, H
     __shared__ float tota[2][kWaves][CH];              // A
     Place q;
-    if (!place(p, sg, &q)) return;
+    if (!place(p, cut, &q)) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const Lane l = lane_of<CH, V>(p, q);
-    const bool first = lane < S::lanes;                // of the lanes that share channels
-    const int col = lane % S::lanes * V;
-    const int s0 = q.seg * sg.len, all = min(sg.len, p.T - s0);
+    const Lane l = lane_of<CH>(p, q);
+    const int col = lane % CH, cc = min(l.c, p.D - 1);
+    const bool first = lane < CH;                      // of the lanes that share a channel
+    const int s0 = q.seg * cut.len, all = min(cut.len, p.T - s0);
     const int n = __builtin_amdgcn_readfirstlane(min(max(clamp_len(p.lengths, (int)q.b, p.T) - s0, 0), all));
-    const int cc = min(l.c, l.last);
     const int64_t nc = (p.T + kChunk - 1) / kChunk;
-    Walk<T, V, BUF, LA> wx, wu, wv, wg;
-    Walk<T, V, BUF, SA> ox, ou, ov;
-    wx.open(p.x, q.b, s0, l);
-    wu.open(p.fgate, q.b, s0, l);
-    wg.open(p.dy, q.b, s0, l);
-    ox.open(p.dx, q.b, s0, l);
-    ou.open(p.dfgate, q.b, s0, l);
+    In wx, wu, wv, wg;
+    Out ox, ou, ov;
+    wx.open(p.x, q.b, s0, l, p.D);
+    wu.open(p.fgate, q.b, s0, l, p.D);
+    wg.open(p.dy, q.b, s0, l, p.D);
+    ox.open(p.dx, q.b, s0, l, p.D);
+    ou.open(p.dfgate, q.b, s0, l, p.D);
     if (KIND != kCoupled) {
-        wv.open(p.igate, q.b, s0, l);
-        ov.open(p.digate, q.b, s0, l);
+        wv.open(p.igate, q.b, s0, l, p.D);
+        ov.open(p.digate, q.b, s0, l, p.D);
     }
-    Rate decay[V];
-    float a0[V], dd[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-        decay[k] = Rate(KIND == kDecay ? p.decay[cc + k] : 0.0f);
-        dd[k] = 0.0f;
-    }
-    adjoint_behind<V>(p, sg, q, cc, ends, a0);
-    typename RawOf<sizeof(T) * V>::type rx[R], ru[R], rv[R], rg[R];
-    float rh[V];
+    const Rate decay(KIND == kDecay ? p.decay[cc] : 0.0f);
+    float a0 = adjoint_behind(p, cut, q, cc, ends), dd = 0.0f;
     ox.template clear<CH>(n, all, q.cb * CH, p.D);
     ou.template clear<CH>(n, all, q.cb * CH, p.D);
     if (KIND != kCoupled) ov.template clear<CH>(n, all, q.cb * CH, p.D);
     const int last = (n - 1) / kTile * kTile;
-    auto start = [&](int t0) {                         // the state at a tile's start
-#pragma unroll
-        for (int k = 0; k < V; ++k) rh[k] = p.starts[(q.b * nc + (s0 + max(t0, 0)) / kChunk) * p.D + cc + k];
-    };
+    auto start = [&](int t0) { return p.starts[(q.b * nc + (s0 + t0) / kChunk) * p.D + cc]; };   // the state before row t0
+    T rx[kRows], ru[kRows], rv[kRows], rg[kRows];      // the tile under way
+    float rh = 0.0f;
     if (n > 0) {
         const auto tu = wu.tile(last, n - last, n), tv = wv.tile(last, n - last, n), tx = wx.tile(last, n - last, n),
                    tg = wg.tile(last, n - last, n);
-        start(last);
+        rh = start(last);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
+        for (int r = 0; r < kRows; ++r) {
             ru[r] = wu.load(tu, r, l);
             if (KIND != kCoupled) rv[r] = wv.load(tv, r, l);
             rx[r] = wx.load(tx, r, l);
@@ -111,22 +99,20 @@ __global__ __launch_bounds__(64 * kWaves, 2) void diag_bwd_kernel(DiagProblem p,
     for (int t0 = last; n > 0 && t0 >= 0; t0 -= kTile, buf ^= 1) {
         const int rows = min(n - t0, kTile), t1 = max(t0 - kTile, 0), rows1 = t0 ? kTile : 0;   // the next tile is whole, or none
         const auto tu = wu.tile(t1, rows1, n), tv = wv.tile(t1, rows1, n), tx = wx.tile(t1, rows1, n), tg = wg.tile(t1, rows1, n);
-        Gate g[R][V];
-        typename RawOf<sizeof(T) * V>::type ax[R], ag[R];    // x and dy as they were loaded
-        float h[V];
+        Gate g[kRows];
+        T ax[kRows], ag[kRows];                        // x and dy as they were loaded
+        float h = rh;
+        rh = start(t1);
 #pragma unroll
-        for (int k = 0; k < V; ++k) h[k] = rh[k];
-        start(t1);
-#pragma unroll
-        for (int r0 = 0; r0 < R; r0 += kGroup) {
-            float u[kGroup][V], v[kGroup][V];
+        for (int r0 = 0; r0 < kRows; r0 += kGroup) {
+            float u[kGroup], v[kGroup];
 #pragma unroll
             for (int i = 0; i < kGroup; ++i) {         // the next tile's rows into the registers of those taken
                 const int r = r0 + i;
-                decode<T, V>(ru[r], u[i]);
+                u[i] = to_float(ru[r]);
                 ru[r] = wu.load(tu, r, l);
                 if (KIND != kCoupled) {
-                    decode<T, V>(rv[r], v[i]);
+                    v[i] = to_float(rv[r]);
                     rv[r] = wv.load(tv, r, l);
                 }
                 ax[r] = rx[r];
@@ -136,144 +122,106 @@ __global__ __launch_bounds__(64 * kWaves, 2) void diag_bwd_kernel(DiagProblem p,
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i = 0; i < kGroup; ++i)
-#pragma unroll
-                for (int k = 0; k < V; ++k) g[r0 + i][k] = gate_of<T, KIND>(u[i][k], KIND != kCoupled ? v[i][k] : 0.0f, decay[k]);
+            for (int i = 0; i < kGroup; ++i) g[r0 + i] = gate_of<T, KIND>(u[i], KIND != kCoupled ? v[i] : 0.0f, decay);
         }
         if (rows < kTile) {                            // rows behind the end change nothing
             const int end = (int)hidden((unsigned)rows);   // a branch, not selections in every tile
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int k = 0; k < V; ++k)
-                    if (l.row + r >= end) {
-                        g[r][k].f = 1.0f;
-                        g[r][k].i = 0.0f;
-                        ax[r] = ag[r] = {};
-                        if (KIND == kDecay) g[r][k].r = 0.0f;   // nothing for ddecay
-                    }
+            for (int r = 0; r < kRows; ++r)
+                if (l.row + r >= end) {
+                    g[r].f = 1.0f;
+                    g[r].i = 0.0f;
+                    ax[r] = ag[r] = from_float<T>(0.0f);
+                    if (KIND == kDecay) g[r].r = 0.0f;     // nothing for ddecay
+                }
         }
-        float x[R][V], dy[R][V];
+        float x[kRows], dy[kRows];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            decode<T, V>(ax[r], x[r]);
-            decode<T, V>(ag[r], dy[r]);
+        for (int r = 0; r < kRows; ++r) {
+            x[r] = to_float(ax[r]);
+            dy[r] = to_float(ag[r]);
         }
-        float fl[V], hl[V], fa[V], aa[V];              // the state before the lane's rows, the adjoint behind them
+        float F = 1.0f, H = 0.0f, A = 0.0f;
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            float F = 1.0f, H = 0.0f, A = 0.0f;
+        for (int r = 0; r < kRows; ++r) {
+            H = g[r].f * H + g[r].i * x[r];
+            F *= g[r].f;
+        }
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                H = g[r][k].f * H + g[r][k].i * x[r][k];
-                F *= g[r][k].f;
-            }
-#pragma unroll
-            for (int r = R - 1; r >= 0; --r) A = g[r][k].f * (dy[r][k] + A);
-            fl[k] = fa[k] = 1.0f;
-            hl[k] = aa[k] = 0.0f;
-            join_both<S::lanes>(lane, &F, &H, &A, &fl[k], &hl[k], &fa[k], &aa[k]);
-            if (first) {
-                totf[buf][wave][col + k] = f32x2{F, H};
-                tota[buf][wave][col + k] = A;
-            }
+        for (int r = kRows - 1; r >= 0; --r) A = g[r].f * (dy[r] + A);
+        float pf = 1.0f, ph = 0.0f, qf = 1.0f, qa = 0.0f;   // the map before the lane's rows, the adjoint's behind them
+        join_both<CH>(lane, &F, &H, &A, &pf, &ph, &qf, &qa);
+        if (first) {
+            totf[buf][wave][col] = f32x2{F, H};
+            tota[buf][wave][col] = A;
         }
         __syncthreads();
-        float a[V];
+        float a;
 #pragma unroll
-        for (int w = kWaves - 1; w >= 0; --w)
+        for (int w = kWaves - 1; w >= 0; --w) {
+            if (w == wave) a = a0;
+            a0 = totf[buf][w][col][0] * a0 + tota[buf][w][col];
+        }
+        for (int w = 0; w < wave; ++w) {
+            const f32x2 m = totf[buf][w][col];
+            h = m[0] * h + m[1];
+        }
+        h = pf * h + ph;
+        a = qf * a + qa;
+        float before[kRows];
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                if (w == wave) a[k] = a0[k];
-                a0[k] = totf[buf][w][col + k][0] * a0[k] + tota[buf][w][col + k];
-            }
-        for (int w = 0; w < wave; ++w)
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const f32x2 m = totf[buf][w][col + k];
-                h[k] = m[0] * h[k] + m[1];
-            }
-        float before[R][V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            h[k] = fl[k] * h[k] + hl[k];
-            a[k] = fa[k] * a[k] + aa[k];
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                before[r][k] = h[k];
-                h[k] = g[r][k].f * h[k] + g[r][k].i * x[r][k];
-            }
+        for (int r = 0; r < kRows; ++r) {
+            before[r] = h;
+            h = g[r].f * h + g[r].i * x[r];
         }
         const auto tdx = ox.tile(t0, rows, n), tdu = ou.tile(t0, rows, n), tdv = ov.tile(t0, rows, n);
 #pragma unroll
-        for (int r = R - 1; r >= 0; --r) {
-            float dx[V], du[V], dv[V];
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const float gr = dy[r][k] + a[k];
-                const GateGrads o = grads_of<KIND>(g[r][k], x[r][k], before[r][k], gr, decay[k]);
-                a[k] = g[r][k].f * gr;
-                dx[k] = o.dx;
-                du[k] = o.du;
-                dv[k] = o.dv;
-                dd[k] += o.dd;
-            }
-            ox.store(tdx, encode<T, V>(dx), r, l);
-            ou.store(tdu, encode<T, V>(du), r, l);
-            if (KIND != kCoupled) ov.store(tdv, encode<T, V>(dv), r, l);
+        for (int r = kRows - 1; r >= 0; --r) {
+            const float gr = dy[r] + a;
+            const GateGrads o = grads_of<KIND>(g[r], x[r], before[r], gr, decay);
+            a = g[r].f * gr;
+            dd += o.dd;
+            ox.store(tdx, o.dx, r, l);
+            ou.store(tdu, o.du, r, l);
+            if (KIND != kCoupled) ov.store(tdv, o.dv, r, l);
         }
     }
-    if (p.dstate && q.seg == 0 && wave == 0 && first && l.live)
-#pragma unroll
-        for (int k = 0; k < V; ++k) p.dstate[q.b * p.D + l.c + k] = a0[k];
+    if (p.dstate && q.seg == 0 && wave == 0 && first && l.live) p.dstate[q.b * p.D + l.c] = a0;
     if (KIND != kDecay) return;
     __syncthreads();
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-        dd[k] = sum_groups<S::lanes>(lane, dd[k]);
-        if (first) tota[0][wave][col + k] = dd[k];
-    }
+    dd = sum_groups<CH>(dd);
+    if (first) tota[0][wave][col] = dd;
     __syncthreads();
     const int c = q.cb * CH + (int)threadIdx.x;
     if (threadIdx.x >= CH || c >= p.D) return;
     float s = 0.0f;
     for (int w = 0; w < kWaves; ++w) s += tota[0][w][threadIdx.x];
-    part[(q.b * sg.nseg + q.seg) * p.D + c] = s;
+    part[(q.b * cut.nseg + q.seg) * p.D + c] = s;
 }
 
 // The adjoint maps of all segments but the first.
-template <typename T, int KIND, int CH, int V, bool BUF>
-__global__ __launch_bounds__(64 * kWaves, 2) void diag_adjoint_kernel(DiagProblem p, Cut sg, f32x2* __restrict__ ends)
+template <typename T, int KIND, bool BUF>
+__global__ __launch_bounds__(64 * kWaves, 2) void diag_adjoint_kernel(DiagProblem p, Cut cut, f32x2* __restrict__ ends)
 {
-    typedef Shape<CH, V> S;
-    constexpr int R = S::R, kTile = S::tile;
+    constexpr int CH = 64, kTile = Shape<CH>::tile;
     __shared__ f32x2 tot[2][kWaves][CH];
     Place q;
-    if (!place(p, sg, &q) || q.seg == 0) return;
+    if (!place(p, cut, &q) || q.seg == 0) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const Lane l = lane_of<CH, V>(p, q);
-    const bool first = lane < S::lanes;                // of the lanes that share channels
-    const int col = lane % S::lanes * V;
-    const int s0 = q.seg * sg.len, all = min(sg.len, p.T - s0);
+    const Lane l = lane_of<CH>(p, q);
+    const int s0 = q.seg * cut.len, all = min(cut.len, p.T - s0);
     const int n = __builtin_amdgcn_readfirstlane(min(max(clamp_len(p.lengths, (int)q.b, p.T) - s0, 0), all));
-    const int cc = min(l.c, l.last);
-    Walk<T, V, BUF, 0> wu, wg;
-    wu.open(p.fgate, q.b, s0, l);
-    wg.open(p.dy, q.b, s0, l);
-    Rate decay[V];
-    float a0[V], f0[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-        decay[k] = Rate(KIND == kDecay ? p.decay[cc + k] : 0.0f);
-        a0[k] = 0.0f;
-        f0[k] = 1.0f;
-    }
-    typename RawOf<sizeof(T) * V>::type ru[R], rg[R];
+    Walk<T, BUF, 0> wu, wg;
+    wu.open(p.fgate, q.b, s0, l, p.D);
+    wg.open(p.dy, q.b, s0, l, p.D);
+    const Rate decay(KIND == kDecay ? p.decay[min(l.c, p.D - 1)] : 0.0f);
+    float a0 = 0.0f, f0 = 1.0f;
+    T ru[kRows], rg[kRows];
     const int last = (n - 1) / kTile * kTile;
     if (n > 0) {
         const auto tu = wu.tile(last, n - last, n), tg = wg.tile(last, n - last, n);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
+        for (int r = 0; r < kRows; ++r) {
             ru[r] = wu.load(tu, r, l);
             rg[r] = wg.load(tg, r, l);
         }
@@ -282,58 +230,47 @@ __global__ __launch_bounds__(64 * kWaves, 2) void diag_adjoint_kernel(DiagProble
     for (int t0 = last; n > 0 && t0 >= 0; t0 -= kTile, buf ^= 1) {
         const int rows = min(n - t0, kTile), t1 = max(t0 - kTile, 0), rows1 = t0 ? kTile : 0;
         const auto tu = wu.tile(t1, rows1, n), tg = wg.tile(t1, rows1, n);
-        float f[R][V], dy[R][V];
+        float f[kRows], dy[kRows];
 #pragma unroll
-        for (int r0 = 0; r0 < R; r0 += kGroup) {
-            float u[kGroup][V];
+        for (int r0 = 0; r0 < kRows; r0 += kGroup) {
+            float u[kGroup];
 #pragma unroll
             for (int i = 0; i < kGroup; ++i) {
-                decode<T, V>(ru[r0 + i], u[i]);
-                ru[r0 + i] = wu.load(tu, r0 + i, l);
-                decode<T, V>(rg[r0 + i], dy[r0 + i]);
-                rg[r0 + i] = wg.load(tg, r0 + i, l);
+                const int r = r0 + i;
+                u[i] = to_float(ru[r]);
+                ru[r] = wu.load(tu, r, l);
+                dy[r] = to_float(rg[r]);
+                rg[r] = wg.load(tg, r, l);
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i = 0; i < kGroup; ++i)
-#pragma unroll
-                for (int k = 0; k < V; ++k) f[r0 + i][k] = forget_of<T, KIND>(u[i][k], decay[k]);
+            for (int i = 0; i < kGroup; ++i) f[r0 + i] = forget_of<T, KIND>(u[i], decay);
         }
         if (rows < kTile) {
             const int end = (int)hidden((unsigned)rows);
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int k = 0; k < V; ++k)
-                    if (l.row + r >= end) {
-                        f[r][k] = 1.0f;
-                        dy[r][k] = 0.0f;
-                    }
+            for (int r = 0; r < kRows; ++r)
+                if (l.row + r >= end) {
+                    f[r] = 1.0f;
+                    dy[r] = 0.0f;
+                }
         }
+        float F = 1.0f, A = 0.0f;
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            float F = 1.0f, A = 0.0f;
-#pragma unroll
-            for (int r = R - 1; r >= 0; --r) {
-                A = f[r][k] * (dy[r][k] + A);
-                F *= f[r][k];
-            }
-            join_behind<S::lanes>(lane, &F, &A);
-            if (first) tot[buf][wave][col + k] = f32x2{F, A};
+        for (int r = kRows - 1; r >= 0; --r) {
+            A = f[r] * (dy[r] + A);
+            F *= f[r];
         }
+        tot[buf][wave][lane] = f32x2{F, A};
         __syncthreads();
 #pragma unroll
-        for (int w = kWaves - 1; w >= 0; --w)
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const f32x2 m = tot[buf][w][col + k];
-                a0[k] = m[0] * a0[k] + m[1];
-                f0[k] *= m[0];
-            }
+        for (int w = kWaves - 1; w >= 0; --w) {
+            const f32x2 m = tot[buf][w][lane];
+            a0 = m[0] * a0 + m[1];
+            f0 *= m[0];
+        }
     }
-    if (wave == 0 && first && l.live)
-#pragma unroll
-        for (int k = 0; k < V; ++k) ends[(q.b * sg.nseg + q.seg) * p.D + l.c + k] = f32x2{f0[k], a0[k]};
+    if (wave == 0 && l.live) ends[(q.b * cut.nseg + q.seg) * p.D + l.c] = f32x2{f0, a0};
 }
 
 __global__ __launch_bounds__(1024) void diag_params_kernel(DiagProblem p, const float* part, int64_t parts)
@@ -344,8 +281,8 @@ __global__ __launch_bounds__(1024) void diag_params_kernel(DiagProblem p, const 
     if (threadIdx.x < 64 && i < p.D) p.ddecay[i] = s;
 }
 
-template <typename T, int KIND, int CH, int V, bool BUF>
-hipError_t bwd_v(const DiagProblem& p, const Cut& cut, hipStream_t stream)
+template <typename T, int KIND, int CH, bool BUF>
+hipError_t bwd_c(const DiagProblem& p, const Cut& cut, hipStream_t stream)
 {
     f32x2* ends = (f32x2*)p.ws;
     const int64_t parts = (int64_t)p.B * cut.nseg;
@@ -353,37 +290,28 @@ hipError_t bwd_v(const DiagProblem& p, const Cut& cut, hipStream_t stream)
     hipError_t e;
     if constexpr (CH == 64) {
         if (cut.nseg > 1) {
-            diag_adjoint_kernel<T, KIND, CH, V, BUF><<<grid_of(cut.blocks), 64 * kWaves, 0, stream>>>(p, cut, ends);
+            diag_adjoint_kernel<T, KIND, BUF><<<grid_of(cut.blocks), 64 * kWaves, 0, stream>>>(p, cut, ends);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
     }
-    diag_bwd_kernel<T, KIND, CH, V, BUF><<<grid_of(cut.blocks), 64 * kWaves, 0, stream>>>(p, cut, ends, part);
+    diag_bwd_kernel<T, KIND, CH, BUF><<<grid_of(cut.blocks), 64 * kWaves, 0, stream>>>(p, cut, ends, part);
     if ((e = hipGetLastError()) != hipSuccess || KIND != kDecay || parts == 1) return e;
     diag_params_kernel<<<(unsigned)((p.D + 63) / 64), 1024, 0, stream>>>(p, part, parts);
     return hipGetLastError();
 }
 
-template <typename T, int KIND, int V>
-hipError_t bwd_c(const DiagProblem& p, hipStream_t stream)
-{
-    const Cut cut = cut_of(p, true, true);
-    switch (cut.ch) {
-    case 64: return bwd_v<T, KIND, 64, V, true>(p, cut, stream);
-    case 32: return bwd_v<T, KIND, 32, V, true>(p, cut, stream);
-    default: return bwd_v<T, KIND, 16, V, true>(p, cut, stream);
-    }
-}
-
 template <typename T, int KIND>
 hipError_t bwd_k(const DiagProblem& p, hipStream_t stream)
 {
-    bool buf = true, two = sizeof(T) == 2 && p.D % 2 == 0;
-    for (const Rows* m : {&p.x, &p.fgate, &p.igate, &p.dy, (const Rows*)&p.dx, (const Rows*)&p.dfgate, (const Rows*)&p.digate}) {
-        buf = buf && walks(*m, p);
-        two = two && aligned(*m, p, 2 * sizeof(T));
+    const bool buf = walks(p.x, p) && walks(p.fgate, p) && walks(p.igate, p) && walks(p.dy, p) && walks(p.dx, p) &&
+                     walks(p.dfgate, p) && walks(p.digate, p);
+    const Cut cut = cut_of(p, buf, true);
+    if (!buf) return bwd_c<T, KIND, 64, false>(p, cut, stream);
+    switch (cut.ch) {
+    case 64: return bwd_c<T, KIND, 64, true>(p, cut, stream);
+    case 32: return bwd_c<T, KIND, 32, true>(p, cut, stream);
+    default: return bwd_c<T, KIND, 16, true>(p, cut, stream);
     }
-    if (!buf) return bwd_v<T, KIND, 64, 1, false>(p, cut_of(p, false, true), stream);
-    return two ? bwd_c<T, KIND, 2>(p, stream) : bwd_c<T, KIND, 1>(p, stream);
 }
 
 template <typename T>

@@ -110,63 +110,30 @@ template <int KIND> __device__ __forceinline__ GateGrads grads_of(const Gate& k,
 // ---- tiles ---------------------------------------------------------------------------
 //
 // A workgroup owns CH neighbouring channels of a sequence and walks their rows in
-// tiles; a lane holds V neighbouring channels of 16 / V consecutive rows, CH / V
-// lanes side by side make a row group, the wave's groups and the eight waves
-// follow each other in time.  CH is 64 (a row of 128 bytes in bf16), or 32 or 16
-// for more workgroups (cut_of), whose neighbours share lines: they are put on one
-// XCD, whose L2 reads a line once for them.
+// tiles; a lane holds 16 consecutive rows of a channel, CH lanes side by side make
+// a row group, the wave's groups and the eight waves follow each other in time.
+// CH is 64, or 32 or 16 for more workgroups (cut_of), whose neighbours share lines:
+// they are put on one XCD, whose L2 reads a line once for them.  (Two channels and
+// eight rows to a lane: 3 to 7 % slower backward, whose registers they take, equal
+// forward; 16 waves to a tile instead of eight 7 %.)
 
 constexpr int kWaves = 8;
+constexpr int kRows = 16;                                 // of a lane
+constexpr int kGroup = 2;                                 // rows whose gates a lane forms together
 constexpr int kStreamed = 2;                              // of a buffer access: past the caches (nt)
-constexpr int kPer = 16;                                  // elements of a tensor that a lane holds
 
-template <int CH, int V> struct Shape {
-    static constexpr int lanes = CH / V;                  // of a row
-    static constexpr int groups = 64 / lanes;             // row groups of a wave
-    static constexpr int R = kPer / V;                    // rows of a lane
-    static constexpr int rows = groups * R;               // of a wave
+template <int CH> struct Shape {
+    static constexpr int groups = 64 / CH;                // row groups of a wave
+    static constexpr int rows = groups * kRows;           // of a wave
     static constexpr int tile = kWaves * rows;
 };
-static_assert(Shape<64, 2>::tile == kChunk && Shape<64, 1>::tile == kChunk && Shape<16, 2>::tile == 4 * kChunk,
-              "a tile starts where the forward pass leaves a state");
-
-template <int BYTES> struct RawOf;
-template <> struct RawOf<2> { typedef unsigned short type; };
-template <> struct RawOf<4> { typedef unsigned type; };
-template <> struct RawOf<8> { typedef unsigned type __attribute__((ext_vector_type(2))); };
-
-// V elements as they were loaded, and back.
-template <typename T, int V> __device__ __forceinline__ void decode(typename RawOf<sizeof(T) * V>::type raw, float* o)
-{
-    typedef T vec __attribute__((ext_vector_type(V)));
-    if constexpr (V == 1) {
-        o[0] = to_float(__builtin_bit_cast(T, raw));
-    } else {
-        const vec v = __builtin_bit_cast(vec, raw);
-#pragma unroll
-        for (int k = 0; k < V; ++k) o[k] = to_float((T)v[k]);
-    }
-}
-template <typename T, int V> __device__ __forceinline__ typename RawOf<sizeof(T) * V>::type encode(const float* x)
-{
-    typedef T vec __attribute__((ext_vector_type(V)));
-    typedef typename RawOf<sizeof(T) * V>::type raw;
-    if constexpr (V == 1) {
-        return __builtin_bit_cast(raw, from_float<T>(x[0]));
-    } else {
-        vec v;
-#pragma unroll
-        for (int k = 0; k < V; ++k) v[k] = from_float<T>(x[k]);
-        return __builtin_bit_cast(raw, v);
-    }
-}
+static_assert(Shape<64>::tile == kChunk && Shape<16>::tile == 4 * kChunk, "a tile starts where the forward pass leaves a state");
 
 // A lane's place in a tile.
 struct Lane {
     int row;        // its first row
-    int c;          // its first channel
+    int c;          // its channel
     bool live;      // whether that is one
-    int last;       // the last channel's vector, read in the place of those behind it
 };
 
 // A uniform value that the compiler takes for a new one in every tile: a lane's offsets of all rows of all tensors,
@@ -180,21 +147,23 @@ __device__ __forceinline__ unsigned hidden(unsigned x)
 // The rows of a tensor that a workgroup walks.  BUF: by buffer instructions, whose bounds check makes rows behind the
 // tile's last valid one, and channels behind the last, read as 0 and never written, at one 32-bit addition a row;
 // else by 64-bit addresses held inside the tensor (rows further apart than a buffer spans, or sharing memory).
-template <typename T, int V, bool BUF, int AUX> struct Walk {
-    typedef typename RawOf<sizeof(T) * V>::type raw;
+// AUX: the buffer accesses' cache policy.
+template <typename T, bool BUF, int AUX> struct Walk {
     char* base = nullptr;   // row 0 of the walk, channel 0
     int64_t row = 0;        // bytes
     unsigned at = 0;        // BUF: the lane's offset within a tile
-    __device__ __forceinline__ void open(const Rows& m, int64_t b, int64_t first, const Lane& l)
+    int c = 0;              // else the channel, one inside the tensor
+    __device__ __forceinline__ void open(const Rows& m, int64_t b, int64_t first, const Lane& l, int D)
     {
         row = m.row * (int64_t)sizeof(T);
         base = (char*)m.p + (b * m.batch + first * m.row) * (int64_t)sizeof(T);
         at = l.live ? (unsigned)(l.row * row) + (unsigned)l.c * (unsigned)sizeof(T) : 0x80000000u;
+        c = min(l.c, D - 1);
     }
-    // A tile of the walk: the rows from t0 on, of which `rows` are valid (may be <= 0); end: rows of the walk.
+    // A tile of the walk: the rows from t0 on, of which `rows` are valid (may be <= 0); end: rows of the walk, >= 1
+    // where anything is loaded.
     struct Tile {
         decltype(__builtin_amdgcn_make_buffer_rsrc((void*)nullptr, 0, 0, 0)) rs;
-        char* at;
         unsigned step;
         int t0, rows, end;
     };
@@ -208,75 +177,58 @@ template <typename T, int V, bool BUF, int AUX> struct Walk {
             o.rs = __builtin_amdgcn_make_buffer_rsrc(base + t0 * row, 0, (int)(valid * row), 0x27000);
             o.step = hidden((unsigned)row);
         }
-        o.at = base;
         o.t0 = t0;
         o.rows = rows;
         o.end = end;
         return o;
     }
-    __device__ __forceinline__ raw load(const Tile& t, int r, const Lane& l) const
-    {
-        if constexpr (BUF) {
-            const int v = (int)(at + r * t.step);
-            if constexpr (sizeof(raw) == 2) return __builtin_amdgcn_raw_buffer_load_b16(t.rs, v, 0, AUX);
-            else if constexpr (sizeof(raw) == 4) return __builtin_amdgcn_raw_buffer_load_b32(t.rs, v, 0, AUX);
-            else return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b64(t.rs, v, 0, AUX));
-        } else {
-            return *(const raw*)(t.at + (int64_t)min(l.c, l.last) * (int64_t)sizeof(T) + min(t.t0 + l.row + r, t.end - 1) * row);
-        }
-    }
-    __device__ __forceinline__ void store(const Tile& t, raw v, int r, const Lane& l) const
+    __device__ __forceinline__ T load(const Tile& t, int r, const Lane& l) const
     {
         if constexpr (BUF) {
             const int o = (int)(at + r * t.step);
-            if constexpr (sizeof(raw) == 2) __builtin_amdgcn_raw_buffer_store_b16(v, t.rs, o, 0, AUX);
-            else if constexpr (sizeof(raw) == 4) __builtin_amdgcn_raw_buffer_store_b32(v, t.rs, o, 0, AUX);
-            else {
-                typedef int i32x2 __attribute__((ext_vector_type(2)));
-                __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(i32x2, v), t.rs, o, 0, AUX);
-            }
+            if constexpr (sizeof(T) == 2) return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(t.rs, o, 0, AUX));
+            else return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(t.rs, o, 0, AUX));
+        } else {
+            return *(const T*)(base + c * (int64_t)sizeof(T) + min(t.t0 + l.row + r, t.end - 1) * row);
+        }
+    }
+    __device__ __forceinline__ void store(const Tile& t, float x, int r, const Lane& l) const
+    {
+        const T v = from_float<T>(x);
+        if constexpr (BUF) {
+            const int o = (int)(at + r * t.step);
+            if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, v), t.rs, o, 0, AUX);
+            else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), t.rs, o, 0, AUX);
         } else if (l.live && l.row + r < t.rows) {
-            *(raw*)(t.at + (t.t0 + l.row + r) * row + (int64_t)l.c * (int64_t)sizeof(T)) = v;
+            *(T*)(base + c * (int64_t)sizeof(T) + (t.t0 + l.row + r) * row) = v;
         }
     }
     // Zeros in rows [from, to) of CH channels from c0 on, by the whole workgroup.
     template <int CH> __device__ __forceinline__ void clear(int from, int to, int c0, int D) const
     {
-        const int c = c0 + (int)(threadIdx.x % CH);
-        if (c >= D) return;
+        const int k = c0 + (int)(threadIdx.x % CH);
+        if (k >= D) return;
         for (int64_t t = from + (int)(threadIdx.x / CH); t < to; t += 64 * kWaves / CH)
-            *(T*)(base + t * row + c * (int64_t)sizeof(T)) = from_float<T>(0.0f);
+            *(T*)(base + t * row + k * (int64_t)sizeof(T)) = from_float<T>(0.0f);
     }
 };
 
-// Whether a tensor's rows can be walked by buffer instructions, and whether they lie at multiples of `bytes`.
+// Whether a tensor's rows can be walked by buffer instructions: apart from each other, the longest tile below 2^31 bytes.
 inline bool walks(const Rows& m, const DiagProblem& p)
 {
-    constexpr int tile = Shape<16, 1>::tile;           // the longest
     const int64_t row = m.row * (p.bf16 ? 2 : 4);
-    return !m.p || (m.row >= p.D && row <= ((int64_t(1) << 31) - 1) / tile);
-}
-inline bool aligned(const Rows& m, const DiagProblem& p, size_t bytes)
-{
-    const size_t e = p.bf16 ? 2 : 4;
-    return !m.p || ((uintptr_t)m.p % bytes == 0 && (p.B == 1 || m.batch * e % bytes == 0) && (p.T == 1 || m.row * e % bytes == 0));
+    return !m.p || (m.row >= p.D && row <= ((int64_t(1) << 31) - 1) / Shape<16>::tile);
 }
 
 // The value of the lower and of the upper of the two lanes D apart (the one with bit D clear, and set), in both.
-template <int D> __device__ __forceinline__ void pair_of(float v, int lane, float* low, float* high)
+template <int D> __device__ __forceinline__ void pair_of(float v, float* low, float* high)
 {
     const unsigned u = __builtin_bit_cast(unsigned, v);
-    if constexpr (D == 8) {
-        const float o = __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp((int)u, 0x128, 0xf, 0xf, true));   // rotated by 8 of 16
-        *low = lane & 8 ? o : v;
-        *high = lane & 8 ? v : o;
-    } else {
-        const auto r = D == 16 ? __builtin_amdgcn_permlane16_swap(u, u, false, false)
-                               : __builtin_amdgcn_permlane32_swap(u, u, false, false);
-        const unsigned x = r[0], y = r[1];
-        *low = __builtin_bit_cast(float, x);
-        *high = __builtin_bit_cast(float, y);
-    }
+    const auto r = D == 16 ? __builtin_amdgcn_permlane16_swap(u, u, false, false)
+                           : __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const unsigned x = r[0], y = r[1];
+    *low = __builtin_bit_cast(float, x);
+    *high = __builtin_bit_cast(float, y);
 }
 
 // Joins the row groups of a wave, D lanes apart and more: F, H go from the map of a lane's group to the wave's, pf, ph
@@ -285,8 +237,8 @@ template <int D> __device__ __forceinline__ void join(int lane, float* F, float*
 {
     if constexpr (D < 64) {
         float lf, uf, lh, uh;
-        pair_of<D>(*F, lane, &lf, &uf);
-        pair_of<D>(*H, lane, &lh, &uh);
+        pair_of<D>(*F, &lf, &uf);
+        pair_of<D>(*H, &lh, &uh);
         const bool upper = lane & D;
         *ph += *pf * (upper ? lh : 0.0f);
         *pf *= upper ? lf : 1.0f;
@@ -301,9 +253,9 @@ __device__ __forceinline__ void join_both(int lane, float* F, float* H, float* A
 {
     if constexpr (D < 64) {
         float lf, uf, lh, uh, la, ua;
-        pair_of<D>(*F, lane, &lf, &uf);
-        pair_of<D>(*H, lane, &lh, &uh);
-        pair_of<D>(*A, lane, &la, &ua);
+        pair_of<D>(*F, &lf, &uf);
+        pair_of<D>(*H, &lh, &uh);
+        pair_of<D>(*A, &la, &ua);
         const bool upper = lane & D;
         *ph += *pf * (upper ? lh : 0.0f);
         *pf *= upper ? lf : 1.0f;
@@ -317,24 +269,24 @@ __device__ __forceinline__ void join_both(int lane, float* F, float* H, float* A
 }
 
 // F and A alone.
-template <int D> __device__ __forceinline__ void join_behind(int lane, float* F, float* A)
+template <int D> __device__ __forceinline__ void join_behind(float* F, float* A)
 {
     if constexpr (D < 64) {
         float lf, uf, la, ua;
-        pair_of<D>(*F, lane, &lf, &uf);
-        pair_of<D>(*A, lane, &la, &ua);
+        pair_of<D>(*F, &lf, &uf);
+        pair_of<D>(*A, &la, &ua);
         *F = lf * uf;
         *A = lf * ua + la;
-        join_behind<2 * D>(lane, F, A);
+        join_behind<2 * D>(F, A);
     }
 }
 // The sum over the row groups.
-template <int D> __device__ __forceinline__ float sum_groups(int lane, float v)
+template <int D> __device__ __forceinline__ float sum_groups(float v)
 {
     if constexpr (D < 64) {
         float a, b;
-        pair_of<D>(v, lane, &a, &b);
-        return sum_groups<2 * D>(lane, a + b);
+        pair_of<D>(v, &a, &b);
+        return sum_groups<2 * D>(a + b);
     }
     return v;
 }
@@ -362,15 +314,13 @@ __device__ __forceinline__ bool place(const DiagProblem& p, const Cut& cut, Plac
     return q->b < p.B;
 }
 
-template <int CH, int V> __device__ __forceinline__ Lane lane_of(const DiagProblem& p, const Place& q)
+template <int CH> __device__ __forceinline__ Lane lane_of(const DiagProblem& p, const Place& q)
 {
-    typedef Shape<CH, V> S;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Lane l;
-    l.row = wave * S::rows + lane / S::lanes * S::R;
-    l.c = q.cb * CH + lane % S::lanes * V;
+    l.row = wave * Shape<CH>::rows + lane / CH * kRows;
+    l.c = q.cb * CH + lane % CH;
     l.live = l.c < p.D;
-    l.last = p.D - V;
     return l;
 }
 
@@ -396,7 +346,7 @@ inline Cut cut_of(const DiagProblem& p, bool buf, bool bwd)
     }
     c.ncb = (p.D + c.ch - 1) / c.ch;
     c.near = 64 / c.ch;
-    const int tile = kWaves * kPer * 64 / c.ch;
+    const int tile = kWaves * kRows * 64 / c.ch;
     const int tiles = (p.T + tile - 1) / tile;
     const int64_t blocks = (int64_t)p.B * c.ncb;
     int64_t n = whole ? 1 : (256 + blocks - 1) / blocks;
