@@ -258,3 +258,25 @@ def test_offsets_beyond_32_bits():
     got, want = tfla.addnorm_backward(view, view, w, dx=out), tfla.addnorm_backward(x, x, w)
     assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("act,stream", TYPES)
+def test_many_rows(act, stream):
+    """More rows than workgroups take at once, and parts of the weights' gradients that add up many of them."""
+    check(act, stream, 3, 7001, 40, rms=True)
+    check(act, stream, 1, 3001, 520)
+
+
+def test_a_call_that_streams():
+    """Large enough for loads past the caches; against the same rows in two smaller calls."""
+    B, T, C = 2, 20000, 2048
+    t, dy, dt = (torch.randn(B, T, C, device="cuda").to(BF) for _ in range(3))
+    w = torch.randn(C, device="cuda")
+    dx, _, dw, db = tfla.addnorm_backward(t, dy, w, bias=True, dtotal=dt)
+    parts = [tfla.addnorm_backward(t[:, a:b], dy[:, a:b], w, bias=True, dtotal=dt[:, a:b]) for a, b in ((0, 3000), (3000, 20000))]
+    torch.cuda.synchronize()
+    assert torch.equal(dx, torch.cat([p[0] for p in parts], 1))
+    mag = dy.double().abs()
+    # sums of 40000 terms in two orders; |th| is at most 6 here
+    assert bool(((dw - sum(p[2] for p in parts)).abs() <= 2 * 40100 * U * 6 * mag.sum((0, 1))).all())
+    assert bool(((db - sum(p[3] for p in parts)).abs() <= 2 * 40100 * U * mag.sum((0, 1))).all())

@@ -381,3 +381,33 @@ def test_offsets_beyond_32_bits(D):
         assert torch.allclose(view.float(), wg.dfgate.float(), **tol)
         torch.cuda.synchronize()
         del full, view
+
+
+def test_very_many_sequences():
+    """More workgroups than one dimension of a grid holds."""
+    B, T, D = (1 << 21) + 5, 5, 1
+    x, fg, dy = (torch.randn(B, T, D, device="cuda") for _ in range(3))
+    y, end, starts = tfla.diag_forward(x, fg, want_state=True, want_starts=True)
+    g = tfla.diag_backward(x, fg, dy, starts, want_dstate=True)
+    f = torch.sigmoid(fg.double())
+    h, hs = torch.zeros(B, D, dtype=torch.float64, device="cuda"), []
+    for t in range(T):
+        hs.append(h)
+        h = f[:, t] * h + (1 - f[:, t]) * x[:, t]
+    a = torch.zeros_like(h)
+    for t in reversed(range(T)):
+        gt = dy[:, t] + a
+        a = f[:, t] * gt
+        # up to 5 terms of order 5, gates within 20 U
+        assert float((g.dx[:, t] - (1 - f[:, t]) * gt).abs().max()) <= 5 * 5 * 40 * U
+        assert float((g.dfgate[:, t] - f[:, t] * (1 - f[:, t]) * gt * (hs[t] - x[:, t])).abs().max()) <= 25 * 5 * 40 * U
+    torch.cuda.synchronize()
+    assert float((end - h).abs().max()) <= 5 * 5 * 40 * U and float((g.dstate - a).abs().max()) <= 5 * 5 * 40 * U
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("B,T,D", [(2, 700, 520), (9, 140, 1000), (3, 900, 1100), (33, 130, 520), (1, 2500, 64)])
+def test_cuts(dtype, kind, B, T, D):
+    """Blocks of 16, 32 and 64 channels, whole and in segments."""
+    check(dtype, kind, B, T, D)

@@ -235,3 +235,18 @@ def test_offsets_beyond_32_bits():
     want, _ = tfla.rotary_forward(x, None, f)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+def test_very_many_sequences():
+    """More workgroups than one dimension of a grid holds."""
+    B = (1 << 21) + 3
+    x = torch.randn(B, 1, 1, 4, device="cuda")
+    freqs, _ = tfla.rotary_frequencies(4)
+    start = torch.arange(B, dtype=torch.int32, device="cuda")
+    y, _ = tfla.rotary_forward(x, None, freqs, start=start)
+    ang = start.double()[:, None] * freqs
+    a, b = x[:, 0, 0, :2].double(), x[:, 0, 0, 2:].double()
+    want = torch.cat([a * ang.cos() - b * ang.sin(), b * ang.cos() + a * ang.sin()], -1)
+    tol = (12 * U + 2.0 ** 22 * 2.0 ** -51) * (a.abs() + b.abs()).repeat(1, 2) + U * want.abs()
+    torch.cuda.synchronize()
+    assert bool(((y[:, 0, 0] - want).abs() <= tol).all())
