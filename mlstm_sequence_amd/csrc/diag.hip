@@ -24,7 +24,9 @@ using namespace diag;
 
 constexpr int kAhead = 2;   // tiles under way (even: two LDS buffers in turn)
 
-// OUT: outputs; else the segment's map.  The first reading of a segmented walk goes through the caches, for the second
+// OUT: outputs; else the segment's map.  No segment starts from the last one's map: in its place the first pass leaves
+// the state before the first row, since the second may update that in place (one workgroup writes it at its end, which
+// may be before another begins).  The first reading of a segmented walk goes through the caches, for the second
 // (B=1 T=30000 D=1024 bf16, coupled: 63 us and 68 past them).
 template <typename T, int KIND, int CH, bool BUF, bool OUT>
 __global__ __launch_bounds__(64 * kWaves, 2) void diag_fwd_kernel(DiagProblem p, Cut cut, f32x2* __restrict__ ends)
@@ -34,7 +36,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void diag_fwd_kernel(DiagProblem p,
     constexpr int kTile = S::tile;
     __shared__ f32x2 tot[2][kWaves][CH];
     Place q;
-    if (!place(p, cut, &q) || (!OUT && q.seg == cut.nseg - 1)) return;   // no segment starts from the last one's map
+    if (!place(p, cut, &q)) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const Lane l = lane_of<CH>(p, q);
     const int col = lane % CH, cc = min(l.c, p.D - 1);
@@ -43,6 +45,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void diag_fwd_kernel(DiagProblem p,
     // rows of this segment; the same for all lanes, which the compiler cannot tell of a loaded value
     const int n = __builtin_amdgcn_readfirstlane(min(max(clamp_len(p.lengths, (int)q.b, p.T) - s0, 0), all));
     const int64_t nc = (p.T + kChunk - 1) / kChunk;
+    f32x2* e = ends + q.b * cut.nseg * p.D + cc;       // of the lane's channel, a segment p.D apart
+    if (!OUT && q.seg == cut.nseg - 1) {
+        if (wave == 0 && first && l.live) e[(int64_t)q.seg * p.D] = f32x2{1.0f, p.state ? p.state[q.b * p.D + cc] : 0.0f};
+        return;
+    }
     In wx, wu, wv;
     Walk<T, BUF, 0> wy;
     wx.open(p.x, q.b, s0, l, p.D);
@@ -50,10 +57,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void diag_fwd_kernel(DiagProblem p,
     if (KIND != kCoupled) wv.open(p.igate, q.b, s0, l, p.D);
     if (OUT) wy.open(p.y, q.b, s0, l, p.D);
     const Rate decay(KIND == kDecay ? p.decay[cc] : 0.0f);
-    float h0 = OUT && p.state ? p.state[q.b * p.D + cc] : 0.0f, f0 = 1.0f;   // the state before the tile; !OUT: the map so far
+    float h0 = 0.0f, f0 = 1.0f;                        // the state before the tile; !OUT: the map so far
     if (OUT) {
         constexpr int LINKS = 8;                       // in batches, whose loads are under way together
-        const f32x2* e = ends + q.b * cut.nseg * p.D + cc;
+        if (cut.nseg > 1) h0 = e[(int64_t)(cut.nseg - 1) * p.D][1];
+        else if (p.state) h0 = p.state[q.b * p.D + cc];
         for (int j0 = 0; j0 < q.seg; j0 += LINKS) {
             f32x2 m[LINKS];
 #pragma unroll
@@ -149,7 +157,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void diag_fwd_kernel(DiagProblem p,
         for (int i = 0; i < kAhead; ++i)
             if (t0 + i * kTile < n) tile(t0 + i * kTile, i & 1, raw[i]);
     if (!OUT) {
-        if (wave == 0 && first && l.live) ends[(q.b * cut.nseg + q.seg) * p.D + l.c] = f32x2{f0, h0};
+        if (wave == 0 && first && l.live) e[(int64_t)q.seg * p.D] = f32x2{f0, h0};
         return;
     }
     wy.template clear<CH>(n, all, q.cb * CH, p.D);

@@ -411,3 +411,30 @@ def test_very_many_sequences():
 def test_cuts(dtype, kind, B, T, D):
     """Blocks of 16, 32 and 64 channels, whole and in segments."""
     check(dtype, kind, B, T, D)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_state_in_place_of_a_long_call(dtype):
+    """Cut into segments, every one of which starts from the state that the last one replaces."""
+    dev, _ = make(dtype, "decay", 2, 3000, 200)
+    x, fg, ig, dc, st = (dev[k].cuda() for k in ("x", "fg", "ig", "decay", "state"))
+    kw = dict(kind=tfla.DIAG_DECAY, want_starts=True)
+    assert tfla.lib().tfla_diag_workspace_bytes(2, 3000, 200, 2, 0x100 if dtype == BF else 0) > 0
+    want, end, starts = tfla.diag_forward(x, fg, ig, dc, state=st, want_state=True, **kw)
+    got, same, again = tfla.diag_forward(x, fg, ig, dc, state=st, state_out=st, **kw)
+    torch.cuda.synchronize()
+    assert same is st and torch.equal(got, want) and torch.equal(st, end) and torch.equal(again, starts)
+
+
+def test_a_states_copy_serves_every_segment():
+    """The workspace holds the state before the first row once a call is cut: what a workgroup that starts late reads."""
+    dev, _ = make(F32, "coupled", 1, 3000, 64)
+    x, fg, st = (dev[k].cuda() for k in ("x", "fg", "state"))
+    n = tfla.lib().tfla_diag_workspace_bytes(1, 3000, 64, 0, 0)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    before = st.clone()
+    tfla.diag_forward(x, fg, state=st, state_out=st, workspace=ws)
+    torch.cuda.synchronize()
+    pairs = ws.view(torch.float32).view(-1, 2)
+    held = [i for i in range(0, pairs.shape[0] - 63, 64) if torch.equal(pairs[i:i + 64, 1], before[0])]
+    assert held and not torch.equal(st, before)
