@@ -99,7 +99,16 @@ def _first(x, name, dims):
 
 def _new(x):
     """A contiguous tensor of the shape and type of ``x``."""
-    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
+def _out(t, name, like, dtype, dev):
+    """An output [B,T,D], new where ``t`` is None, and its tfla_rows."""
+    if t is not None:
+        return t, _rows(t, name, like.shape, dtype, dev)
+    t = _new(like)
+    _, T, D = like.shape
+    return t, (t.data_ptr(), T * D, D)
 
 
 def _flat(t, name, shape, dtype, dev):
@@ -182,8 +191,17 @@ def _rotary(name, q, k, freqs, layout, scale, positions, start, lengths, q_out, 
     if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
         raise ValueError("freqs must be a one-dimensional fp64 tensor")
     half = freqs.shape
-    if q_out is None:
-        q_out = q.new_empty((B, H, T, C)).transpose(1, 2) if head_major else _new(q)
+
+    def out(t, name, like, n):   # a new tensor's strides are known
+        if t is not None:
+            return t, _heads(t, name, (B, T, n, C), dtype, dev)
+        if head_major:
+            t = like.new_empty((B, n, T, C)).transpose(1, 2)
+            return t, (t.data_ptr(), n * T * C, C, T * C)
+        t = _new(like)
+        return t, (t.data_ptr(), T * n * C, n * C, C)
+
+    q_out, queries_out = out(q_out, "q_out", q, H)
     Hk, keys, keys_out = 0, _NO_HEADS, _NO_HEADS
     if k is not None:
         if not isinstance(k, torch.Tensor) or k.dim() != 4:
@@ -191,9 +209,7 @@ def _rotary(name, q, k, freqs, layout, scale, positions, start, lengths, q_out, 
         Hk = k.shape[2]
         kshape = (B, T, Hk, C)
         keys = _heads(k, "k", kshape, dtype, dev)
-        if k_out is None:
-            k_out = k.new_empty((B, Hk, T, C)).transpose(1, 2) if head_major else _new(k)
-        keys_out = _heads(k_out, "k_out", kshape, dtype, dev)
+        k_out, keys_out = out(k_out, "k_out", k, Hk)
     elif k_out is not None:
         raise ValueError("k_out is given without k")
     at = stride = 0
@@ -207,7 +223,7 @@ def _rotary(name, q, k, freqs, layout, scale, positions, start, lengths, q_out, 
     packed = _ROTARY.pack(B, T, H, Hk, C, 2 * half[0], _IO[dtype] | layout, scale,
                           _flat(freqs, "freqs", half, torch.float64, dev), at, stride,
                           _flat(start, "start", (B,), torch.int32, dev), _flat(lengths, "lengths", (B,), torch.int32, dev),
-                          *_heads(q, "q", shape, dtype, dev), *keys, *_heads(q_out, "q_out", shape, dtype, dev), *keys_out)
+                          *_heads(q, "q", shape, dtype, dev), *keys, *queries_out, *keys_out)
     _call(name, packed, dev, None, None, fn)
     return q_out, k_out
 
@@ -290,13 +306,12 @@ def diag_forward(x, fgate, igate=None, decay=None, kind: int = DIAG_COUPLED, sta
     fields, sizes, dev = _diag_args(x, fgate, igate, decay, kind, lengths)
     shape, dtype, f32 = x.shape, x.dtype, torch.float32
     bd = (shape[0], shape[2])
-    if y is None:
-        y = _new(x)
+    y, yr = _out(y, "y", x, dtype, dev)
     if state_out is None and want_state:
         state_out = x.new_empty(bd, dtype=f32)
     if starts is None and want_starts:
         starts = x.new_empty(_chunks(shape), dtype=f32)
-    packed = _DIAG.pack(*fields, _flat(state, "state", bd, f32, dev), *_rows(y, "y", shape, dtype, dev),
+    packed = _DIAG.pack(*fields, _flat(state, "state", bd, f32, dev), *yr,
                         _flat(state_out, "state_out", bd, f32, dev),
                         0 if starts is None else _flat(starts, "starts", _chunks(shape), f32, dev),
                         *_NO_ROWS, 0, *_NO_ROWS * 3, 0, 0)
@@ -320,22 +335,18 @@ def diag_backward(x, fgate, dy, starts, igate=None, decay=None, kind: int = DIAG
     bd = (shape[0], shape[2])
     if starts is None:
         raise ValueError("starts is needed: the states that diag_forward leaves with want_starts")
-    if dx is None:
-        dx = _new(x)
-    if dfgate is None:
-        dfgate = _new(x)
-    gate = _NO_ROWS
+    dx, dxr = _out(dx, "dx", x, dtype, dev)
+    dfgate, dur = _out(dfgate, "dfgate", x, dtype, dev)
+    dvr = _NO_ROWS
     if igate is not None:
-        if digate is None:
-            digate = _new(x)
-        gate = _rows(digate, "digate", shape, dtype, dev)
+        digate, dvr = _out(digate, "digate", x, dtype, dev)
     elif digate is not None:
         raise ValueError("digate is given without igate")
     ddecay = None if decay is None else torch.empty_like(decay)
     dstate = x.new_empty(bd, dtype=f32) if want_dstate else None
     packed = _DIAG.pack(*fields, 0, *_NO_ROWS, 0, _flat(starts, "starts", _chunks(shape), f32, dev),
                         *_rows(dy, "dy", shape, dtype, dev), _flat(dstate_out, "dstate_out", bd, f32, dev),
-                        *_rows(dx, "dx", shape, dtype, dev), *_rows(dfgate, "dfgate", shape, dtype, dev), *gate,
+                        *dxr, *dur, *dvr,
                         0 if ddecay is None else ddecay.data_ptr(), 0 if dstate is None else dstate.data_ptr())
     _call("tfla_diag_bwd", packed, dev, need(*sizes), workspace, _fn["tfla_diag_bwd"])
     return DiagGrads(dx, dfgate, digate, ddecay, dstate)
@@ -369,21 +380,18 @@ def addnorm_forward(x, residual=None, weight=None, bias=None, eps: float = 1e-5,
     shape, dtype, f32 = x.shape, x.dtype, torch.float32
     flags, c = _IO[dtype] | (_RMS if rms else 0), shape[2:]
     res = tot = _NO_ROWS
-    if y is None:
-        y = _new(x)
+    y, yr = _out(y, "y", x, dtype, dev)
     if residual is not None:
         st = _stream_type(residual, "residual", dtype)
         if st is not dtype:
             flags |= _SUM_FP32
         res = _rows(residual, "residual", shape, st, dev)
-        if total is None:
-            total = _new(residual)
-        tot = _rows(total, "total", shape, st, dev)
+        total, tot = _out(total, "total", residual, st, dev)
     elif total is not None:
         raise ValueError("total is given without a residual")
     packed = _ADDNORM.pack(*shape, flags, eps, *_rows(x, "x", shape, dtype, dev), *res,
                            _flat(weight, "weight", c, f32, dev), _flat(bias, "bias", c, f32, dev),
-                           *_rows(y, "y", shape, dtype, dev), *tot, *_NO_ROWS * 4, 0, 0)
+                           *yr, *tot, *_NO_ROWS * 4, 0, 0)
     _call("tfla_addnorm_fwd", packed, dev, None, None, fn)
     return y, total
 
@@ -406,23 +414,21 @@ def addnorm_backward(total, dy, weight=None, bias: bool = False, eps: float = 1e
     flags, c = _IO[dtype] | (_RMS if rms else 0), shape[2:]
     st = _stream_type(total, "total", dtype)
     res = _NO_ROWS
-    if dx is None:
-        dx = _new(dy)
+    dx, dxr = _out(dx, "dx", dy, dtype, dev)
     if st is dtype:
         if dresidual is not None and dresidual is not dx:
             raise ValueError("dresidual is dx where dy and total have one type")
         dresidual = dx
     else:
         flags |= _SUM_FP32
-        if dresidual is None:
-            dresidual = _new(total)
-        res = _rows(dresidual, "dresidual", shape, st, dev)
+        _rows(total, "total", shape, st, dev)   # before an output takes its shape
+        dresidual, res = _out(dresidual, "dresidual", total, st, dev)
     dweight = None if weight is None else torch.empty_like(weight)
     dbias = dy.new_empty(c, dtype=f32) if bias else None
     packed = _ADDNORM.pack(*shape, flags, eps, *_NO_ROWS * 2, _flat(weight, "weight", c, f32, dev), 0, *_NO_ROWS,
                            *_rows(total, "total", shape, st, dev), *_rows(dy, "dy", shape, dtype, dev),
                            *(_NO_ROWS if dtotal is None else _rows(dtotal, "dtotal", shape, st, dev)),
-                           *_rows(dx, "dx", shape, dtype, dev), *res,
+                           *dxr, *res,
                            0 if dweight is None else dweight.data_ptr(), 0 if dbias is None else dbias.data_ptr())
     wanted = need(*shape, flags) if weight is not None or bias else None
     _call("tfla_addnorm_bwd", packed, dev, wanted or 0, workspace if wanted else None, _fn["tfla_addnorm_bwd"])
