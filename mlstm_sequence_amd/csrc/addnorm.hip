@@ -16,28 +16,26 @@ using namespace addnorm;
 constexpr unsigned kBlocks = 2048;
 
 // T: activations, S: the stream.  NV vectors a lane.
-template <typename T, typename S, int VEC, int NV>
+template <typename T, typename S, int NV, bool EDGE>
 __global__ __launch_bounds__(1024) void addnorm_fwd_kernel(AddNormProblem p, RowMap m)
 {
+    constexpr int VEC = vec_of<T, S>();
     __shared__ float red[2][16][1];
     const int slot = threadIdx.x / m.L, lv = threadIdx.x & (m.L - 1);
     const bool sum = p.residual.p != nullptr, shift = !p.rms;
-    int c[NV];
-    bool in[NV];
+    const Columns<VEC, NV, EDGE> cols(lv, m.L, m.nv, p.C);
+    const int* c = cols.c;
     float w[NV][VEC], bs[NV][VEC];
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        in[k] = lv + k * m.L < m.nv;
-        c[k] = min(lv + k * m.L, m.nv - 1) * VEC;
+    for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             w[k][v] = p.weight ? p.weight[c[k] + v] : 1.0f;
             bs[k][v] = p.bias ? p.bias[c[k] + v] : 0.0f;
         }
-    }
     const float inv = 1.0f / (float)p.C;
-    Pack<T, VEC, false> rx[NV];
-    Pack<S, VEC, false> rr[NV];
+    Pack<T, VEC, EDGE, false> rx[NV];
+    Pack<S, VEC, EDGE, false> rr[NV];
     auto fetch = [&](unsigned i) {                    // behind the last row: the last
         i = min(i, m.rows - 1);
         const int64_t b = i / (unsigned)p.T, t = i % (unsigned)p.T;
@@ -65,7 +63,7 @@ __global__ __launch_bounds__(1024) void addnorm_fwd_kernel(AddNormProblem p, Row
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) s += in[k] ? x[k][v] : 0.0f;
+                for (int v = 0; v < VEC; ++v) s += cols.counts(k, v) ? x[k][v] : 0.0f;
             row_sums<1>(&s, m.L, red, turn);
             turn ^= 1;
             mean = s * inv;
@@ -75,7 +73,7 @@ __global__ __launch_bounds__(1024) void addnorm_fwd_kernel(AddNormProblem p, Row
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
                 const float d = x[k][v] - mean;
-                q += in[k] ? d * d : 0.0f;
+                q += cols.counts(k, v) ? d * d : 0.0f;
             }
         row_sums<1>(&q, m.L, red, turn);
         turn ^= 1;
@@ -84,9 +82,9 @@ __global__ __launch_bounds__(1024) void addnorm_fwd_kernel(AddNormProblem p, Row
         const int64_t b = i / (unsigned)p.T, t = i % (unsigned)p.T;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            if (!in[k]) continue;
-            Pack<T, VEC, false> o;
-            Pack<S, VEC, false> ot;
+            if (!cols.in[k]) continue;
+            Pack<T, VEC, EDGE, false> o;
+            Pack<S, VEC, EDGE, false> ot;
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
                 o.set(v, (x[k][v] - mean) * rstd * w[k][v] + bs[k][v]);
@@ -127,26 +125,24 @@ __global__ __launch_bounds__(256) void addnorm_fwd_long_kernel(AddNormProblem p)
     }
 }
 
-template <typename T, typename S, int VEC>
-hipError_t fwd_v(const AddNormProblem& p, hipStream_t stream)
+template <typename T, typename S, bool EDGE>
+hipError_t fwd_e(const AddNormProblem& p, hipStream_t stream)
 {
-    if (!in_registers(p, VEC)) {
-        addnorm_fwd_long_kernel<T, S><<<grid_of((int64_t)p.B * p.T), 256, 0, stream>>>(p);
-        return hipGetLastError();
-    }
-    const RowMap m = row_map(p, VEC, most_vectors(p, VEC), kBlocks);
+    const RowMap m = row_map(p, most_vectors(p), kBlocks);
     const int v = (m.nv + m.L - 1) / m.L;
-    if (v == 1) addnorm_fwd_kernel<T, S, VEC, 1><<<m.blocks, m.threads, 0, stream>>>(p, m);
-    else if (v == 2) addnorm_fwd_kernel<T, S, VEC, 2><<<m.blocks, m.threads, 0, stream>>>(p, m);
-    else if constexpr (most_vectors<T, S, VEC>() == 4) addnorm_fwd_kernel<T, S, VEC, 4><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    if (v == 1) addnorm_fwd_kernel<T, S, 1, EDGE><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    else if (v == 2) addnorm_fwd_kernel<T, S, 2, EDGE><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    else if constexpr (most_vectors<T, S>() == 4) addnorm_fwd_kernel<T, S, 4, EDGE><<<m.blocks, m.threads, 0, stream>>>(p, m);
     return hipGetLastError();
 }
 
 template <typename T, typename S>
 hipError_t fwd_t(const AddNormProblem& p, hipStream_t stream)
 {
-    constexpr int wide = 16 / (sizeof(T) > sizeof(S) ? sizeof(T) : sizeof(S));
-    return vec_of(p, {&p.x, &p.residual, &p.y, &p.total}) == wide ? fwd_v<T, S, wide>(p, stream) : fwd_v<T, S, 1>(p, stream);
+    if (in_registers(p))
+        return edged(p, {&p.x, &p.residual, &p.y, &p.total}) ? fwd_e<T, S, true>(p, stream) : fwd_e<T, S, false>(p, stream);
+    addnorm_fwd_long_kernel<T, S><<<grid_of((int64_t)p.B * p.T), 256, 0, stream>>>(p);
+    return hipGetLastError();
 }
 
 }  // namespace

@@ -21,10 +21,10 @@ using namespace addnorm;
 // How the rows fall to workgroups, and the parts of the weights' gradients: enough to fill the chip, of 16 rows or
 // more beyond that.  Rows of 512 to 1024 vectors take one vector a lane, as two leave room for one workgroup of 8 waves
 // on a CU.
-RowMap map_of(const AddNormProblem& p, int vec)
+RowMap map_of(const AddNormProblem& p)
 {
-    const int nv = p.C / vec, most = nv > 512 && nv <= 1024 ? 1 : most_vectors(p, vec);
-    RowMap m = row_map(p, vec, most, 768);
+    const int nv = vectors(p), most = nv > 512 && nv <= 1024 ? 1 : most_vectors(p);
+    RowMap m = row_map(p, most, 768);
     const unsigned few = (m.rows + 16 * m.slots - 1) / (16 * m.slots);
     if (m.blocks > few) m.blocks = few > 512 ? few : m.blocks < 512 ? m.blocks : 512;
     return m;
@@ -38,30 +38,28 @@ bool streams(const AddNormProblem& p)
 }
 
 // THREADS: the workgroup's size is at most that.
-template <typename T, typename S, int VEC, int NV, int THREADS, bool NT>
+template <typename T, typename S, int NV, int THREADS, bool EDGE, bool NT>
 __global__ __launch_bounds__(THREADS) void addnorm_bwd_kernel(AddNormProblem p, RowMap m)
 {
     constexpr bool TWO = sizeof(T) != sizeof(S);
+    constexpr int VEC = vec_of<T, S>();
     __shared__ float red1[2][16][1], red3[2][16][3];
     __shared__ float acc[THREADS > 256 ? 1 : 256 * NV * VEC];
     const int slot = threadIdx.x / m.L, lv = threadIdx.x & (m.L - 1);
     const bool shift = !p.rms, behind = p.dtotal.p != nullptr;
-    int c[NV];
-    bool in[NV];
+    const Columns<VEC, NV, EDGE> cols(lv, m.L, m.nv, p.C);
+    const int* c = cols.c;
     float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        in[k] = lv + k * m.L < m.nv;
-        c[k] = min(lv + k * m.L, m.nv - 1) * VEC;
+    for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             w[k][v] = p.weight ? p.weight[c[k] + v] : 1.0f;
             dw[k][v] = db[k][v] = 0.0f;
         }
-    }
     const float inv = 1.0f / (float)p.C;
-    Pack<S, VEC, NT> rt[NV], re[NV];
-    Pack<T, VEC, NT> rg[NV];
+    Pack<S, VEC, EDGE, NT> rt[NV], re[NV];
+    Pack<T, VEC, EDGE, NT> rg[NV];
     auto fetch = [&](unsigned i) {                    // behind the last row: the last
         i = min(i, m.rows - 1);
         const int64_t b = i / (unsigned)p.T, t = i % (unsigned)p.T;
@@ -79,7 +77,7 @@ __global__ __launch_bounds__(THREADS) void addnorm_bwd_kernel(AddNormProblem p, 
         const unsigned i = i0 + slot;
         const bool live = i < m.rows;
         float d[NV][VEC], g[NV][VEC], s = 0.0f, mean = 0.0f;
-        Pack<S, VEC, NT> e[NV];
+        Pack<S, VEC, EDGE, NT> e[NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             e[k] = re[k];
@@ -94,7 +92,7 @@ __global__ __launch_bounds__(THREADS) void addnorm_bwd_kernel(AddNormProblem p, 
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) s += in[k] ? d[k][v] : 0.0f;
+                for (int v = 0; v < VEC; ++v) s += cols.counts(k, v) ? d[k][v] : 0.0f;
             row_sums<1>(&s, m.L, red1, turn);
             mean = s * inv;
         }
@@ -105,9 +103,9 @@ __global__ __launch_bounds__(THREADS) void addnorm_bwd_kernel(AddNormProblem p, 
             for (int v = 0; v < VEC; ++v) {
                 d[k][v] -= mean;
                 const float u = g[k][v] * w[k][v];
-                q[0] += in[k] ? d[k][v] * d[k][v] : 0.0f;
-                q[1] += in[k] ? u : 0.0f;
-                q[2] += in[k] ? u * d[k][v] : 0.0f;
+                q[0] += cols.counts(k, v) ? d[k][v] * d[k][v] : 0.0f;
+                q[1] += cols.counts(k, v) ? u : 0.0f;
+                q[2] += cols.counts(k, v) ? u * d[k][v] : 0.0f;
             }
         row_sums<3>(q, m.L, red3, turn);
         const float rstd = 1.0f / sqrtf(q[0] * inv + p.eps);
@@ -116,9 +114,9 @@ __global__ __launch_bounds__(THREADS) void addnorm_bwd_kernel(AddNormProblem p, 
         const int64_t b = i / (unsigned)p.T, t = i % (unsigned)p.T;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            if (!in[k]) continue;
-            Pack<T, VEC, false> o;
-            Pack<S, VEC, false> o2;
+            if (!cols.in[k]) continue;
+            Pack<T, VEC, EDGE, false> o;
+            Pack<S, VEC, EDGE, false> o2;
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
                 dw[k][v] += g[k][v] * (d[k][v] * rstd);
@@ -139,7 +137,7 @@ __global__ __launch_bounds__(THREADS) void addnorm_bwd_kernel(AddNormProblem p, 
         for (int k = 0; k < NV; ++k)
 #pragma unroll
             for (int v = 0; v < VEC; ++v)
-                if (in[k]) {
+                if (cols.in[k]) {
                     part[c[k] + v] = dw[k][v];
                     part[p.C + c[k] + v] = db[k][v];
                 }
@@ -154,12 +152,12 @@ __global__ __launch_bounds__(THREADS) void addnorm_bwd_kernel(AddNormProblem p, 
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) acc[(k * 256 + threadIdx.x) * VEC + v] = which ? db[k][v] : dw[k][v];
             __syncthreads();
-            const int cols = m.L * VEC;
-            for (int e = threadIdx.x; e < NV * cols; e += 256) {
-                const int k = e / cols, at = e % cols, col = k * cols + at;
+            const int n = m.L * VEC;
+            for (int e = threadIdx.x; e < NV * n; e += 256) {
+                const int k = e / n, at = e % n, i = k * m.L + at / VEC;
                 float s = 0.0f;
-                for (int j = 0; j < m.slots; ++j) s += acc[k * 256 * VEC + j * cols + at];
-                if (col < p.C) part[which * p.C + col] = s;
+                for (int j = 0; j < m.slots; ++j) s += acc[k * 256 * VEC + j * n + at];
+                if (i < m.nv) part[which * p.C + column<VEC, EDGE>(i, p.C) + at % VEC] = s;
             }
         }
     }
@@ -249,59 +247,47 @@ hipError_t params(const AddNormProblem& p, int64_t parts, hipStream_t stream)
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 int64_t runs_of(const AddNormProblem& p) { return ((int64_t)p.B * p.T + kRun - 1) / kRun; }
 
-template <typename T, typename S, int VEC, bool NT>
-hipError_t bwd_n(const AddNormProblem& p, const RowMap& m, hipStream_t stream)
+template <typename T, typename S, bool EDGE, bool NT>
+hipError_t bwd_n(const AddNormProblem& p, hipStream_t stream)
 {
+    const RowMap m = map_of(p);
     const int v = (m.nv + m.L - 1) / m.L;
-    constexpr int most = most_vectors<T, S, VEC>();
-    if (m.threads > 512 && v == 1) addnorm_bwd_kernel<T, S, VEC, 1, 1024, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
-    else if (m.threads > 512) addnorm_bwd_kernel<T, S, VEC, most, 1024, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
-    else if (m.threads > 256) addnorm_bwd_kernel<T, S, VEC, most, 512, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
-    else if (v == 1) addnorm_bwd_kernel<T, S, VEC, 1, 256, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
-    else if (v == 2) addnorm_bwd_kernel<T, S, VEC, 2, 256, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
-    else if constexpr (most == 4) addnorm_bwd_kernel<T, S, VEC, 4, 256, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    constexpr int most = most_vectors<T, S>();
+    if (m.threads > 512 && v == 1) addnorm_bwd_kernel<T, S, 1, 1024, EDGE, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    else if (m.threads > 512) addnorm_bwd_kernel<T, S, most, 1024, EDGE, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    else if (m.threads > 256) addnorm_bwd_kernel<T, S, most, 512, EDGE, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    else if (v == 1) addnorm_bwd_kernel<T, S, 1, 256, EDGE, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    else if (v == 2) addnorm_bwd_kernel<T, S, 2, 256, EDGE, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    else if constexpr (most == 4) addnorm_bwd_kernel<T, S, 4, 256, EDGE, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
     return params(p, m.blocks, stream);
 }
 
-template <typename T, typename S, int VEC>
-hipError_t bwd_v(const AddNormProblem& p, hipStream_t stream)
+template <typename T, typename S>
+hipError_t bwd_long(const AddNormProblem& p, hipStream_t stream)
 {
-    if (!in_registers(p, VEC)) {
-        f32x2* stats = (f32x2*)(p.ws + align256((size_t)runs_of(p) * 2 * p.C * sizeof(float)));
-        addnorm_bwd_long_kernel<T, S><<<grid_of((int64_t)p.B * p.T), 256, 0, stream>>>(p, stats);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess || (!p.dweight && !p.dbias)) return e;
-        addnorm_columns_kernel<T, S><<<grid_of(runs_of(p) * ((p.C + 255) / 256)), 256, 0, stream>>>(p, stats);
-        return params(p, runs_of(p), stream);
-    }
-    const RowMap m = map_of(p, VEC);
-    if constexpr (VEC > 1)
-        if (streams(p)) return bwd_n<T, S, VEC, true>(p, m, stream);
-    return bwd_n<T, S, VEC, false>(p, m, stream);
+    f32x2* stats = (f32x2*)(p.ws + align256((size_t)runs_of(p) * 2 * p.C * sizeof(float)));
+    addnorm_bwd_long_kernel<T, S><<<grid_of((int64_t)p.B * p.T), 256, 0, stream>>>(p, stats);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || (!p.dweight && !p.dbias)) return e;
+    addnorm_columns_kernel<T, S><<<grid_of(runs_of(p) * ((p.C + 255) / 256)), 256, 0, stream>>>(p, stats);
+    return params(p, runs_of(p), stream);
 }
 
 template <typename T, typename S>
 hipError_t bwd_t(const AddNormProblem& p, hipStream_t stream)
 {
-    constexpr int wide = 16 / (sizeof(T) > sizeof(S) ? sizeof(T) : sizeof(S));
-    return vec_of(p, {&p.total, &p.dy, &p.dtotal, &p.dx, &p.dresidual}) == wide ? bwd_v<T, S, wide>(p, stream)
-                                                                                : bwd_v<T, S, 1>(p, stream);
+    if (!in_registers(p)) return bwd_long<T, S>(p, stream);
+    const bool edge = edged(p, {&p.total, &p.dy, &p.dtotal, &p.dx, &p.dresidual});
+    if (streams(p)) return edge ? bwd_n<T, S, true, true>(p, stream) : bwd_n<T, S, false, true>(p, stream);
+    return edge ? bwd_n<T, S, true, false>(p, stream) : bwd_n<T, S, false, false>(p, stream);
 }
 
 }  // namespace
 
-// For whichever width the call's addresses allow.
 size_t addnorm_bwd_workspace(const AddNormProblem& p)
 {
     const size_t row = 2 * (size_t)p.C * sizeof(float);
-    size_t most = 0;
-    for (const int v : {1, p.bf16 && !p.sum_fp32 ? 8 : 4}) {
-        if (p.C % v) continue;
-        const size_t n = !in_registers(p, v) ? align256((size_t)runs_of(p) * row) + (size_t)p.B * p.T * sizeof(f32x2)
-                                                : map_of(p, v).blocks * row;
-        if (n > most) most = n;
-    }
-    return most;
+    return in_registers(p) ? map_of(p).blocks * row : align256((size_t)runs_of(p) * row) + (size_t)p.B * p.T * sizeof(f32x2);
 }
 
 hipError_t launch_addnorm_bwd(const AddNormProblem& p, hipStream_t stream)

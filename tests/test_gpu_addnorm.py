@@ -267,6 +267,40 @@ def test_many_rows(act, stream):
     check(act, stream, 1, 3001, 520)
 
 
+@pytest.mark.parametrize("act,stream", TYPES)
+@pytest.mark.parametrize("C", [9, 41, 521, 2047])
+def test_many_rows_of_odd_widths(act, stream, C):
+    check(act, stream, 2, 1703, C)
+
+
+@pytest.mark.parametrize("act,stream", TYPES)
+@pytest.mark.parametrize("C", [3, 8, 13, 269, 1025])
+def test_what_lies_between_rows(act, stream, C):
+    """Columns beside the rows: NaN read from there would show, and what lies there stays."""
+    B, T, L, R = 2, 37, 3, 5
+    g = torch.Generator().manual_seed(C)
+
+    def inside(dt, fill):
+        big = torch.full((B, T, L + C + R), fill, device="cuda", dtype=dt)
+        return big, big[..., L:L + C]
+
+    def data(dt):
+        big, v = inside(dt, NAN)
+        v.copy_(torch.randn(B, T, C, generator=g))
+        return v
+
+    x, r, dy, de, w = data(act), data(stream), data(act), data(stream), torch.randn(C, generator=g).cuda()
+    (by, y), (bt, total), (bx, dx) = (inside(dt, 7.0) for dt in (act, stream, act))
+    br, dr = inside(stream, 7.0) if act != stream else (None, None)
+    tfla.addnorm_forward(x, r, w, y=y, total=total)
+    _, _, dw, _ = tfla.addnorm_backward(total, dy, w, dtotal=de, dx=dx, dresidual=dr)
+    torch.cuda.synchronize()
+    for out in (y, total, dx, dw) + ((dr,) if br is not None else ()):
+        assert torch.isfinite(out).all() and not bool((out == 7).all(-1).any())   # read within the rows, all of them written
+    for b in (by, bt, bx) + ((br,) if br is not None else ()):
+        assert bool((b[..., :L] == 7).all()) and bool((b[..., L + C:] == 7).all())
+
+
 def test_a_call_that_streams():
     """Large enough for loads past the caches; against the same rows in two smaller calls."""
     B, T, C = 2, 20000, 2048
