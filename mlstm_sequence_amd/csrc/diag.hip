@@ -28,11 +28,11 @@ constexpr int kAhead = 2;   // tiles under way (even: two LDS buffers in turn)
 // the state before the first row, since the second may update that in place (one workgroup writes it at its end, which
 // may be before another begins).  The first reading of a segmented walk goes through the caches, for the second
 // (B=1 T=30000 D=1024 bf16, coupled: 63 us and 68 past them).
-template <typename T, int KIND, int CH, bool BUF, bool OUT>
+template <typename T, int KIND, int CH, bool BUF, bool NT, bool OUT>
 __global__ __launch_bounds__(64 * kWaves, 2) void diag_fwd_kernel(DiagProblem p, Cut cut, f32x2* __restrict__ ends)
 {
     typedef Shape<CH> S;
-    typedef Walk<T, BUF, CH == 64 && OUT ? kStreamed : 0> In;
+    typedef Walk<T, BUF, NT && OUT ? kStreamed : 0> In;
     constexpr int kTile = S::tile;
     __shared__ f32x2 tot[2][kWaves][CH];
     Place q;
@@ -196,18 +196,18 @@ __global__ __launch_bounds__(256) void diag_step_kernel(DiagProblem p)
 // Calls of up to this many rows go to the step kernel.
 constexpr int kStepRows = 4;
 
-template <typename T, int KIND, int CH, bool BUF>
+template <typename T, int KIND, int CH, bool BUF, bool NT>
 hipError_t fwd_c(const DiagProblem& p, const Cut& cut, hipStream_t stream)
 {
     f32x2* ends = (f32x2*)p.ws;
     if constexpr (CH == 64) {
         if (cut.nseg > 1) {
-            diag_fwd_kernel<T, KIND, CH, BUF, false><<<grid_of(cut.blocks), 64 * kWaves, 0, stream>>>(p, cut, ends);
+            diag_fwd_kernel<T, KIND, CH, BUF, NT, false><<<grid_of(cut.blocks), 64 * kWaves, 0, stream>>>(p, cut, ends);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
         }
     }
-    diag_fwd_kernel<T, KIND, CH, BUF, true><<<grid_of(cut.blocks), 64 * kWaves, 0, stream>>>(p, cut, ends);
+    diag_fwd_kernel<T, KIND, CH, BUF, NT, true><<<grid_of(cut.blocks), 64 * kWaves, 0, stream>>>(p, cut, ends);
     return hipGetLastError();
 }
 
@@ -218,13 +218,17 @@ hipError_t fwd_k(const DiagProblem& p, hipStream_t stream)
         diag_step_kernel<T, KIND><<<grid_of((int64_t)p.B * ((p.D + 255) / 256)), 256, 0, stream>>>(p);
         return hipGetLastError();
     }
-    const bool buf = walks(p.x, p) && walks(p.fgate, p) && walks(p.igate, p) && walks(p.y, p);
-    const Cut cut = cut_of(p, buf, false);
-    if (!buf) return fwd_c<T, KIND, 64, false>(p, cut, stream);
+    bool buf = true, lines = true;
+    for (const Rows* m : {&p.x, &p.fgate, &p.igate, &p.y}) {
+        buf = buf && walks(*m, p);
+        lines = lines && on_lines(*m, p);
+    }
+    const Cut cut = cut_of(p, buf, false, lines);
+    if (!buf) return fwd_c<T, KIND, 64, false, false>(p, cut, stream);
     switch (cut.ch) {
-    case 64: return fwd_c<T, KIND, 64, true>(p, cut, stream);
-    case 32: return fwd_c<T, KIND, 32, true>(p, cut, stream);
-    default: return fwd_c<T, KIND, 16, true>(p, cut, stream);
+    case 64: return lines ? fwd_c<T, KIND, 64, true, true>(p, cut, stream) : fwd_c<T, KIND, 64, true, false>(p, cut, stream);
+    case 32: return fwd_c<T, KIND, 32, true, false>(p, cut, stream);
+    default: return fwd_c<T, KIND, 16, true, false>(p, cut, stream);
     }
 }
 

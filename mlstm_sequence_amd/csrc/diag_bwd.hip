@@ -44,13 +44,13 @@ __device__ __forceinline__ float adjoint_behind(const DiagProblem& p, const Cut&
 
 // Loads and stores of full width go past the caches (B=4 T=4096 D=4096 bf16 with a decay: 219 us, neither so 226), but
 // not the stores of bf16 gradients of coupled gates (133 us, 150 so).
-template <typename T, int KIND, int CH, bool BUF>
+template <typename T, int KIND, int CH, bool BUF, bool NT>
 __global__ __launch_bounds__(64 * kWaves, 2) void diag_bwd_kernel(DiagProblem p, Cut cut, const f32x2* __restrict__ ends,
                                                                    float* __restrict__ part)
 {
     typedef Shape<CH> S;
-    typedef Walk<T, BUF, CH == 64 ? kStreamed : 0> In;
-    typedef Walk<T, BUF, CH == 64 && (KIND != kCoupled || sizeof(T) == 4) ? kStreamed : 0> Out;
+    typedef Walk<T, BUF, NT ? kStreamed : 0> In;
+    typedef Walk<T, BUF, NT && (KIND != kCoupled || sizeof(T) == 4) ? kStreamed : 0> Out;
     constexpr int kTile = S::tile;
     __shared__ f32x2 totf[2][kWaves][CH];              // F, H
     __shared__ float tota[2][kWaves][CH];              // A
@@ -281,7 +281,7 @@ __global__ __launch_bounds__(1024) void diag_params_kernel(DiagProblem p, const 
     if (threadIdx.x < 64 && i < p.D) p.ddecay[i] = s;
 }
 
-template <typename T, int KIND, int CH, bool BUF>
+template <typename T, int KIND, int CH, bool BUF, bool NT>
 hipError_t bwd_c(const DiagProblem& p, const Cut& cut, hipStream_t stream)
 {
     f32x2* ends = (f32x2*)p.ws;
@@ -294,7 +294,7 @@ hipError_t bwd_c(const DiagProblem& p, const Cut& cut, hipStream_t stream)
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
     }
-    diag_bwd_kernel<T, KIND, CH, BUF><<<grid_of(cut.blocks), 64 * kWaves, 0, stream>>>(p, cut, ends, part);
+    diag_bwd_kernel<T, KIND, CH, BUF, NT><<<grid_of(cut.blocks), 64 * kWaves, 0, stream>>>(p, cut, ends, part);
     if ((e = hipGetLastError()) != hipSuccess || KIND != kDecay || parts == 1) return e;
     diag_params_kernel<<<(unsigned)((p.D + 63) / 64), 1024, 0, stream>>>(p, part, parts);
     return hipGetLastError();
@@ -303,14 +303,17 @@ hipError_t bwd_c(const DiagProblem& p, const Cut& cut, hipStream_t stream)
 template <typename T, int KIND>
 hipError_t bwd_k(const DiagProblem& p, hipStream_t stream)
 {
-    const bool buf = walks(p.x, p) && walks(p.fgate, p) && walks(p.igate, p) && walks(p.dy, p) && walks(p.dx, p) &&
-                     walks(p.dfgate, p) && walks(p.digate, p);
-    const Cut cut = cut_of(p, buf, true);
-    if (!buf) return bwd_c<T, KIND, 64, false>(p, cut, stream);
+    bool buf = true, lines = true;
+    for (const Rows* m : {&p.x, &p.fgate, &p.igate, &p.dy, &p.dx, &p.dfgate, &p.digate}) {
+        buf = buf && walks(*m, p);
+        lines = lines && on_lines(*m, p);
+    }
+    const Cut cut = cut_of(p, buf, true, lines);
+    if (!buf) return bwd_c<T, KIND, 64, false, false>(p, cut, stream);
     switch (cut.ch) {
-    case 64: return bwd_c<T, KIND, 64, true>(p, cut, stream);
-    case 32: return bwd_c<T, KIND, 32, true>(p, cut, stream);
-    default: return bwd_c<T, KIND, 16, true>(p, cut, stream);
+    case 64: return lines ? bwd_c<T, KIND, 64, true, true>(p, cut, stream) : bwd_c<T, KIND, 64, true, false>(p, cut, stream);
+    case 32: return bwd_c<T, KIND, 32, true, false>(p, cut, stream);
+    default: return bwd_c<T, KIND, 16, true, false>(p, cut, stream);
     }
 }
 

@@ -116,6 +116,11 @@ template <int KIND> __device__ __forceinline__ GateGrads grads_of(const Gate& k,
 // they are put on one XCD, whose L2 reads a line once for them.  (Two channels and
 // eight rows to a lane: 3 to 7 % slower backward, whose registers they take, equal
 // forward; 16 waves to a tile instead of eight 7 %.)
+//
+// Rows that begin off the lines (D=4097) make all neighbours share them: eight of
+// 64 channels then go to an XCD, through the caches (B=4 T=4096 D=4097 bf16 with a
+// decay: forward 204 us, backward 356, as rows on lines 253 and 643; fp32 coupled
+// 241 and 398, 258 and 535).
 
 constexpr int kWaves = 8;
 constexpr int kRows = 16;                                 // of a lane
@@ -220,6 +225,13 @@ inline bool walks(const Rows& m, const DiagProblem& p)
     return !m.p || (m.row >= p.D && row <= ((int64_t(1) << 31) - 1) / Shape<16>::tile);
 }
 
+// Whether a tensor's rows begin on lines of 128 bytes.
+inline bool on_lines(const Rows& m, const DiagProblem& p)
+{
+    const int64_t e = p.bf16 ? 2 : 4;
+    return !m.p || ((uintptr_t)m.p % 128 == 0 && (p.T == 1 || m.row * e % 128 == 0) && (p.B == 1 || m.batch * e % 128 == 0));
+}
+
 // The value of the lower and of the upper of the two lanes D apart (the one with bit D clear, and set), in both.
 template <int D> __device__ __forceinline__ void pair_of(float v, float* low, float* high)
 {
@@ -291,6 +303,8 @@ template <int D> __device__ __forceinline__ float sum_groups(float v)
     return v;
 }
 
+constexpr int kNear = 8;   // 16: within 4 %, but long few channels (B=12 T=15822 D=158 fp32 backward 364, 378 us)
+
 // How the work is cut: ncb blocks of ch channels, nseg segments of len rows (whole tiles), each walked by a workgroup
 // of its own; `near` blocks share lines.
 struct Cut {
@@ -334,7 +348,7 @@ inline int64_t blocks_of(const DiagProblem& p, int ch) { return (int64_t)p.B * (
 // 14.9 and 11.3) or, forward in fp32, where they are 4096 or more (T=8192 D=4096: 101 and 109 us); else segments of 64
 // (T=30000 D=1024 bf16: 64 and 88 us; 16 channels in four segments 119 and 166).  A segmented walk reads the inputs
 // twice, narrow blocks read lines that they share.
-inline Cut cut_of(const DiagProblem& p, bool buf, bool bwd)
+inline Cut cut_of(const DiagProblem& p, bool buf, bool bwd, bool lines = true)
 {
     Cut c;
     c.ch = 64;
@@ -345,7 +359,7 @@ inline Cut cut_of(const DiagProblem& p, bool buf, bool bwd)
         whole = c.ch != 64;
     }
     c.ncb = (p.D + c.ch - 1) / c.ch;
-    c.near = 64 / c.ch;
+    c.near = lines ? 64 / c.ch : kNear;
     const int tile = kWaves * kRows * 64 / c.ch;
     const int tiles = (p.T + tile - 1) / tile;
     const int64_t blocks = (int64_t)p.B * c.ncb;

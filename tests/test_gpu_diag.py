@@ -414,6 +414,13 @@ def test_cuts(dtype, kind, B, T, D):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("B,T,D", [(33, 130, 512), (33, 130, 528), (33, 130, 513), (2, 2500, 192), (2, 2500, 163)])
+def test_rows_on_lines_and_off_them(dtype, kind, B, T, D):
+    check(dtype, kind, B, T, D)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_state_in_place_of_a_long_call(dtype):
     """Cut into segments, every one of which starts from the state that the last one replaces."""
     dev, _ = make(dtype, "decay", 2, 3000, 200)
