@@ -342,28 +342,30 @@ inline int64_t blocks_of(const DiagProblem& p, int ch) { return (int64_t)p.B * (
 
 // The cut of a call whose tensors are walked by buffer instructions (buf), else by segments of 64 channels always.
 //
-// 256 workgroups fill the chip.  64 channels to one where that gives as many, else 32 (B=8 T=1024 D=1024 bf16,
-// coupled, forward and backward: 14 and 19 us, in two segments of 64 channels 18 and 31); with fewer channels 16 where
-// the axis is short (T=512 D=2048: 5.3 and 6.8 us, segments 9.1 and 10.1; T=1500 D=768 forward 8.8 and 10.3, backward
-// 14.9 and 11.3) or, forward in fp32, where they are 4096 or more (T=8192 D=4096: 101 and 109 us); else segments of 64
-// (T=30000 D=1024 bf16: 64 and 88 us; 16 channels in four segments 119 and 166).  A segmented walk reads the inputs
-// twice, narrow blocks read lines that they share.
+// A CU holds one workgroup (two of the forward pass's coupled gates), so time goes with the rounds of 256 workgroups: 64
+// channels to one where that gives more than 128 (B=5 T=3000 D=2048 bf16, coupled, forward and backward: 53 and 89 us,
+// of 32 channels 75 and 126), 32 where it gives more than 64 (B=4 T=1000 D=2048: 14.6 and 20.6 us, two segments of 64
+// channels 22.4 and 27.7) unless the backward pass is long and in bf16 (T=8000, a decay: 271 us, segments 240).  With
+// fewer 16 where the axis is short (T=1000 D=2048: 8.1 and 14.1 us, segments 11.1 and 13.7; T=3000 20.6 and 30.1, 19.7
+// and 22.4) or, forward in fp32, where they give 256 (B=2 T=8000 D=2048: 105 us, segments 120); else segments of 64, as
+// many as one round takes (B=3 T=10825 D=722: 59 and 88 us, one more to each sequence, which opens a second round, 83 and
+// 119).  A segmented walk reads the inputs twice, narrow blocks read lines that they share.
 inline Cut cut_of(const DiagProblem& p, bool buf, bool bwd, bool lines = true)
 {
     Cut c;
     c.ch = 64;
-    bool whole = blocks_of(p, 64) >= 256;
-    if (buf && !whole) {
-        if (blocks_of(p, 32) >= 256) c.ch = 32;
+    const int64_t full = blocks_of(p, 64);
+    if (buf && full <= 128) {
+        if (full > 64) c.ch = bwd && p.bf16 && p.T > 2048 ? 64 : 32;
         else if (p.T <= (bwd ? 768 : 2048) || (!bwd && !p.bf16 && blocks_of(p, 16) >= 256)) c.ch = 16;
-        whole = c.ch != 64;
     }
+    const bool narrow = c.ch != 64;
     c.ncb = (p.D + c.ch - 1) / c.ch;
     c.near = lines ? 64 / c.ch : kNear;
     const int tile = kWaves * kRows * 64 / c.ch;
     const int tiles = (p.T + tile - 1) / tile;
     const int64_t blocks = (int64_t)p.B * c.ncb;
-    int64_t n = whole ? 1 : (256 + blocks - 1) / blocks;
+    int64_t n = narrow || blocks > 128 ? 1 : 256 / blocks;
     if (n > 64) n = 64;                                // a segment's start folds the maps of those before it
     if (n > tiles) n = tiles;
     const int per = (int)((tiles + n - 1) / n);

@@ -415,7 +415,8 @@ def test_cuts(dtype, kind, B, T, D):
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("B,T,D", [(33, 130, 512), (33, 130, 528), (33, 130, 513), (2, 2500, 192), (2, 2500, 163)])
+@pytest.mark.parametrize("B,T,D", [(33, 130, 512), (33, 130, 528), (33, 130, 513), (2, 2500, 192), (2, 2500, 163),
+                                   (5, 300, 1024), (5, 300, 1000), (70, 2100, 2), (40, 2300, 3)])
 def test_rows_on_lines_and_off_them(dtype, kind, B, T, D):
     check(dtype, kind, B, T, D)
 
