@@ -21,7 +21,7 @@ __global__ __launch_bounds__(1024) void addnorm_fwd_kernel(AddNormProblem p, Row
 {
     constexpr int VEC = vec_of<T, S>();
     __shared__ float red[2][16][1];
-    const int slot = threadIdx.x / m.L, lv = threadIdx.x & (m.L - 1);
+    const int slot = threadIdx.x / m.L, lv = threadIdx.x - slot * m.L;
     const bool sum = p.residual.p != nullptr, shift = !p.rms;
     const Columns<VEC, NV, EDGE> cols(lv, m.L, m.nv, p.C);
     const int* c = cols.c;
@@ -128,7 +128,7 @@ __global__ __launch_bounds__(256) void addnorm_fwd_long_kernel(AddNormProblem p)
 template <typename T, typename S, bool EDGE>
 hipError_t fwd_e(const AddNormProblem& p, hipStream_t stream)
 {
-    const RowMap m = row_map(p, most_vectors(p), kBlocks);
+    const RowMap m = row_map(p, most_vectors(p), kBlocks, false);
     const int v = (m.nv + m.L - 1) / m.L;
     if (v == 1) addnorm_fwd_kernel<T, S, 1, EDGE><<<m.blocks, m.threads, 0, stream>>>(p, m);
     else if (v == 2) addnorm_fwd_kernel<T, S, 2, EDGE><<<m.blocks, m.threads, 0, stream>>>(p, m);

@@ -10,6 +10,8 @@
 // memory: the stream, its gradient and dy are read once, dt written once.
 #include "gfx950.hpp"
 
+#include <algorithm>
+
 #include "addnorm_impl.hpp"
 #include "sums.hpp"
 
@@ -18,15 +20,20 @@ namespace {
 
 using namespace addnorm;
 
-// How the rows fall to workgroups, and the parts of the weights' gradients: enough to fill the chip, of 16 rows or
-// more beyond that.  Rows of 512 to 1024 vectors take one vector a lane, as two leave room for one workgroup of 8 waves
-// on a CU.
+// How the rows fall to workgroups, and the parts of the weights' gradients, which each writes once.  At most as many
+// workgroups as the chip holds, by the registers of their variant: beyond 256 lanes to a row one on a CU ([4, 4096, 5120]
+// bf16 189 us, two 198, three 208), with sums kept in fp32 and a vector a lane two up to 768 ([4, 4096, 2560]: 126 us, one
+// 178); below three of bf16 or of a vector a lane ([4, 4096, 2560]: 90 us, two 104, four 112) and two else ([4, 4096,
+// 2048] with a stream of fp32 96 us, three 113).  One on each CU, and more only where each has eight rows ([2, 1024, 8192]
+// bf16 49 us, twice as many 65).  Rows of 512 to 1024 vectors take one vector a lane, as two leave room for one workgroup
+// of 8 waves on a CU ([4, 4096, 8192] bf16 256 and 289 us).
 RowMap map_of(const AddNormProblem& p)
 {
     const int nv = vectors(p), most = nv > 512 && nv <= 1024 ? 1 : most_vectors(p);
-    RowMap m = row_map(p, most, 768);
-    const unsigned few = (m.rows + 16 * m.slots - 1) / (16 * m.slots);
-    if (m.blocks > few) m.blocks = few > 512 ? few : m.blocks < 512 ? m.blocks : 512;
+    RowMap m = row_map(p, most, ~0u, true);
+    const unsigned wide = p.sum_fp32 && most == 1 && m.L <= 768 ? 512 : 256;
+    const unsigned cap = m.threads > 256 ? wide : (p.bf16 && !p.sum_fp32) || nv <= m.L ? 768 : 512;
+    m.blocks = std::min(m.blocks, std::min(cap, std::max(m.rows / 8, 256u)));
     return m;
 }
 
@@ -45,7 +52,7 @@ __global__ __launch_bounds__(THREADS) void addnorm_bwd_kernel(AddNormProblem p, 
     constexpr int VEC = vec_of<T, S>();
     __shared__ float red1[2][16][1], red3[2][16][3];
     __shared__ float acc[THREADS > 256 ? 1 : 256 * NV * VEC];
-    const int slot = threadIdx.x / m.L, lv = threadIdx.x & (m.L - 1);
+    const int slot = threadIdx.x / m.L, lv = threadIdx.x - slot * m.L;
     const bool shift = !p.rms, behind = p.dtotal.p != nullptr;
     const Columns<VEC, NV, EDGE> cols(lv, m.L, m.nv, p.C);
     const int* c = cols.c;

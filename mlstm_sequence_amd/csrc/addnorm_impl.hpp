@@ -73,14 +73,15 @@ inline int vectors(const AddNormProblem& p) { return (p.C + vec_of(p) - 1) / vec
 inline bool in_registers(const AddNormProblem& p) { return p.C >= vec_of(p) && vectors(p) <= 1024 * most_vectors(p); }
 
 // most: vectors of a lane where a row takes more than a wave.
-inline RowMap row_map(const AddNormProblem& p, int most, unsigned most_blocks)
+inline RowMap row_map(const AddNormProblem& p, int most, unsigned most_blocks, bool tight)
 {
     RowMap m;
     m.nv = vectors(p);
     m.L = 1;
     while (m.L < 64 && m.L < m.nv) m.L *= 2;
     while (m.L < 1024 && most * m.L < m.nv) m.L *= 2;
-    m.threads = m.L > 256 ? m.L : 256;
+    if (tight && m.L > 128) m.L = (m.nv + 64 * most - 1) / (64 * most) * 64;
+    m.threads = m.L > 128 ? m.L : 256;
     m.slots = m.threads / m.L;
     m.rows = (unsigned)p.B * (unsigned)p.T;
     const unsigned need = (m.rows + m.slots - 1) / m.slots;
