@@ -168,9 +168,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void diag_fwd_kernel(DiagProblem p,
     if (p.state_out && q.seg == cut.nseg - 1) p.state_out[q.b * p.D + l.c] = h0;
 }
 
-// Single tokens and very short calls: a thread to a channel.  B=64 T=1 D=4096: 3.3 us, the least that a launch takes.
-template <typename T, int KIND>
-__global__ __launch_bounds__(256) void diag_step_kernel(DiagProblem p)
+// Single tokens and short axes: a thread to a channel, N rows' loads under way together.  No row is computed twice and
+// no tile is part empty, but it takes many channels to fill the chip.  B=64 T=1 D=4096: 3.3 us, the least that a launch
+// takes; N rows of four and eight are equal to 10 %, one row at a time is not (B=8 T=32 D=4096 bf16, coupled: 8.8 us,
+// eight 6.7).
+template <typename T, int KIND, int N>
+__global__ __launch_bounds__(256) void diag_short_kernel(DiagProblem p)
 {
     const int nb = (p.D + 255) / 256, c = (int)(block_id() % nb) * 256 + threadIdx.x;
     const int64_t b = block_id() / nb;
@@ -182,19 +185,39 @@ __global__ __launch_bounds__(256) void diag_step_kernel(DiagProblem p)
     T* y = (T*)p.y.p + b * p.y.batch + c;
     const Rate decay(KIND == kDecay ? p.decay[c] : 0.0f);
     float h = p.state ? p.state[b * p.D + c] : 0.0f;
-    if (p.starts) p.starts[b * p.D + c] = h;
-    for (int64_t t = 0; t < p.T; ++t) {
-        if (t < len) {
-            const Gate g = gate_of<T, KIND>(to_float(u[t * p.fgate.row]), v ? to_float(v[t * p.igate.row]) : 0.0f, decay);
-            h = g.f * h + g.i * to_float(x[t * p.x.row]);
+    if (p.starts) p.starts[b * p.D + c] = h;           // one chunk
+    for (int t0 = 0; t0 < p.T; t0 += N) {
+        T rx[N], ru[N], rv[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {                  // behind the last row: the last
+            const int64_t t = min(t0 + i, p.T - 1);
+            ru[i] = u[t * p.fgate.row];
+            if (KIND != kCoupled) rv[i] = v[t * p.igate.row];
+            rx[i] = x[t * p.x.row];
         }
-        y[t * p.y.row] = from_float<T>(t < len ? h : 0.0f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int t = t0 + i;
+            if (t >= p.T) break;
+            if (t < len) {
+                const Gate g = gate_of<T, KIND>(to_float(ru[i]), KIND != kCoupled ? to_float(rv[i]) : 0.0f, decay);
+                h = g.f * h + g.i * to_float(rx[i]);
+            }
+            y[(int64_t)t * p.y.row] = from_float<T>(t < len ? h : 0.0f);
+        }
     }
     if (p.state_out) p.state_out[b * p.D + c] = h;
 }
 
-// Calls of up to this many rows go to the step kernel.
-constexpr int kStepRows = 4;
+// Whether a call goes to the kernel above: up to 16 rows (B=1 T=16 D=1024 bf16, coupled: 4.4 us, tiles 5.5; T=32 6.4 and
+// 5.5), and up to a tile's 128, in fp32 with coupled gates 64, where b blocks of 64 channels are 16 for each row (B=16
+// T=64 D=4096 bf16, coupled and with a decay: 14.3 and 17.7 us, tiles 14.5 and 26.3; B=128 T=128 82 and 118, tiles 105
+// and 198; B=8 T=64 11 and 17, tiles 8 and 14; fp32 coupled B=128 T=128 172, tiles 143).
+bool is_short(const DiagProblem& p)
+{
+    const int64_t filled = std::min<int64_t>(blocks_of(p, 64) / 16, p.bf16 || p.kind != kCoupled ? kChunk : kChunk / 2);
+    return p.T <= std::max<int64_t>(16, filled);
+}
 
 template <typename T, int KIND, int CH, bool BUF, bool NT>
 hipError_t fwd_c(const DiagProblem& p, const Cut& cut, hipStream_t stream)
@@ -214,8 +237,10 @@ hipError_t fwd_c(const DiagProblem& p, const Cut& cut, hipStream_t stream)
 template <typename T, int KIND>
 hipError_t fwd_k(const DiagProblem& p, hipStream_t stream)
 {
-    if (p.T <= kStepRows) {
-        diag_step_kernel<T, KIND><<<grid_of((int64_t)p.B * ((p.D + 255) / 256)), 256, 0, stream>>>(p);
+    if (is_short(p)) {
+        const dim3 grid = grid_of((int64_t)p.B * ((p.D + 255) / 256));
+        if (p.T == 1) diag_short_kernel<T, KIND, 1><<<grid, 256, 0, stream>>>(p);
+        else diag_short_kernel<T, KIND, 8><<<grid, 256, 0, stream>>>(p);
         return hipGetLastError();
     }
     bool buf = true, lines = true;
@@ -247,7 +272,7 @@ hipError_t fwd_t(const DiagProblem& p, hipStream_t stream)
 // For whichever way the call's strides allow.
 size_t diag_workspace(const DiagProblem& p)
 {
-    return p.T <= kStepRows ? 0 : std::max(ends_bytes(p, cut_of(p, true, false)), ends_bytes(p, cut_of(p, false, false)));
+    return is_short(p) ? 0 : std::max(ends_bytes(p, cut_of(p, true, false)), ends_bytes(p, cut_of(p, false, false)));
 }
 
 hipError_t launch_diag_fwd(const DiagProblem& p, hipStream_t stream)

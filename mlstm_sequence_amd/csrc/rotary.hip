@@ -6,6 +6,14 @@
 // an angle in fp32 is off by 0.03.  The remainder, at most an eighth of a
 // turn, is small enough for the first terms of the series of sine and cosine
 // in fp32.
+//
+// A token's angles serve all its heads: a workgroup forms those of its tokens
+// once into LDS, and its threads then turn units of two vectors, a pair's two
+// halves, of one head and token after another.  Bound by memory, each element
+// read and written once: B=8 T=4096, 32 + 32 heads of 128 in bf16 into
+// head-major outputs, 1.07 GB in 202 us (5.3 TB/s; a copy moves 5.0), backward
+// B=1 T=65536 671 MB in 121 us (5.5).  Accesses past the caches gained nothing
+// (210 to 216 us, when that case took 210; backward 139 to 189 for 128).
 #include "gfx950.hpp"
 
 #include "blocks.hpp"
@@ -73,7 +81,7 @@ struct Geom {
 };
 
 constexpr int kEntries = 4096;   // angles of a workgroup's tokens, 32 KB
-constexpr int kAhead = 4;        // units whose loads a thread has under way together
+constexpr int kAhead = 2;        // units whose loads a thread has under way together (four: B=4 T=512 16 + 4 heads 8.4 us for 7.2)
 
 template <typename T, int P, bool INTER>
 __global__ __launch_bounds__(256) void rotary_kernel(RotaryProblem p, Geom gm)
@@ -163,10 +171,11 @@ hipError_t launch_p(const RotaryProblem& p, hipStream_t stream)
     g.heads = divisor((unsigned)p.H);
     g.kheads = divisor((unsigned)(p.Hk > 0 ? p.Hk : 1));
     g.turned = turned;
-    // a workgroup's tokens: eight units to a thread, but a thousand workgroups before that
+    // a workgroup's tokens: as many as two units to a thread take (eight: B=8 T=4096 32 + 32 heads of 128 bf16 210 us for
+    // 202, backward B=1 T=65536 128 for 121), but 256 workgroups before that (B=1 T=4096 1 + 1 heads of 64: 4.4 us, without 6.4)
     const int64_t per = (int64_t)(turned + passing) * (p.H + p.Hk);
-    int64_t tok = 2048 / per;
-    if (tok > (int64_t)p.B * p.T / 1024) tok = (int64_t)p.B * p.T / 1024;
+    int64_t tok = 512 / per;
+    if (tok > (int64_t)p.B * p.T / 256) tok = (int64_t)p.B * p.T / 256;
     if (p.R && tok > kEntries / (p.R / 2)) tok = kEntries / (p.R / 2);
     if (tok > p.T) tok = p.T;
     if (tok < 1) tok = 1;
@@ -187,7 +196,7 @@ bool fits(const Heads& h, const RotaryProblem& p, int n, size_t bytes)
 }
 
 // Elements of a vector: the most, up to 16 bytes, that divide the pairs and the channels and that addresses and
-// strides allow.
+// strides allow (B=1 T=65536 16 + 2 heads of 128 bf16: 109 us, 8 bytes 152; 32 + 32 heads of B=8 T=4096 199 and 192).
 int vector_of(const RotaryProblem& p)
 {
     const int e = p.bf16 ? 2 : 4;
