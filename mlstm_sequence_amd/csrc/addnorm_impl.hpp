@@ -62,17 +62,20 @@ struct RowMap {
     unsigned rows, blocks;
 };
 
-// Vectors a lane holds at most: 16 values of either type.
+// Vectors a lane holds at most: 16 values of either type, 8 of fp32 alone.
 template <typename T, typename S> constexpr int most_vectors() { return sizeof(T) < sizeof(S) ? 4 : 2; }
 inline int most_vectors(const AddNormProblem& p) { return p.sum_fp32 ? 4 : 2; }
 // Elements of a vector: 16 bytes of the wider type.
 template <typename T, typename S> constexpr int vec_of() { return 16 / (sizeof(T) > sizeof(S) ? sizeof(T) : sizeof(S)); }
 inline int vec_of(const AddNormProblem& p) { return p.bf16 && !p.sum_fp32 ? 8 : 4; }
-// Vectors of a row, and whether it has one and fits in the registers of 16 waves.
+// Vectors of a row, and whether it has one and fits in the registers of 16 waves; longer rows are read two and three
+// times (bf16 [2, 4096, 16384], which still fits, backward at 2.2 TB/s, as the registers of 16 waves spill).
 inline int vectors(const AddNormProblem& p) { return (p.C + vec_of(p) - 1) / vec_of(p); }
 inline bool in_registers(const AddNormProblem& p) { return p.C >= vec_of(p) && vectors(p) <= 1024 * most_vectors(p); }
 
-// most: vectors of a lane where a row takes more than a wave.
+// most: vectors of a lane where a row takes more than a wave.  tight: beyond two waves a row takes as many as it needs,
+// not a power of two (backward [4, 4096, 2560] with a stream of fp32 138 us, 198 by powers; forward equal to 4 % either
+// way, so it keeps the powers).
 inline RowMap row_map(const AddNormProblem& p, int most, unsigned most_blocks, bool tight)
 {
     RowMap m;
