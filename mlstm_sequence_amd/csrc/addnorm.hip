@@ -14,8 +14,12 @@ namespace {
 using namespace addnorm;
 
 // Workgroups at most, their rows in turn (bf16 [4, 4096, 4096] 107 us, a workgroup to each row 179; [2, 1024, 4096] 18.5 us,
-// 2048 of them 23.4; [8, 4096, 256] with a stream of fp32 18.1 us, 512 of them 20.3).
-constexpr unsigned kBlocks = 1024;
+// 2048 of them 23.4; [8, 4096, 256] with a stream of fp32 18.1 us, 512 of them 20.3), twice as many where a stream of fp32
+// gives each eight rows that take all of it ([4, 4096, 4096]: 153 us, 1024 of them 157).
+unsigned most_blocks(const AddNormProblem& p)
+{
+    return p.sum_fp32 && p.C >= 1024 && (int64_t)p.B * p.T >= 8 * 2048 ? 2048 : 1024;
+}
 
 // T: activations, S: the stream.  NV vectors a lane.
 template <typename T, typename S, int NV, bool EDGE>
@@ -130,7 +134,7 @@ __global__ __launch_bounds__(256) void addnorm_fwd_long_kernel(AddNormProblem p)
 template <typename T, typename S, bool EDGE>
 hipError_t fwd_e(const AddNormProblem& p, hipStream_t stream)
 {
-    const RowMap m = row_map(p, most_vectors(p), kBlocks, false);
+    const RowMap m = row_map(p, most_vectors(p), most_blocks(p), false);
     const int v = (m.nv + m.L - 1) / m.L;
     if (v == 1) addnorm_fwd_kernel<T, S, 1, EDGE><<<m.blocks, m.threads, 0, stream>>>(p, m);
     else if (v == 2) addnorm_fwd_kernel<T, S, 2, EDGE><<<m.blocks, m.threads, 0, stream>>>(p, m);
