@@ -8,7 +8,7 @@
 // row before it in the same register is taken.  Each input is read once and y
 // written once: bound by memory.  B=4 T=4096 D=4096 bf16, coupled gates 403 MB
 // in 80 us, two gates or a decay 537 MB in 109 and 111 (5.0 to 4.8 TB/s, where
-// a copy moves 5.1; 4.2 with loads through the caches); fp32 139, 194, 196.
+// a copy moves 5.0; 4.2 with loads through the caches); fp32 139, 194, 196.
 //
 // A long axis over few channels is cut into segments: their maps first (one
 // more reading of the inputs), then each from the state that the maps before

@@ -9,8 +9,8 @@
 // them, the gates kept in registers between the two; the next tile's loads are
 // under way meanwhile.  Inputs and dy are read once, the gradients written
 // once: bound by memory.  B=4 T=4096 D=4096 bf16, coupled gates 671 MB in 128 us,
-// two gates or a decay 940 MB in 198 and 206 (5.2 to 4.6 TB/s, where a copy
-// moves 5.1); fp32 250, 356, 362.
+// two gates or a decay 940 MB in 203 and 208 (5.2 to 4.5 TB/s, where a copy
+// moves 5.0); fp32 270, 353, 361.
 //
 // A long axis over few channels is cut into segments, whose adjoint maps are
 // formed first from fgate and dy alone: B=1 T=8192 D=4096 bf16 96, 114, 126 us.
@@ -42,8 +42,8 @@ __device__ __forceinline__ float adjoint_behind(const DiagProblem& p, const Cut&
     return a;
 }
 
-// Loads and stores of full width go past the caches (B=4 T=4096 D=4096 bf16 with a decay: 219 us, neither so 226), but
-// not the stores of bf16 gradients of coupled gates (133 us, 150 so).
+// NT: rows on lines, whose loads and stores go past the caches (B=4 T=4096 D=4096 bf16 with a decay, before the blocks
+// of today: 219 us, neither so 226), but not the stores of bf16 gradients of coupled gates (133 us, 150 so).
 template <typename T, int KIND, int CH, bool BUF, bool NT>
 __global__ __launch_bounds__(64 * kWaves, 2) void diag_bwd_kernel(DiagProblem p, Cut cut, const f32x2* __restrict__ ends,
                                                                    float* __restrict__ part)
