@@ -21,19 +21,23 @@ namespace {
 
 using namespace addnorm;
 
-// How the rows fall to workgroups, and the parts of the weights' gradients, which each writes once.  At most as many
-// workgroups as the chip holds, by the registers of their variant: beyond 256 lanes to a row one on a CU ([4, 4096, 5120]
-// bf16 189 us, two 198, three 208), with sums kept in fp32 and a vector a lane two up to 768 ([4, 4096, 2560]: 126 us, one
-// 178); below three of bf16 or of a vector a lane ([4, 4096, 2560]: 90 us, two 104, four 112) and two else ([4, 4096,
-// 2048] with a stream of fp32 96 us, three 113).  One on each CU, and more only where each has eight rows ([2, 1024, 8192]
-// bf16 49 us, twice as many 65).  Rows of 512 to 1024 vectors take one vector a lane, as two leave room for one workgroup
-// of 8 waves on a CU ([4, 4096, 8192] bf16 256 and 289 us).
+// How the rows fall to workgroups, and the parts of the weights' gradients, which each writes once.
+//
+// bf16 rows of 512 to 1024 vectors take one vector a lane ([4, 4096, 5120] 188 us, two 218; [4, 4096, 8192] 226 and 253),
+// not fp32 ones ([4, 4096, 2560]: 176 and 124) nor those of both types ([4, 4096, 4096]: 215, four 208).
+//
+// At most as many workgroups as the chip holds, by the registers of their variant: beyond 256 lanes to a row one on a CU
+// (bf16 [4, 4096, 5120]: 188 us, two 198, three 208), with fp32 alone two up to 384 ([4, 4096, 2560]: 124 us, one 133;
+// [4, 4096, 4096] 193 and 177); below three of bf16 or of a vector a lane ([4, 4096, 2560]: 90 us, two 104, four 112) and
+// two else ([4, 4096, 2048] with a stream of fp32 96 us, three 113).  One on each CU, and more only where each has eight
+// rows (bf16 [2, 1024, 8192] 49 us, twice as many 65).
 RowMap map_of(const AddNormProblem& p)
 {
-    const int nv = vectors(p), most = nv > 512 && nv <= 1024 ? 1 : most_vectors(p);
-    RowMap m = row_map(p, most, ~0u, true);
-    const unsigned wide = p.sum_fp32 && most == 1 && m.L <= 768 ? 512 : 256;
-    const unsigned cap = m.threads > 256 ? wide : (p.bf16 && !p.sum_fp32) || nv <= m.L ? 768 : 512;
+    const int nv = vectors(p);
+    const bool half = p.bf16 && !p.sum_fp32;
+    RowMap m = row_map(p, half && nv > 512 && nv <= 1024 ? 1 : most_vectors(p), ~0u, true);
+    const unsigned wide = !p.bf16 && m.L <= 384 ? 512 : 256;
+    const unsigned cap = m.threads > 256 ? wide : half || nv <= m.L ? 768 : 512;
     m.blocks = std::min(m.blocks, std::min(cap, std::max(m.rows / 8, 256u)));
     return m;
 }
@@ -262,8 +266,12 @@ hipError_t bwd_n(const AddNormProblem& p, hipStream_t stream)
     const RowMap m = map_of(p);
     const int v = (m.nv + m.L - 1) / m.L;
     constexpr int most = most_vectors<T, S>();
-    if (m.threads > 512 && v == 1) addnorm_bwd_kernel<T, S, 1, 1024, EDGE, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
-    else if (m.threads > 512) addnorm_bwd_kernel<T, S, most, 1024, EDGE, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
+    if constexpr (sizeof(T) == 2 && sizeof(S) == 2)
+        if (m.threads > 256 && v == 1) {
+            addnorm_bwd_kernel<T, S, 1, 1024, EDGE, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
+            return params(p, m.blocks, stream);
+        }
+    if (m.threads > 512) addnorm_bwd_kernel<T, S, most, 1024, EDGE, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
     else if (m.threads > 256) addnorm_bwd_kernel<T, S, most, 512, EDGE, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
     else if (v == 1) addnorm_bwd_kernel<T, S, 1, 256, EDGE, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
     else if (v == 2) addnorm_bwd_kernel<T, S, 2, 256, EDGE, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
