@@ -415,6 +415,14 @@ def test_cuts(dtype, kind, B, T, D):
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("B,T,D", [(40, 20, 512), (40, 21, 512), (1030, 64, 3), (2050, 128, 1), (2050, 129, 1), (3, 16, 70), (3, 17, 70)])
+def test_short_axes_of_many_channels(dtype, kind, B, T, D):
+    """On both sides of where a thread takes a channel; padded, with sequences of no row and of one."""
+    check(dtype, kind, B, T, D, lengths=[(0, 1, T, T // 2, T - 1)[i % 5] for i in range(B)])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("B,T,D", [(33, 130, 512), (33, 130, 528), (33, 130, 513), (2, 2500, 192), (2, 2500, 163),
                                    (5, 300, 1024), (5, 300, 1000), (70, 2100, 2), (40, 2300, 3)])
 def test_rows_on_lines_and_off_them(dtype, kind, B, T, D):
