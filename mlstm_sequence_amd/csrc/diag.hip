@@ -185,8 +185,10 @@ __global__ __launch_bounds__(256) void diag_short_kernel(DiagProblem p)
     T* y = (T*)p.y.p + b * p.y.batch + c;
     const Rate decay(KIND == kDecay ? p.decay[c] : 0.0f);
     float h = p.state ? p.state[b * p.D + c] : 0.0f;
-    if (p.starts) p.starts[b * p.D + c] = h;           // one chunk
+    float* starts = p.starts ? p.starts + b * ((p.T + kChunk - 1) / kChunk) * p.D + c : nullptr;
+    static_assert(kChunk % N == 0, "chunks start where batches do");
     for (int t0 = 0; t0 < p.T; t0 += N) {
+        if (starts && t0 % kChunk == 0) starts[(int64_t)(t0 / kChunk) * p.D] = h;
         T rx[N], ru[N], rv[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {                  // behind the last row: the last
@@ -210,13 +212,15 @@ __global__ __launch_bounds__(256) void diag_short_kernel(DiagProblem p)
 }
 
 // Whether a call goes to the kernel above: up to 16 rows (B=1 T=16 D=1024 bf16, coupled: 4.4 us, tiles 5.5; T=32 6.4 and
-// 5.5), and up to a tile's 128, in fp32 with coupled gates 64, where b blocks of 64 channels are 16 for each row (B=16
-// T=64 D=4096 bf16, coupled and with a decay: 14.3 and 17.7 us, tiles 14.5 and 26.3; B=128 T=128 82 and 118, tiles 105
-// and 198; B=8 T=64 11 and 17, tiles 8 and 14; fp32 coupled B=128 T=128 172, tiles 143).
+// 5.5), and where b blocks of 64 channels are 16 for each row (B=16 T=64 D=4096 bf16, coupled and with a decay: 14.3 and
+// 17.7 us, tiles 14.5 and 26.3; B=8 T=64 11 and 17, tiles 8 and 14) as long as tiles, whose arithmetic counts, do not
+// catch up: bf16 with coupled gates 256 rows (B=128 D=4096 T=256: 158 us, tiles 173; T=512 322 and 330), else 512 (T=512
+// with a decay 433 and 515; T=1024 873 and 923, but B=64 438 and 466, B=32 317 and 237), fp32 64 (T=64 88 and 103; T=128
+// 172 and 143) and 256 (T=192 with a decay 328 and 414; T=512 901 and 856).
 bool is_short(const DiagProblem& p)
 {
-    const int64_t filled = std::min<int64_t>(blocks_of(p, 64) / 16, p.bf16 || p.kind != kCoupled ? kChunk : kChunk / 2);
-    return p.T <= std::max<int64_t>(16, filled);
+    const int64_t most = p.bf16 ? (p.kind == kCoupled ? 256 : 512) : (p.kind == kCoupled ? 64 : 256);
+    return p.T <= std::max<int64_t>(16, std::min(most, blocks_of(p, 64) / 16));
 }
 
 template <typename T, int KIND, int CH, bool BUF, bool NT>

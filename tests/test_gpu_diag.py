@@ -415,9 +415,16 @@ def test_cuts(dtype, kind, B, T, D):
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("B,T,D", [(40, 20, 512), (40, 21, 512), (1030, 64, 3), (2050, 128, 1), (2050, 129, 1), (3, 16, 70), (3, 17, 70)])
-def test_short_axes_of_many_channels(dtype, kind, B, T, D):
+@pytest.mark.parametrize("B,T,D", [(40, 20, 512), (40, 21, 512), (3, 16, 70), (3, 17, 70)])
+def test_short_axes(dtype, kind, B, T, D):
     """On both sides of where a thread takes a channel; padded, with sequences of no row and of one."""
+    check(dtype, kind, B, T, D, lengths=[(0, 1, T, T // 2, T - 1)[i % 5] for i in range(B)])
+
+
+@pytest.mark.parametrize("dtype,kind,B,T,D", [(F32, "coupled", 1030, 64, 3), (F32, "coupled", 1044, 65, 3), (BF, "coupled", 2050, 128, 1),
+                                              (BF, "decay", 4100, 256, 1), (F32, "sigmoid", 2050, 129, 1)])
+def test_short_axes_of_many_channels(dtype, kind, B, T, D):
+    """Longer ones, over one chunk and more."""
     check(dtype, kind, B, T, D, lengths=[(0, 1, T, T // 2, T - 1)[i % 5] for i in range(B)])
 
 
