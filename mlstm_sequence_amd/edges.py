@@ -424,7 +424,7 @@ def addnorm_backward(total, dy, weight=None, bias: bool = False, eps: float = 1e
         _rows(total, "total", shape, st, dev)   # before an output takes its shape
         dresidual, res = _out(dresidual, "dresidual", total, st, dev)
     dweight = None if weight is None else torch.empty_like(weight)
-    dbias = dy.new_empty(c, dtype=f32) if bias else None
+    dbias = None if not bias else dy.new_empty(c, dtype=f32) if weight is None else torch.empty_like(weight)
     packed = _ADDNORM.pack(*shape, flags, eps, *_NO_ROWS * 2, _flat(weight, "weight", c, f32, dev), 0, *_NO_ROWS,
                            *_rows(total, "total", shape, st, dev), *_rows(dy, "dy", shape, dtype, dev),
                            *(_NO_ROWS if dtotal is None else _rows(dtotal, "dtotal", shape, st, dev)),
