@@ -31,6 +31,9 @@ using namespace addnorm;
 // [4, 4096, 4096] 193 and 177); below three of bf16 or of a vector a lane ([4, 4096, 2560]: 90 us, two 104, four 112) and
 // two else ([4, 4096, 2048] with a stream of fp32 96 us, three 113).  One on each CU, and more only where each has eight
 // rows (bf16 [2, 1024, 8192] 49 us, twice as many 65).
+//
+// Up to eight rows, two for each that a workgroup holds, go to one, whose sums are the gradients: no workspace, no
+// second launch (bf16 [1, 8, 1024] from Python 10.2 us, else 14.1; eight for each, [1, 8, 4096], 21 and 14.2).
 RowMap map_of(const AddNormProblem& p)
 {
     const int nv = vectors(p);
@@ -38,7 +41,8 @@ RowMap map_of(const AddNormProblem& p)
     RowMap m = row_map(p, half && nv > 512 && nv <= 1024 ? 1 : most_vectors(p), ~0u, true);
     const unsigned wide = !p.bf16 && m.L <= 384 ? 512 : 256;
     const unsigned cap = m.threads > 256 ? wide : half || nv <= m.L ? 768 : 512;
-    m.blocks = std::min(m.blocks, std::min(cap, std::max(m.rows / 8, 256u)));
+    m.only = m.rows <= (unsigned)std::min(8, 2 * m.slots);
+    m.blocks = m.only ? 1 : std::min(m.blocks, std::min(cap, std::max(m.rows / 8, 256u)));
     return m;
 }
 
@@ -145,20 +149,23 @@ __global__ __launch_bounds__(THREADS) void addnorm_bwd_kernel(AddNormProblem p, 
     }
     if (!p.dweight && !p.dbias) return;
     float* part = (float*)p.ws + (int64_t)blockIdx.x * 2 * p.C;
+    float *pw = m.only ? p.dweight : part, *pb = m.only ? p.dbias : part + p.C;
     if (m.slots == 1) {
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
             for (int v = 0; v < VEC; ++v)
                 if (cols.in[k]) {
-                    part[c[k] + v] = dw[k][v];
-                    part[p.C + c[k] + v] = db[k][v];
+                    if (pw) pw[c[k] + v] = dw[k][v];
+                    if (pb) pb[c[k] + v] = db[k][v];
                 }
         return;
     }
     if constexpr (THREADS == 256) {
         // the slots' sums in order
         for (int which = 0; which < 2; ++which) {
+            float* to = which ? pb : pw;
+            if (!to) continue;
             __syncthreads();
 #pragma unroll
             for (int k = 0; k < NV; ++k)
@@ -170,7 +177,7 @@ __global__ __launch_bounds__(THREADS) void addnorm_bwd_kernel(AddNormProblem p, 
                 const int k = e / n, at = e % n, i = k * m.L + at / VEC;
                 float s = 0.0f;
                 for (int j = 0; j < m.slots; ++j) s += acc[k * 256 * VEC + j * n + at];
-                if (i < m.nv) part[which * p.C + column<VEC, EDGE>(i, p.C) + at % VEC] = s;
+                if (i < m.nv) to[column<VEC, EDGE>(i, p.C) + at % VEC] = s;
             }
         }
     }
@@ -269,14 +276,14 @@ hipError_t bwd_n(const AddNormProblem& p, hipStream_t stream)
     if constexpr (sizeof(T) == 2 && sizeof(S) == 2)
         if (m.threads > 256 && v == 1) {
             addnorm_bwd_kernel<T, S, 1, 1024, EDGE, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
-            return params(p, m.blocks, stream);
+            return m.only ? hipGetLastError() : params(p, m.blocks, stream);
         }
     if (m.threads > 512) addnorm_bwd_kernel<T, S, most, 1024, EDGE, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
     else if (m.threads > 256) addnorm_bwd_kernel<T, S, most, 512, EDGE, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
     else if (v == 1) addnorm_bwd_kernel<T, S, 1, 256, EDGE, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
     else if (v == 2) addnorm_bwd_kernel<T, S, 2, 256, EDGE, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
     else if constexpr (most == 4) addnorm_bwd_kernel<T, S, 4, 256, EDGE, NT><<<m.blocks, m.threads, 0, stream>>>(p, m);
-    return params(p, m.blocks, stream);
+    return m.only ? hipGetLastError() : params(p, m.blocks, stream);
 }
 
 template <typename T, typename S>
@@ -304,7 +311,8 @@ hipError_t bwd_t(const AddNormProblem& p, hipStream_t stream)
 size_t addnorm_bwd_workspace(const AddNormProblem& p)
 {
     const size_t row = 2 * (size_t)p.C * sizeof(float);
-    return in_registers(p) ? map_of(p).blocks * row : align256((size_t)runs_of(p) * row) + (size_t)p.B * p.T * sizeof(f32x2);
+    if (in_registers(p)) return map_of(p).only ? 0 : map_of(p).blocks * row;
+    return align256((size_t)runs_of(p) * row) + (size_t)p.B * p.T * sizeof(f32x2);
 }
 
 hipError_t launch_addnorm_bwd(const AddNormProblem& p, hipStream_t stream)

@@ -60,6 +60,7 @@ template <int VEC, int NV, bool EDGE> struct Columns {
 struct RowMap {
     int L, nv, slots, threads;
     unsigned rows, blocks;
+    bool only = false;   // backward: the one workgroup's sums are the weights' gradients
 };
 
 // Vectors a lane holds at most: 16 values of either type, 8 of fp32 alone.

@@ -274,6 +274,16 @@ def test_many_rows_of_odd_widths(act, stream, C):
 
 
 @pytest.mark.parametrize("act,stream", TYPES)
+@pytest.mark.parametrize("C", [8, 40, 382, 4096, 5761])
+@pytest.mark.parametrize("T", [1, 4, 8, 9])
+def test_few_rows(act, stream, T, C):
+    """One workgroup for all rows, and more."""
+    check(act, stream, 1, T, C)
+    check(act, stream, 1, T, C, bias=False)
+    check(act, stream, 1, T, C, affine=False)
+
+
+@pytest.mark.parametrize("act,stream", TYPES)
 @pytest.mark.parametrize("C", [3, 8, 13, 269, 1025])
 def test_what_lies_between_rows(act, stream, C):
     """Columns beside the rows: NaN read from there would show, and what lies there stays."""
