@@ -57,7 +57,9 @@ template <typename T, int KIND> __device__ __forceinline__ Gate gate_of(float u,
     if (KIND == kCoupled) {
         const float e = exp_t<T>(-u);
         g.f = __builtin_amdgcn_rcpf(1.0f + e);
-        g.i = e == __builtin_inff() ? 1.0f : e * g.f;   // 1 - f without its cancellation
+        // 1 - f without its cancellation; from e = 2^25 on it rounds to 1, and above 2^126, where the reciprocal is below
+        // the smallest normal number, v_rcp_f32 gives f = 0, of which e f would make 0 (of an infinite e NaN)
+        g.i = e >= 0x1p60f ? 1.0f : e * g.f;
     } else {
         g.s = sigmoid_t<T>(v);
         g.r = sigmoid_t<T>(u);

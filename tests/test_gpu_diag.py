@@ -461,3 +461,59 @@ def test_a_states_copy_serves_every_segment():
     pairs = ws.view(torch.float32).view(-1, 2)
     held = [i for i in range(0, pairs.shape[0] - 63, 64) if torch.equal(pairs[i:i + 64, 1], before[0])]
     assert held and not torch.equal(st, before)
+
+
+def compare(dtype, kind, dev, ref, lengths=None, extra=0.0):
+    """A forward and a backward call on the tensors of `dev` against the reference on `ref`; extra: added to every bound."""
+    B, T, D = ref["x"].shape
+    print("diag", dtype, kind, B, T, D, lengths, flush=True)
+    d = {k: cuda(v) for k, v in dev.items()}
+    kw = dict(kind=KIND[kind], lengths=d["lengths"])
+    y, end, starts = tfla.diag_forward(d["x"], d["fg"], d["ig"], d["decay"], state=d["state"], want_state=True, want_starts=True,
+                                       **kw)
+    g = tfla.diag_backward(d["x"], d["fg"], d["dy"], starts, d["ig"], d["decay"], dstate_out=d["dend"], want_dstate=True, **kw)
+    torch.cuda.synchronize()
+    want, tol = reference(ref, kind, lengths)
+    rows = np.arange(0, T, tfla.DIAG_CHUNK)
+    within("starts", starts, want["before"][:, rows], tol["before"][:, rows] + 1e-37 + extra)
+    for name, got, half in (("y", y, HALF[dtype]), ("end", end, U), ("dx", g.dx, HALF[dtype]), ("dfgate", g.dfgate, HALF[dtype]),
+                            ("digate", g.digate, HALF[dtype]), ("ddecay", g.ddecay, U), ("dstate", g.dstate, U)):
+        if got is not None:
+            within(f"{kind} {name}", got, want[name], half * np.abs(want[name]) + tol[name] + 1e-36 + extra)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T", [1, 12, 40, 140])
+def test_gates_whose_reciprocal_is_below_the_smallest_number(dtype, kind, T):
+    """Pre-activations around -88, where 1 / (1 + e^-u) is finite and below 2^-126, and as far on the other side: a single
+    token, a short axis, tiles."""
+    u = torch.tensor([87.0, 87.25, 87.5, 88.0, 88.5, 88.7, 88.75, 89.0])
+    u = torch.cat([u, -u])
+    D = 4 * len(u)
+    for which in ("fg", "ig"):
+        if which == "ig" and kind == "coupled":
+            continue
+        dev, ref = make(dtype, kind, 2, T, D)
+        gate = u.repeat_interleave(4).expand(2, T, D).contiguous().to(dtype)
+        gate[:, :, 3::4] = dev[which][:, :, 3::4]          # every fourth channel ordinary, and every third row of others
+        gate[:, ::3, 2::4] = dev[which][:, ::3, 2::4]
+        dev[which], ref[which] = gate, gate.double().numpy()
+        # A sigmoid below 2^-126 may come out 0: f and i are off by that, and with a decay w by 2^-125, sqrt(1 - f^2) by
+        # 2^-62 (decay <= 2), what the root's slope leaves out of du by sqrt(w / 2), of ddecay by sqrt(s(u) / 2 decay), at
+        # most 2^-58 (decay >= 1e-3).  Each is met with |x g| at most: x and dy below 5, g a sum of T + 1 terms, T + 1 rows
+        # of two sequences to a sum.
+        compare(dtype, kind, dev, ref, extra=(2.0 ** -58 if kind == "decay" else 2.0 ** -126) * 25 * 2 * (T + 1) ** 2)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [1, 40])
+def test_a_closed_coupled_gate_passes_its_input(dtype, T):
+    """f below 2^-126 and i = 1: rows are their inputs and dx is dy, to the last bit."""
+    x, dy = (torch.randn(2, T, 64, device="cuda").to(dtype) for _ in range(2))
+    for u in (-87.5, -88.0, -88.5, -100.0, -float("inf")):
+        fg = torch.full_like(x, u)
+        y, end, starts = tfla.diag_forward(x, fg, state=torch.ones(2, 64, device="cuda"), want_state=True, want_starts=True)
+        g = tfla.diag_backward(x, fg, dy, starts)
+        torch.cuda.synchronize()
+        assert torch.equal(y, x) and torch.equal(end, x[:, -1].float()) and torch.equal(g.dx, dy), u
