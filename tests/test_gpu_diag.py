@@ -517,3 +517,35 @@ def test_a_closed_coupled_gate_passes_its_input(dtype, T):
         g = tfla.diag_backward(x, fg, dy, starts)
         torch.cuda.synchronize()
         assert torch.equal(y, x) and torch.equal(end, x[:, -1].float()) and torch.equal(g.dx, dy), u
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("B,T,D,lengths", [
+    (2, 600, 4160, (600, 430)),          # 64 channels, whole axes of 5 tiles on lines
+    (3, 640, 2816, (640, 512, 301)),     # the same, ending with a tile
+    (2, 600, 4161, (513, 600)),          # off the lines
+    (3, 5200, 512, (5200, 3000, 4480)),  # 64 channels in segments of 5 tiles
+    (2, 2000, 520, (2000, 1300)),        # 16 channels forward, tiles of 512 rows
+    (2, 1100, 2560, (1100, 900)),        # 32 channels, tiles of 256
+    (2, 2100, 2560, (2100, 1025)),       # 32 forward; backward 32 in fp32, segments in bf16
+    (1, 2100, 4096, (2100,)),            # 16 channels forward in fp32, segments else
+])
+def test_walks_of_several_tiles(dtype, kind, B, T, D, lengths):
+    """Tiles whose loads were issued in the loop, not before it."""
+    dev, ref = make(dtype, kind, B, T, D, lengths=lengths)
+    compare(dtype, kind, dev, ref, lengths)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,T,D", [(2, 600, 4160), (1, 3000, 200)])
+def test_walks_of_several_tiles_over_shared_rows(dtype, B, T, D):
+    """Rows that share memory (a stride of 0) go by 64-bit addresses: whole axes and segments, ragged."""
+    lengths = [T - 170 * b - 5 for b in range(B)]
+    for kind in KINDS:
+        dev, ref = make(dtype, kind, B, T, D)
+        for k in ("fg", "dy"):
+            dev[k] = dev[k][:, :1].cuda().expand(B, T, D)
+            ref[k] = np.broadcast_to(ref[k][:, :1], (B, T, D))
+        dev["lengths"] = torch.tensor(lengths, dtype=torch.int32)
+        compare(dtype, kind, dev, ref, lengths)
