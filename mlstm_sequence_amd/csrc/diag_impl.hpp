@@ -25,7 +25,8 @@ __device__ __forceinline__ int clamp_len(const int* lengths, int b, int T)
 template <typename T> __device__ __forceinline__ float exp_t(float x) { return sizeof(T) == 2 ? exp2_fast(x * kLog2e) : exp_f(x); }
 
 // 1 - f^2 = 1 - e^{-z}, z = 2 w: below 0.4, where the difference would cancel, z times a polynomial of degree 4 fitted
-// to (1 - e^{-z}) / z on [0, 0.4] (Chebyshev nodes; off by 0.9 half steps at most).
+// to (1 - e^{-z}) / z on [0, 0.4] (Chebyshev nodes).  The fit is off by 0.9 half steps at most, its value in fp32 by 1.6
+// and the product by 2.4 (the worst of five million z).
 __device__ __forceinline__ float one_minus_square(float z, float f)
 {
     float s = fmaf(z, 7.0668478e-3f, -4.1237194e-2f);
