@@ -8,7 +8,7 @@
 // gradients add up in registers over the rows that a workgroup takes and
 // leave it once, to be added over the workgroups in a fixed order.  Bound by
 // memory: the stream, its gradient and dy are read once, dt written once.
-// [8, 4096, 4096] of bf16: 1.07 GB in 207 us (5.2 TB/s; a copy moves 5.0).
+// [8, 4096, 4096] of bf16: 1.07 GB in 213 us (5.0 TB/s, as a copy).
 #include "gfx950.hpp"
 
 #include <algorithm>
@@ -26,10 +26,12 @@ using namespace addnorm;
 // bf16 rows of 512 to 1024 vectors take one vector a lane ([4, 4096, 5120] 188 us, two 218; [4, 4096, 8192] 226 and 253),
 // not fp32 ones ([4, 4096, 2560]: 176 and 124) nor those of both types ([4, 4096, 4096]: 215, four 208).
 //
-// At most as many workgroups as the chip holds, by the registers of their variant: beyond 256 lanes to a row one on a CU
-// (bf16 [4, 4096, 5120]: 188 us, two 198, three 208), with fp32 alone two up to 384 ([4, 4096, 2560]: 124 us, one 133;
-// [4, 4096, 4096] 193 and 177); below three of bf16 or of a vector a lane ([4, 4096, 2560]: 90 us, two 104, four 112) and
-// two else ([4, 4096, 2048] with a stream of fp32 96 us, three 113).  One on each CU, and more only where each has eight
+// At most as many workgroups as the chip holds, by the registers of their variant: beyond 256 lanes to a row one on a CU,
+// since a CU has 16 waves of bf16 (107 registers), whose rows take nine or more, and eight of both types (198), whose rows
+// take five or more; a second or third for each CU only comes after the first and leaves sums of its own (bf16 [4, 4096,
+// 5120]: 188 us, 198, 208).  With fp32 alone two up to 384 ([4, 4096, 2560]: 124 us, one 133; [4, 4096, 4096] 193 and 177);
+// below three of bf16 or of a vector a lane ([4, 4096, 2560]: 90 us, two 104, four 112) and two else ([4, 4096, 2048] with
+// a stream of fp32 96 us, three 113).  One on each CU, and more only where each has eight
 // rows (bf16 [2, 1024, 8192] 49 us, twice as many 65).
 //
 // Up to eight rows, two for each that a workgroup holds, go to one, whose sums are the gradients: no workspace, no
@@ -54,7 +56,8 @@ bool streams(const AddNormProblem& p)
     return (int64_t)p.B * p.T * p.C * (2 * e + (p.dtotal.p ? 2 : 1) * es) >= (int64_t(256) << 20);
 }
 
-// THREADS: the workgroup's size is at most that.
+// THREADS: the workgroup's size is at most that.  1024 leave a lane 128 registers: bf16 rows of more than 8192 channels
+// keep 47 to 51 values in scratch, those with a stream of fp32 100; no other variant keeps any.
 template <typename T, typename S, int NV, int THREADS, bool EDGE, bool NT>
 __global__ __launch_bounds__(THREADS) void addnorm_bwd_kernel(AddNormProblem p, RowMap m)
 {
