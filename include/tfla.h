@@ -649,6 +649,10 @@ int tfla_rotary_bwd(const tfla_rotary_args* args, void* stream);
  * receives the states before rows 0, TFLA_DIAG_CHUNK, 2 TFLA_DIAG_CHUNK, ...:
  * what the backward pass starts from.
  *
+ * Rows are joined as maps h -> F h + H in fp32, F a product of f: what an F
+ * below 2^-126 leaves of a state may be lost (under 2^-26, the state being
+ * below 2^100), and it leaves NaN of an infinite state.
+ *
  *   B, T, D >= 1, B T <= 2^30, D <= 2^24
  *   x, fgate, igate, y  [B,T,D]; igate only where the kind has it (not looked at else)
  *   decay [D], >= 0, for TFLA_DIAG_DECAY (not looked at else); state, state_out [B,D] or NULL;
