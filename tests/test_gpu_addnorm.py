@@ -324,3 +324,29 @@ def test_a_call_that_streams():
     # sums of 40000 terms in two orders; |th| is at most 6 here
     assert bool(((dw - sum(p[2] for p in parts)).abs() <= 2 * 40100 * U * 6 * mag.sum((0, 1))).all())
     assert bool(((db - sum(p[3] for p in parts)).abs() <= 2 * 40100 * U * mag.sum((0, 1))).all())
+
+
+@pytest.mark.parametrize("act,stream", TYPES)
+@pytest.mark.parametrize("B,T,C", [(2, 1100, 2560), (2, 1100, 4096), (3, 700, 4099), (3, 700, 5120), (2, 600, 8192), (2, 600, 8199),
+                                   (2, 560, 16384)])
+def test_many_wide_rows(act, stream, B, T, C):
+    """Rows of several waves, more of them than workgroups take at once in either direction."""
+    check(act, stream, B, T, C, rms=C == 5120)
+
+
+@pytest.mark.parametrize("act,stream", TYPES)
+@pytest.mark.parametrize("C", [4096, 5120, 5125, 10000])
+def test_wide_calls_that_stream(act, stream, C):
+    """Wide rows in calls large enough for loads past the caches, against the same rows in calls that are not."""
+    T = (36 << 20) // C                                  # 8 to 16 bytes an element are read and written: above 256 MiB
+    t, dt = (torch.randn(1, T, C, device="cuda").to(stream) for _ in range(2))
+    dy, w = torch.randn(1, T, C, device="cuda").to(act), torch.randn(C, device="cuda")
+    dx, dr, dw, db = tfla.addnorm_backward(t, dy, w, bias=True, dtotal=dt)
+    parts = [tfla.addnorm_backward(t[:, a:b], dy[:, a:b], w, bias=True, dtotal=dt[:, a:b])
+             for a, b in zip(range(0, T, T // 4), [*range(T // 4, T, T // 4), T])]
+    torch.cuda.synchronize()
+    assert torch.equal(dx, torch.cat([p[0] for p in parts], 1)) and torch.equal(dr, torch.cat([p[1] for p in parts], 1))
+    mag, n = dy.double().abs().sum((0, 1)), T + 100
+    # sums of T terms in two orders; |th| is at most 6 here
+    assert bool(((dw - sum(p[2] for p in parts)).abs() <= 2 * n * U * 6 * mag).all())
+    assert bool(((db - sum(p[3] for p in parts)).abs() <= 2 * n * U * mag).all())
